@@ -286,6 +286,103 @@ int semicrf_logz_static(const float* emissions, const int32_t* lengths, const fl
  * length was outside [1, T], or SEMICRF_ERR_DEVICE if the copy failed. */
 int semicrf_read_status(const void* workspace, hipStream_t stream);
 
+/* ------------------------------------------------------------------ encoder operators
+ * What makes the emissions: an embedding of tokens, layer norm, and linear attention with a
+ * decay for each head, whose cost is linear in T like the CRF's.  Conventions as above
+ * (device pointers, work enqueued on `stream`, no allocation, status codes, fixed-order
+ * sums), and:
+ *  - dtype is the type of the arrays given as void*: SEMICRF_F32 or SEMICRF_BF16.  Sums,
+ *    statistics and states are held in float32; an output is rounded once.
+ *  - lengths [B] int32 may be NULL (every length is T), and here a length may be 0.  A
+ *    length outside [0, T] is taken as clamped.  What lies at t >= lengths[b] is not read,
+ *    whatever it holds, and outputs are 0 there.
+ *  - status: NULL, or a device word the caller has cleared; the call sets bit 0 in it when a
+ *    length, or a token, was out of range.
+ *  - B * T and V are below 2^30, B below 2^16 for the attention calls (else
+ *    SEMICRF_ERR_UNSUPPORTED).  Arrays need the alignment of their elements only. */
+typedef enum { SEMICRF_F32 = 0, SEMICRF_BF16 = 1 } semicrf_dtype;
+
+/* out[b, t, :] = scale * table[tokens[b, t], :].  tokens [B, T] int32 or int64 (token_bits 32
+ * or 64), table [V, N], out [B, T, N].  A token outside [0, V) gives a row of NaN. */
+int semicrf_embed(const void* tokens, int token_bits, const int32_t* lengths, const void* table,
+                  int dtype, int B, int T, int V, int N, float scale, hipStream_t stream,
+                  void* out, int32_t* status);
+
+/* grad_table[v, :] = scale * sum of grad_out[b, t, :] over the positions with token v (0 for a
+ * token that does not appear; a token outside [0, V) counts for nothing).  Positions are
+ * sorted by token and each row's sum has a fixed order.  Workspace:
+ * semicrf_embed_grad_bytes, 256-byte aligned. */
+size_t semicrf_embed_grad_bytes(int dtype, int B, int T, int V, int N);
+int semicrf_embed_grad(const void* tokens, int token_bits, const int32_t* lengths,
+                       const void* grad_out, int dtype, int B, int T, int V, int N, float scale,
+                       hipStream_t stream, void* workspace, size_t workspace_bytes,
+                       void* grad_table, int32_t* status);
+
+/* Layer norm of each row of x [B, T, N]: y = (x - mean) * rstd * weight + bias with rstd =
+ * 1 / sqrt(variance + eps).  weight, bias [N] of type wdtype (dtype or SEMICRF_F32), or NULL
+ * for ones and zeros.  mean, rstd [B, T] float32 (0 at padding), or NULL.  N <= 32768. */
+int semicrf_layer_norm(const void* x, int dtype, const void* weight, const void* bias, int wdtype,
+                       const int32_t* lengths, int B, int T, int N, float eps, hipStream_t stream,
+                       void* y, float* mean, float* rstd, int32_t* status);
+
+/* Its gradients from the mean and rstd the forward call left: grad_x [B, T, N] and, summed over
+ * all rows, grad_weight and grad_bias [N] of type wdtype (each may be NULL).  Workspace:
+ * semicrf_layer_norm_grad_bytes, 256-byte aligned. */
+size_t semicrf_layer_norm_grad_bytes(int dtype, int B, int T, int N);
+int semicrf_layer_norm_grad(const void* grad_out, const void* x, int dtype, const void* weight,
+                            int wdtype, const float* mean, const float* rstd,
+                            const int32_t* lengths, int B, int T, int N, hipStream_t stream,
+                            void* workspace, size_t workspace_bytes, void* grad_x,
+                            void* grad_weight, void* grad_bias, int32_t* status);
+
+/* Linear attention with a decay for each head:
+ *   S_t = gamma_h S_{t-1} + k_t v_t^T,   o_t = scale * q_t^T S_t,   gamma_h = exp(log_decay[h]),
+ * S [Dk, Dv] for every sequence and query head, starting from `state` or 0.  Query head h reads
+ * key / value head h / (Hq / Hk).  log_decay [Hq] is meant to be <= 0 (-inf forgets everything
+ * but the position itself).  A value that is not finite, at a position before the length, may
+ * spoil the outputs of up to 63 positions before it, and all after it. */
+typedef struct semicrf_attention {
+    const void* q;               /* [B, T, Hq, Dk] */
+    const void* k;               /* [B, T, Hk, Dk] */
+    const void* v;               /* [B, T, Hk, Dv] */
+    int64_t q_stride[3];         /* elements between sequences, positions, heads; the last */
+    int64_t k_stride[3];         /* axis is dense */
+    int64_t v_stride[3];
+    const int32_t* lengths;      /* [B] or NULL */
+    const float* log_decay;      /* [Hq] */
+    const float* state;          /* [B, Hq, Dk, Dv] before the first position, or NULL for 0 */
+    float scale;
+    int dtype;                   /* of q, k, v and the outputs shaped like them */
+    int B, T, Hq, Hk, Dk, Dv;    /* Hq a multiple of Hk; Dk, Dv <= 128 */
+} semicrf_attention;
+
+/* Whole sequences.  out [B, T, Hq, Dv] dense; state_out [B, Hq, Dk, Dv] float32 after position
+ * lengths[b] - 1, or NULL (it may be the array `state` points to).  Workspace:
+ * semicrf_decay_attention_bytes(attention, 0), 256-byte aligned. */
+size_t semicrf_decay_attention_bytes(const semicrf_attention* attention, int grad);
+int semicrf_decay_attention(const semicrf_attention* attention, hipStream_t stream,
+                            void* workspace, size_t workspace_bytes, void* out,
+                            float* state_out, int32_t* status);
+
+/* Gradients: of out (grad_out [B, T, Hq, Dv], dense) and of state_out (grad_state_out [B, Hq,
+ * Dk, Dv] float32, or NULL for 0).  grad_q [B, T, Hq, Dk], grad_k [B, T, Hk, Dk], grad_v [B, T,
+ * Hk, Dv], dense, shared heads summed; grad_state [B, Hq, Dk, Dv] float32 or NULL.  The decay
+ * is a constant of the head: it has no gradient.  Workspace:
+ * semicrf_decay_attention_bytes(attention, 1). */
+int semicrf_decay_attention_grad(const semicrf_attention* attention, const void* grad_out,
+                                 const float* grad_state_out, hipStream_t stream, void* workspace,
+                                 size_t workspace_bytes, void* grad_q, void* grad_k, void* grad_v,
+                                 float* grad_state, int32_t* status);
+
+/* One token of B streams (attention->T is 1, lengths NULL): the recurrence once, on states
+ * kept in a pool.  attention->state and state_out are [pool, Hq, Dk, Dv] float32 and may be the
+ * same array; stream b uses row slots[b] (b itself where slots is NULL, then pool >= B).  A
+ * slot outside [0, pool) marks an idle row: its output is 0 and no state is touched.  The
+ * slots in [0, pool) must be distinct.  Rows of state_out that no slot names are left alone.
+ * out [B, Hq, Dv]. */
+int semicrf_decay_attention_step(const semicrf_attention* attention, const int32_t* slots,
+                                 int pool, hipStream_t stream, void* out, float* state_out);
+
 #ifdef __cplusplus
 }
 #endif

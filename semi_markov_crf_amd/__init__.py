@@ -15,6 +15,9 @@ Shapes: em [B, T, C] float32, lengths [B] int32, trans [C, C] float32 (row =
 previous label), dur [K, C] float32 (row k-1 scores length k).  Every call also
 takes optional boundary projections proj_start / proj_end [B, T, C] float32: a
 segment [s, e) of label c gains proj_start[b, s, c] + proj_end[b, e-1, c].
+
+The operators of an encoder that makes the emissions (embedding, layer norm, decayed linear
+attention, each with its gradient) are in ``encoder`` and are exported here too.
 """
 
 from __future__ import annotations
@@ -23,10 +26,14 @@ import torch
 
 from . import _native
 from ._native import OP_BACKWARD, OP_LOGZ, OP_PREFIX, OP_VITERBI, SemiCRFError
+from .encoder import (decay_attention, decay_attention_grad, decay_attention_step, embed,
+                      embed_grad, layer_norm, layer_norm_grad)
 
 __all__ = ["prefix", "logz", "backward", "viterbi", "nll", "log_partition", "workspace_bytes",
            "checkpoint_interval", "default_interval", "read_status", "SemiCRFError",
-           "OP_LOGZ", "OP_BACKWARD", "OP_VITERBI", "OP_PREFIX"]
+           "OP_LOGZ", "OP_BACKWARD", "OP_VITERBI", "OP_PREFIX",
+           "embed", "embed_grad", "layer_norm", "layer_norm_grad", "decay_attention",
+           "decay_attention_grad", "decay_attention_step"]
 
 
 def checkpoint_interval(T: int, K: int, delta: int = 0) -> int:

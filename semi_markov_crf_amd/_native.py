@@ -15,11 +15,13 @@ import torch  # noqa: F401  (must precede the dlopen below, see module docstring
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsemicrf.so")
 
 OP_LOGZ, OP_BACKWARD, OP_VITERBI, OP_PREFIX = 0, 1, 2, 3
+F32, BF16 = 0, 1      # semicrf_dtype
 STATUS_NAMES = {0: "SEMICRF_OK", 1: "SEMICRF_ERR_INVALID", 2: "SEMICRF_ERR_WORKSPACE",
                 3: "SEMICRF_ERR_UNSUPPORTED", 4: "SEMICRF_ERR_DEVICE",
                 5: "SEMICRF_ERR_UNIMPLEMENTED"}
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_c_float, _strides = ctypes.c_float, ctypes.c_int64 * 3
 
 
 class Options(ctypes.Structure):
@@ -30,7 +32,17 @@ class Options(ctypes.Structure):
                 ("seam_tolerance", ctypes.c_double)]
 
 
+class Attention(ctypes.Structure):
+    """struct semicrf_attention (include/semicrf.h), field for field."""
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_stride", _strides),
+                ("k_stride", _strides), ("v_stride", _strides), ("lengths", _vp),
+                ("log_decay", _vp), ("state", _vp), ("scale", _c_float), ("dtype", _c_int),
+                ("B", _c_int), ("T", _c_int), ("Hq", _c_int), ("Hk", _c_int), ("Dk", _c_int),
+                ("Dv", _c_int)]
+
+
 _opt = ctypes.POINTER(Options)
+_att = ctypes.POINTER(Attention)
 
 # the problem statement's argument lists: (emissions, lengths, trans, dur, B, T, C, K, ...)
 _LOGZ = [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_size, _vp]
@@ -56,6 +68,21 @@ SIGNATURES = {
     "semicrf_read_status": (_c_int, [_vp, _vp]),
     "semicrf_logz_static": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                      _vp, _vp]),
+    "semicrf_embed": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                               _c_float, _vp, _vp, _vp]),
+    "semicrf_embed_grad_bytes": (_c_size, [_c_int] * 5),
+    "semicrf_embed_grad": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                    _c_float, _vp, _vp, _c_size, _vp, _vp]),
+    "semicrf_layer_norm": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
+                                    _c_float, _vp, _vp, _vp, _vp, _vp]),
+    "semicrf_layer_norm_grad_bytes": (_c_size, [_c_int] * 4),
+    "semicrf_layer_norm_grad": (_c_int, [_vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _vp, _c_int,
+                                         _c_int, _c_int, _vp, _vp, _c_size, _vp, _vp, _vp, _vp]),
+    "semicrf_decay_attention_bytes": (_c_size, [_att, _c_int]),
+    "semicrf_decay_attention": (_c_int, [_att, _vp, _vp, _c_size, _vp, _vp, _vp]),
+    "semicrf_decay_attention_grad": (_c_int, [_att, _vp, _vp, _vp, _vp, _c_size, _vp, _vp, _vp,
+                                              _vp, _vp]),
+    "semicrf_decay_attention_step": (_c_int, [_att, _vp, _c_int, _vp, _vp, _vp]),
 }
 STATIC_SCRATCH_BYTES = 32 << 20
 STAGES = {"logz": 2, "backward": 5, "viterbi": 3}

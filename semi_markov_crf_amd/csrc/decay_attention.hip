@@ -1,0 +1,752 @@
+// Linear attention with a decay for each head, on gfx950: whole sequences in chunks, forward
+// and backward, and one token at a time.
+//
+//   S_t = gamma S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t,   gamma = exp(log_decay[h])
+//
+// One sweep does it all.  It takes three roles a, b [., Da] and c [., Dc] and a state
+// S [Da, Dc], and for each chunk of C positions (i, j local)
+//
+//   out_i = scale sum_{j <= i} gamma^(i-j) (a_i . b_j) c_j + si gamma^(i+1-e) a_i S
+//   S     = gamma^C S + su sum_j gamma^(C-1-j+e) b_j c_j^T
+//
+//   forward  a, b, c = q, k, v          in order,  state S,   e = 0, si = scale, su = 1
+//   dq       a, b, c = do, v, k         in order,  state S^T, e = 0, si = scale, su = 1
+//   dv       a, b, c = k, q, do         reversed,  state R,   e = 1, si = 1, su = scale
+//   dk       a, b, c = v, do, q         reversed,  state R^T, e = 1, si = 1, su = scale
+//
+// R is what the later positions send back, R = sum gamma^(i-j) scale q_i do_i^T, and starts
+// from the gradient of the final state; at the end it is the gradient of the initial one.
+//
+// A long sequence is cut into segments: k_attn_state sweeps every segment's state alone from
+// zero, k_attn_scan joins them in order, and the sweep then runs over all segments at once,
+// each from its own start.
+//
+// The products run on the matrix cores.  A wavefront owns VT columns tiles of c (and of the
+// state, which stays in fp32 accumulators for the whole sweep) and all rows; the masked
+// products a.b^T of a chunk are shared out by rows and exchanged through LDS.
+//
+// Rounding (bfloat16): inputs are exact.  The masked products are rounded to bfloat16 once
+// before the second product, like the output.  The state is taken as the sum of two bfloat16
+// numbers (16 bits) when rows read it, and c scaled by its decay as the sum of three (24 bits)
+// when the state is updated, so that the state itself keeps fp32 accuracy.
+#include "common.h"
+#include "encoder.h"
+
+namespace semicrf {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// ------------------------------------------------------------------ matrix products
+// A product step contracts KS indices.  Lane l = 16 g + r holds E consecutive contraction
+// indices E g .. E g + E - 1 of row (or column) r: 16 bytes of a row.  The result tile holds
+// column r, rows 4 g .. 4 g + 3.
+template <class T>
+struct Mma;
+
+template <>
+struct Mma<bf16> {
+    static constexpr int E = 8, KS = 32;
+    typedef bf16x8 Frag;
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <>
+struct Mma<float> {
+    static constexpr int E = 4, KS = 16;
+    typedef f32x4 Frag;
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// Row of the state that tile `t` holds at its row `rho`: chosen so that the accumulator tiles
+// of the state are, as they lie in registers, the right operand of a product step.
+template <class T>
+__device__ __forceinline__ constexpr int state_row(int t, int rho) {
+    return sizeof(T) == 4 ? 16 * t + rho : 32 * (t >> 1) + 8 * (rho >> 2) + 4 * (t & 1) + (rho & 3);
+}
+
+// 16 bytes of row `row + r`, contraction indices from k0
+template <class T>
+__device__ __forceinline__ typename Mma<T>::Frag frag_row(const T* buf, int ld, int row, int k0) {
+    const int l = threadIdx.x & 63;
+    return *(const typename Mma<T>::Frag*)(buf + (row + (l & 15)) * ld + k0 + (l >> 4) * Mma<T>::E);
+}
+
+// Columns as rows: element j of the lane is buf[k0 + E g + j][col(r)], with col(r) = c0 + r, or
+// with PERM the state row of tile `t` (c0 is then the tile number).
+template <bool PERM>
+__device__ __forceinline__ bf16x8 frag_col(const bf16* buf, int ld, int k0, int c0) {
+    // the transposing read gives lane 16 g + i the i-th column of the 4 x 16 block whose row j
+    // is what lanes 16 g + 4 j .. + 3 point at, four elements each
+    const int l = threadIdx.x & 63, g = l >> 4, p = l & 15;
+    const int col = PERM ? state_row<bf16>(c0, 4 * (p & 3)) : c0 + 4 * (p & 3);
+    typedef __attribute__((address_space(3))) bf16x4 Lds;
+    const bf16* at = buf + (k0 + 8 * g + (p >> 2)) * ld + col;
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds*)at);
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds*)(at + 4 * ld));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <bool PERM>
+__device__ __forceinline__ f32x4 frag_col(const float* buf, int ld, int k0, int c0) {
+    const int l = threadIdx.x & 63, g = l >> 4, r = l & 15;
+    const float* at = buf + (k0 + 4 * g) * ld + (PERM ? 16 * c0 : c0) + r;
+    return f32x4{at[0], at[ld], at[2 * ld], at[3 * ld]};
+}
+
+// Parts of an fp32 fragment that add up to it: one in fp32, n in bfloat16 (8 bits each).
+template <class T, int N>
+struct Parts {
+    typename Mma<T>::Frag f[N];
+    __device__ __forceinline__ void set(int j, float x) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const T h = (T)x;
+            f[n][j] = h;
+            x -= (float)h;
+        }
+    }
+};
+template <class T>
+constexpr int state_parts() { return sizeof(T) == 4 ? 1 : 2; }
+template <class T>
+constexpr int update_parts() { return sizeof(T) == 4 ? 1 : 3; }
+
+// ------------------------------------------------------------------ a sweep
+struct Role {
+    const void* p;
+    long sb, st, sh;         // strides in elements
+    int group;               // query heads that share a head of this role
+};
+
+struct Sweep {
+    Role a, b, c;
+    int B, T, H, Da, Dc;     // H: query heads
+    const int32_t* lengths;
+    const float* log_decay;
+    float scale, si, su;
+    int e, reverse;
+    int seg, nseg;           // positions per segment (a multiple of the chunk), segments
+    const float* state;      // start of every segment [B, H, nseg, ...] or NULL for zeros
+    int state_nseg;          // segments of `state`
+    int transposed;          // the state in memory is [Dc, Da]
+    float* state_out;        // after the last position (one segment only), or NULL
+    float* local;            // k_attn_state: state of each segment alone
+    void* out;               // [B, T, H, Dc] in T, or fp32 where `out32`
+    int out32;
+    int32_t* status;
+};
+
+__device__ __forceinline__ float power(float g2, int n) {
+    return n == 0 ? 1.0f : __builtin_amdgcn_exp2f(g2 * (float)n);
+}
+
+// Position of sweep index t: the order of the sequence, or its reverse; padding stays in place.
+__device__ __forceinline__ int position(int t, int L, bool reverse) {
+    return reverse && t < L ? L - 1 - t : t;
+}
+
+// A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces.
+template <class T, int P, int C, int NT>
+struct Tile {
+    static constexpr int V = Piece<T>::V, PPR = P / V, LD = P + V;
+    static constexpr int NP = C * PPR / NT;
+    static_assert(C * PPR % NT == 0, "pieces per thread");
+    uint4 x[NP];
+    __device__ __forceinline__ void load(const T* base, long st, int D, int t0, int L, bool reverse) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int q = n * NT + threadIdx.x, row = q / PPR, c = (q % PPR) * V;
+            const int t = t0 + row;
+            x[n] = uint4{0, 0, 0, 0};
+            if (t < L && c < D) {
+                const T* p = base + (long)position(t, L, reverse) * st + c;
+                if (c + V <= D) {
+                    __builtin_memcpy(&x[n], p, 16);
+                } else {
+                    T e[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) e[i] = c + i < D ? p[i] : (T)0.0f;
+                    __builtin_memcpy(&x[n], e, 16);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void put(T* buf) const {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int q = n * NT + threadIdx.x, row = q / PPR, c = (q % PPR) * V;
+            *(uint4*)(buf + row * LD + c) = x[n];
+        }
+    }
+};
+
+template <class T>
+__device__ __forceinline__ const T* role_base(const Role& r, int b, int h) {
+    return (const T*)r.p + (long)b * r.sb + (long)(h / r.group) * r.sh;
+}
+
+constexpr int sweep_waves(int P) { return P >= 64 ? 4 : P / 16; }
+
+// State tiles of a wavefront: rows of the state by state_row, its own columns.
+template <class T, int P>
+struct State {
+    static constexpr int NW = sweep_waves(P), VT = P / 16 / NW, ST = P / 16;
+    static constexpr int KS = Mma<T>::KS, E = Mma<T>::E, TPK = KS / 16;   // state tiles a step
+    f32x4 s[ST][VT];
+
+    __device__ __forceinline__ int col(int vt) const {
+        return ((threadIdx.x >> 6) * VT + vt) * 16 + (threadIdx.x & 15);
+    }
+    __device__ __forceinline__ int row(int t, int r) const {
+        return state_row<T>(t, 4 * ((threadIdx.x & 63) >> 4) + r);
+    }
+    __device__ __forceinline__ void load(const float* p, int Da, int Dc, bool transposed) {
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = row(t, r), j = col(v);
+                    s[t][v][r] = p && i < Da && j < Dc ? p[transposed ? j * Da + i : i * Dc + j] : 0.0f;
+                }
+    }
+    __device__ __forceinline__ void store(float* p, int Da, int Dc, bool transposed) const {
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = row(t, r), j = col(v);
+                    if (i < Da && j < Dc) p[transposed ? j * Da + i : i * Dc + j] = s[t][v][r];
+                }
+    }
+    // S *= gamma^m.  Near 1 the factor is applied as S + (gamma^m - 1) S: over thousands of
+    // chunks a factor rounded once would bend every old contribution the same way.
+    __device__ __forceinline__ void decay(float g, int m) {
+        if (m == 0) return;
+        const float f = expf(g * (float)m);
+        const bool near1 = f > 0.5f;
+        const float d = near1 ? expm1f(g * (float)m) : f, keep = near1 ? 1.0f : 0.0f;
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[t][v][r] = fmaf(s[t][v][r], d, keep * s[t][v][r]);
+    }
+    // S += sum_j w_j b_j c_j^T over one product step from row k0; `c` the columns' fragments
+    __device__ __forceinline__ void update(const T* bbuf, int ld, int k0,
+                                           const typename Mma<T>::Frag (&c)[VT], const float (&w)[E]) {
+        Parts<T, update_parts<T>()> p[VT];
+#pragma unroll
+        for (int v = 0; v < VT; ++v)
+#pragma unroll
+            for (int j = 0; j < E; ++j) p[v].set(j, (float)c[v][j] * w[j]);
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+            const auto a = frag_col<true>(bbuf, ld, k0, t);
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+#pragma unroll
+                for (int n = 0; n < update_parts<T>(); ++n) s[t][v] = Mma<T>::mma(a, p[v].f[n], s[t][v]);
+        }
+    }
+};
+
+// su gamma^(m-1-j+e) for the E rows of this lane from k0 (0 past m)
+template <int E>
+__device__ __forceinline__ void update_weights(float g2, float su, int k0, int m, int e, float (&w)[E]) {
+    const int j0 = k0 + ((threadIdx.x & 63) >> 4) * E;
+#pragma unroll
+    for (int j = 0; j < E; ++j) w[j] = j0 + j < m ? su * power(g2, m - 1 - j0 - j + e) : 0.0f;
+}
+
+// grid (nseg, H, B)
+template <class T, int P, int C>
+__global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_state(const Sweep w) {
+    using M = Mma<T>;
+    using St = State<T, P>;
+    constexpr int NT = 64 * St::NW, VT = St::VT;
+    using Tl = Tile<T, P, C, NT>;
+    __shared__ __align__(16) T sb[C * Tl::LD], sc[C * Tl::LD];
+    const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int L = seq_length(w.lengths, b, w.T, w.status);
+    const int t_begin = seg * w.seg, t_end = min(L, t_begin + w.seg);
+    const float g = w.log_decay[h], g2 = g * (float)LOG2E;
+    const T* pb = role_base<T>(w.b, b, h);
+    const T* pc = role_base<T>(w.c, b, h);
+    St S;
+    S.load(nullptr, 0, 0, false);
+    Tl tb, tc;
+    tb.load(pb, w.b.st, w.Da, t_begin, L, w.reverse);
+    tc.load(pc, w.c.st, w.Dc, t_begin, L, w.reverse);
+    for (int t0 = t_begin; t0 < t_end; t0 += C) {
+        const int m = min(C, t_end - t0);
+        __syncthreads();
+        tb.put(sb);
+        tc.put(sc);
+        __syncthreads();
+        if (t0 + C < t_end) {
+            tb.load(pb, w.b.st, w.Da, t0 + C, L, w.reverse);
+            tc.load(pc, w.c.st, w.Dc, t0 + C, L, w.reverse);
+        }
+        S.decay(g, m);
+#pragma unroll
+        for (int k0 = 0; k0 < C; k0 += M::KS) {
+            typename M::Frag c[VT];
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+                c[v] = frag_col<false>(sc, Tl::LD, k0, ((threadIdx.x >> 6) * VT + v) * 16);
+            float u[M::E];
+            update_weights<M::E>(g2, w.su, k0, m, w.e, u);
+            S.update(sb, Tl::LD, k0, c, u);
+        }
+    }
+    S.store(w.local + (((size_t)b * w.H + h) * w.nseg + seg) * w.Da * w.Dc, w.Da, w.Dc, false);
+}
+
+// Start of every segment from the segments' own states, in place, in order; the state after
+// the last position to `out`.  grid (ceil(D / 256), H, B), D = Da Dc
+__global__ __launch_bounds__(256) void k_attn_scan(float* local, const float* init, float* out,
+                                                   const int32_t* lengths, const float* log_decay,
+                                                   int T, int H, int seg, int nseg, int D) {
+    const int i = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
+    if (i >= D) return;
+    const size_t bh = (size_t)b * H + h;
+    const int L = seq_length(lengths, b, T, nullptr);
+    const double g = log_decay[h];
+    float cur = init ? init[bh * D + i] : 0.0f;
+    const float full = (float)exp(g * seg);
+    for (int s = 0; s < nseg; ++s) {
+        float* p = local + (bh * nseg + s) * D + i;
+        const float own = *p;
+        *p = cur;
+        const int m = min(seg, max(0, L - s * seg));
+        const float f = m == seg ? full : m == 0 ? 1.0f : (float)exp(g * m);
+        cur = fmaf(cur, f, own);
+    }
+    if (out) out[bh * D + i] = cur;
+}
+
+// grid (nseg, H, B)
+template <class T, int P, int C>
+__global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep w) {
+    using M = Mma<T>;
+    using St = State<T, P>;
+    constexpr int NW = St::NW, NT = 64 * NW, VT = St::VT, IT = C / 16, KS = M::KS, E = M::E;
+    using Tl = Tile<T, P, C, NT>;
+    constexpr int LDM = C + Piece<T>::V;
+    __shared__ __align__(16) T sa[C * Tl::LD], sb[C * Tl::LD], sc[C * Tl::LD], sm[C * LDM];
+    const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), gr = lane >> 4, r16 = lane & 15;
+    const int L = seq_length(w.lengths, b, w.T, w.status);
+    const int t_begin = seg * w.seg, t_end = min(w.T, t_begin + w.seg);
+    const float g = w.log_decay[h], g2 = g * (float)LOG2E;
+    const T* pa = role_base<T>(w.a, b, h);
+    const T* pb = role_base<T>(w.b, b, h);
+    const T* pc = role_base<T>(w.c, b, h);
+    const size_t bh = (size_t)b * w.H + h;
+    const size_t D = (size_t)w.Da * w.Dc;
+    St S;
+    S.load(w.state ? w.state + (bh * w.state_nseg + (w.state_nseg > 1 ? seg : 0)) * D : nullptr, w.Da,
+           w.Dc, w.transposed);
+    // masked products above the diagonal stay zero
+    for (int i = threadIdx.x; i < C * LDM; i += NT) sm[i] = (T)0.0f;
+    // scale gamma^(i-j) of a result tile: on the diagonal, and one tile below it
+    float diag[4], below[4], inter[IT][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int d = 4 * gr + r - r16;
+        diag[r] = d >= 0 ? w.scale * power(g2, d) : 0.0f;
+        below[r] = w.scale * power(g2, 16 + d);
+    }
+#pragma unroll
+    for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) inter[it][r] = w.si * power(g2, 16 * it + 4 * gr + r + 1 - w.e);
+    Tl ta, tb, tc;
+    ta.load(pa, w.a.st, w.Da, t_begin, L, w.reverse);
+    tb.load(pb, w.b.st, w.Da, t_begin, L, w.reverse);
+    tc.load(pc, w.c.st, w.Dc, t_begin, L, w.reverse);
+    for (int t0 = t_begin; t0 < t_end; t0 += C) {
+        const int m = max(0, min(C, L - t0));
+        __syncthreads();
+        ta.put(sa);
+        tb.put(sb);
+        tc.put(sc);
+        __syncthreads();
+        if (t0 + C < t_end) {
+            ta.load(pa, w.a.st, w.Da, t0 + C, L, w.reverse);
+            tb.load(pb, w.b.st, w.Da, t0 + C, L, w.reverse);
+            tc.load(pc, w.c.st, w.Dc, t0 + C, L, w.reverse);
+        }
+        // masked products, by rows
+#pragma unroll
+        for (int n = 0; n < (IT + NW - 1) / NW; ++n) {
+            const int it = n * NW + wave;
+            if (it >= IT) break;
+            for (int jt = 0; jt <= it; ++jt) {
+                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k0 = 0; k0 < P; k0 += KS)
+                    acc = M::mma(frag_row<T>(sa, Tl::LD, 16 * it, k0), frag_row<T>(sb, Tl::LD, 16 * jt, k0), acc);
+                const float step = jt < it ? power(g2, 16 * (it - jt - 1)) : 1.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sm[(16 * it + 4 * gr + r) * LDM + 16 * jt + r16] =
+                        (T)(acc[r] * (jt < it ? below[r] * step : diag[r]));
+            }
+        }
+        __syncthreads();
+        // what the state gives each row
+        f32x4 acc[IT][VT];
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+            for (int v = 0; v < VT; ++v) acc[it][v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kb = 0; kb < P / KS; ++kb) {
+            Parts<T, state_parts<T>()> p[VT];
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+#pragma unroll
+                for (int j = 0; j < E; ++j) p[v].set(j, S.s[kb * St::TPK + j / 4][v][j % 4]);
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const auto a = frag_row<T>(sa, Tl::LD, 16 * it, kb * KS);
+#pragma unroll
+                for (int v = 0; v < VT; ++v)
+#pragma unroll
+                    for (int n = 0; n < state_parts<T>(); ++n) acc[it][v] = M::mma(a, p[v].f[n], acc[it][v]);
+            }
+        }
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[it][v][r] *= inter[it][r];
+        // what the chunk's own rows give, and the state's update
+        S.decay(g, m);
+#pragma unroll
+        for (int k0 = 0; k0 < C; k0 += KS) {
+            typename M::Frag c[VT];
+#pragma unroll
+            for (int v = 0; v < VT; ++v) c[v] = frag_col<false>(sc, Tl::LD, k0, (wave * VT + v) * 16);
+#pragma unroll
+            for (int it = k0 / 16; it < IT; ++it) {
+                const auto a = frag_row<T>(sm, LDM, 16 * it, k0);
+#pragma unroll
+                for (int v = 0; v < VT; ++v) acc[it][v] = M::mma(a, c[v], acc[it][v]);
+            }
+            float u[E];
+            update_weights<E>(g2, w.su, k0, m, w.e, u);
+            S.update(sb, Tl::LD, k0, c, u);
+        }
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = t0 + 16 * it + 4 * gr + r;
+                if (t >= t_end) continue;
+                const size_t at = (((size_t)b * w.T + position(t, L, w.reverse)) * w.H + h) * w.Dc;
+#pragma unroll
+                for (int v = 0; v < VT; ++v) {
+                    const int j = S.col(v);
+                    if (j >= w.Dc) continue;
+                    const float x = t < L ? acc[it][v][r] : 0.0f;
+                    if (w.out32) ((float*)w.out)[at + j] = x;
+                    else ((T*)w.out)[at + j] = (T)x;
+                }
+            }
+    }
+    if (w.state_out) S.store(w.state_out + bh * D, w.Da, w.Dc, w.transposed);
+}
+
+// out[row, hk, :] = sum over the group's query heads, in order.  One element a thread.
+template <class T>
+__global__ __launch_bounds__(256) void k_attn_group(const float* x, T* out, long n, int group, int D) {
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const long head = i / D;
+    const int j = (int)(i - head * D);
+    const float* p = x + head * group * D + j;
+    float s = 0.0f;
+    for (int q = 0; q < group; ++q) s += p[(long)q * D];
+    out[i] = (T)s;
+}
+
+// ------------------------------------------------------------------ one token
+// grid (Hq, B), block 256: LR lanes take 4 columns each of a state row, 256 / LR row groups.
+template <class T>
+__global__ __launch_bounds__(256) void k_attn_step(const semicrf_attention p, const int32_t* slots,
+                                                   int pool, T* out, float* state_out, int LR) {
+    __shared__ float sq[ATTN_MAX_D], sk[ATTN_MAX_D];
+    __shared__ float part[256 * 4];
+    const int h = blockIdx.x, b = blockIdx.y, Dk = p.Dk, Dv = p.Dv, hk = h / (p.Hq / p.Hk);
+    const int tid = threadIdx.x;
+    const int slot = slots ? slots[b] : b;
+    T* o = out + ((size_t)b * p.Hq + h) * Dv;
+    if (slot < 0 || slot >= pool) {
+        for (int j = tid; j < Dv; j += 256) o[j] = (T)0.0f;
+        return;
+    }
+    const T* q = (const T*)p.q + b * p.q_stride[0] + h * p.q_stride[2];
+    const T* k = (const T*)p.k + b * p.k_stride[0] + hk * p.k_stride[2];
+    const T* v = (const T*)p.v + b * p.v_stride[0] + hk * p.v_stride[2];
+    if (tid < Dk) {
+        sq[tid] = (float)q[tid] * p.scale;
+        sk[tid] = (float)k[tid];
+    }
+    __syncthreads();
+    const int lr = tid & (LR - 1), grp = tid / LR, ng = 256 / LR, c = lr * 4;
+    const float gamma = expf(p.log_decay[h]);
+    float vv[4], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vv[i] = c + i < Dv ? (float)v[c + i] : 0.0f;
+    const size_t base = ((size_t)slot * p.Hq + h) * Dk * Dv;
+    for (int r = grp; r < Dk; r += ng) {
+        float s[4];
+        load_piece<float>(p.state + base + (size_t)r * Dv + c, Dv - c, s);
+        const float kr = sk[r], qr = sq[r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = fmaf(s[i], gamma, kr * vv[i]);
+            acc[i] = fmaf(qr, s[i], acc[i]);
+        }
+        store_piece<float>(state_out + base + (size_t)r * Dv + c, Dv - c, s);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[tid * 4 + i] = acc[i];
+    __syncthreads();
+    if (tid < Dv) {
+        float s = 0.0f;
+        for (int n = 0; n < ng; ++n) s += part[n * LR * 4 + tid];
+        o[tid] = (T)s;
+    }
+}
+
+// ------------------------------------------------------------------ host
+int head_pad(const semicrf_attention& p) {
+    const int d = p.Dk > p.Dv ? p.Dk : p.Dv;
+    return d <= 32 ? 32 : d <= 64 ? 64 : 128;
+}
+int chunk_of(const semicrf_attention& p) { return p.dtype == SEMICRF_F32 && head_pad(p) == 128 ? 32 : 64; }
+
+// Segments of a sequence.
+int segment(const semicrf_attention& p) {
+    const int C = chunk_of(p);
+    const long bh = (long)p.B * p.Hq;
+    long n = (1024 + bh - 1) / bh;
+    const long most = p.T / 512;
+    if (n > most) n = most;
+    if (n < 1) n = 1;
+    const long len = (p.T + n - 1) / n;
+    return (int)((len + C - 1) / C * C);
+}
+
+struct AttnLayout {
+    int seg, nseg;
+    size_t S, R, gk, gv, total;
+};
+
+AttnLayout attn_layout(const semicrf_attention& p, bool grad) {
+    AttnLayout l{};
+    l.seg = segment(p);
+    l.nseg = (p.T + l.seg - 1) / l.seg;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    const size_t st = l.nseg > 1 ? (size_t)p.B * p.Hq * l.nseg * p.Dk * p.Dv * 4 : 0;
+    l.S = take(st);
+    if (grad) {
+        l.R = take(st);
+        const size_t rows = p.Hq > p.Hk ? (size_t)p.B * p.T * p.Hq * 4 : 0;
+        l.gk = take(rows * p.Dk);
+        l.gv = take(rows * p.Dv);
+    }
+    l.total = off ? off : 256;
+    return l;
+}
+
+template <class F>
+hipError_t with_kernel(const semicrf_attention& p, F&& f) {
+    const int P = head_pad(p);
+    using I32 = std::integral_constant<int, 32>;
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    if (p.dtype == SEMICRF_F32) {
+        if (P == 32) return f(0.0f, I32(), I64());
+        if (P == 64) return f(0.0f, I64(), I64());
+        return f(0.0f, I128(), I32());
+    }
+    if (P == 32) return f((bf16)0.0f, I32(), I64());
+    if (P == 64) return f((bf16)0.0f, I64(), I64());
+    return f((bf16)0.0f, I128(), I64());
+}
+
+Sweep base_sweep(const AttnArgs& a, const AttnLayout& l) {
+    const semicrf_attention& p = a.p;
+    Sweep w{};
+    w.B = p.B; w.T = p.T; w.H = p.Hq;
+    w.lengths = p.lengths;
+    w.log_decay = p.log_decay;
+    w.scale = p.scale;
+    w.seg = l.seg; w.nseg = l.nseg;
+    w.status = a.status;
+    return w;
+}
+
+Role role(const void* p, const int64_t* s, int group) { return Role{p, (long)s[0], (long)s[1], (long)s[2], group}; }
+
+hipError_t run_state(const semicrf_attention& p, const Sweep& w, hipStream_t stream) {
+    return with_kernel(p, [&](auto t, auto pp, auto cc) {
+        using T = decltype(t);
+        constexpr int P = decltype(pp)::value, C = decltype(cc)::value;
+        hipLaunchKernelGGL((k_attn_state<T, P, C>), dim3(w.nseg, w.H, w.B), dim3(64 * sweep_waves(P)), 0,
+                           stream, w);
+        return hipGetLastError();
+    });
+}
+
+hipError_t run_sweep(const semicrf_attention& p, const Sweep& w, hipStream_t stream) {
+    return with_kernel(p, [&](auto t, auto pp, auto cc) {
+        using T = decltype(t);
+        constexpr int P = decltype(pp)::value, C = decltype(cc)::value;
+        hipLaunchKernelGGL((k_attn_sweep<T, P, C>), dim3(w.nseg, w.H, w.B), dim3(64 * sweep_waves(P)), 0,
+                           stream, w);
+        return hipGetLastError();
+    });
+}
+
+hipError_t run_scan(const semicrf_attention& p, const AttnLayout& l, float* local, const float* init,
+                    float* out, hipStream_t stream) {
+    const int D = p.Dk * p.Dv;
+    hipLaunchKernelGGL(k_attn_scan, dim3((D + 255) / 256, p.Hq, p.B), dim3(256), 0, stream, local, init,
+                       out, p.lengths, p.log_decay, p.T, p.Hq, l.seg, l.nseg, D);
+    return hipGetLastError();
+}
+
+#define TRY(x)                              \
+    do {                                    \
+        const hipError_t e_ = (x);          \
+        if (e_ != hipSuccess) return e_;    \
+    } while (0)
+
+}  // namespace
+
+size_t decay_attention_bytes(const semicrf_attention& p, bool grad) { return attn_layout(p, grad).total; }
+
+hipError_t launch_decay_attention(const AttnArgs& a, void* ws, hipStream_t stream) {
+    const semicrf_attention& p = a.p;
+    const AttnLayout l = attn_layout(p, false);
+    const int group = p.Hq / p.Hk;
+    Sweep w = base_sweep(a, l);
+    w.a = role(p.q, p.q_stride, 1);
+    w.b = role(p.k, p.k_stride, group);
+    w.c = role(p.v, p.v_stride, group);
+    w.Da = p.Dk; w.Dc = p.Dv;
+    w.si = p.scale; w.su = 1.0f;
+    w.out = a.out;
+    w.state = p.state;
+    w.state_nseg = 1;
+    if (l.nseg > 1) {
+        w.local = (float*)((char*)ws + l.S);
+        TRY(run_state(p, w, stream));
+        TRY(run_scan(p, l, w.local, p.state, a.state_out, stream));
+        w.state = w.local;
+        w.state_nseg = l.nseg;
+    } else {
+        w.state_out = a.state_out;
+    }
+    return run_sweep(p, w, stream);
+}
+
+hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t stream) {
+    const semicrf_attention& p = a.p;
+    const AttnLayout l = attn_layout(p, true);
+    const int group = p.Hq / p.Hk;
+    const int64_t gs[3] = {(int64_t)p.T * p.Hq * p.Dv, (int64_t)p.Hq * p.Dv, p.Dv};
+    const Role q = role(p.q, p.q_stride, 1), k = role(p.k, p.k_stride, group),
+               v = role(p.v, p.v_stride, group), g = role(a.grad_out, gs, 1);
+    float* S = (float*)((char*)ws + l.S);
+    float* R = (float*)((char*)ws + l.R);
+    Sweep w = base_sweep(a, l);
+    w.state_nseg = l.nseg;
+    Sweep f = w, r = w;
+    f.si = p.scale; f.su = 1.0f;
+    r.si = 1.0f; r.su = p.scale; r.e = 1; r.reverse = 1;
+    f.state = p.state;
+    r.state = a.grad_state_out;
+    if (l.nseg > 1) {
+        f.b = k; f.c = v; f.Da = p.Dk; f.Dc = p.Dv; f.local = S;
+        TRY(run_state(p, f, stream));
+        TRY(run_scan(p, l, S, p.state, nullptr, stream));
+        r.b = q; r.c = g; r.Da = p.Dk; r.Dc = p.Dv; r.local = R;
+        TRY(run_state(p, r, stream));
+        TRY(run_scan(p, l, R, a.grad_state_out, a.grad_state, stream));
+        f.state = S;
+        r.state = R;
+    }
+    // dq
+    f.a = g; f.b = v; f.c = k; f.Da = p.Dv; f.Dc = p.Dk; f.transposed = 1;
+    f.out = a.grad_q;
+    TRY(run_sweep(p, f, stream));
+    // dv, and the gradient of the initial state
+    r.a = k; r.b = q; r.c = g; r.Da = p.Dk; r.Dc = p.Dv; r.transposed = 0;
+    r.out32 = group > 1;
+    r.out = group > 1 ? (void*)((char*)ws + l.gv) : a.grad_v;
+    r.state_out = l.nseg > 1 ? nullptr : a.grad_state;
+    TRY(run_sweep(p, r, stream));
+    // dk
+    r.a = v; r.b = g; r.c = q; r.Da = p.Dv; r.Dc = p.Dk; r.transposed = 1;
+    r.out = group > 1 ? (void*)((char*)ws + l.gk) : a.grad_k;
+    r.state_out = nullptr;
+    TRY(run_sweep(p, r, stream));
+    if (group > 1) {
+        const long rows = (long)p.B * p.T * p.Hk;
+        auto sum = [&](const float* x, void* out, int D) {
+            const long n = rows * D;
+            const dim3 grid((unsigned)((n + 255) / 256));
+            if (p.dtype == SEMICRF_F32)
+                hipLaunchKernelGGL((k_attn_group<float>), grid, dim3(256), 0, stream, x, (float*)out, n,
+                                   group, D);
+            else
+                hipLaunchKernelGGL((k_attn_group<bf16>), grid, dim3(256), 0, stream, x, (bf16*)out, n,
+                                   group, D);
+            return hipGetLastError();
+        };
+        TRY(sum((const float*)((char*)ws + l.gk), a.grad_k, p.Dk));
+        TRY(sum((const float*)((char*)ws + l.gv), a.grad_v, p.Dv));
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_decay_attention_step(const semicrf_attention& p, const int32_t* slots, int pool,
+                                       void* out, float* state_out, hipStream_t stream) {
+    int LR = 1;
+    while (LR * 4 < p.Dv) LR *= 2;
+    if (p.dtype == SEMICRF_F32)
+        hipLaunchKernelGGL((k_attn_step<float>), dim3(p.Hq, p.B), dim3(256), 0, stream, p, slots, pool,
+                           (float*)out, state_out, LR);
+    else
+        hipLaunchKernelGGL((k_attn_step<bf16>), dim3(p.Hq, p.B), dim3(256), 0, stream, p, slots, pool,
+                           (bf16*)out, state_out, LR);
+    return hipGetLastError();
+}
+
+}  // namespace semicrf

@@ -1,0 +1,301 @@
+// Layer norm over the last axis, forward and backward, on gfx950.
+//
+//   mu = mean_j x_j,  r = 1 / sqrt(mean_j (x_j - mu)^2 + eps),  y_j = (x_j - mu) r w_j + b_j
+//   backward, with h_j = (x_j - mu) r and g_j = dy_j w_j:
+//     dx_j = r (g_j - mean g - h_j mean(g h)),  dw_j = sum over rows dy_j h_j,  db_j = sum dy_j
+//
+// Both are bound by HBM: a row is read once and kept in registers (the variance is taken
+// about the mean from the registers, not as a difference of sums), and every sum is in fp32.
+// G lanes of a workgroup share a row, each with KP pieces of 16 bytes; G grows with the width
+// so that a lane keeps few pieces and narrow rows still fill a wavefront.
+//
+// The weight's gradient sums over all rows.  A workgroup of the backward pass takes every
+// nwg-th row block and keeps its columns' sums in registers; its G-groups are joined through
+// LDS and written as one partial row, and k_norm_partials adds the partial rows in a fixed
+// order (no atomics: the same inputs give the same bits).
+#include "common.h"
+#include "encoder.h"
+
+namespace semicrf {
+
+namespace {
+
+// Sum over the G lanes of a row (G <= 64: inside a wavefront; else the whole workgroup of G
+// threads, through `red`, which alternates between two slots so one barrier is enough).
+template <int G>
+__device__ __forceinline__ float row_sum(float v, float* red, int& slot) {
+    if constexpr (G <= 64) {
+        return group_reduce<G>(v, OpSum());
+    } else {
+        v = group_reduce<64>(v, OpSum());
+        float* s = red + slot * (G / 64);
+        slot ^= 1;
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+        __syncthreads();
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G / 64; ++i) t += s[i];
+        return t;
+    }
+}
+
+// Row -> (b, t < length).  Rows are numbered b * T + t.
+__device__ __forceinline__ bool row_valid(const NormArgs& a, long row) {
+    if (!a.lengths) return true;
+    const int b = (int)(row / a.T);
+    return (int)(row - (long)b * a.T) < seq_length(a.lengths, b, a.T, a.status);
+}
+
+template <class W, int V>
+__device__ __forceinline__ void load_weights(const void* p, int c, int N, float dflt,
+                                             float (&w)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        w[i] = (p && c + i < N) ? (float)((const W*)p)[c + i] : (c + i < N ? dflt : 0.0f);
+}
+
+template <class T, class W, int G, int KP, int NT>
+__global__ __launch_bounds__(NT) void k_layer_norm(const NormArgs a) {
+    constexpr int V = Piece<T>::V, RPB = NT / G;
+    __shared__ float red[2 * (G > 64 ? G / 64 : 1)];
+    int slot = 0;
+    const int N = a.N, lane = threadIdx.x % G;
+    const long rows = (long)a.B * a.T;
+    const long row = (long)blockIdx.x * RPB + threadIdx.x / G;
+    const bool in = row < rows;
+    const bool ok = in && row_valid(a, row);
+    const T* x = (const T*)a.x + (in ? row : 0) * N;
+    float v[KP][V];
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+        const int c = (k * G + lane) * V;
+        load_piece<T>(x + c, ok ? N - c : 0, v[k]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += v[k][i];
+    }
+    const float mean = row_sum<G>(s, red, slot) / (float)N;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+        const int c = (k * G + lane) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[k][i] -= mean;
+            s += c + i < N ? v[k][i] * v[k][i] : 0.0f;
+        }
+    }
+    const float var = row_sum<G>(s, red, slot) / (float)N;
+    const float r = 1.0f / sqrtf(var + a.eps);
+    if (!in) return;
+    if (lane == 0) {
+        if (a.mean) a.mean[row] = ok ? mean : 0.0f;
+        if (a.rstd) a.rstd[row] = ok ? r : 0.0f;
+    }
+    T* y = (T*)a.y + row * N;
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+        const int c = (k * G + lane) * V;
+        if (c >= N) break;
+        float w[V], b[V];
+        load_weights<W, V>(a.weight, c, N, 1.0f, w);
+        load_weights<W, V>(a.bias, c, N, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] = ok ? fmaf(v[k][i] * r, w[i], b[i]) : 0.0f;
+        store_piece<T>(y + c, N - c, v[k]);
+    }
+}
+
+template <class T, class W, int G, int KP, int NT>
+__global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float* part) {
+    constexpr int V = Piece<T>::V, RPB = NT / G;
+    __shared__ float red[2 * (G > 64 ? G / 64 : 1)];
+    __shared__ float join[RPB > 1 ? (RPB - 1) * G * V * 2 : 1];
+    int slot = 0;
+    const int N = a.N, lane = threadIdx.x % G, sub = threadIdx.x / G;
+    const long rows = (long)a.B * a.T;
+    const float inv = 1.0f / (float)N;
+    float w[KP][V], dw[KP][V], db[KP][V];
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+        load_weights<W, V>(a.weight, (k * G + lane) * V, N, 1.0f, w[k]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
+    }
+    for (long r0 = (long)blockIdx.x * RPB; r0 < rows; r0 += (long)gridDim.x * RPB) {
+        const long row = r0 + sub;
+        const bool in = row < rows;
+        const bool ok = in && row_valid(a, row);
+        const long at = in ? row : 0;
+        const T* x = (const T*)a.x + at * N;
+        const T* g = (const T*)a.grad_out + at * N;
+        const float mean = ok ? a.mean_in[at] : 0.0f, r = ok ? a.rstd_in[at] : 0.0f;
+        float h[KP][V], dy[KP][V];
+        float sg = 0.0f, sgh = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            const int c = (k * G + lane) * V;
+            load_piece<T>(x + c, ok ? N - c : 0, h[k]);
+            load_piece<T>(g + c, ok ? N - c : 0, dy[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                h[k][i] = (h[k][i] - mean) * r;
+                const float t = dy[k][i] * w[k][i];
+                sg += t;
+                sgh += t * h[k][i];
+                dw[k][i] += dy[k][i] * h[k][i];
+                db[k][i] += dy[k][i];
+            }
+        sg = row_sum<G>(sg, red, slot) * inv;
+        sgh = row_sum<G>(sgh, red, slot) * inv;
+        if (!in) continue;
+        T* dx = (T*)a.grad_x + row * N;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            const int c = (k * G + lane) * V;
+            if (c >= N) break;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                dy[k][i] = ok ? r * (dy[k][i] * w[k][i] - sg - h[k][i] * sgh) : 0.0f;
+            store_piece<T>(dx + c, N - c, dy[k]);
+        }
+    }
+    // join the row groups of the workgroup in order, then one partial row [2][N]
+    float* out = part + (size_t)blockIdx.x * 2 * N;
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+        if constexpr (RPB > 1) {
+            __syncthreads();
+            if (sub > 0) {
+                float* j = join + ((sub - 1) * G + lane) * V * 2;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    j[i] = dw[k][i];
+                    j[V + i] = db[k][i];
+                }
+            }
+            __syncthreads();
+            if (sub == 0)
+                for (int q = 0; q < RPB - 1; ++q) {
+                    const float* j = join + (q * G + lane) * V * 2;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        dw[k][i] += j[i];
+                        db[k][i] += j[V + i];
+                    }
+                }
+        }
+        if (sub == 0) {
+            const int c = (k * G + lane) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (c + i < N) {
+                    out[c + i] = dw[k][i];
+                    out[N + c + i] = db[k][i];
+                }
+        }
+    }
+}
+
+// grid (ceil(2N / 64)), block 1024: 64 columns, 16 groups of partial rows, joined in order
+template <class W>
+__global__ __launch_bounds__(1024) void k_norm_partials(const float* part, int nwg, int N, W* gw,
+                                                        W* gb) {
+    __shared__ float s[16][64];
+    const int c = blockIdx.x * 64 + (threadIdx.x & 63), grp = threadIdx.x >> 6;
+    const int per = (nwg + 15) / 16;
+    const int r1 = min(nwg, (grp + 1) * per);
+    float v = 0.0f;
+    if (c < 2 * N)
+        for (int r = grp * per; r < r1; ++r) v += part[(size_t)r * 2 * N + c];
+    s[grp][threadIdx.x & 63] = v;
+    __syncthreads();
+    if (grp == 0 && c < 2 * N) {
+        for (int i = 1; i < 16; ++i) v += s[i][threadIdx.x];
+        W* out = c < N ? gw : gb;
+        if (out) out[c < N ? c : c - N] = (W)v;
+    }
+}
+
+// Lanes per row and pieces per lane for a width.  Pieces per lane are kept at two until the
+// row takes a whole workgroup of 1024.
+struct Shape2 {
+    int G, KP;
+};
+Shape2 norm_shape(int N, int V) {
+    const int np = (N + V - 1) / V;
+    int G = 8;
+    while (G < 64 && G < np) G *= 2;
+    if (np > 2 * 64) G = 256;
+    if (np > 2 * 256) G = 1024;
+    int KP = 1;
+    while (KP * G < np) KP *= 2;
+    return {G, KP};
+}
+
+int norm_grad_wgs(long rows, int RPB) {
+    const long need = (rows + RPB - 1) / RPB;
+    return (int)(need < 1024 ? need : 1024);
+}
+
+template <class F>
+hipError_t with_shape(int N, int V, F&& f) {
+    const Shape2 s = norm_shape(N, V);
+#define CASE(g, kp) \
+    if (s.G == g && s.KP == kp) return f(std::integral_constant<int, g>(), std::integral_constant<int, kp>())
+    CASE(8, 1); CASE(16, 1); CASE(32, 1); CASE(64, 1); CASE(64, 2); CASE(256, 1); CASE(256, 2);
+    CASE(1024, 1); CASE(1024, 2); CASE(1024, 4); CASE(1024, 8);
+#undef CASE
+    return hipErrorInvalidValue;
+}
+
+template <class T, class W>
+hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
+    return with_shape(a.N, Piece<T>::V, [&](auto g, auto kp) {
+        constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = G > 256 ? G : 256;
+        const long rows = (long)a.B * a.T, rpb = NT / G;
+        hipLaunchKernelGGL((k_layer_norm<T, W, G, KP, NT>), dim3((unsigned)((rows + rpb - 1) / rpb)),
+                           dim3(NT), 0, stream, a);
+        return hipGetLastError();
+    });
+}
+
+template <class T, class W>
+hipError_t run_norm_grad(const NormArgs& a, float* part, hipStream_t stream) {
+    return with_shape(a.N, Piece<T>::V, [&](auto g, auto kp) {
+        constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = G > 256 ? G : 256;
+        const int nwg = norm_grad_wgs((long)a.B * a.T, NT / G);
+        hipLaunchKernelGGL((k_layer_norm_grad<T, W, G, KP, NT>), dim3(nwg), dim3(NT), 0, stream, a,
+                           part);
+        if (a.grad_weight || a.grad_bias)
+            hipLaunchKernelGGL((k_norm_partials<W>), dim3((2 * a.N + 63) / 64), dim3(1024), 0, stream,
+                               part, nwg, a.N, (W*)a.grad_weight, (W*)a.grad_bias);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
+    if (a.dtype == SEMICRF_F32) return run_norm<float, float>(a, stream);
+    return a.wdtype == SEMICRF_F32 ? run_norm<bf16, float>(a, stream) : run_norm<bf16, bf16>(a, stream);
+}
+
+size_t layer_norm_grad_bytes(int B, int T, int N, int dtype) {
+    const int V = dtype == SEMICRF_F32 ? 4 : 8;
+    const Shape2 s = norm_shape(N, V);
+    const int NT = s.G > 256 ? s.G : 256;
+    return (size_t)norm_grad_wgs((long)B * T, NT / s.G) * 2 * N * sizeof(float);
+}
+
+hipError_t launch_layer_norm_grad(const NormArgs& a, void* ws, hipStream_t stream) {
+    float* part = (float*)ws;
+    if (a.dtype == SEMICRF_F32) return run_norm_grad<float, float>(a, part, stream);
+    return a.wdtype == SEMICRF_F32 ? run_norm_grad<bf16, float>(a, part, stream)
+                                   : run_norm_grad<bf16, bf16>(a, part, stream);
+}
+
+}  // namespace semicrf
