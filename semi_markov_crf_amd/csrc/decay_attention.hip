@@ -39,6 +39,11 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// raw buffer: no stride, no swizzle, 32-bit data format, out of range reads 0 and drops writes
+constexpr int BUFFER_FLAGS = 0x00027000;
 
 // ------------------------------------------------------------------ matrix products
 // A product step contracts KS indices.  Lane l = 16 g + r holds E consecutive contraction
@@ -125,6 +130,7 @@ struct Role {
     const void* p;
     long sb, st, sh;         // strides in elements
     int group;               // query heads that share a head of this role
+    int fast;                // rows are whole 16-byte pieces that do not overlap
 };
 
 struct Sweep {
@@ -141,7 +147,7 @@ struct Sweep {
     float* state_out;        // after the last position (one segment only), or NULL
     float* local;            // k_attn_state: state of each segment alone
     void* out;               // [B, T, H, Dc] in T, or fp32 where `out32`
-    int out32;
+    int out32, fast_out;
     int32_t* status;
 };
 
@@ -149,43 +155,54 @@ __device__ __forceinline__ float power(float g2, int n) {
     return n == 0 ? 1.0f : __builtin_amdgcn_exp2f(g2 * (float)n);
 }
 
-// Position of sweep index t: the order of the sequence, or its reverse; padding stays in place.
-__device__ __forceinline__ int position(int t, int L, bool reverse) {
-    return reverse && t < L ? L - 1 - t : t;
-}
-
-// A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces.
+// A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces: the thread's
+// column piece is the same in all its rows.  Loads go through a buffer descriptor over exactly
+// the chunk's valid rows, so rows and columns out of range read as zeros with no branch; offsets
+// in a chunk stay below 2^29 bytes (Role::fast), and bit 31 puts one out of range.
 template <class T, int P, int C, int NT>
 struct Tile {
-    static constexpr int V = Piece<T>::V, PPR = P / V, LD = P + V;
-    static constexpr int NP = C * PPR / NT;
-    static_assert(C * PPR % NT == 0, "pieces per thread");
-    uint4 x[NP];
-    __device__ __forceinline__ void load(const T* base, long st, int D, int t0, int L, bool reverse) {
+    static constexpr int V = Piece<T>::V, PPR = P / V, LD = P + V, RPS = NT / PPR;
+    static constexpr int NP = C / RPS;
+    static_assert(NT % PPR == 0 && C % RPS == 0, "pieces per thread");
+    u32x4 x[NP];
+
+    // m valid rows from sweep index t0 (position L - t0 - m is the lowest of a reversed chunk)
+    __device__ __forceinline__ void load(const Role& w, const T* seq, int D, int t0, int m, int L, int reverse) {
+        const int row0 = threadIdx.x / PPR, c = (threadIdx.x % PPR) * V;
+        if (w.fast) {
+            const int stb = (int)w.st * (int)sizeof(T);
+            const T* base = seq + (long)(reverse ? L - t0 - m : t0) * w.st;
+            const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)base, 0, m > 0 ? (m - 1) * stb + D * (int)sizeof(T) : 0, BUFFER_FLAGS);
+            const uint32_t cb = c < D ? c * (uint32_t)sizeof(T) : 0x80000000u;
+            uint32_t off = cb + (uint32_t)(reverse ? (m - 1 - row0) * stb : row0 * stb);
+            const uint32_t step = (uint32_t)(reverse ? -RPS * stb : RPS * stb);
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            const int q = n * NT + threadIdx.x, row = q / PPR, c = (q % PPR) * V;
-            const int t = t0 + row;
-            x[n] = uint4{0, 0, 0, 0};
-            if (t < L && c < D) {
-                const T* p = base + (long)position(t, L, reverse) * st + c;
-                if (c + V <= D) {
-                    __builtin_memcpy(&x[n], p, 16);
-                } else {
-                    T e[V];
+            for (int n = 0; n < NP; ++n) {
+                x[n] = __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0);
+                off += step;
+            }
+        } else {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) e[i] = c + i < D ? p[i] : (T)0.0f;
-                    __builtin_memcpy(&x[n], e, 16);
+            for (int n = 0; n < NP; ++n) {
+                const int row = row0 + n * RPS;
+                T e[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) e[i] = (T)0.0f;
+                if (row < m && c < D) {
+                    const T* p = seq + (long)(reverse ? L - 1 - t0 - row : t0 + row) * w.st + c;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (c + i < D) e[i] = p[i];
                 }
+                __builtin_memcpy(&x[n], e, 16);
             }
         }
     }
     __device__ __forceinline__ void put(T* buf) const {
+        const int row0 = threadIdx.x / PPR, c = (threadIdx.x % PPR) * V;
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            const int q = n * NT + threadIdx.x, row = q / PPR, c = (q % PPR) * V;
-            *(uint4*)(buf + row * LD + c) = x[n];
-        }
+        for (int n = 0; n < NP; ++n) *(u32x4*)(buf + (row0 + n * RPS) * LD + c) = x[n];
     }
 };
 
@@ -195,6 +212,18 @@ __device__ __forceinline__ const T* role_base(const Role& r, int b, int h) {
 }
 
 constexpr int sweep_waves(int P) { return P >= 64 ? 4 : P / 16; }
+
+// gamma^m of the state.  Near 1 it is applied as S + (gamma^m - 1) S: over thousands of chunks a
+// factor rounded once would bend every old contribution the same way.
+struct Decay {
+    float f;
+    bool near1;
+    __device__ __forceinline__ void set(float g, int m) {
+        f = m == 0 ? 1.0f : expf(g * (float)m);
+        near1 = f > 0.5f;
+        if (near1) f = m == 0 ? 0.0f : expm1f(g * (float)m);
+    }
+};
 
 // State tiles of a wavefront: rows of the state by state_row, its own columns.
 template <class T, int P>
@@ -231,19 +260,14 @@ struct State {
                     if (i < Da && j < Dc) p[transposed ? j * Da + i : i * Dc + j] = s[t][v][r];
                 }
     }
-    // S *= gamma^m.  Near 1 the factor is applied as S + (gamma^m - 1) S: over thousands of
-    // chunks a factor rounded once would bend every old contribution the same way.
-    __device__ __forceinline__ void decay(float g, int m) {
-        if (m == 0) return;
-        const float f = expf(g * (float)m);
-        const bool near1 = f > 0.5f;
-        const float d = near1 ? expm1f(g * (float)m) : f, keep = near1 ? 1.0f : 0.0f;
+    __device__ __forceinline__ void decay(Decay d) {
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
             for (int v = 0; v < VT; ++v)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[t][v][r] = fmaf(s[t][v][r], d, keep * s[t][v][r]);
+                for (int r = 0; r < 4; ++r)
+                    s[t][v][r] = d.near1 ? fmaf(s[t][v][r], d.f, s[t][v][r]) : s[t][v][r] * d.f;
     }
     // S += sum_j w_j b_j c_j^T over one product step from row k0; `c` the columns' fragments
     __device__ __forceinline__ void update(const T* bbuf, int ld, int k0,
@@ -264,12 +288,16 @@ struct State {
     }
 };
 
-// su gamma^(m-1-j+e) for the E rows of this lane from k0 (0 past m)
-template <int E>
-__device__ __forceinline__ void update_weights(float g2, float su, int k0, int m, int e, float (&w)[E]) {
-    const int j0 = k0 + ((threadIdx.x & 63) >> 4) * E;
+// su gamma^(m-1-j+e) for the lane's rows of every product step of a chunk (0 past m)
+template <int E, int C>
+__device__ __forceinline__ void update_weights(float g2, float su, int m, int e, float (&w)[C / (4 * E)][E]) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) w[j] = j0 + j < m ? su * power(g2, m - 1 - j0 - j + e) : 0.0f;
+    for (int k = 0; k < C / (4 * E); ++k)
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const int i = (k * 4 + ((threadIdx.x & 63) >> 4)) * E + j;
+            w[k][j] = i < m ? su * power(g2, m - 1 - i + e) : 0.0f;
+        }
 }
 
 // grid (nseg, H, B)
@@ -288,9 +316,13 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_state(const Sweep 
     const T* pc = role_base<T>(w.c, b, h);
     St S;
     S.load(nullptr, 0, 0, false);
+    float u[C / M::KS][M::E];
+    update_weights<M::E, C>(g2, w.su, C, w.e, u);
+    Decay d;
+    d.set(g, C);
     Tl tb, tc;
-    tb.load(pb, w.b.st, w.Da, t_begin, L, w.reverse);
-    tc.load(pc, w.c.st, w.Dc, t_begin, L, w.reverse);
+    tb.load(w.b, pb, w.Da, t_begin, min(C, t_end - t_begin), L, w.reverse);
+    tc.load(w.c, pc, w.Dc, t_begin, min(C, t_end - t_begin), L, w.reverse);
     for (int t0 = t_begin; t0 < t_end; t0 += C) {
         const int m = min(C, t_end - t0);
         __syncthreads();
@@ -298,19 +330,22 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_state(const Sweep 
         tc.put(sc);
         __syncthreads();
         if (t0 + C < t_end) {
-            tb.load(pb, w.b.st, w.Da, t0 + C, L, w.reverse);
-            tc.load(pc, w.c.st, w.Dc, t0 + C, L, w.reverse);
+            const int mn = min(C, t_end - t0 - C);
+            tb.load(w.b, pb, w.Da, t0 + C, mn, L, w.reverse);
+            tc.load(w.c, pc, w.Dc, t0 + C, mn, L, w.reverse);
         }
-        S.decay(g, m);
+        if (m < C) {                           // the sequence's last rows
+            update_weights<M::E, C>(g2, w.su, m, w.e, u);
+            d.set(g, m);
+        }
+        S.decay(d);
 #pragma unroll
         for (int k0 = 0; k0 < C; k0 += M::KS) {
             typename M::Frag c[VT];
 #pragma unroll
             for (int v = 0; v < VT; ++v)
                 c[v] = frag_col<false>(sc, Tl::LD, k0, ((threadIdx.x >> 6) * VT + v) * 16);
-            float u[M::E];
-            update_weights<M::E>(g2, w.su, k0, m, w.e, u);
-            S.update(sb, Tl::LD, k0, c, u);
+            S.update(sb, Tl::LD, k0, c, u[k0 / M::KS]);
         }
     }
     S.store(w.local + (((size_t)b * w.H + h) * w.nseg + seg) * w.Da * w.Dc, w.Da, w.Dc, false);
@@ -339,6 +374,56 @@ __global__ __launch_bounds__(256) void k_attn_scan(float* local, const float* in
     if (out) out[bh * D + i] = cur;
 }
 
+// Four consecutive columns of an output row.
+template <class O>
+__device__ __forceinline__ void store4(const __amdgpu_buffer_rsrc_t& buf, uint32_t off, const f32x4& x) {
+    if constexpr (sizeof(O) == 4) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), buf, off, 0, 0);
+    } else {
+        const bf16x4 h = {(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, h), buf, off, 0, 0);
+    }
+}
+
+// Rows i < m of a chunk from result tiles that hold column i = 16 it + r, rows (of the tile)
+// four consecutive output columns from `col`.
+template <class O, int IT, int VT>
+__device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m, int L, int col,
+                                           const f32x4 (&acc)[IT][VT]) {
+    const int r16 = threadIdx.x & 15;
+    const long ost = (long)w.H * w.Dc;
+    if (w.fast_out) {
+        const int stb = (int)ost * (int)sizeof(O);
+        O* base = seq + (long)(w.reverse ? L - t0 - m : t0) * ost;
+        const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)base, 0, (m - 1) * stb + w.Dc * (int)sizeof(O), BUFFER_FLAGS);
+        uint32_t off = (uint32_t)(w.reverse ? (m - 1 - r16) * stb : r16 * stb);
+        const uint32_t step = (uint32_t)(w.reverse ? -16 * stb : 16 * stb);
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+#pragma unroll
+            for (int v = 0; v < VT; ++v) {
+                const int c = col + 16 * v;
+                store4<O>(buf, off + (c < w.Dc ? c * (uint32_t)sizeof(O) : 0x80000000u), acc[it][v]);
+            }
+            off += step;
+        }
+    } else {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int i = 16 * it + r16;
+            if (i < m) {
+                O* p = seq + (long)(w.reverse ? L - 1 - t0 - i : t0 + i) * ost;
+#pragma unroll
+                for (int v = 0; v < VT; ++v)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (col + 16 * v + r < w.Dc) p[col + 16 * v + r] = (O)acc[it][v][r];
+            }
+        }
+    }
+}
+
 // grid (nseg, H, B)
 template <class T, int P, int C>
 __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep w) {
@@ -349,67 +434,87 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
     constexpr int LDM = C + Piece<T>::V;
     __shared__ __align__(16) T sa[C * Tl::LD], sb[C * Tl::LD], sc[C * Tl::LD], sm[C * LDM];
     const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), gr = lane >> 4, r16 = lane & 15;
-    const int L = seq_length(w.lengths, b, w.T, w.status);
-    const int t_begin = seg * w.seg, t_end = min(w.T, t_begin + w.seg);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int gr = lane >> 4, r16 = lane & 15;
+    const int L = __builtin_amdgcn_readfirstlane(seq_length(w.lengths, b, w.T, w.status));
+    const int t_begin = seg * w.seg, t_last = min(w.T, t_begin + w.seg), t_end = min(L, t_last);
     const float g = w.log_decay[h], g2 = g * (float)LOG2E;
+    const size_t bh = (size_t)b * w.H + h;
+    const size_t D = (size_t)w.Da * w.Dc;
+    const size_t out0 = (size_t)b * w.T * w.H * w.Dc + (size_t)h * w.Dc;
+    // padding: positions from the length on
+    for (int t = max(t_begin, L) + threadIdx.x / 16; t < t_last; t += NT / 16)
+        for (int j = r16; j < w.Dc; j += 16) {
+            const size_t at = out0 + (size_t)t * w.H * w.Dc + j;
+            if (w.out32) ((float*)w.out)[at] = 0.0f;
+            else ((T*)w.out)[at] = (T)0.0f;
+        }
     const T* pa = role_base<T>(w.a, b, h);
     const T* pb = role_base<T>(w.b, b, h);
     const T* pc = role_base<T>(w.c, b, h);
-    const size_t bh = (size_t)b * w.H + h;
-    const size_t D = (size_t)w.Da * w.Dc;
+    Tl ta, tb, tc;
+    {
+        const int m = min(C, t_end - t_begin);
+        ta.load(w.a, pa, w.Da, t_begin, m, L, w.reverse);
+        tb.load(w.b, pb, w.Da, t_begin, m, L, w.reverse);
+        tc.load(w.c, pc, w.Dc, t_begin, m, L, w.reverse);
+    }
     St S;
     S.load(w.state ? w.state + (bh * w.state_nseg + (w.state_nseg > 1 ? seg : 0)) * D : nullptr, w.Da,
            w.Dc, w.transposed);
     // masked products above the diagonal stay zero
     for (int i = threadIdx.x; i < C * LDM; i += NT) sm[i] = (T)0.0f;
-    // scale gamma^(i-j) of a result tile: on the diagonal, and one tile below it
-    float diag[4], below[4], inter[IT][4];
+    // scale gamma^(i-j) in a tile of products (rows j = 4 gr + r, column i = r16): on the
+    // diagonal, and one tile off it
+    float diag[4], below[4], inter[IT];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const int d = 4 * gr + r - r16;
+        const int d = r16 - 4 * gr - r;
         diag[r] = d >= 0 ? w.scale * power(g2, d) : 0.0f;
         below[r] = w.scale * power(g2, 16 + d);
     }
 #pragma unroll
-    for (int it = 0; it < IT; ++it)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) inter[it][r] = w.si * power(g2, 16 * it + 4 * gr + r + 1 - w.e);
-    Tl ta, tb, tc;
-    ta.load(pa, w.a.st, w.Da, t_begin, L, w.reverse);
-    tb.load(pb, w.b.st, w.Da, t_begin, L, w.reverse);
-    tc.load(pc, w.c.st, w.Dc, t_begin, L, w.reverse);
+    for (int it = 0; it < IT; ++it) inter[it] = w.si * power(g2, 16 * it + r16 + 1 - w.e);
+    const float g16 = power(g2, 16);
+    float u[C / KS][E];
+    update_weights<E, C>(g2, w.su, C, w.e, u);
+    Decay d;
+    d.set(g, C);
     for (int t0 = t_begin; t0 < t_end; t0 += C) {
-        const int m = max(0, min(C, L - t0));
+        const int m = min(C, t_end - t0);
         __syncthreads();
         ta.put(sa);
         tb.put(sb);
         tc.put(sc);
         __syncthreads();
         if (t0 + C < t_end) {
-            ta.load(pa, w.a.st, w.Da, t0 + C, L, w.reverse);
-            tb.load(pb, w.b.st, w.Da, t0 + C, L, w.reverse);
-            tc.load(pc, w.c.st, w.Dc, t0 + C, L, w.reverse);
+            const int mn = min(C, t_end - t0 - C);
+            ta.load(w.a, pa, w.Da, t0 + C, mn, L, w.reverse);
+            tb.load(w.b, pb, w.Da, t0 + C, mn, L, w.reverse);
+            tc.load(w.c, pc, w.Dc, t0 + C, mn, L, w.reverse);
         }
-        // masked products, by rows
+        // masked products: the tiles on and below the diagonal, dealt out to the wavefronts
 #pragma unroll
-        for (int n = 0; n < (IT + NW - 1) / NW; ++n) {
-            const int it = n * NW + wave;
-            if (it >= IT) break;
-            for (int jt = 0; jt <= it; ++jt) {
+        for (int n0 = 0; n0 < IT * (IT + 1) / 2; n0 += NW) {
+            const int n = n0 + wave;
+            if (n < IT * (IT + 1) / 2) {
+                const int it = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, jt = n - it * (it + 1) / 2;
                 f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int k0 = 0; k0 < P; k0 += KS)
-                    acc = M::mma(frag_row<T>(sa, Tl::LD, 16 * it, k0), frag_row<T>(sb, Tl::LD, 16 * jt, k0), acc);
-                const float step = jt < it ? power(g2, 16 * (it - jt - 1)) : 1.0f;
+                    acc = M::mma(frag_row<T>(sb, Tl::LD, 16 * jt, k0), frag_row<T>(sa, Tl::LD, 16 * it, k0), acc);
+                const float step = it - jt <= 1 ? 1.0f : it - jt == 2 ? g16 : g16 * g16;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    sm[(16 * it + 4 * gr + r) * LDM + 16 * jt + r16] =
-                        (T)(acc[r] * (jt < it ? below[r] * step : diag[r]));
+                for (int r = 0; r < 4; ++r) acc[r] *= jt < it ? below[r] * step : diag[r];
+                T* to = sm + (16 * it + r16) * LDM + 16 * jt + 4 * gr;
+                if constexpr (sizeof(T) == 4)
+                    *(f32x4*)to = acc;
+                else
+                    *(bf16x4*)to = bf16x4{(bf16)acc[0], (bf16)acc[1], (bf16)acc[2], (bf16)acc[3]};
             }
         }
         __syncthreads();
-        // what the state gives each row
+        // what the state gives each row; result tiles hold columns of c by rows
         f32x4 acc[IT][VT];
 #pragma unroll
         for (int it = 0; it < IT; ++it)
@@ -428,7 +533,7 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
 #pragma unroll
                 for (int v = 0; v < VT; ++v)
 #pragma unroll
-                    for (int n = 0; n < state_parts<T>(); ++n) acc[it][v] = M::mma(a, p[v].f[n], acc[it][v]);
+                    for (int n = 0; n < state_parts<T>(); ++n) acc[it][v] = M::mma(p[v].f[n], a, acc[it][v]);
             }
         }
 #pragma unroll
@@ -436,9 +541,13 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
 #pragma unroll
             for (int v = 0; v < VT; ++v)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[it][v][r] *= inter[it][r];
+                for (int r = 0; r < 4; ++r) acc[it][v][r] *= inter[it];
         // what the chunk's own rows give, and the state's update
-        S.decay(g, m);
+        if (m < C) {                           // the sequence's last rows
+            update_weights<E, C>(g2, w.su, m, w.e, u);
+            d.set(g, m);
+        }
+        S.decay(d);
 #pragma unroll
         for (int k0 = 0; k0 < C; k0 += KS) {
             typename M::Frag c[VT];
@@ -448,28 +557,13 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
             for (int it = k0 / 16; it < IT; ++it) {
                 const auto a = frag_row<T>(sm, LDM, 16 * it, k0);
 #pragma unroll
-                for (int v = 0; v < VT; ++v) acc[it][v] = M::mma(a, c[v], acc[it][v]);
+                for (int v = 0; v < VT; ++v) acc[it][v] = M::mma(c[v], a, acc[it][v]);
             }
-            float u[E];
-            update_weights<E>(g2, w.su, k0, m, w.e, u);
-            S.update(sb, Tl::LD, k0, c, u);
+            S.update(sb, Tl::LD, k0, c, u[k0 / KS]);
         }
-#pragma unroll
-        for (int it = 0; it < IT; ++it)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = t0 + 16 * it + 4 * gr + r;
-                if (t >= t_end) continue;
-                const size_t at = (((size_t)b * w.T + position(t, L, w.reverse)) * w.H + h) * w.Dc;
-#pragma unroll
-                for (int v = 0; v < VT; ++v) {
-                    const int j = S.col(v);
-                    if (j >= w.Dc) continue;
-                    const float x = t < L ? acc[it][v][r] : 0.0f;
-                    if (w.out32) ((float*)w.out)[at + j] = x;
-                    else ((T*)w.out)[at + j] = (T)x;
-                }
-            }
+        const int col = wave * VT * 16 + 4 * gr;
+        if (w.out32) store_rows<float, IT, VT>(w, (float*)w.out + out0, t0, m, L, col, acc);
+        else store_rows<T, IT, VT>(w, (T*)w.out + out0, t0, m, L, col, acc);
     }
     if (w.state_out) S.store(w.state_out + bh * D, w.Da, w.Dc, w.transposed);
 }
@@ -611,7 +705,19 @@ Sweep base_sweep(const AttnArgs& a, const AttnLayout& l) {
     return w;
 }
 
-Role role(const void* p, const int64_t* s, int group) { return Role{p, (long)s[0], (long)s[1], (long)s[2], group}; }
+// D: the role's width, of elements of `es` bytes
+Role role(const void* p, const int64_t* s, int group, int D, int es) {
+    // buffer loads want addresses of whole dwords
+    const bool dword = (uintptr_t)p % 4 == 0 && s[0] * es % 4 == 0 && s[1] * es % 4 == 0 && s[2] * es % 4 == 0;
+    const bool fast = dword && D * es % 16 == 0 && s[1] >= D && s[1] * es * 64 < (1l << 29);
+    return Role{p, (long)s[0], (long)s[1], (long)s[2], group, fast};
+}
+
+void set_out(Sweep& w, void* out, bool out32, int es) {
+    w.out = out;
+    w.out32 = out32;
+    w.fast_out = (uintptr_t)out % 4 == 0 && w.Dc % 4 == 0 && (long)w.H * w.Dc * (out32 ? 4 : es) * 64 < (1l << 29);
+}
 
 hipError_t run_state(const semicrf_attention& p, const Sweep& w, hipStream_t stream) {
     return with_kernel(p, [&](auto t, auto pp, auto cc) {
@@ -654,14 +760,14 @@ size_t decay_attention_bytes(const semicrf_attention& p, bool grad) { return att
 hipError_t launch_decay_attention(const AttnArgs& a, void* ws, hipStream_t stream) {
     const semicrf_attention& p = a.p;
     const AttnLayout l = attn_layout(p, false);
-    const int group = p.Hq / p.Hk;
+    const int group = p.Hq / p.Hk, es = p.dtype == SEMICRF_F32 ? 4 : 2;
     Sweep w = base_sweep(a, l);
-    w.a = role(p.q, p.q_stride, 1);
-    w.b = role(p.k, p.k_stride, group);
-    w.c = role(p.v, p.v_stride, group);
+    w.a = role(p.q, p.q_stride, 1, p.Dk, es);
+    w.b = role(p.k, p.k_stride, group, p.Dk, es);
+    w.c = role(p.v, p.v_stride, group, p.Dv, es);
     w.Da = p.Dk; w.Dc = p.Dv;
     w.si = p.scale; w.su = 1.0f;
-    w.out = a.out;
+    set_out(w, a.out, false, es);
     w.state = p.state;
     w.state_nseg = 1;
     if (l.nseg > 1) {
@@ -679,10 +785,10 @@ hipError_t launch_decay_attention(const AttnArgs& a, void* ws, hipStream_t strea
 hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t stream) {
     const semicrf_attention& p = a.p;
     const AttnLayout l = attn_layout(p, true);
-    const int group = p.Hq / p.Hk;
+    const int group = p.Hq / p.Hk, es = p.dtype == SEMICRF_F32 ? 4 : 2;
     const int64_t gs[3] = {(int64_t)p.T * p.Hq * p.Dv, (int64_t)p.Hq * p.Dv, p.Dv};
-    const Role q = role(p.q, p.q_stride, 1), k = role(p.k, p.k_stride, group),
-               v = role(p.v, p.v_stride, group), g = role(a.grad_out, gs, 1);
+    const Role q = role(p.q, p.q_stride, 1, p.Dk, es), k = role(p.k, p.k_stride, group, p.Dk, es),
+               v = role(p.v, p.v_stride, group, p.Dv, es), g = role(a.grad_out, gs, 1, p.Dv, es);
     float* S = (float*)((char*)ws + l.S);
     float* R = (float*)((char*)ws + l.R);
     Sweep w = base_sweep(a, l);
@@ -704,17 +810,16 @@ hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t 
     }
     // dq
     f.a = g; f.b = v; f.c = k; f.Da = p.Dv; f.Dc = p.Dk; f.transposed = 1;
-    f.out = a.grad_q;
+    set_out(f, a.grad_q, false, es);
     TRY(run_sweep(p, f, stream));
     // dv, and the gradient of the initial state
     r.a = k; r.b = q; r.c = g; r.Da = p.Dk; r.Dc = p.Dv; r.transposed = 0;
-    r.out32 = group > 1;
-    r.out = group > 1 ? (void*)((char*)ws + l.gv) : a.grad_v;
+    set_out(r, group > 1 ? (void*)((char*)ws + l.gv) : a.grad_v, group > 1, es);
     r.state_out = l.nseg > 1 ? nullptr : a.grad_state;
     TRY(run_sweep(p, r, stream));
     // dk
     r.a = v; r.b = g; r.c = q; r.Da = p.Dv; r.Dc = p.Dk; r.transposed = 1;
-    r.out = group > 1 ? (void*)((char*)ws + l.gk) : a.grad_k;
+    set_out(r, group > 1 ? (void*)((char*)ws + l.gk) : a.grad_k, group > 1, es);
     r.state_out = nullptr;
     TRY(run_sweep(p, r, stream));
     if (group > 1) {
