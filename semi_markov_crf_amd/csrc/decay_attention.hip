@@ -46,9 +46,12 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int BUFFER_FLAGS = 0x00027000;
 
 // ------------------------------------------------------------------ matrix products
-// A product step contracts KS indices.  Lane l = 16 g + r holds E consecutive contraction
-// indices E g .. E g + E - 1 of row (or column) r: 16 bytes of a row.  The result tile holds
-// column r, rows 4 g .. 4 g + 3.
+// A product step contracts KS indices.  Lane l = 16 g + r holds, of row (or column) r, the E
+// contraction indices that `order` lists; both operands list the same ones, so any order gives
+// the same product.  The result tile holds column r, rows 4 g .. 4 g + 3.  The order used is the
+// one in which result tiles lie in registers, four rows of a 16-row tile after four of the
+// next: the state's accumulators are an operand as they are, and the transposing LDS read
+// fetches four rows at a time.
 template <class T>
 struct Mma;
 
@@ -72,40 +75,56 @@ struct Mma<float> {
     }
 };
 
-// Row of the state that tile `t` holds at its row `rho`: chosen so that the accumulator tiles
-// of the state are, as they lie in registers, the right operand of a product step.
+// Where index i of a row stands when it is stored in the order of product steps: in blocks of
+// 32, 8 g + e holds index 4 g + e, 8 g + 4 + e index 16 + 4 g + e (fp32 steps take 16: no change).
 template <class T>
-__device__ __forceinline__ constexpr int state_row(int t, int rho) {
-    return sizeof(T) == 4 ? 16 * t + rho : 32 * (t >> 1) + 8 * (rho >> 2) + 4 * (t & 1) + (rho & 3);
+__device__ __forceinline__ constexpr int ordered(int i) {
+    return sizeof(T) == 4 ? i : (i & ~31) + 8 * ((i & 15) >> 2) + 4 * ((i & 31) >> 4) + (i & 3);
 }
 
-// 16 bytes of row `row + r`, contraction indices from k0
+// Row `row + r` of a buffer whose rows are stored in the order of product steps
 template <class T>
-__device__ __forceinline__ typename Mma<T>::Frag frag_row(const T* buf, int ld, int row, int k0) {
+__device__ __forceinline__ typename Mma<T>::Frag frag_ordered(const T* buf, int ld, int row, int k0) {
     const int l = threadIdx.x & 63;
     return *(const typename Mma<T>::Frag*)(buf + (row + (l & 15)) * ld + k0 + (l >> 4) * Mma<T>::E);
 }
+// ... and of one whose rows are stored as they are
+__device__ __forceinline__ bf16x8 frag_row(const bf16* buf, int ld, int row, int k0) {
+    const int l = threadIdx.x & 63;
+    const bf16* at = buf + (row + (l & 15)) * ld + k0 + (l >> 4) * 4;
+    return __builtin_shufflevector(*(const bf16x4*)at, *(const bf16x4*)(at + 16), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ f32x4 frag_row(const float* buf, int ld, int row, int k0) {
+    return frag_ordered<float>(buf, ld, row, k0);
+}
 
-// Columns as rows: element j of the lane is buf[k0 + E g + j][col(r)], with col(r) = c0 + r, or
-// with PERM the state row of tile `t` (c0 is then the tile number).
-template <bool PERM>
+// Column c0 + r, rows k0 .. of a step
 __device__ __forceinline__ bf16x8 frag_col(const bf16* buf, int ld, int k0, int c0) {
     // the transposing read gives lane 16 g + i the i-th column of the 4 x 16 block whose row j
     // is what lanes 16 g + 4 j .. + 3 point at, four elements each
     const int l = threadIdx.x & 63, g = l >> 4, p = l & 15;
-    const int col = PERM ? state_row<bf16>(c0, 4 * (p & 3)) : c0 + 4 * (p & 3);
     typedef __attribute__((address_space(3))) bf16x4 Lds;
-    const bf16* at = buf + (k0 + 8 * g + (p >> 2)) * ld + col;
+    const bf16* at = buf + (k0 + 4 * g + (p >> 2)) * ld + c0 + 4 * (p & 3);
     const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds*)at);
-    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds*)(at + 4 * ld));
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds*)(at + 16 * ld));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-template <bool PERM>
 __device__ __forceinline__ f32x4 frag_col(const float* buf, int ld, int k0, int c0) {
     const int l = threadIdx.x & 63, g = l >> 4, r = l & 15;
-    const float* at = buf + (k0 + 4 * g) * ld + (PERM ? 16 * c0 : c0) + r;
+    const float* at = buf + (k0 + 4 * g) * ld + c0 + r;
     return f32x4{at[0], at[ld], at[2 * ld], at[3 * ld]};
 }
+// Row of a step that element j of this lane's fragment holds
+template <class T>
+__device__ __forceinline__ int step_row(int j) {
+    const int g = (threadIdx.x & 63) >> 4;
+    return sizeof(T) == 4 ? 4 * g + j : 4 * g + (j & 3) + 16 * (j >> 2);
+}
+
+// Elements between rows in LDS.  Measured on row reads, transposing reads and piece writes: 16
+// bfloat16 of padding cost no bank conflicts in any of them, 8 do in all.
+template <class T>
+constexpr int lds_pitch(int width) { return width + (sizeof(T) == 4 ? 4 : 16); }
 
 // Parts of an fp32 fragment that add up to it: one in fp32, n in bfloat16 (8 bits each).
 template <class T, int N>
@@ -130,7 +149,6 @@ struct Role {
     const void* p;
     long sb, st, sh;         // strides in elements
     int group;               // query heads that share a head of this role
-    int fast;                // rows are whole 16-byte pieces that do not overlap
 };
 
 struct Sweep {
@@ -147,7 +165,7 @@ struct Sweep {
     float* state_out;        // after the last position (one segment only), or NULL
     float* local;            // k_attn_state: state of each segment alone
     void* out;               // [B, T, H, Dc] in T, or fp32 where `out32`
-    int out32, fast_out;
+    int out32;
     int32_t* status;
 };
 
@@ -155,13 +173,15 @@ __device__ __forceinline__ float power(float g2, int n) {
     return n == 0 ? 1.0f : __builtin_amdgcn_exp2f(g2 * (float)n);
 }
 
-// A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces: the thread's
-// column piece is the same in all its rows.  Loads go through a buffer descriptor over exactly
-// the chunk's valid rows, so rows and columns out of range read as zeros with no branch; offsets
-// in a chunk stay below 2^29 bytes (Role::fast), and bit 31 puts one out of range.
-template <class T, int P, int C, int NT>
+// A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces; a thread's
+// column piece is the same in all its rows.
+//   FAST: rows are whole pieces that do not overlap, and a chunk spans less than 2^29 bytes.  Loads
+//   go through a buffer descriptor over exactly the chunk's valid rows, so that rows and columns
+//   out of range read as zeros with no branch (bit 31 of the offset puts a column out of range).
+//   Otherwise element by element.
+template <class T, int P, int C, int NT, bool FAST>
 struct Tile {
-    static constexpr int V = Piece<T>::V, PPR = P / V, LD = P + V, RPS = NT / PPR;
+    static constexpr int V = Piece<T>::V, PPR = P / V, LD = lds_pitch<T>(P), RPS = NT / PPR;
     static constexpr int NP = C / RPS;
     static_assert(NT % PPR == 0 && C % RPS == 0, "pieces per thread");
     u32x4 x[NP];
@@ -169,19 +189,16 @@ struct Tile {
     // m valid rows from sweep index t0 (position L - t0 - m is the lowest of a reversed chunk)
     __device__ __forceinline__ void load(const Role& w, const T* seq, int D, int t0, int m, int L, int reverse) {
         const int row0 = threadIdx.x / PPR, c = (threadIdx.x % PPR) * V;
-        if (w.fast) {
+        if constexpr (FAST) {
             const int stb = (int)w.st * (int)sizeof(T);
             const T* base = seq + (long)(reverse ? L - t0 - m : t0) * w.st;
             const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
                 (void*)base, 0, m > 0 ? (m - 1) * stb + D * (int)sizeof(T) : 0, BUFFER_FLAGS);
-            const uint32_t cb = c < D ? c * (uint32_t)sizeof(T) : 0x80000000u;
-            uint32_t off = cb + (uint32_t)(reverse ? (m - 1 - row0) * stb : row0 * stb);
-            const uint32_t step = (uint32_t)(reverse ? -RPS * stb : RPS * stb);
+            const int step = reverse ? -stb : stb;
+            uint32_t off = (c < D ? c * (uint32_t)sizeof(T) : 0x80000000u) + (uint32_t)(row0 * step) +
+                           (uint32_t)(reverse ? (m - 1) * stb : 0);
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                x[n] = __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0);
-                off += step;
-            }
+            for (int n = 0; n < NP; ++n) x[n] = __builtin_amdgcn_raw_buffer_load_b128(buf, off + n * RPS * step, 0, 0);
         } else {
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
@@ -199,10 +216,20 @@ struct Tile {
             }
         }
     }
+    // ORDERED: columns in the order of product steps
+    template <bool ORDERED>
     __device__ __forceinline__ void put(T* buf) const {
         const int row0 = threadIdx.x / PPR, c = (threadIdx.x % PPR) * V;
 #pragma unroll
-        for (int n = 0; n < NP; ++n) *(u32x4*)(buf + (row0 + n * RPS) * LD + c) = x[n];
+        for (int n = 0; n < NP; ++n) {
+            T* row = buf + (row0 + n * RPS) * LD;
+            if constexpr (ORDERED && sizeof(T) == 2) {
+                *(u32x2*)(row + ordered<T>(c)) = u32x2{x[n][0], x[n][1]};
+                *(u32x2*)(row + ordered<T>(c + 4)) = u32x2{x[n][2], x[n][3]};
+            } else {
+                *(u32x4*)(row + c) = x[n];
+            }
+        }
     }
 };
 
@@ -211,7 +238,11 @@ __device__ __forceinline__ const T* role_base(const Role& r, int b, int h) {
     return (const T*)r.p + (long)b * r.sb + (long)(h / r.group) * r.sh;
 }
 
-constexpr int sweep_waves(int P) { return P >= 64 ? 4 : P / 16; }
+// One wavefront for each 16 columns of the state.
+constexpr int sweep_waves(int P) { return P / 16; }
+// Wavefronts a SIMD of the sweep: what its registers allow without spills (LDS allows as many).
+template <class T, int P>
+constexpr int sweep_occupancy() { return P <= 64 && sizeof(T) == 2 ? 3 : 2; }
 
 // gamma^m of the state.  Near 1 it is applied as S + (gamma^m - 1) S: over thousands of chunks a
 // factor rounded once would bend every old contribution the same way.
@@ -225,7 +256,7 @@ struct Decay {
     }
 };
 
-// State tiles of a wavefront: rows of the state by state_row, its own columns.
+// State tiles of a wavefront: all rows, its own columns.
 template <class T, int P>
 struct State {
     static constexpr int NW = sweep_waves(P), VT = P / 16 / NW, ST = P / 16;
@@ -236,7 +267,7 @@ struct State {
         return ((threadIdx.x >> 6) * VT + vt) * 16 + (threadIdx.x & 15);
     }
     __device__ __forceinline__ int row(int t, int r) const {
-        return state_row<T>(t, 4 * ((threadIdx.x & 63) >> 4) + r);
+        return 16 * t + 4 * ((threadIdx.x & 63) >> 4) + r;
     }
     __device__ __forceinline__ void load(const float* p, int Da, int Dc, bool transposed) {
 #pragma unroll
@@ -279,7 +310,7 @@ struct State {
             for (int j = 0; j < E; ++j) p[v].set(j, (float)c[v][j] * w[j]);
 #pragma unroll
         for (int t = 0; t < ST; ++t) {
-            const auto a = frag_col<true>(bbuf, ld, k0, t);
+            const auto a = frag_col(bbuf, ld, k0, 16 * t);
 #pragma unroll
             for (int v = 0; v < VT; ++v)
 #pragma unroll
@@ -288,66 +319,108 @@ struct State {
     }
 };
 
-// su gamma^(m-1-j+e) for the lane's rows of every product step of a chunk (0 past m)
-template <int E, int C>
-__device__ __forceinline__ void update_weights(float g2, float su, int m, int e, float (&w)[C / (4 * E)][E]) {
+// su gamma^(m-1-j+e) for the rows j this lane holds of the step from row k0 (0 past m).
+template <class T>
+__device__ __forceinline__ void update_weights(float g2, float su, int k0, int m, int e, float (&w)[Mma<T>::E]) {
 #pragma unroll
-    for (int k = 0; k < C / (4 * E); ++k)
+    for (int j = 0; j < Mma<T>::E; ++j) {
+        const int i = k0 + step_row<T>(j);
+        w[j] = i < m ? su * power(g2, m - 1 - i + e) : 0.0f;
+    }
+}
+
+// The update of full chunks: weights of the last product step (earlier steps are gamma^KS
+// apart) and the state's decay.  A sequence's last, partial chunk is left out of it (`skip`) and
+// added by update_rest after the loop, where it matters.
+template <class T, int C>
+struct Update {
+    static constexpr int KS = Mma<T>::KS, E = Mma<T>::E;
+    float last[E], step;
+    Decay d;
+    __device__ __forceinline__ void set(float g, float g2, float su, int e) {
+        update_weights<T>(g2, su, 0, KS, e, last);
+        step = power(g2, KS);
+        d.set(g, C);
+    }
+    __device__ __forceinline__ void skip() {
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int i = (k * 4 + ((threadIdx.x & 63) >> 4)) * E + j;
-            w[k][j] = i < m ? su * power(g2, m - 1 - i + e) : 0.0f;
-        }
+        for (int j = 0; j < E; ++j) last[j] = 0.0f;
+        d.set(0.0f, 0);
+    }
+    __device__ __forceinline__ void get(int k0, float (&w)[E]) const {
+        float f = 1.0f;
+#pragma unroll
+        for (int k = k0 + KS; k < C; k += KS) f *= step;
+#pragma unroll
+        for (int j = 0; j < E; ++j) w[j] = last[j] * f;
+    }
+};
+template <class T, int P, int C>
+__device__ __forceinline__ void update_rest(State<T, P>& S, const T* sb, const T* sc, int m, float g, float g2,
+                                            float su, int e) {
+    constexpr int LD = lds_pitch<T>(P), VT = State<T, P>::VT;
+    Decay d;
+    d.set(g, m);
+    S.decay(d);
+#pragma unroll 1
+    for (int k0 = 0; k0 < C; k0 += Mma<T>::KS) {
+        typename Mma<T>::Frag c[VT];
+#pragma unroll
+        for (int v = 0; v < VT; ++v) c[v] = frag_col(sc, LD, k0, ((threadIdx.x >> 6) * VT + v) * 16);
+        float u[Mma<T>::E];
+        update_weights<T>(g2, su, k0, m, e, u);
+        S.update(sb, LD, k0, c, u);
+    }
 }
 
 // grid (nseg, H, B)
-template <class T, int P, int C>
-__global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_state(const Sweep w) {
+template <class T, int P, int C, bool FAST>
+__global__ __launch_bounds__(64 * sweep_waves(P), P == 128 ? 2 : 4) void
+k_attn_state(const Sweep w) {
     using M = Mma<T>;
     using St = State<T, P>;
     constexpr int NT = 64 * St::NW, VT = St::VT;
-    using Tl = Tile<T, P, C, NT>;
+    using Tl = Tile<T, P, C, NT, FAST>;
     __shared__ __align__(16) T sb[C * Tl::LD], sc[C * Tl::LD];
     const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const int L = seq_length(w.lengths, b, w.T, w.status);
+    const int L = __builtin_amdgcn_readfirstlane(seq_length(w.lengths, b, w.T, w.status));
     const int t_begin = seg * w.seg, t_end = min(L, t_begin + w.seg);
     const float g = w.log_decay[h], g2 = g * (float)LOG2E;
     const T* pb = role_base<T>(w.b, b, h);
     const T* pc = role_base<T>(w.c, b, h);
-    St S;
-    S.load(nullptr, 0, 0, false);
-    float u[C / M::KS][M::E];
-    update_weights<M::E, C>(g2, w.su, C, w.e, u);
-    Decay d;
-    d.set(g, C);
     Tl tb, tc;
     tb.load(w.b, pb, w.Da, t_begin, min(C, t_end - t_begin), L, w.reverse);
     tc.load(w.c, pc, w.Dc, t_begin, min(C, t_end - t_begin), L, w.reverse);
+    St S;
+    S.load(nullptr, 0, 0, false);
+    Update<T, C> up;
+    up.set(g, g2, w.su, w.e);
     for (int t0 = t_begin; t0 < t_end; t0 += C) {
         const int m = min(C, t_end - t0);
         __syncthreads();
-        tb.put(sb);
-        tc.put(sc);
+        tb.template put<false>(sb);
+        tc.template put<false>(sc);
         __syncthreads();
         if (t0 + C < t_end) {
             const int mn = min(C, t_end - t0 - C);
             tb.load(w.b, pb, w.Da, t0 + C, mn, L, w.reverse);
             tc.load(w.c, pc, w.Dc, t0 + C, mn, L, w.reverse);
         }
-        if (m < C) {                           // the sequence's last rows
-            update_weights<M::E, C>(g2, w.su, m, w.e, u);
-            d.set(g, m);
-        }
-        S.decay(d);
+        if (m < C) up.skip();
+        S.decay(up.d);
 #pragma unroll
         for (int k0 = 0; k0 < C; k0 += M::KS) {
             typename M::Frag c[VT];
 #pragma unroll
             for (int v = 0; v < VT; ++v)
-                c[v] = frag_col<false>(sc, Tl::LD, k0, ((threadIdx.x >> 6) * VT + v) * 16);
-            S.update(sb, Tl::LD, k0, c, u[k0 / M::KS]);
+                c[v] = frag_col(sc, Tl::LD, k0, ((threadIdx.x >> 6) * VT + v) * 16);
+            float u[M::E];
+            up.get(k0, u);
+            S.update(sb, Tl::LD, k0, c, u);
         }
     }
+    if (t_end > t_begin && (t_end - t_begin) % C)
+        update_rest<T, P, C>(S, sb, sc, (t_end - t_begin) % C, g, g2, w.su, w.e);
     S.store(w.local + (((size_t)b * w.H + h) * w.nseg + seg) * w.Da * w.Dc, w.Da, w.Dc, false);
 }
 
@@ -363,13 +436,22 @@ __global__ __launch_bounds__(256) void k_attn_scan(float* local, const float* in
     const double g = log_decay[h];
     float cur = init ? init[bh * D + i] : 0.0f;
     const float full = (float)exp(g * seg);
-    for (int s = 0; s < nseg; ++s) {
-        float* p = local + (bh * nseg + s) * D + i;
-        const float own = *p;
-        *p = cur;
-        const int m = min(seg, max(0, L - s * seg));
-        const float f = m == seg ? full : m == 0 ? 1.0f : (float)exp(g * m);
-        cur = fmaf(cur, f, own);
+    float* p = local + bh * nseg * D + i;
+    // the loads do not wait for one another: U at a time
+    constexpr int U = 16;
+    for (int s0 = 0; s0 < nseg; s0 += U) {
+        float own[U];
+#pragma unroll
+        for (int n = 0; n < U; ++n) own[n] = s0 + n < nseg ? p[(size_t)(s0 + n) * D] : 0.0f;
+#pragma unroll
+        for (int n = 0; n < U; ++n) {
+            const int s = s0 + n;
+            if (s >= nseg) break;
+            p[(size_t)s * D] = cur;
+            const int m = min(seg, max(0, L - s * seg));
+            const float f = m == seg ? full : m == 0 ? 1.0f : (float)exp(g * m);
+            cur = fmaf(cur, f, own[n]);
+        }
     }
     if (out) out[bh * D + i] = cur;
 }
@@ -387,26 +469,23 @@ __device__ __forceinline__ void store4(const __amdgpu_buffer_rsrc_t& buf, uint32
 
 // Rows i < m of a chunk from result tiles that hold column i = 16 it + r, rows (of the tile)
 // four consecutive output columns from `col`.
-template <class O, int IT, int VT>
+template <class O, bool FAST, int IT, int VT>
 __device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m, int L, int col,
                                            const f32x4 (&acc)[IT][VT]) {
     const int r16 = threadIdx.x & 15;
     const long ost = (long)w.H * w.Dc;
-    if (w.fast_out) {
-        const int stb = (int)ost * (int)sizeof(O);
+    if constexpr (FAST) {
+        const int stb = (int)ost * (int)sizeof(O), step = w.reverse ? -stb : stb;
         O* base = seq + (long)(w.reverse ? L - t0 - m : t0) * ost;
         const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
             (void*)base, 0, (m - 1) * stb + w.Dc * (int)sizeof(O), BUFFER_FLAGS);
-        uint32_t off = (uint32_t)(w.reverse ? (m - 1 - r16) * stb : r16 * stb);
-        const uint32_t step = (uint32_t)(w.reverse ? -16 * stb : 16 * stb);
+        const uint32_t off = (uint32_t)(r16 * step) + (uint32_t)(w.reverse ? (m - 1) * stb : 0);
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
+        for (int v = 0; v < VT; ++v) {
+            const int c = col + 16 * v;
+            const uint32_t at = off + (c < w.Dc ? c * (uint32_t)sizeof(O) : 0x80000000u);
 #pragma unroll
-            for (int v = 0; v < VT; ++v) {
-                const int c = col + 16 * v;
-                store4<O>(buf, off + (c < w.Dc ? c * (uint32_t)sizeof(O) : 0x80000000u), acc[it][v]);
-            }
-            off += step;
+            for (int it = 0; it < IT; ++it) store4<O>(buf, at + it * 16 * step, acc[it][v]);
         }
     } else {
 #pragma unroll
@@ -425,13 +504,14 @@ __device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m
 }
 
 // grid (nseg, H, B)
-template <class T, int P, int C>
-__global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep w) {
+template <class T, int P, int C, bool FAST>
+__global__ __launch_bounds__(64 * sweep_waves(P), (sweep_occupancy<T, P>())) void
+k_attn_sweep(const Sweep w) {
     using M = Mma<T>;
     using St = State<T, P>;
     constexpr int NW = St::NW, NT = 64 * NW, VT = St::VT, IT = C / 16, KS = M::KS, E = M::E;
-    using Tl = Tile<T, P, C, NT>;
-    constexpr int LDM = C + Piece<T>::V;
+    using Tl = Tile<T, P, C, NT, FAST>;
+    constexpr int LDM = lds_pitch<T>(C);
     __shared__ __align__(16) T sa[C * Tl::LD], sb[C * Tl::LD], sc[C * Tl::LD], sm[C * LDM];
     const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -442,13 +522,6 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
     const size_t bh = (size_t)b * w.H + h;
     const size_t D = (size_t)w.Da * w.Dc;
     const size_t out0 = (size_t)b * w.T * w.H * w.Dc + (size_t)h * w.Dc;
-    // padding: positions from the length on
-    for (int t = max(t_begin, L) + threadIdx.x / 16; t < t_last; t += NT / 16)
-        for (int j = r16; j < w.Dc; j += 16) {
-            const size_t at = out0 + (size_t)t * w.H * w.Dc + j;
-            if (w.out32) ((float*)w.out)[at] = 0.0f;
-            else ((T*)w.out)[at] = (T)0.0f;
-        }
     const T* pa = role_base<T>(w.a, b, h);
     const T* pb = role_base<T>(w.b, b, h);
     const T* pc = role_base<T>(w.c, b, h);
@@ -459,6 +532,13 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
         tb.load(w.b, pb, w.Da, t_begin, m, L, w.reverse);
         tc.load(w.c, pc, w.Dc, t_begin, m, L, w.reverse);
     }
+    // padding: positions from the length on
+    for (int t = max(t_begin, L) + threadIdx.x / 16; t < t_last; t += NT / 16)
+        for (int j = r16; j < w.Dc; j += 16) {
+            const size_t at = out0 + (size_t)t * w.H * w.Dc + j;
+            if (w.out32) ((float*)w.out)[at] = 0.0f;
+            else ((T*)w.out)[at] = (T)0.0f;
+        }
     St S;
     S.load(w.state ? w.state + (bh * w.state_nseg + (w.state_nseg > 1 ? seg : 0)) * D : nullptr, w.Da,
            w.Dc, w.transposed);
@@ -476,16 +556,14 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
 #pragma unroll
     for (int it = 0; it < IT; ++it) inter[it] = w.si * power(g2, 16 * it + r16 + 1 - w.e);
     const float g16 = power(g2, 16);
-    float u[C / KS][E];
-    update_weights<E, C>(g2, w.su, C, w.e, u);
-    Decay d;
-    d.set(g, C);
+    Update<T, C> up;
+    up.set(g, g2, w.su, w.e);
     for (int t0 = t_begin; t0 < t_end; t0 += C) {
         const int m = min(C, t_end - t0);
         __syncthreads();
-        ta.put(sa);
-        tb.put(sb);
-        tc.put(sc);
+        ta.template put<true>(sa);
+        tb.template put<false>(sb);
+        tc.template put<false>(sc);
         __syncthreads();
         if (t0 + C < t_end) {
             const int mn = min(C, t_end - t0 - C);
@@ -502,11 +580,11 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
                 f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int k0 = 0; k0 < P; k0 += KS)
-                    acc = M::mma(frag_row<T>(sb, Tl::LD, 16 * jt, k0), frag_row<T>(sa, Tl::LD, 16 * it, k0), acc);
+                    acc = M::mma(frag_row(sb, Tl::LD, 16 * jt, k0), frag_ordered<T>(sa, Tl::LD, 16 * it, k0), acc);
                 const float step = it - jt <= 1 ? 1.0f : it - jt == 2 ? g16 : g16 * g16;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[r] *= jt < it ? below[r] * step : diag[r];
-                T* to = sm + (16 * it + r16) * LDM + 16 * jt + 4 * gr;
+                T* to = sm + (16 * it + r16) * LDM + ordered<T>(16 * jt + 4 * gr);
                 if constexpr (sizeof(T) == 4)
                     *(f32x4*)to = acc;
                 else
@@ -529,12 +607,13 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
                 for (int j = 0; j < E; ++j) p[v].set(j, S.s[kb * St::TPK + j / 4][v][j % 4]);
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-                const auto a = frag_row<T>(sa, Tl::LD, 16 * it, kb * KS);
+                const auto a = frag_ordered<T>(sa, Tl::LD, 16 * it, kb * KS);
 #pragma unroll
                 for (int v = 0; v < VT; ++v)
 #pragma unroll
                     for (int n = 0; n < state_parts<T>(); ++n) acc[it][v] = M::mma(p[v].f[n], a, acc[it][v]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int it = 0; it < IT; ++it)
@@ -543,29 +622,33 @@ __global__ __launch_bounds__(64 * sweep_waves(P)) void k_attn_sweep(const Sweep 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[it][v][r] *= inter[it];
         // what the chunk's own rows give, and the state's update
-        if (m < C) {                           // the sequence's last rows
-            update_weights<E, C>(g2, w.su, m, w.e, u);
-            d.set(g, m);
-        }
-        S.decay(d);
+        if (m < C) up.skip();
+        S.decay(up.d);
 #pragma unroll
         for (int k0 = 0; k0 < C; k0 += KS) {
             typename M::Frag c[VT];
 #pragma unroll
-            for (int v = 0; v < VT; ++v) c[v] = frag_col<false>(sc, Tl::LD, k0, (wave * VT + v) * 16);
+            for (int v = 0; v < VT; ++v) c[v] = frag_col(sc, Tl::LD, k0, (wave * VT + v) * 16);
 #pragma unroll
             for (int it = k0 / 16; it < IT; ++it) {
-                const auto a = frag_row<T>(sm, LDM, 16 * it, k0);
+                const auto a = frag_ordered<T>(sm, LDM, 16 * it, k0);
 #pragma unroll
                 for (int v = 0; v < VT; ++v) acc[it][v] = M::mma(c[v], a, acc[it][v]);
             }
-            S.update(sb, Tl::LD, k0, c, u[k0 / KS]);
+            float u[E];
+            up.get(k0, u);
+            S.update(sb, Tl::LD, k0, c, u);
+            __builtin_amdgcn_sched_barrier(0);
         }
         const int col = wave * VT * 16 + 4 * gr;
-        if (w.out32) store_rows<float, IT, VT>(w, (float*)w.out + out0, t0, m, L, col, acc);
-        else store_rows<T, IT, VT>(w, (T*)w.out + out0, t0, m, L, col, acc);
+        if (w.out32) store_rows<float, FAST, IT, VT>(w, (float*)w.out + out0, t0, m, L, col, acc);
+        else store_rows<T, FAST, IT, VT>(w, (T*)w.out + out0, t0, m, L, col, acc);
     }
-    if (w.state_out) S.store(w.state_out + bh * D, w.Da, w.Dc, w.transposed);
+    if (w.state_out) {
+        if (t_end > t_begin && (t_end - t_begin) % C)
+            update_rest<T, P, C>(S, sb, sc, (t_end - t_begin) % C, g, g2, w.su, w.e);
+        S.store(w.state_out + bh * D, w.Da, w.Dc, w.transposed);
+    }
 }
 
 // out[row, hk, :] = sum over the group's query heads, in order.  One element a thread.
@@ -638,11 +721,12 @@ int head_pad(const semicrf_attention& p) {
 }
 int chunk_of(const semicrf_attention& p) { return p.dtype == SEMICRF_F32 && head_pad(p) == 128 ? 32 : 64; }
 
-// Segments of a sequence.
+// Positions per segment.  Workgroups that run at once: 2 or 3 wavefronts on each of 1,024 SIMDs.
 int segment(const semicrf_attention& p) {
-    const int C = chunk_of(p);
+    const int C = chunk_of(p), P = head_pad(p);
+    const long slots = 1024 * (P <= 64 && p.dtype == SEMICRF_BF16 ? 3 : 2) / sweep_waves(P);
     const long bh = (long)p.B * p.Hq;
-    long n = (1024 + bh - 1) / bh;
+    long n = slots / bh;
     const long most = p.T / 512;
     if (n > most) n = most;
     if (n < 1) n = 1;
@@ -705,26 +789,27 @@ Sweep base_sweep(const AttnArgs& a, const AttnLayout& l) {
     return w;
 }
 
-// D: the role's width, of elements of `es` bytes
-Role role(const void* p, const int64_t* s, int group, int D, int es) {
-    // buffer loads want addresses of whole dwords
-    const bool dword = (uintptr_t)p % 4 == 0 && s[0] * es % 4 == 0 && s[1] * es % 4 == 0 && s[2] * es % 4 == 0;
-    const bool fast = dword && D * es % 16 == 0 && s[1] >= D && s[1] * es * 64 < (1l << 29);
-    return Role{p, (long)s[0], (long)s[1], (long)s[2], group, fast};
-}
+Role role(const void* p, const int64_t* s, int group) { return Role{p, (long)s[0], (long)s[1], (long)s[2], group}; }
 
-void set_out(Sweep& w, void* out, bool out32, int es) {
-    w.out = out;
-    w.out32 = out32;
-    w.fast_out = (uintptr_t)out % 4 == 0 && w.Dc % 4 == 0 && (long)w.H * w.Dc * (out32 ? 4 : es) * 64 < (1l << 29);
+// Whether a role's rows can be read through buffer descriptors (Tile), addresses being whole
+// dwords, and whether the output's rows can be written so.
+bool fast_role(const Role& r, int D, int es) {
+    return (uintptr_t)r.p % 4 == 0 && r.sb * es % 4 == 0 && r.st * es % 4 == 0 && r.sh * es % 4 == 0 &&
+           D * es % 16 == 0 && r.st >= D && r.st * es * 64 < (1l << 29);
+}
+bool fast_out(const Sweep& w, int es) {
+    return (uintptr_t)w.out % 4 == 0 && w.Dc % 4 == 0 && (long)w.H * w.Dc * (w.out32 ? 4 : es) * 64 < (1l << 29);
 }
 
 hipError_t run_state(const semicrf_attention& p, const Sweep& w, hipStream_t stream) {
     return with_kernel(p, [&](auto t, auto pp, auto cc) {
         using T = decltype(t);
-        constexpr int P = decltype(pp)::value, C = decltype(cc)::value;
-        hipLaunchKernelGGL((k_attn_state<T, P, C>), dim3(w.nseg, w.H, w.B), dim3(64 * sweep_waves(P)), 0,
-                           stream, w);
+        constexpr int P = decltype(pp)::value, C = decltype(cc)::value, es = sizeof(T);
+        const dim3 grid(w.nseg, w.H, w.B), block(64 * sweep_waves(P));
+        if (fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es))
+            hipLaunchKernelGGL((k_attn_state<T, P, C, true>), grid, block, 0, stream, w);
+        else
+            hipLaunchKernelGGL((k_attn_state<T, P, C, false>), grid, block, 0, stream, w);
         return hipGetLastError();
     });
 }
@@ -732,9 +817,12 @@ hipError_t run_state(const semicrf_attention& p, const Sweep& w, hipStream_t str
 hipError_t run_sweep(const semicrf_attention& p, const Sweep& w, hipStream_t stream) {
     return with_kernel(p, [&](auto t, auto pp, auto cc) {
         using T = decltype(t);
-        constexpr int P = decltype(pp)::value, C = decltype(cc)::value;
-        hipLaunchKernelGGL((k_attn_sweep<T, P, C>), dim3(w.nseg, w.H, w.B), dim3(64 * sweep_waves(P)), 0,
-                           stream, w);
+        constexpr int P = decltype(pp)::value, C = decltype(cc)::value, es = sizeof(T);
+        const dim3 grid(w.nseg, w.H, w.B), block(64 * sweep_waves(P));
+        if (fast_role(w.a, w.Da, es) && fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es) && fast_out(w, es))
+            hipLaunchKernelGGL((k_attn_sweep<T, P, C, true>), grid, block, 0, stream, w);
+        else
+            hipLaunchKernelGGL((k_attn_sweep<T, P, C, false>), grid, block, 0, stream, w);
         return hipGetLastError();
     });
 }
@@ -760,14 +848,14 @@ size_t decay_attention_bytes(const semicrf_attention& p, bool grad) { return att
 hipError_t launch_decay_attention(const AttnArgs& a, void* ws, hipStream_t stream) {
     const semicrf_attention& p = a.p;
     const AttnLayout l = attn_layout(p, false);
-    const int group = p.Hq / p.Hk, es = p.dtype == SEMICRF_F32 ? 4 : 2;
+    const int group = p.Hq / p.Hk;
     Sweep w = base_sweep(a, l);
-    w.a = role(p.q, p.q_stride, 1, p.Dk, es);
-    w.b = role(p.k, p.k_stride, group, p.Dk, es);
-    w.c = role(p.v, p.v_stride, group, p.Dv, es);
+    w.a = role(p.q, p.q_stride, 1);
+    w.b = role(p.k, p.k_stride, group);
+    w.c = role(p.v, p.v_stride, group);
     w.Da = p.Dk; w.Dc = p.Dv;
     w.si = p.scale; w.su = 1.0f;
-    set_out(w, a.out, false, es);
+    w.out = a.out;
     w.state = p.state;
     w.state_nseg = 1;
     if (l.nseg > 1) {
@@ -785,10 +873,10 @@ hipError_t launch_decay_attention(const AttnArgs& a, void* ws, hipStream_t strea
 hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t stream) {
     const semicrf_attention& p = a.p;
     const AttnLayout l = attn_layout(p, true);
-    const int group = p.Hq / p.Hk, es = p.dtype == SEMICRF_F32 ? 4 : 2;
+    const int group = p.Hq / p.Hk;
     const int64_t gs[3] = {(int64_t)p.T * p.Hq * p.Dv, (int64_t)p.Hq * p.Dv, p.Dv};
-    const Role q = role(p.q, p.q_stride, 1, p.Dk, es), k = role(p.k, p.k_stride, group, p.Dk, es),
-               v = role(p.v, p.v_stride, group, p.Dv, es), g = role(a.grad_out, gs, 1, p.Dv, es);
+    const Role q = role(p.q, p.q_stride, 1), k = role(p.k, p.k_stride, group),
+               v = role(p.v, p.v_stride, group), g = role(a.grad_out, gs, 1);
     float* S = (float*)((char*)ws + l.S);
     float* R = (float*)((char*)ws + l.R);
     Sweep w = base_sweep(a, l);
@@ -810,16 +898,17 @@ hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t 
     }
     // dq
     f.a = g; f.b = v; f.c = k; f.Da = p.Dv; f.Dc = p.Dk; f.transposed = 1;
-    set_out(f, a.grad_q, false, es);
+    f.out = a.grad_q;
     TRY(run_sweep(p, f, stream));
     // dv, and the gradient of the initial state
     r.a = k; r.b = q; r.c = g; r.Da = p.Dk; r.Dc = p.Dv; r.transposed = 0;
-    set_out(r, group > 1 ? (void*)((char*)ws + l.gv) : a.grad_v, group > 1, es);
+    r.out32 = group > 1;
+    r.out = group > 1 ? (void*)((char*)ws + l.gv) : a.grad_v;
     r.state_out = l.nseg > 1 ? nullptr : a.grad_state;
     TRY(run_sweep(p, r, stream));
     // dk
     r.a = v; r.b = g; r.c = q; r.Da = p.Dv; r.Dc = p.Dk; r.transposed = 1;
-    set_out(r, group > 1 ? (void*)((char*)ws + l.gk) : a.grad_k, group > 1, es);
+    r.out = group > 1 ? (void*)((char*)ws + l.gk) : a.grad_k;
     r.state_out = nullptr;
     TRY(run_sweep(p, r, stream));
     if (group > 1) {
