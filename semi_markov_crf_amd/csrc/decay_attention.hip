@@ -169,6 +169,33 @@ struct Sweep {
     int32_t* status;
 };
 
+// Sweeps of one shape that run in one launch.
+template <int N>
+struct Sweeps {
+    Sweep s[N];
+};
+
+// Workgroup -> (sweep, batch row, query head, segment).  What shares a key / value head and a
+// segment reads the same rows, so it runs at the same time on the same chiplet: consecutive
+// workgroups go to the 8 chiplets in turn, and members of a unit are 8 apart.
+struct Place {
+    int sweep, b, h, seg;
+};
+constexpr int CHIPLETS = 8;
+__device__ __forceinline__ bool place(const Sweep& w, int sweeps, int group, Place& p) {
+    const int members = sweeps * group;
+    const int id = blockIdx.x, lane = id % CHIPLETS, rest = id / CHIPLETS;
+    const int m = rest % members;
+    int u = rest / members * CHIPLETS + lane;
+    p.sweep = m / group;
+    const int hk = w.H / group;
+    p.seg = u % w.nseg;
+    u /= w.nseg;
+    p.h = u % hk * group + m % group;
+    p.b = u / hk;
+    return p.b < w.B;
+}
+
 __device__ __forceinline__ float power(float g2, int n) {
     return n == 0 ? 1.0f : __builtin_amdgcn_exp2f(g2 * (float)n);
 }
@@ -373,16 +400,18 @@ __device__ __forceinline__ void update_rest(State<T, P>& S, const T* sb, const T
     }
 }
 
-// grid (nseg, H, B)
-template <class T, int P, int C, bool FAST>
+template <class T, int P, int C, bool FAST, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), P == 128 ? 2 : 4) void
-k_attn_state(const Sweep w) {
+k_attn_state(const Sweeps<N> set, int group) {
     using M = Mma<T>;
     using St = State<T, P>;
     constexpr int NT = 64 * St::NW, VT = St::VT;
     using Tl = Tile<T, P, C, NT, FAST>;
     __shared__ __align__(16) T sb[C * Tl::LD], sc[C * Tl::LD];
-    const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    Place at;
+    if (!place(set.s[0], N, group, at)) return;
+    const Sweep w = set.s[N == 1 ? 0 : at.sweep];
+    const int seg = at.seg, h = at.h, b = at.b;
     const int L = __builtin_amdgcn_readfirstlane(seq_length(w.lengths, b, w.T, w.status));
     const int t_begin = seg * w.seg, t_end = min(L, t_begin + w.seg);
     const float g = w.log_decay[h], g2 = g * (float)LOG2E;
@@ -503,17 +532,19 @@ __device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m
     }
 }
 
-// grid (nseg, H, B)
-template <class T, int P, int C, bool FAST>
+template <class T, int P, int C, bool FAST, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), (sweep_occupancy<T, P>())) void
-k_attn_sweep(const Sweep w) {
+k_attn_sweep(const Sweeps<N> set, int group) {
     using M = Mma<T>;
     using St = State<T, P>;
     constexpr int NW = St::NW, NT = 64 * NW, VT = St::VT, IT = C / 16, KS = M::KS, E = M::E;
     using Tl = Tile<T, P, C, NT, FAST>;
     constexpr int LDM = lds_pitch<T>(C);
     __shared__ __align__(16) T sa[C * Tl::LD], sb[C * Tl::LD], sc[C * Tl::LD], sm[C * LDM];
-    const int seg = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    Place at;
+    if (!place(set.s[0], N, group, at)) return;
+    const Sweep w = set.s[N == 1 ? 0 : at.sweep];
+    const int seg = at.seg, h = at.h, b = at.b;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int gr = lane >> 4, r16 = lane & 15;
     const int L = __builtin_amdgcn_readfirstlane(seq_length(w.lengths, b, w.T, w.status));
@@ -535,9 +566,9 @@ k_attn_sweep(const Sweep w) {
     // padding: positions from the length on
     for (int t = max(t_begin, L) + threadIdx.x / 16; t < t_last; t += NT / 16)
         for (int j = r16; j < w.Dc; j += 16) {
-            const size_t at = out0 + (size_t)t * w.H * w.Dc + j;
-            if (w.out32) ((float*)w.out)[at] = 0.0f;
-            else ((T*)w.out)[at] = (T)0.0f;
+            const size_t to = out0 + (size_t)t * w.H * w.Dc + j;
+            if (w.out32) ((float*)w.out)[to] = 0.0f;
+            else ((T*)w.out)[to] = (T)0.0f;
         }
     St S;
     S.load(w.state ? w.state + (bh * w.state_nseg + (w.state_nseg > 1 ? seg : 0)) * D : nullptr, w.Da,
@@ -801,28 +832,43 @@ bool fast_out(const Sweep& w, int es) {
     return (uintptr_t)w.out % 4 == 0 && w.Dc % 4 == 0 && (long)w.H * w.Dc * (w.out32 ? 4 : es) * 64 < (1l << 29);
 }
 
-hipError_t run_state(const semicrf_attention& p, const Sweep& w, hipStream_t stream) {
+unsigned sweep_grid(const Sweep& w, int sweeps, int group) {
+    const long units = (long)w.B * (w.H / group) * w.nseg;
+    return (unsigned)((units + CHIPLETS - 1) / CHIPLETS * CHIPLETS * sweeps * group);
+}
+
+template <int N>
+hipError_t run_state(const semicrf_attention& p, const Sweeps<N>& set, hipStream_t stream) {
     return with_kernel(p, [&](auto t, auto pp, auto cc) {
         using T = decltype(t);
         constexpr int P = decltype(pp)::value, C = decltype(cc)::value, es = sizeof(T);
-        const dim3 grid(w.nseg, w.H, w.B), block(64 * sweep_waves(P));
-        if (fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es))
-            hipLaunchKernelGGL((k_attn_state<T, P, C, true>), grid, block, 0, stream, w);
+        const int group = p.Hq / p.Hk;
+        const dim3 grid(sweep_grid(set.s[0], N, group)), block(64 * sweep_waves(P));
+        bool fast = true;
+        for (const Sweep& w : set.s) fast = fast && fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es);
+        if (fast)
+            hipLaunchKernelGGL((k_attn_state<T, P, C, true, N>), grid, block, 0, stream, set, group);
         else
-            hipLaunchKernelGGL((k_attn_state<T, P, C, false>), grid, block, 0, stream, w);
+            hipLaunchKernelGGL((k_attn_state<T, P, C, false, N>), grid, block, 0, stream, set, group);
         return hipGetLastError();
     });
 }
 
-hipError_t run_sweep(const semicrf_attention& p, const Sweep& w, hipStream_t stream) {
+template <int N>
+hipError_t run_sweep(const semicrf_attention& p, const Sweeps<N>& set, hipStream_t stream) {
     return with_kernel(p, [&](auto t, auto pp, auto cc) {
         using T = decltype(t);
         constexpr int P = decltype(pp)::value, C = decltype(cc)::value, es = sizeof(T);
-        const dim3 grid(w.nseg, w.H, w.B), block(64 * sweep_waves(P));
-        if (fast_role(w.a, w.Da, es) && fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es) && fast_out(w, es))
-            hipLaunchKernelGGL((k_attn_sweep<T, P, C, true>), grid, block, 0, stream, w);
+        const int group = p.Hq / p.Hk;
+        const dim3 grid(sweep_grid(set.s[0], N, group)), block(64 * sweep_waves(P));
+        bool fast = true;
+        for (const Sweep& w : set.s)
+            fast = fast && fast_role(w.a, w.Da, es) && fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es) &&
+                   fast_out(w, es);
+        if (fast)
+            hipLaunchKernelGGL((k_attn_sweep<T, P, C, true, N>), grid, block, 0, stream, set, group);
         else
-            hipLaunchKernelGGL((k_attn_sweep<T, P, C, false>), grid, block, 0, stream, w);
+            hipLaunchKernelGGL((k_attn_sweep<T, P, C, false, N>), grid, block, 0, stream, set, group);
         return hipGetLastError();
     });
 }
@@ -860,14 +906,14 @@ hipError_t launch_decay_attention(const AttnArgs& a, void* ws, hipStream_t strea
     w.state_nseg = 1;
     if (l.nseg > 1) {
         w.local = (float*)((char*)ws + l.S);
-        TRY(run_state(p, w, stream));
+        TRY(run_state(p, Sweeps<1>{{w}}, stream));
         TRY(run_scan(p, l, w.local, p.state, a.state_out, stream));
         w.state = w.local;
         w.state_nseg = l.nseg;
     } else {
         w.state_out = a.state_out;
     }
-    return run_sweep(p, w, stream);
+    return run_sweep(p, Sweeps<1>{{w}}, stream);
 }
 
 hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t stream) {
@@ -888,10 +934,9 @@ hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t 
     r.state = a.grad_state_out;
     if (l.nseg > 1) {
         f.b = k; f.c = v; f.Da = p.Dk; f.Dc = p.Dv; f.local = S;
-        TRY(run_state(p, f, stream));
-        TRY(run_scan(p, l, S, p.state, nullptr, stream));
         r.b = q; r.c = g; r.Da = p.Dk; r.Dc = p.Dv; r.local = R;
-        TRY(run_state(p, r, stream));
+        TRY(run_state(p, Sweeps<2>{{f, r}}, stream));
+        TRY(run_scan(p, l, S, p.state, nullptr, stream));
         TRY(run_scan(p, l, R, a.grad_state_out, a.grad_state, stream));
         f.state = S;
         r.state = R;
@@ -899,18 +944,17 @@ hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t 
     // dq
     f.a = g; f.b = v; f.c = k; f.Da = p.Dv; f.Dc = p.Dk; f.transposed = 1;
     f.out = a.grad_q;
-    TRY(run_sweep(p, f, stream));
     // dv, and the gradient of the initial state
     r.a = k; r.b = q; r.c = g; r.Da = p.Dk; r.Dc = p.Dv; r.transposed = 0;
     r.out32 = group > 1;
     r.out = group > 1 ? (void*)((char*)ws + l.gv) : a.grad_v;
     r.state_out = l.nseg > 1 ? nullptr : a.grad_state;
-    TRY(run_sweep(p, r, stream));
+    const Sweep dv = r;
     // dk
     r.a = v; r.b = g; r.c = q; r.Da = p.Dv; r.Dc = p.Dk; r.transposed = 1;
     r.out = group > 1 ? (void*)((char*)ws + l.gk) : a.grad_k;
     r.state_out = nullptr;
-    TRY(run_sweep(p, r, stream));
+    TRY(run_sweep(p, Sweeps<3>{{dv, r, f}}, stream));
     if (group > 1) {
         const long rows = (long)p.B * p.T * p.Hk;
         auto sum = [&](const float* x, void* out, int D) {
