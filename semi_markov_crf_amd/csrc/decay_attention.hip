@@ -267,9 +267,9 @@ __device__ __forceinline__ const T* role_base(const Role& r, int b, int h) {
 
 // One wavefront for each 16 columns of the state.
 constexpr int sweep_waves(int P) { return P / 16; }
-// Wavefronts a SIMD of the sweep: what its registers allow without spills (LDS allows as many).
+// Wavefronts a SIMD that the sweep's registers are held to: as many as run without spills.
 template <class T, int P>
-constexpr int sweep_occupancy() { return P <= 64 && sizeof(T) == 2 ? 3 : 2; }
+constexpr int sweep_occupancy() { return P == 128 ? 2 : sizeof(T) == 2 ? 3 : 4; }
 
 // gamma^m of the state.  Near 1 it is applied as S + (gamma^m - 1) S: over thousands of chunks a
 // factor rounded once would bend every old contribution the same way.
@@ -750,14 +750,21 @@ int head_pad(const semicrf_attention& p) {
     const int d = p.Dk > p.Dv ? p.Dk : p.Dv;
     return d <= 32 ? 32 : d <= 64 ? 64 : 128;
 }
-int chunk_of(const semicrf_attention& p) { return p.dtype == SEMICRF_F32 && head_pad(p) == 128 ? 32 : 64; }
+int chunk_of(const semicrf_attention& p) { return p.dtype == SEMICRF_F32 ? 32 : 64; }
 
-// Positions per segment.  Workgroups that run at once: 2 or 3 wavefronts on each of 1,024 SIMDs.
-int segment(const semicrf_attention& p) {
-    const int C = chunk_of(p), P = head_pad(p);
-    const long slots = 1024 * (P <= 64 && p.dtype == SEMICRF_BF16 ? 3 : 2) / sweep_waves(P);
-    const long bh = (long)p.B * p.Hq;
-    long n = slots / bh;
+// Workgroups of the sweep that run at once on 256 compute units, by registers (sweep_occupancy)
+// and, for bfloat16 of width 32, by LDS (28 KB of 160).
+int sweep_slots(const semicrf_attention& p) {
+    const int P = head_pad(p);
+    const bool f32 = p.dtype == SEMICRF_F32;
+    return 256 * (P == 128 ? 1 : P == 64 ? (f32 ? 4 : 3) : (f32 ? 8 : 5));
+}
+
+// Positions per segment: as many segments as fill the device once with all sweeps of the launch,
+// none shorter than 512.
+int segment(const semicrf_attention& p, int sweeps) {
+    const int C = chunk_of(p);
+    long n = sweep_slots(p) / ((long)p.B * p.Hq * sweeps);
     const long most = p.T / 512;
     if (n > most) n = most;
     if (n < 1) n = 1;
@@ -772,7 +779,7 @@ struct AttnLayout {
 
 AttnLayout attn_layout(const semicrf_attention& p, bool grad) {
     AttnLayout l{};
-    l.seg = segment(p);
+    l.seg = segment(p, grad ? 3 : 1);
     l.nseg = (p.T + l.seg - 1) / l.seg;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -799,8 +806,8 @@ hipError_t with_kernel(const semicrf_attention& p, F&& f) {
     using I64 = std::integral_constant<int, 64>;
     using I128 = std::integral_constant<int, 128>;
     if (p.dtype == SEMICRF_F32) {
-        if (P == 32) return f(0.0f, I32(), I64());
-        if (P == 64) return f(0.0f, I64(), I64());
+        if (P == 32) return f(0.0f, I32(), I32());
+        if (P == 64) return f(0.0f, I64(), I32());
         return f(0.0f, I128(), I32());
     }
     if (P == 32) return f((bf16)0.0f, I32(), I64());
