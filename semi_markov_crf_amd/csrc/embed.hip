@@ -17,97 +17,157 @@ namespace semicrf {
 
 namespace {
 
-__device__ __forceinline__ long load_token(const EmbedArgs& a, long i) {
-    return a.token_bits == 64 ? ((const int64_t*)a.tokens)[i] : (long)((const int32_t*)a.tokens)[i];
+// Keys of U positions (b * T + t, below 2^30): the token, V where the position counts for nothing
+// (padding, past n), V + 1 for a token outside [0, V).  The loads do not wait for one another.
+template <int U>
+__device__ __forceinline__ void load_keys(const EmbedArgs& a, const unsigned (&at)[U], unsigned n,
+                                          uint32_t (&key)[U]) {
+    long tok[U];
+    int t[U], L[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        t[u] = 0;
+        L[u] = at[u] < n;
+    }
+    if (a.lengths) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned i = min(at[u], n - 1), b = i / (unsigned)a.T;
+            t[u] = (int)(i - b * (unsigned)a.T);
+            L[u] = a.lengths[b];
+        }
+    }
+    if (a.token_bits == 64) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) tok[u] = ((const int64_t*)a.tokens)[min(at[u], n - 1)];
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) tok[u] = ((const int32_t*)a.tokens)[min(at[u], n - 1)];
+    }
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool known = tok[u] >= 0 && tok[u] < a.V, in = at[u] < n;
+        if (a.lengths) bad |= in && (L[u] < 0 || L[u] > a.T);
+        const bool live = in && t[u] < L[u];
+        bad |= live && !known;
+        key[u] = !live ? (uint32_t)a.V : known ? (uint32_t)tok[u] : (uint32_t)a.V + 1;
+    }
+    if (bad && a.status) atomicOr(a.status, 1);
 }
 
-__device__ __forceinline__ bool position_valid(const EmbedArgs& a, long i) {
-    if (!a.lengths) return true;
-    const int b = (int)(i / a.T);
-    return (int)(i - (long)b * a.T) < seq_length(a.lengths, b, a.T, a.status);
-}
-
-// G lanes a row, U rows a lane group.
-template <class T, int G, int U>
+// G lanes a row, U rows a lane group, a group's rows 256 / G apart.
+template <class T, int G, int U, bool STREAM>
 __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
     constexpr int V = Piece<T>::V, RPB = 256 / G;
     const int N = a.N, lane = threadIdx.x % G;
-    const long n = (long)a.B * a.T;
-    const long i0 = ((long)blockIdx.x * RPB + threadIdx.x / G) * U;
-    const T* src[U];
-    float mul[U];
-    bool live[U];
+    const unsigned n = (unsigned)a.B * a.T;
+    const unsigned i0 = blockIdx.x * RPB * U + threadIdx.x / G;
+    unsigned at[U];
+    uint32_t key[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const long i = i0 + u;
-        live[u] = false;
-        mul[u] = 0.0f;
-        src[u] = (const T*)a.table;
-        if (i < n && position_valid(a, i)) {
-            const long tok = load_token(a, i);
-            if (tok >= 0 && tok < a.V) {
-                live[u] = true;
-                src[u] += tok * N;
-            } else {
-                mul[u] = __builtin_nanf("");
-                if (a.status && lane == 0) atomicOr(a.status, 1);
-            }
-        }
-    }
+    for (int u = 0; u < U; ++u) at[u] = i0 + u * RPB;
+    load_keys<U>(a, at, n, key);
     for (int c = lane * V; c < N; c += G * V) {
-        float x[U][V];
-#pragma unroll
-        for (int u = 0; u < U; ++u) load_piece<T>(src[u] + c, live[u] ? N - c : 0, x[u]);
+        raw_piece x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i0 + u >= n) break;
+            const bool known = key[u] < (uint32_t)a.V;
+            x[u] = load_raw<T>((const T*)a.table + (size_t)(known ? key[u] : 0) * N + c, known ? N - c : 0);
+        }
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[u][j] = live[u] ? x[u][j] * a.scale : mul[u];
-            store_piece<T>((T*)a.out + (i0 + u) * N + c, N - c, x[u]);
+        for (int u = 0; u < U; ++u) {
+            if (at[u] >= n) break;
+            const float fill = key[u] > (uint32_t)a.V ? __builtin_nanf("") : 0.0f;
+            float y[V];
+            unpack<T>(x[u], y);
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[j] = key[u] < (uint32_t)a.V ? y[j] * a.scale : fill;
+            store_piece<T, STREAM>((T*)a.out + (size_t)at[u] * N + c, N - c, y);
         }
     }
 }
 
 // ------------------------------------------------------------------ sort by token
 // Least-significant-digit radix sort of (key, position), 8 bits a pass, stable.  The key of a
-// position that counts for nothing (padding, a token outside [0, V)) is V: it sorts last.
-constexpr int BINS = 256, TILE = 4096, SORT_NT = 256, PER = TILE / SORT_NT;
+// position that counts for nothing is V here, for unknown tokens too: it sorts last.
+//
+// counts says how many items of each tile have each digit of the pass; the first pass counts in
+// k_grad_begin.
+// Up to 64 tiles every scatter workgroup adds the counts up by itself and they lie tile by tile;
+// beyond, k_sort_scan does it once, digit by digit.
+constexpr int BINS = 256, SCAN_TILES = 64, TILE = 1024, SORT_NT = 256, PER = TILE / SORT_NT;
 
-__device__ __forceinline__ uint32_t first_key(const EmbedArgs& a, long i) {
-    if (!position_valid(a, i)) return (uint32_t)a.V;
-    const long tok = load_token(a, i);
-    if (tok >= 0 && tok < a.V) return (uint32_t)tok;
-    if (a.status) atomicOr(a.status, 1);
-    return (uint32_t)a.V;
+struct SortArgs {
+    const uint32_t* keys;    // NULL: the tokens themselves, positions in order
+    const int* pos;          // with keys
+    int n, shift, ntiles;
+    int by_digit, by_tile;   // strides of the counts
+    int* counts;             // counts, or exclusive over the tiles once scanned
+    const int* totals;       // NULL: counts are not scanned yet
+    uint32_t* keys_out;
+    int* pos_out;
+};
+
+// One tile's count of a digit.  Each wavefront counts for itself: few distinct tokens make the
+// atomics of a counter wait for each other.
+__device__ __forceinline__ void count_tile(const uint32_t (&key)[PER], const unsigned (&from)[PER], int n,
+                                           int shift, int* counts) {
+    __shared__ int h[4][BINS];
+    const int w = threadIdx.x >> 6;
+    for (int i = 0; i < 4; ++i) h[i][threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        if (from[p] < (unsigned)n) atomicAdd(&h[w][(key[p] >> shift) & (BINS - 1)], 1);
+    __syncthreads();
+    *counts = h[0][threadIdx.x] + h[1][threadIdx.x] + h[2][threadIdx.x] + h[3][threadIdx.x];
 }
 
-// counts [BINS][nblk] of this pass's digit
-__global__ __launch_bounds__(SORT_NT) void k_sort_count(const EmbedArgs a, const uint32_t* keys,
-                                                        int n, int shift, int nblk, int* counts) {
-    __shared__ int h[BINS];
-    h[threadIdx.x] = 0;
-    __syncthreads();
-    const int base = blockIdx.x * TILE;
+// grid ntiles
+__global__ __launch_bounds__(256) void k_sort_count(const SortArgs s) {
+    uint32_t key[PER];
+    unsigned from[PER];
+#pragma unroll
     for (int p = 0; p < PER; ++p) {
-        const int i = base + p * SORT_NT + threadIdx.x;
-        if (i < n) {
-            const uint32_t key = keys ? keys[i] : first_key(a, i);
-            atomicAdd(&h[(key >> shift) & (BINS - 1)], 1);
-        }
+        from[p] = blockIdx.x * TILE + p * SORT_NT + threadIdx.x;
+        key[p] = s.keys[min(from[p], (unsigned)s.n - 1)];
     }
-    __syncthreads();
-    counts[(size_t)threadIdx.x * nblk + blockIdx.x] = h[threadIdx.x];
+    count_tile(key, from, s.n, s.shift, s.counts + (size_t)threadIdx.x * s.by_digit + (size_t)blockIdx.x * s.by_tile);
 }
 
-// exclusive scan of one bin's counts over the blocks; totals [BINS].  grid BINS, block 256
-__global__ __launch_bounds__(256) void k_sort_scan(int* counts, int nblk, int* totals) {
+// Workgroups 0 .. ntiles - 1 count the first digit of a tile; the others clear the gradient (rows
+// of tokens that do not appear stay 0).
+__global__ __launch_bounds__(256) void k_grad_begin(const EmbedArgs a, int n, int ntiles, int by_digit,
+                                                    int by_tile, int* counts, size_t bytes) {
+    if (blockIdx.x >= (unsigned)ntiles) {
+        char* out = (char*)a.out;
+        const size_t pieces = bytes / 16, step = (size_t)(gridDim.x - ntiles) * 256;
+        const raw_piece zero = {0, 0, 0, 0};
+        const size_t first = (size_t)(blockIdx.x - ntiles) * 256 + threadIdx.x;
+        for (size_t i = first; i < pieces; i += step) __builtin_memcpy(out + i * 16, &zero, 16);
+        if (first < bytes - pieces * 16) out[pieces * 16 + first] = 0;
+        return;
+    }
+    uint32_t key[PER];
+    unsigned from[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) from[p] = blockIdx.x * TILE + p * SORT_NT + threadIdx.x;
+    load_keys<PER>(a, from, n, key);
+#pragma unroll
+    for (int p = 0; p < PER; ++p) key[p] = min(key[p], (uint32_t)a.V);
+    count_tile(key, from, n, 0, counts + (size_t)threadIdx.x * by_digit + (size_t)blockIdx.x * by_tile);
+}
+
+// exclusive scan of one digit's counts over the tiles; totals [BINS].  grid BINS, block 256
+__global__ __launch_bounds__(256) void k_sort_scan(int* counts, int ntiles, int* totals) {
     __shared__ int wsum[4];
-    int* c = counts + (size_t)blockIdx.x * nblk;
+    int* c = counts + (size_t)blockIdx.x * ntiles;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     int carry = 0;
-    for (int j0 = 0; j0 < nblk; j0 += 256) {
+    for (int j0 = 0; j0 < ntiles; j0 += 256) {
         const int j = j0 + threadIdx.x;
-        const int v = j < nblk ? c[j] : 0;
+        const int v = j < ntiles ? c[j] : 0;
         int s = v;
         for (int off = 1; off < 64; off <<= 1) {
             const int t = __shfl_up(s, off, 64);
@@ -117,7 +177,7 @@ __global__ __launch_bounds__(256) void k_sort_scan(int* counts, int nblk, int* t
         __syncthreads();
         int before = carry;
         for (int i = 0; i < w; ++i) before += wsum[i];
-        if (j < nblk) c[j] = before + s - v;
+        if (j < ntiles) c[j] = before + s - v;
         for (int i = 0; i < 4; ++i) carry += wsum[i];
         __syncthreads();
     }
@@ -127,24 +187,52 @@ __global__ __launch_bounds__(256) void k_sort_scan(int* counts, int nblk, int* t
 // Stable scatter of one tile.  A wavefront takes PER * 64 consecutive items, 64 at a time: the
 // lanes with the same digit find each other with one ballot a bit, the lowest of them takes
 // their places from the wavefront's running count.
-__global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, const uint32_t* keys,
-                                                          const int* pos, int n, int shift, int nblk,
-                                                          const int* counts, const int* totals,
-                                                          uint32_t* keys_out, int* pos_out) {
+__global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, const SortArgs s) {
     __shared__ int run[SORT_NT / 64][BINS];
     __shared__ int wsum[4];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = s.n;
     for (int i = 0; i < SORT_NT / 64; ++i) run[i][tid] = 0;
     __syncthreads();
     const int base = blockIdx.x * TILE + w * PER * 64;
     uint32_t key[PER];
+    unsigned from[PER];
     int rank[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) from[p] = base + p * 64 + lane;
+    if (s.keys) {
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const unsigned i = min(from[p], (unsigned)n - 1);
+            key[p] = s.keys[i];
+            from[p] = s.pos[i];
+        }
+    } else {
+        load_keys<PER>(a, from, n, key);
+#pragma unroll
+        for (int p = 0; p < PER; ++p) key[p] = min(key[p], (uint32_t)a.V);
+    }
+    // this tile's share of its digit: items of the digit in earlier tiles
+    int before_tile = 0, total = 0;
+    if (s.totals) {
+        before_tile = s.counts[(size_t)tid * s.by_digit + blockIdx.x];
+        total = s.totals[tid];
+    } else {
+        constexpr int U = 16;                  // loads in flight
+        for (int j0 = 0; j0 < s.ntiles; j0 += U) {
+            int v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = s.counts[min(j0 + u, s.ntiles - 1) * BINS + tid];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                before_tile += j0 + u < (int)blockIdx.x ? v[u] : 0;
+                total += j0 + u < s.ntiles ? v[u] : 0;
+            }
+        }
+    }
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         const int i = base + p * 64 + lane;
-        key[p] = 0;
-        if (i < n) key[p] = keys ? keys[i] : first_key(a, i);
-        const uint32_t d = (key[p] >> shift) & (BINS - 1);
+        const uint32_t d = (key[p] >> s.shift) & (BINS - 1);
         uint64_t same = __ballot(i < n);
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
@@ -160,155 +248,178 @@ __global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, con
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         rank[p] = start + before;
     }
+    // digit start = items of smaller digits + this digit's items in earlier tiles, wavefronts
+    int sum = total;
+    for (int off = 1; off < 64; off <<= 1) {
+        const int t = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += t;
+    }
+    if (lane == 63) wsum[w] = sum;
     __syncthreads();
-    // digit start = items of smaller digits + this digit's items in earlier tiles, waves
-    {
-        const int v = totals[tid];
-        int s = v;
-        for (int off = 1; off < 64; off <<= 1) {
-            const int t = __shfl_up(s, off, 64);
-            if (lane >= off) s += t;
-        }
-        if (lane == 63) wsum[w] = s;
-        __syncthreads();
-        int at = s - v + counts[(size_t)tid * nblk + blockIdx.x];
-        for (int i = 0; i < w; ++i) at += wsum[i];
-        for (int i = 0; i < SORT_NT / 64; ++i) {
-            const int c = run[i][tid];
-            run[i][tid] = at;
-            at += c;
-        }
+    int at = sum - total + before_tile;
+    for (int i = 0; i < w; ++i) at += wsum[i];
+    for (int i = 0; i < SORT_NT / 64; ++i) {
+        const int v = run[i][tid];
+        run[i][tid] = at;
+        at += v;
     }
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         const int i = base + p * 64 + lane;
         if (i < n) {
-            const int to = run[w][(key[p] >> shift) & (BINS - 1)] + rank[p];
-            keys_out[to] = key[p];
-            pos_out[to] = pos ? pos[i] : i;
+            const int to = run[w][(key[p] >> s.shift) & (BINS - 1)] + rank[p];
+            s.keys_out[to] = key[p];
+            s.pos_out[to] = from[p];
         }
     }
 }
 
 // ------------------------------------------------------------------ sums over runs
-__global__ __launch_bounds__(256) void k_grad_fill(char* out, size_t pieces, int ntail) {
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    const uint4 zero{0, 0, 0, 0};
-    if (i < pieces) __builtin_memcpy(out + i * 16, &zero, 16);
-    if (blockIdx.x == 0 && (int)threadIdx.x < ntail) out[pieces * 16 + threadIdx.x] = 0;
-}
-
-// One wavefront adds the rows of one chunk over 64 pieces of columns.
-// Partial rows: part[chunk][0] = the run that comes from the chunk before, part[chunk][1] =
-// the run that starts here and goes on.  grid (ceil(nchunks / 4), column slabs), block 256
+// One wavefront adds the rows of one chunk (R <= 64) over 64 pieces of columns, U rows on their way
+// at a time.  Partial rows: part[chunk][0] = the run that comes from the chunk before,
+// part[chunk][1] = the run that starts here and goes on.
+// grid (ceil(nchunks / 4), column slabs), block 256
 template <class T>
 __global__ __launch_bounds__(256) void k_grad_chunks(const EmbedArgs a, const uint32_t* keys,
                                                      const int* pos, int n, int R, int nchunks,
                                                      float* part) {
-    constexpr int V = Piece<T>::V;
+    constexpr int V = Piece<T>::V, U = 8;
     const int N = a.N, lane = threadIdx.x & 63;
     const int chunk = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
     if (chunk >= nchunks) return;
     const int c = (blockIdx.y * 64 + lane) * V;
-    const int r0 = chunk * R, r1 = min(n, r0 + R);
-    const T* g = (const T*)a.grad_out;
+    const int r0 = chunk * R, m = min(n - r0, R);
+    const T* g = (const T*)a.grad_out + c;
+    // every lane keeps one row's key and position; row r is read from lane r
+    const uint32_t my_key = lane < m ? keys[r0 + lane] : (uint32_t)a.V;
+    const int my_pos = lane < m ? pos[r0 + lane] : 0;
+    const uint32_t key_before = r0 > 0 ? keys[r0 - 1] : ~0u, key_after = r0 + m < n ? keys[r0 + m] : ~0u;
+    auto key_of = [&](int r) { return (uint32_t)__builtin_amdgcn_readlane((int)my_key, r); };
+    auto row_of = [&](int r) {
+        return load_raw<T>(g + (size_t)(unsigned)__builtin_amdgcn_readlane(my_pos, r) * N, N - c);
+    };
+    // the positions that count for nothing come last
+    const int live = __popcll(__ballot(my_key < (uint32_t)a.V));
+    if (live == 0) return;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    bool from_before = r0 > 0 && keys[r0 - 1] == keys[r0];
-    uint32_t cur = keys[r0];
-    for (int r = r0; r < r1; ++r) {
-        const uint32_t key = keys[r];
-        if (key != cur) {
-            if (from_before) {
-                float* p = part + (size_t)chunk * 2 * N + c;
+    uint32_t cur = key_of(0);
+    bool from_before = key_before == cur;
+    auto flush = [&](bool goes_on) {
+        if (from_before || goes_on) {
+            float* p = part + ((size_t)chunk * 2 + (from_before ? 0 : 1)) * N + c;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i < N) p[i] = acc[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] *= a.scale;
-                store_piece<T>((T*)a.out + (size_t)cur * N + c, N - c, acc);
+            for (int i = 0; i < V; i += 4) {
+                const float x[4] = {acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+                store_piece<float>(p + i, N - c - i, x);
             }
+        } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-            from_before = false;
-            cur = key;
+            for (int i = 0; i < V; ++i) acc[i] *= a.scale;
+            store_piece<T>((T*)a.out + (size_t)cur * N + c, N - c, acc);
         }
-        if (key >= (uint32_t)a.V) return;      // the positions that count for nothing
-        float x[V];
-        load_piece<T>(g + (size_t)pos[r] * N + c, N - c, x);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += x[i];
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+        from_before = false;
+    };
+    raw_piece x[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (u < live) x[u] = row_of(u);
+    for (int r = 0; r < live; r += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + U + u < live) y[u] = row_of(r + U + u);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r + u < live) {
+                const uint32_t key = key_of(r + u);
+                if (key != cur) {
+                    flush(false);
+                    cur = key;
+                }
+                float f[V];
+                unpack<T>(x[u], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += f[i];
+            }
+            x[u] = y[u];
+        }
     }
-    const bool goes_on = r1 < n && keys[r1] == cur;
-    if (from_before || goes_on) {
-        float* p = part + ((size_t)chunk * 2 + (from_before ? 0 : 1)) * N + c;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (c + i < N) p[i] = acc[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] *= a.scale;
-        store_piece<T>((T*)a.out + (size_t)cur * N + c, N - c, acc);
-    }
+    flush(live == m && key_after == cur);
 }
 
-// The run that starts in this chunk and goes on: its partial rows, in order.  The 16 wavefronts
-// take consecutive shares of them.  grid (nchunks, ceil(N / 64)), block 1024
-template <class T>
-__global__ __launch_bounds__(1024) void k_grad_join(const EmbedArgs a, const uint32_t* keys, int n,
-                                                    int R, int nchunks, const float* part) {
-    __shared__ float s[16][64];
+// The run that starts in this chunk and goes on: its partial rows, in order.  CL lanes take four
+// columns each, the workgroup's 512 / CL groups consecutive shares of the partial rows.
+// grid (nchunks, ceil(N / (4 CL))), block 512
+template <class T, int CL>
+__global__ __launch_bounds__(512) void k_grad_join(const EmbedArgs a, const uint32_t* keys, int n,
+                                                   int R, int nchunks, const float* part) {
+    constexpr int GR = 512 / CL, U = 8;
+    __shared__ float s[GR][CL][4];
     const int chunk = blockIdx.x, N = a.N;
-    const int r1 = (chunk + 1) * R;
+    const int r0 = chunk * R, r1 = r0 + R;
     if (r1 >= n) return;
-    const uint32_t key = keys[r1];
-    if (keys[r1 - 1] != key || key >= (uint32_t)a.V) return;
-    // started before this chunk: its first chunk joins it
-    const int r0 = chunk * R;
-    if (r0 > 0 && keys[r0 - 1] == key) return;
-    // last row of the run: the first row past it, by halving
-    int lo = r1, hi = n;
+    const uint32_t key = keys[r1], last_key = keys[r1 - 1], before = r0 > 0 ? keys[r0 - 1] : ~0u;
+    // only a run that starts here and goes on: an earlier start is joined by its first chunk
+    if (last_key != key || key >= (uint32_t)a.V || before == key) return;
+    // the first row past the run: chunk ends first, then inside one
+    int lo = chunk + 1, hi = nchunks;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (keys[mid] == key) lo = mid + 1; else hi = mid;
+        const int e = min(n, (mid + 1) * R) - 1;
+        if (keys[e] == key) lo = mid + 1; else hi = mid;
     }
-    const int last = (lo - 1) / R;             // chunk that holds the run's last row
+    // chunk lo (if any) ends with another key: the run reaches into it if its first row has the key
+    const int last = lo < nchunks && keys[lo * R] == key ? lo : lo - 1;
     const int m = last - chunk;                // partial rows after the first
-    const int w = threadIdx.x >> 6, c = blockIdx.y * 64 + (threadIdx.x & 63);
-    const int per = (m + 15) / 16;
-    float v = 0.0f;
+    const int lane = threadIdx.x % CL, grp = threadIdx.x / CL, c = (blockIdx.y * CL + lane) * 4;
+    const int per = (m + GR - 1) / GR;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < N) {
-        if (w == 0) v = part[((size_t)chunk * 2 + 1) * N + c];
-        const int q1 = min(m, (w + 1) * per);
-        for (int q = w * per; q < q1; ++q) v += part[(size_t)(chunk + 1 + q) * 2 * N + c];
+        if (grp == 0) load_piece<float>(part + ((size_t)chunk * 2 + 1) * N + c, N - c, v);
+        const int q1 = min(m, (grp + 1) * per);
+        const float* p = part + (size_t)(chunk + 1) * 2 * N + c;
+        for (int q = grp * per; q < q1; q += U) {
+            float x[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) load_piece<float>(p + (size_t)(q + u) * 2 * N, q + u < q1 ? N - c : 0, x[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += x[u][i];
+        }
     }
-    s[w][threadIdx.x & 63] = v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[grp][lane][i] = v[i];
     __syncthreads();
-    if (w == 0 && c < N) {
-        for (int i = 1; i < 16; ++i) v += s[i][threadIdx.x];
-        ((T*)a.out)[(size_t)key * N + c] = (T)(v * a.scale);
+    if (grp == 0 && c < N) {
+        for (int q = 1; q < GR; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += s[q][lane][i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < N) ((T*)a.out)[(size_t)key * N + c + i] = (T)(v[i] * a.scale);
     }
 }
 
 struct GradLayout {
-    int n, nblk, passes, R, nchunks;
+    int n, ntiles, passes, R, nchunks;
     size_t key[2], pos[2], counts, totals, part, total;
 };
 
-GradLayout grad_layout(int B, int T, int V, int N, int dtype) {
-    (void)dtype;
+GradLayout grad_layout(int B, int T, int V, int N) {
     GradLayout l{};
     l.n = B * T;
-    l.nblk = (l.n + TILE - 1) / TILE;
+    l.ntiles = (l.n + TILE - 1) / TILE;
     int bits = 1;
     while (((long)V >> bits) != 0) ++bits;
     l.passes = (bits + 7) / 8;
     // rows per chunk: enough chunks to fill the device, few enough partial rows
     l.R = 16;
-    while (l.R < 128 && l.n / l.R > 4096) l.R *= 2;
+    while (l.R < 64 && l.n / l.R > 4096) l.R *= 2;
     l.nchunks = (l.n + l.R - 1) / l.R;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -320,7 +431,7 @@ GradLayout grad_layout(int B, int T, int V, int N, int dtype) {
         l.key[i] = take((size_t)l.n * 4);
         l.pos[i] = take((size_t)l.n * 4);
     }
-    l.counts = take((size_t)BINS * l.nblk * 4);
+    l.counts = take((size_t)BINS * l.ntiles * 4);
     l.totals = take(BINS * 4);
     l.part = take((size_t)l.nchunks * 2 * N * 4);
     l.total = off;
@@ -332,11 +443,17 @@ hipError_t run_embed(const EmbedArgs& a, hipStream_t stream) {
     constexpr int V = Piece<T>::V;
     const long n = (long)a.B * a.T;
     const int np = (a.N + V - 1) / V;
+    // Outputs past the memory-side cache (256 MB) are written as a stream: what reads them finds
+    // nothing of them in a cache either way, and the table stays there.  Measured in bfloat16, the
+    // lookup alone and followed by two layer norms: 410 MB 67 against 107 us, 403 against 432; 52 MB
+    // 14 against 15, but 59 against 53, so smaller outputs are written as usual.
+    const bool stream_out = (size_t)n * a.N * sizeof(T) > (size_t)256 << 20;
     auto go = [&](auto g) {
-        constexpr int G = decltype(g)::value, U = 4;
+        constexpr int G = decltype(g)::value, U = 2;
         const long per = (256 / G) * U;
-        hipLaunchKernelGGL((k_embed<T, G, U>), dim3((unsigned)((n + per - 1) / per)), dim3(256), 0,
-                           stream, a);
+        const dim3 grid((unsigned)((n + per - 1) / per)), block(256);
+        if (stream_out) hipLaunchKernelGGL((k_embed<T, G, U, true>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((k_embed<T, G, U, false>), grid, block, 0, stream, a);
         return hipGetLastError();
     };
     if (np <= 4) return go(std::integral_constant<int, 4>());
@@ -347,31 +464,49 @@ hipError_t run_embed(const EmbedArgs& a, hipStream_t stream) {
 template <class T>
 hipError_t run_embed_grad(const EmbedArgs& a, char* ws, hipStream_t stream) {
     constexpr int V = Piece<T>::V;
-    const GradLayout l = grad_layout(a.B, a.T, a.V, a.N, a.dtype);
-    const size_t bytes = (size_t)a.V * a.N * sizeof(T);
-    const size_t pieces = bytes / 16;
-    hipLaunchKernelGGL(k_grad_fill, dim3((unsigned)((pieces + 255) / 256 + 1)), dim3(256), 0, stream,
-                       (char*)a.out, pieces, (int)(bytes - pieces * 16));
-    const uint32_t* keys = nullptr;
-    const int* pos = nullptr;
+    const GradLayout l = grad_layout(a.B, a.T, a.V, a.N);
+    const size_t bytes = (size_t)a.V * a.N * sizeof(T), pieces = bytes / 16;
+    const size_t fill = pieces / 1024 + 1;     // four pieces a thread, up to 4,096 workgroups
     int* counts = (int*)(ws + l.counts);
-    int* totals = (int*)(ws + l.totals);
+    const bool scan = l.ntiles > SCAN_TILES;
+    const int by_digit = scan ? l.ntiles : 1, by_tile = scan ? 1 : BINS;
+    hipLaunchKernelGGL(k_grad_begin, dim3(l.ntiles + (unsigned)(fill < 4096 ? fill : 4096)), dim3(256), 0,
+                       stream, a, l.n, l.ntiles, by_digit, by_tile, counts, bytes);
+    SortArgs s{};
+    s.n = l.n;
+    s.ntiles = l.ntiles;
+    s.by_digit = by_digit;
+    s.by_tile = by_tile;
+    s.counts = counts;
     for (int p = 0; p < l.passes; ++p) {
-        uint32_t* ko = (uint32_t*)(ws + l.key[p & 1]);
-        int* po = (int*)(ws + l.pos[p & 1]);
-        hipLaunchKernelGGL(k_sort_count, dim3(l.nblk), dim3(SORT_NT), 0, stream, a, keys, l.n, 8 * p,
-                           l.nblk, counts);
-        hipLaunchKernelGGL(k_sort_scan, dim3(BINS), dim3(256), 0, stream, counts, l.nblk, totals);
-        hipLaunchKernelGGL(k_sort_scatter, dim3(l.nblk), dim3(SORT_NT), 0, stream, a, keys, pos, l.n,
-                           8 * p, l.nblk, counts, totals, ko, po);
-        keys = ko;
-        pos = po;
+        s.shift = 8 * p;
+        if (p > 0) hipLaunchKernelGGL(k_sort_count, dim3(l.ntiles), dim3(256), 0, stream, s);
+        s.totals = nullptr;
+        if (scan) {
+            s.totals = (const int*)(ws + l.totals);
+            hipLaunchKernelGGL(k_sort_scan, dim3(BINS), dim3(256), 0, stream, s.counts, l.ntiles,
+                               (int*)(ws + l.totals));
+        }
+        s.keys_out = (uint32_t*)(ws + l.key[p & 1]);
+        s.pos_out = (int*)(ws + l.pos[p & 1]);
+        hipLaunchKernelGGL(k_sort_scatter, dim3(l.ntiles), dim3(SORT_NT), 0, stream, a, s);
+        s.keys = s.keys_out;
+        s.pos = s.pos_out;
     }
     float* part = (float*)(ws + l.part);
     hipLaunchKernelGGL((k_grad_chunks<T>), dim3((l.nchunks + 3) / 4, (a.N + 64 * V - 1) / (64 * V)),
-                       dim3(256), 0, stream, a, keys, pos, l.n, l.R, l.nchunks, part);
-    hipLaunchKernelGGL((k_grad_join<T>), dim3(l.nchunks, (a.N + 63) / 64), dim3(1024), 0, stream, a,
-                       keys, l.n, l.R, l.nchunks, part);
+                       dim3(256), 0, stream, a, s.keys, s.pos, l.n, l.R, l.nchunks, part);
+    if (l.nchunks > 1) {
+        auto join = [&](auto cl) {
+            constexpr int CL = decltype(cl)::value;
+            hipLaunchKernelGGL((k_grad_join<T, CL>), dim3(l.nchunks, (a.N + 4 * CL - 1) / (4 * CL)), dim3(512),
+                               0, stream, a, s.keys, l.n, l.R, l.nchunks, part);
+        };
+        // narrow rows leave more groups for the partial rows
+        if (a.N <= 64) join(std::integral_constant<int, 16>());
+        else if (a.N <= 256) join(std::integral_constant<int, 64>());
+        else join(std::integral_constant<int, 256>());
+    }
     return hipGetLastError();
 }
 
@@ -381,8 +516,8 @@ hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream) {
     return a.dtype == SEMICRF_F32 ? run_embed<float>(a, stream) : run_embed<bf16>(a, stream);
 }
 
-size_t embed_grad_bytes(int B, int T, int V, int N, int dtype) {
-    return grad_layout(B, T, V, N, dtype).total;
+size_t embed_grad_bytes(int B, int T, int V, int N) {
+    return grad_layout(B, T, V, N).total;
 }
 
 hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream) {

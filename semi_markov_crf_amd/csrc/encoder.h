@@ -35,7 +35,11 @@ __device__ __forceinline__ void load_piece(const T* __restrict__ p, int valid,
     }
 }
 
-template <class T>
+typedef uint32_t raw_piece __attribute__((ext_vector_type(4)));
+typedef raw_piece loose_piece __attribute__((aligned(1)));
+
+// STREAM: the store does not keep its line in the caches.
+template <class T, bool STREAM = false>
 __device__ __forceinline__ void store_piece(T* __restrict__ p, int valid,
                                             const float (&x)[Piece<T>::V]) {
     constexpr int V = Piece<T>::V;
@@ -43,12 +47,38 @@ __device__ __forceinline__ void store_piece(T* __restrict__ p, int valid,
         T t[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) t[i] = (T)x[i];
-        __builtin_memcpy(p, t, 16);
+        raw_piece r;
+        __builtin_memcpy(&r, t, 16);
+        if constexpr (STREAM) __builtin_nontemporal_store(r, (loose_piece*)p);
+        else *(loose_piece*)p = r;
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (i < valid) p[i] = (T)x[i];
     }
+}
+
+// A piece as it lies in memory; what is past `valid` elements is zero.
+template <class T>
+__device__ __forceinline__ raw_piece load_raw(const T* __restrict__ p, int valid) {
+    constexpr int V = Piece<T>::V;
+    raw_piece x = {0, 0, 0, 0};
+    if (valid >= V) {
+        __builtin_memcpy(&x, p, 16);
+    } else if (valid > 0) {
+        T t[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = i < valid ? p[i] : (T)0.0f;
+        __builtin_memcpy(&x, t, 16);
+    }
+    return x;
+}
+template <class T>
+__device__ __forceinline__ void unpack(const raw_piece& r, float (&x)[Piece<T>::V]) {
+    T t[Piece<T>::V];
+    __builtin_memcpy(t, &r, 16);
+#pragma unroll
+    for (int i = 0; i < Piece<T>::V; ++i) x[i] = (float)t[i];
 }
 
 // Length of sequence b, clamped to [0, T]; a length outside raises the caller's status word.
@@ -74,7 +104,7 @@ struct EmbedArgs {
     int32_t* status;
 };
 hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream);
-size_t embed_grad_bytes(int B, int T, int V, int N, int dtype);
+size_t embed_grad_bytes(int B, int T, int V, int N);
 hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream);
 
 struct NormArgs {

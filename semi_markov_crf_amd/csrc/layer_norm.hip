@@ -39,70 +39,100 @@ __device__ __forceinline__ float row_sum(float v, float* red, int& slot) {
     }
 }
 
-// Row -> (b, t < length).  Rows are numbered b * T + t.
-__device__ __forceinline__ bool row_valid(const NormArgs& a, long row) {
+// Row -> t < length of its sequence.  Rows are numbered b * T + t, below 2^30.
+__device__ __forceinline__ bool row_valid(const NormArgs& a, unsigned row) {
     if (!a.lengths) return true;
-    const int b = (int)(row / a.T);
-    return (int)(row - (long)b * a.T) < seq_length(a.lengths, b, a.T, a.status);
+    const unsigned b = row / (unsigned)a.T;
+    return (int)(row - b * (unsigned)a.T) < seq_length(a.lengths, b, a.T, a.status);
 }
 
+// V weights from column c in the element type W of theirs
 template <class W, int V>
 __device__ __forceinline__ void load_weights(const void* p, int c, int N, float dflt,
                                              float (&w)[V]) {
+    if (!p) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        w[i] = (p && c + i < N) ? (float)((const W*)p)[c + i] : (c + i < N ? dflt : 0.0f);
+        for (int i = 0; i < V; ++i) w[i] = dflt;
+        return;
+    }
+    constexpr int VW = Piece<W>::V;
+#pragma unroll
+    for (int i = 0; i < V; i += VW) {
+        float x[VW];
+        load_piece<W>((const W*)p + c + i, N - c - i, x);
+#pragma unroll
+        for (int j = 0; j < VW && i + j < V; ++j) w[i + j] = x[j];
+    }
 }
 
+// One pass over the rows of a workgroup: the next row is on its way while this one is summed, and
+// the weights stay in registers.
 template <class T, class W, int G, int KP, int NT>
 __global__ __launch_bounds__(NT) void k_layer_norm(const NormArgs a) {
     constexpr int V = Piece<T>::V, RPB = NT / G;
     __shared__ float red[2 * (G > 64 ? G / 64 : 1)];
     int slot = 0;
     const int N = a.N, lane = threadIdx.x % G;
-    const long rows = (long)a.B * a.T;
-    const long row = (long)blockIdx.x * RPB + threadIdx.x / G;
-    const bool in = row < rows;
-    const bool ok = in && row_valid(a, row);
-    const T* x = (const T*)a.x + (in ? row : 0) * N;
-    float v[KP][V];
-    float s = 0.0f;
+    const unsigned rows = (unsigned)a.B * a.T, step = gridDim.x * RPB;
+    unsigned row = blockIdx.x * RPB + threadIdx.x / G;
+    raw_piece x[KP];
+    bool ok = row < rows && row_valid(a, row);
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
         const int c = (k * G + lane) * V;
-        load_piece<T>(x + c, ok ? N - c : 0, v[k]);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s += v[k][i];
+        x[k] = load_raw<T>((const T*)a.x + (size_t)(ok ? row : 0) * N + c, ok ? N - c : 0);
     }
-    const float mean = row_sum<G>(s, red, slot) / (float)N;
-    s = 0.0f;
+    float w[KP][V], b[KP][V];
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
-        const int c = (k * G + lane) * V;
+        load_weights<W, V>(a.weight, (k * G + lane) * V, N, 1.0f, w[k]);
+        load_weights<W, V>(a.bias, (k * G + lane) * V, N, 0.0f, b[k]);
+    }
+    for (unsigned r0 = blockIdx.x * RPB; r0 < rows; r0 += step, row += step) {
+        float v[KP][V];
+        float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[k][i] -= mean;
-            s += c + i < N ? v[k][i] * v[k][i] : 0.0f;
+        for (int k = 0; k < KP; ++k) {
+            unpack<T>(x[k], v[k]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s += v[k][i];
         }
-    }
-    const float var = row_sum<G>(s, red, slot) / (float)N;
-    const float r = 1.0f / sqrtf(var + a.eps);
-    if (!in) return;
-    if (lane == 0) {
-        if (a.mean) a.mean[row] = ok ? mean : 0.0f;
-        if (a.rstd) a.rstd[row] = ok ? r : 0.0f;
-    }
-    T* y = (T*)a.y + row * N;
+        const bool now = ok, in = row < rows;
+        if (r0 + step < rows) {
+            ok = row + step < rows && row_valid(a, row + step);
 #pragma unroll
-    for (int k = 0; k < KP; ++k) {
-        const int c = (k * G + lane) * V;
-        if (c >= N) break;
-        float w[V], b[V];
-        load_weights<W, V>(a.weight, c, N, 1.0f, w);
-        load_weights<W, V>(a.bias, c, N, 0.0f, b);
+            for (int k = 0; k < KP; ++k) {
+                const int c = (k * G + lane) * V;
+                x[k] = load_raw<T>((const T*)a.x + (size_t)(ok ? row + step : 0) * N + c, ok ? N - c : 0);
+            }
+        }
+        const float mean = row_sum<G>(s, red, slot) / (float)N;
+        s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] = ok ? fmaf(v[k][i] * r, w[i], b[i]) : 0.0f;
-        store_piece<T>(y + c, N - c, v[k]);
+        for (int k = 0; k < KP; ++k) {
+            const int c = (k * G + lane) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[k][i] -= mean;
+                s += c + i < N ? v[k][i] * v[k][i] : 0.0f;
+            }
+        }
+        const float var = row_sum<G>(s, red, slot) / (float)N;
+        const float r = 1.0f / sqrtf(var + a.eps);
+        if (!in) continue;
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = now ? mean : 0.0f;
+            if (a.rstd) a.rstd[row] = now ? r : 0.0f;
+        }
+        T* y = (T*)a.y + (size_t)row * N;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            const int c = (k * G + lane) * V;
+            if (c >= N) break;
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = now ? fmaf(v[k][i] * r, w[k][i], b[k][i]) : 0.0f;
+            store_piece<T>(y + c, N - c, v[k]);
+        }
     }
 }
 
@@ -113,7 +143,7 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
     __shared__ float join[RPB > 1 ? (RPB - 1) * G * V * 2 : 1];
     int slot = 0;
     const int N = a.N, lane = threadIdx.x % G, sub = threadIdx.x / G;
-    const long rows = (long)a.B * a.T;
+    const unsigned rows = (unsigned)a.B * a.T;
     const float inv = 1.0f / (float)N;
     float w[KP][V], dw[KP][V], db[KP][V];
 #pragma unroll
@@ -122,22 +152,35 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
     }
-    for (long r0 = (long)blockIdx.x * RPB; r0 < rows; r0 += (long)gridDim.x * RPB) {
-        const long row = r0 + sub;
-        const bool in = row < rows;
-        const bool ok = in && row_valid(a, row);
-        const long at = in ? row : 0;
-        const T* x = (const T*)a.x + at * N;
-        const T* g = (const T*)a.grad_out + at * N;
-        const float mean = ok ? a.mean_in[at] : 0.0f, r = ok ? a.rstd_in[at] : 0.0f;
+    const unsigned step = gridDim.x * RPB;
+    unsigned row = blockIdx.x * RPB + sub;
+    raw_piece xr[KP], gr[KP];
+    float mean_r, rstd_r;
+    bool ok;
+    auto fetch = [&](unsigned at) {            // the next row is on its way while one is summed
+        ok = at < rows && row_valid(a, at);
+        const size_t first = (size_t)(ok ? at : 0) * N;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            const int c = (k * G + lane) * V;
+            xr[k] = load_raw<T>((const T*)a.x + first + c, ok ? N - c : 0);
+            gr[k] = load_raw<T>((const T*)a.grad_out + first + c, ok ? N - c : 0);
+        }
+        mean_r = ok ? a.mean_in[at] : 0.0f;
+        rstd_r = ok ? a.rstd_in[at] : 0.0f;
+    };
+    fetch(row);
+    for (unsigned r0 = blockIdx.x * RPB; r0 < rows; r0 += step, row += step) {
+        const bool in = row < rows, now = ok;
+        const float mean = mean_r, r = rstd_r;
         float h[KP][V], dy[KP][V];
         float sg = 0.0f, sgh = 0.0f;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            const int c = (k * G + lane) * V;
-            load_piece<T>(x + c, ok ? N - c : 0, h[k]);
-            load_piece<T>(g + c, ok ? N - c : 0, dy[k]);
+            unpack<T>(xr[k], h[k]);
+            unpack<T>(gr[k], dy[k]);
         }
+        if (r0 + step < rows) fetch(row + step);
 #pragma unroll
         for (int k = 0; k < KP; ++k)
 #pragma unroll
@@ -152,14 +195,14 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
         sg = row_sum<G>(sg, red, slot) * inv;
         sgh = row_sum<G>(sgh, red, slot) * inv;
         if (!in) continue;
-        T* dx = (T*)a.grad_x + row * N;
+        T* dx = (T*)a.grad_x + (size_t)row * N;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
             const int c = (k * G + lane) * V;
             if (c >= N) break;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                dy[k][i] = ok ? r * (dy[k][i] * w[k][i] - sg - h[k][i] * sgh) : 0.0f;
+                dy[k][i] = now ? r * (dy[k][i] * w[k][i] - sg - h[k][i] * sgh) : 0.0f;
             store_piece<T>(dx + c, N - c, dy[k]);
         }
     }
@@ -200,18 +243,26 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
     }
 }
 
-// grid (ceil(2N / 64)), block 1024: 64 columns, 16 groups of partial rows, joined in order
+// grid (ceil(2N / 16)), block 256: 16 columns, 16 groups of partial rows, joined in order
 template <class W>
-__global__ __launch_bounds__(1024) void k_norm_partials(const float* part, int nwg, int N, W* gw,
-                                                        W* gb) {
-    __shared__ float s[16][64];
-    const int c = blockIdx.x * 64 + (threadIdx.x & 63), grp = threadIdx.x >> 6;
+__global__ __launch_bounds__(256) void k_norm_partials(const float* part, int nwg, int N, W* gw,
+                                                       W* gb) {
+    __shared__ float s[16][17];
+    const int c = blockIdx.x * 16 + (threadIdx.x & 15), grp = threadIdx.x >> 4;
     const int per = (nwg + 15) / 16;
     const int r1 = min(nwg, (grp + 1) * per);
     float v = 0.0f;
-    if (c < 2 * N)
-        for (int r = grp * per; r < r1; ++r) v += part[(size_t)r * 2 * N + c];
-    s[grp][threadIdx.x & 63] = v;
+    if (c < 2 * N) {
+        constexpr int U = 8;                   // loads in flight
+        for (int r = grp * per; r < r1; r += U) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = r + u < r1 ? part[(size_t)(r + u) * 2 * N + c] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) v += x[u];
+        }
+    }
+    s[grp][threadIdx.x & 15] = v;
     __syncthreads();
     if (grp == 0 && c < 2 * N) {
         for (int i = 1; i < 16; ++i) v += s[i][threadIdx.x];
@@ -236,10 +287,16 @@ Shape2 norm_shape(int N, int V) {
     return {G, KP};
 }
 
-int norm_grad_wgs(long rows, int RPB) {
-    const long need = (rows + RPB - 1) / RPB;
-    return (int)(need < 1024 ? need : 1024);
+// Workgroups of NT threads for the rows: at most as many as make `waves` wavefronts a SIMD.
+int norm_wgs(long rows, int G, int NT, int waves) {
+    const long need = (rows + NT / G - 1) / (NT / G), most = 1024l * waves / (NT / 64);
+    return (int)(need < most ? need : most);
 }
+constexpr int norm_threads(int G) { return G > 256 ? G : 256; }
+// The gradient runs at 4 wavefronts a SIMD: the row on its way hides the latency, and every
+// workgroup leaves a partial row (400,000 rows of 512 bfloat16, with the partials' sum: 238 us
+// at 4, 299 at 6, 267 at 8; workgroups of 512 threads 326 at 4).
+constexpr int GRAD_WAVES = 4;
 
 template <class F>
 hipError_t with_shape(int N, int V, F&& f) {
@@ -255,9 +312,8 @@ hipError_t with_shape(int N, int V, F&& f) {
 template <class T, class W>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
     return with_shape(a.N, Piece<T>::V, [&](auto g, auto kp) {
-        constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = G > 256 ? G : 256;
-        const long rows = (long)a.B * a.T, rpb = NT / G;
-        hipLaunchKernelGGL((k_layer_norm<T, W, G, KP, NT>), dim3((unsigned)((rows + rpb - 1) / rpb)),
+        constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = norm_threads(G);
+        hipLaunchKernelGGL((k_layer_norm<T, W, G, KP, NT>), dim3(norm_wgs((long)a.B * a.T, G, NT, 8)),
                            dim3(NT), 0, stream, a);
         return hipGetLastError();
     });
@@ -266,12 +322,12 @@ hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
 template <class T, class W>
 hipError_t run_norm_grad(const NormArgs& a, float* part, hipStream_t stream) {
     return with_shape(a.N, Piece<T>::V, [&](auto g, auto kp) {
-        constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = G > 256 ? G : 256;
-        const int nwg = norm_grad_wgs((long)a.B * a.T, NT / G);
+        constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = norm_threads(G);
+        const int nwg = norm_wgs((long)a.B * a.T, G, NT, GRAD_WAVES);
         hipLaunchKernelGGL((k_layer_norm_grad<T, W, G, KP, NT>), dim3(nwg), dim3(NT), 0, stream, a,
                            part);
         if (a.grad_weight || a.grad_bias)
-            hipLaunchKernelGGL((k_norm_partials<W>), dim3((2 * a.N + 63) / 64), dim3(1024), 0, stream,
+            hipLaunchKernelGGL((k_norm_partials<W>), dim3((2 * a.N + 15) / 16), dim3(256), 0, stream,
                                part, nwg, a.N, (W*)a.grad_weight, (W*)a.grad_bias);
         return hipGetLastError();
     });
@@ -287,8 +343,7 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
 size_t layer_norm_grad_bytes(int B, int T, int N, int dtype) {
     const int V = dtype == SEMICRF_F32 ? 4 : 8;
     const Shape2 s = norm_shape(N, V);
-    const int NT = s.G > 256 ? s.G : 256;
-    return (size_t)norm_grad_wgs((long)B * T, NT / s.G) * 2 * N * sizeof(float);
+    return (size_t)norm_wgs((long)B * T, s.G, norm_threads(s.G), GRAD_WAVES) * 2 * N * sizeof(float);
 }
 
 hipError_t launch_layer_norm_grad(const NormArgs& a, void* ws, hipStream_t stream) {
