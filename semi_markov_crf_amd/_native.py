@@ -21,7 +21,7 @@ STATUS_NAMES = {0: "SEMICRF_OK", 1: "SEMICRF_ERR_INVALID", 2: "SEMICRF_ERR_WORKS
                 5: "SEMICRF_ERR_UNIMPLEMENTED"}
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
-_c_float, _strides = ctypes.c_float, ctypes.c_int64 * 3
+_c_float, Strides = ctypes.c_float, ctypes.c_int64 * 3
 
 
 class Options(ctypes.Structure):
@@ -34,8 +34,8 @@ class Options(ctypes.Structure):
 
 class Attention(ctypes.Structure):
     """struct semicrf_attention (include/semicrf.h), field for field."""
-    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_stride", _strides),
-                ("k_stride", _strides), ("v_stride", _strides), ("lengths", _vp),
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_stride", Strides),
+                ("k_stride", Strides), ("v_stride", Strides), ("lengths", _vp),
                 ("log_decay", _vp), ("state", _vp), ("scale", _c_float), ("dtype", _c_int),
                 ("B", _c_int), ("T", _c_int), ("Hq", _c_int), ("Hk", _c_int), ("Dk", _c_int),
                 ("Dv", _c_int)]

@@ -136,16 +136,15 @@ __global__ __launch_bounds__(256) void k_sort_count(const SortArgs s) {
     count_tile(key, from, s.n, s.shift, s.counts + (size_t)threadIdx.x * s.by_digit + (size_t)blockIdx.x * s.by_tile);
 }
 
-// Workgroups 0 .. ntiles - 1 count the first digit of a tile; the others clear the gradient (rows
-// of tokens that do not appear stay 0).
-__global__ __launch_bounds__(256) void k_grad_begin(const EmbedArgs a, int n, int ntiles, int by_digit,
-                                                    int by_tile, int* counts, size_t bytes) {
-    if (blockIdx.x >= (unsigned)ntiles) {
+// Workgroups 0 .. ntiles - 1 count the first digit of a tile; the others clear the gradient's
+// `bytes` (rows of tokens that do not appear stay 0).
+__global__ __launch_bounds__(256) void k_grad_begin(const EmbedArgs a, const SortArgs s, size_t bytes) {
+    if (blockIdx.x >= (unsigned)s.ntiles) {
         char* out = (char*)a.out;
-        const size_t pieces = bytes / 16, step = (size_t)(gridDim.x - ntiles) * 256;
+        const size_t pieces = bytes / 16, step = (size_t)(gridDim.x - s.ntiles) * 256;
         const raw_piece zero = {0, 0, 0, 0};
-        const size_t first = (size_t)(blockIdx.x - ntiles) * 256 + threadIdx.x;
-        for (size_t i = first; i < pieces; i += step) __builtin_memcpy(out + i * 16, &zero, 16);
+        const size_t first = (size_t)(blockIdx.x - s.ntiles) * 256 + threadIdx.x;
+        for (size_t i = first; i < pieces; i += step) *(loose_piece*)(out + i * 16) = zero;
         if (first < bytes - pieces * 16) out[pieces * 16 + first] = 0;
         return;
     }
@@ -153,10 +152,10 @@ __global__ __launch_bounds__(256) void k_grad_begin(const EmbedArgs a, int n, in
     unsigned from[PER];
 #pragma unroll
     for (int p = 0; p < PER; ++p) from[p] = blockIdx.x * TILE + p * SORT_NT + threadIdx.x;
-    load_keys<PER>(a, from, n, key);
+    load_keys<PER>(a, from, s.n, key);
 #pragma unroll
     for (int p = 0; p < PER; ++p) key[p] = min(key[p], (uint32_t)a.V);
-    count_tile(key, from, n, 0, counts + (size_t)threadIdx.x * by_digit + (size_t)blockIdx.x * by_tile);
+    count_tile(key, from, s.n, 0, s.counts + (size_t)threadIdx.x * s.by_digit + (size_t)blockIdx.x * s.by_tile);
 }
 
 // exclusive scan of one digit's counts over the tiles; totals [BINS].  grid BINS, block 256
@@ -276,8 +275,8 @@ __global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, con
 }
 
 // ------------------------------------------------------------------ sums over runs
-// One wavefront adds the rows of one chunk (R <= 64) over 64 pieces of columns, U rows on their way
-// at a time.  Partial rows: part[chunk][0] = the run that comes from the chunk before,
+// One wavefront adds the rows of one chunk over 64 pieces of columns, U rows on their way at a
+// time.  Partial rows: part[chunk][0] = the run that comes from the chunk before,
 // part[chunk][1] = the run that starts here and goes on.
 // grid (ceil(nchunks / 4), column slabs), block 256
 template <class T>
@@ -289,23 +288,14 @@ __global__ __launch_bounds__(256) void k_grad_chunks(const EmbedArgs a, const ui
     const int chunk = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
     if (chunk >= nchunks) return;
     const int c = (blockIdx.y * 64 + lane) * V;
-    const int r0 = chunk * R, m = min(n - r0, R);
+    const int r0 = chunk * R, r1 = min(n, r0 + R);
     const T* g = (const T*)a.grad_out + c;
-    // every lane keeps one row's key and position; row r is read from lane r
-    const uint32_t my_key = lane < m ? keys[r0 + lane] : (uint32_t)a.V;
-    const int my_pos = lane < m ? pos[r0 + lane] : 0;
-    const uint32_t key_before = r0 > 0 ? keys[r0 - 1] : ~0u, key_after = r0 + m < n ? keys[r0 + m] : ~0u;
-    auto key_of = [&](int r) { return (uint32_t)__builtin_amdgcn_readlane((int)my_key, r); };
-    auto row_of = [&](int r) {
-        return load_raw<T>(g + (size_t)(unsigned)__builtin_amdgcn_readlane(my_pos, r) * N, N - c);
-    };
-    // the positions that count for nothing come last
-    const int live = __popcll(__ballot(my_key < (uint32_t)a.V));
-    if (live == 0) return;
+    const uint32_t key_before = r0 > 0 ? keys[r0 - 1] : ~0u, key_after = r1 < n ? keys[r1] : ~0u;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    uint32_t cur = key_of(0);
+    uint32_t cur = keys[r0];
+    if (cur >= (uint32_t)a.V) return;          // the positions that count for nothing come last
     bool from_before = key_before == cur;
     auto flush = [&](bool goes_on) {
         if (from_before || goes_on) {
@@ -324,31 +314,42 @@ __global__ __launch_bounds__(256) void k_grad_chunks(const EmbedArgs a, const ui
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
         from_before = false;
     };
-    raw_piece x[U], y[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (u < live) x[u] = row_of(u);
-    for (int r = 0; r < live; r += U) {
+    for (int b0 = r0; b0 < r1; b0 += 64) {
+        // every lane keeps one row's key and position; row r of the block is read from lane r
+        const int m = min(r1 - b0, 64);
+        const uint32_t my_key = lane < m ? keys[b0 + lane] : (uint32_t)a.V;
+        const int my_pos = lane < m ? pos[b0 + lane] : 0;
+        const int live = __popcll(__ballot(my_key < (uint32_t)a.V));
+        auto row_of = [&](int r) {
+            return load_raw<T>(g + (size_t)(unsigned)__builtin_amdgcn_readlane(my_pos, r) * N, N - c);
+        };
+        raw_piece x[U], y[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (r + U + u < live) y[u] = row_of(r + U + u);
+            if (u < live) x[u] = row_of(u);
+        for (int r = 0; r < live; r += U) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (r + u < live) {
-                const uint32_t key = key_of(r + u);
-                if (key != cur) {
-                    flush(false);
-                    cur = key;
+            for (int u = 0; u < U; ++u)
+                if (r + U + u < live) y[u] = row_of(r + U + u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r + u < live) {
+                    const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)my_key, r + u);
+                    if (key != cur) {
+                        flush(false);
+                        cur = key;
+                    }
+                    float f[V];
+                    unpack<T>(x[u], f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] += f[i];
                 }
-                float f[V];
-                unpack<T>(x[u], f);
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += f[i];
+                x[u] = y[u];
             }
-            x[u] = y[u];
         }
+        if (live < m) break;
     }
-    flush(live == m && key_after == cur);
+    flush(key_after == cur);
 }
 
 // The run that starts in this chunk and goes on: its partial rows, in order.  CL lanes take four
@@ -410,16 +411,18 @@ struct GradLayout {
     size_t key[2], pos[2], counts, totals, part, total;
 };
 
-GradLayout grad_layout(int B, int T, int V, int N) {
+GradLayout grad_layout(int B, int T, int V, int N, int es) {
     GradLayout l{};
     l.n = B * T;
     l.ntiles = (l.n + TILE - 1) / TILE;
     int bits = 1;
     while (((long)V >> bits) != 0) ++bits;
     l.passes = (bits + 7) / 8;
-    // rows per chunk: enough chunks to fill the device, few enough partial rows
+    // rows per chunk: about 2,048 wavefronts over the chunks and column slabs fill the device; longer
+    // chunks leave fewer partial rows
+    const long slabs = ((long)N * es + 1023) / 1024;
     l.R = 16;
-    while (l.R < 64 && l.n / l.R > 4096) l.R *= 2;
+    while (l.R < 256 && l.n * slabs / l.R > 2048) l.R *= 2;
     l.nchunks = (l.n + l.R - 1) / l.R;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -464,24 +467,21 @@ hipError_t run_embed(const EmbedArgs& a, hipStream_t stream) {
 template <class T>
 hipError_t run_embed_grad(const EmbedArgs& a, char* ws, hipStream_t stream) {
     constexpr int V = Piece<T>::V;
-    const GradLayout l = grad_layout(a.B, a.T, a.V, a.N);
-    const size_t bytes = (size_t)a.V * a.N * sizeof(T), pieces = bytes / 16;
-    const size_t fill = pieces / 1024 + 1;     // four pieces a thread, up to 4,096 workgroups
-    int* counts = (int*)(ws + l.counts);
-    const bool scan = l.ntiles > SCAN_TILES;
-    const int by_digit = scan ? l.ntiles : 1, by_tile = scan ? 1 : BINS;
-    hipLaunchKernelGGL(k_grad_begin, dim3(l.ntiles + (unsigned)(fill < 4096 ? fill : 4096)), dim3(256), 0,
-                       stream, a, l.n, l.ntiles, by_digit, by_tile, counts, bytes);
+    const GradLayout l = grad_layout(a.B, a.T, a.V, a.N, sizeof(T));
+    const size_t bytes = (size_t)a.V * a.N * sizeof(T);
     SortArgs s{};
     s.n = l.n;
     s.ntiles = l.ntiles;
-    s.by_digit = by_digit;
-    s.by_tile = by_tile;
-    s.counts = counts;
+    s.counts = (int*)(ws + l.counts);
+    const bool scan = l.ntiles > SCAN_TILES;
+    s.by_digit = scan ? l.ntiles : 1;
+    s.by_tile = scan ? 1 : BINS;
+    const size_t fill = bytes / (256 * 64) + 1;    // four pieces a thread, up to 4,096 workgroups
+    hipLaunchKernelGGL(k_grad_begin, dim3(l.ntiles + (unsigned)(fill < 4096 ? fill : 4096)), dim3(256), 0,
+                       stream, a, s, bytes);
     for (int p = 0; p < l.passes; ++p) {
         s.shift = 8 * p;
         if (p > 0) hipLaunchKernelGGL(k_sort_count, dim3(l.ntiles), dim3(256), 0, stream, s);
-        s.totals = nullptr;
         if (scan) {
             s.totals = (const int*)(ws + l.totals);
             hipLaunchKernelGGL(k_sort_scan, dim3(BINS), dim3(256), 0, stream, s.counts, l.ntiles,
@@ -516,8 +516,8 @@ hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream) {
     return a.dtype == SEMICRF_F32 ? run_embed<float>(a, stream) : run_embed<bf16>(a, stream);
 }
 
-size_t embed_grad_bytes(int B, int T, int V, int N) {
-    return grad_layout(B, T, V, N).total;
+size_t embed_grad_bytes(int B, int T, int V, int N, int dtype) {
+    return grad_layout(B, T, V, N, dtype == SEMICRF_F32 ? 4 : 2).total;
 }
 
 hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream) {

@@ -104,7 +104,7 @@ struct EmbedArgs {
     int32_t* status;
 };
 hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream);
-size_t embed_grad_bytes(int B, int T, int V, int N);
+size_t embed_grad_bytes(int B, int T, int V, int N, int dtype);
 hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream);
 
 struct NormArgs {

@@ -75,7 +75,7 @@ int semicrf_embed(const void* tokens, int token_bits, const int32_t* lengths, co
 
 size_t semicrf_embed_grad_bytes(int dtype, int B, int T, int V, int N) {
     if (!type_ok(dtype) || check_rows(B, T, N) || V < 1 || V >= MAX_ROWS) return 0;
-    return embed_grad_bytes(B, T, V, N);
+    return embed_grad_bytes(B, T, V, N, dtype);
 }
 
 int semicrf_embed_grad(const void* tokens, int token_bits, const int32_t* lengths,
@@ -85,7 +85,7 @@ int semicrf_embed_grad(const void* tokens, int token_bits, const int32_t* length
     int rc = check_embed(tokens, token_bits, dtype, B, T, V, N);
     if (rc) return rc;
     if (!grad_out || !grad_table) return SEMICRF_ERR_INVALID;
-    if ((rc = check_ws(workspace, workspace_bytes, embed_grad_bytes(B, T, V, N)))) return rc;
+    if ((rc = check_ws(workspace, workspace_bytes, embed_grad_bytes(B, T, V, N, dtype)))) return rc;
     EmbedArgs a{};
     a.tokens = tokens; a.token_bits = token_bits; a.lengths = lengths; a.grad_out = grad_out;
     a.dtype = dtype; a.B = B; a.T = T; a.V = V; a.N = N; a.scale = scale;

@@ -17,8 +17,6 @@ length or a token was out of range.
 
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _native
@@ -29,40 +27,53 @@ __all__ = ["embed", "embed_grad", "layer_norm", "layer_norm_grad", "decay_attent
 _TYPES = {torch.float32: _native.F32, torch.bfloat16: _native.BF16}
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# the current stream of a device, as an address; single-token calls are host-bound, and the public
+# way builds a Stream object for it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
-def _need(name, x, dtype=None, shape=None, device=None, dense=True):
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+def _index(name, x):
+    """Device index of the tensor that says where a call runs."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if device is not None and x.device != device:
-        raise ValueError(f"{name} is on {x.device}, expected {device}")
-    if dtype is None:
-        if x.dtype not in _TYPES:
-            raise TypeError(f"{name} must be float32 or bfloat16, got {x.dtype}")
-    elif x.dtype != dtype:
+    if x.dtype not in _TYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {x.dtype}")
+    return x.get_device()
+
+
+def _need(name, x, dtype, shape, dev):
+    """Refuses what is not a dense tensor of this type and shape on GPU `dev`."""
+    try:
+        if x.dtype is dtype and x.shape == shape and x.get_device() == dev and x.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, expected cuda:{dev}")
+    if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+    if tuple(x.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(x.shape)}")
-    if dense and not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _lengths(lengths, B, device):
+def _lengths(lengths, B, dev):
     if lengths is not None:
-        _need("lengths", lengths, torch.int32, (B,), device)
+        _need("lengths", lengths, torch.int32, (B,), dev)
 
 
 def _workspace(fn, n, device, workspace):
     if n == 0:
         raise _native.SemiCRFError(fn, 3)
     if workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        return torch.empty(n, dtype=torch.uint8, device=device)
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     if workspace.numel() * workspace.element_size() < n or workspace.data_ptr() % 256:
@@ -70,51 +81,55 @@ def _workspace(fn, n, device, workspace):
     return workspace
 
 
-class _Status:
-    """The status word of one call, present only where it is asked for."""
+def _status(want, device):
+    """The status word of a call, where it is asked for."""
+    return torch.zeros(1, dtype=torch.int32, device=device) if want else None
 
-    def __init__(self, fn, want, device):
-        self.fn = fn
-        self.word = torch.zeros(1, dtype=torch.int32, device=device) if want else None
 
-    def check(self, rc):
-        _native.check(self.fn, rc)
-        if self.word is not None and int(self.word.item()):
-            raise _native.SemiCRFError(self.fn, 1)
+def _check(fn, rc, word=None):
+    if rc:
+        raise _native.SemiCRFError(fn, rc)
+    if word is not None and int(word.item()):
+        raise _native.SemiCRFError(fn, 1)
 
 
 def _tracked(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 # ---------------------------------------------------------------- embedding
 
-def _tokens(tokens, device):
-    if not isinstance(tokens, torch.Tensor) or tokens.device != device:
-        raise ValueError(f"tokens must be on {device}")
+def _tokens(tokens, dev):
+    if not isinstance(tokens, torch.Tensor) or tokens.get_device() != dev:
+        raise ValueError(f"tokens must be on cuda:{dev}")
     if tokens.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"tokens must be int32 or int64, got {tokens.dtype}")
     if tokens.dim() != 2 or not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous [B, T]")
-    return int(tokens.shape[0]), int(tokens.shape[1]), tokens.element_size() * 8
+    B, T = tokens.shape
+    return B, T, tokens.element_size() * 8
 
 
 def embed(tokens, table, *, scale=1.0, lengths=None, check_status=False) -> torch.Tensor:
     """scale * table[tokens]: tokens [B, T] int32 or int64, table [V, N], out [B, T, N].  A
     token outside [0, V) gives a row of NaN."""
+    dev = _index("table", table)
     if _tracked(table):
         return _Embed.apply(tokens, table, float(scale), lengths, check_status)
-    _need("table", table)
-    if table.dim() != 2:
-        raise ValueError("table must be [V, N]")
-    B, T, bits = _tokens(tokens, table.device)
-    _lengths(lengths, B, table.device)
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be contiguous [V, N]")
+    B, T, bits = _tokens(tokens, dev)
+    _lengths(lengths, B, dev)
     V, N = table.shape
-    out = torch.empty((B, T, N), dtype=table.dtype, device=table.device)
-    st = _Status("semicrf_embed", check_status, table.device)
-    st.check(_native.load().semicrf_embed(
+    out = table.new_empty((B, T, N))
+    word = _status(check_status, table.device)
+    _check("semicrf_embed", _native.load().semicrf_embed(
         tokens.data_ptr(), bits, _ptr(lengths), table.data_ptr(), _TYPES[table.dtype], B, T, V, N,
-        scale, _stream(table.device), out.data_ptr(), _ptr(st.word)))
+        scale, _raw_stream(dev), out.data_ptr(), _ptr(word)), word)
     return out
 
 
@@ -122,20 +137,19 @@ def embed_grad(tokens, grad_out, V, *, scale=1.0, lengths=None, workspace=None,
                check_status=False) -> torch.Tensor:
     """Gradient [V, N] of the table: row v is scale times the sum of grad_out [B, T, N] over
     the positions that hold token v, in the order of the positions."""
-    _need("grad_out", grad_out)
-    dev = grad_out.device
+    dev = _index("grad_out", grad_out)
     B, T, bits = _tokens(tokens, dev)
     _lengths(lengths, B, dev)
-    if grad_out.dim() != 3 or grad_out.shape[:2] != tokens.shape:
-        raise ValueError(f"grad_out must be [{B}, {T}, N], got {list(grad_out.shape)}")
-    N, V, lib, typ = int(grad_out.shape[2]), int(V), _native.load(), _TYPES[grad_out.dtype]
+    if grad_out.dim() != 3 or grad_out.shape[:2] != tokens.shape or not grad_out.is_contiguous():
+        raise ValueError(f"grad_out must be contiguous [{B}, {T}, N], got {list(grad_out.shape)}")
+    N, V, lib, typ = grad_out.shape[2], int(V), _native.load(), _TYPES[grad_out.dtype]
     n = lib.semicrf_embed_grad_bytes(typ, B, T, V, N)
-    ws = _workspace("semicrf_embed_grad", n, dev, workspace)
-    out = torch.empty((V, N), dtype=grad_out.dtype, device=dev)
-    st = _Status("semicrf_embed_grad", check_status, dev)
-    st.check(lib.semicrf_embed_grad(
+    ws = _workspace("semicrf_embed_grad", n, grad_out.device, workspace)
+    out = grad_out.new_empty((V, N))
+    word = _status(check_status, grad_out.device)
+    _check("semicrf_embed_grad", lib.semicrf_embed_grad(
         tokens.data_ptr(), bits, _ptr(lengths), grad_out.data_ptr(), typ, B, T, V, N, scale,
-        _stream(dev), ws.data_ptr(), n, out.data_ptr(), _ptr(st.word)))
+        _raw_stream(dev), ws.data_ptr(), n, out.data_ptr(), _ptr(word)), word)
     return out
 
 
@@ -157,21 +171,20 @@ class _Embed(torch.autograd.Function):
 # ---------------------------------------------------------------- layer norm
 
 def _norm_shape(x, weight, bias):
-    _need("x", x)
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, N]")
-    B, T, N = (int(n) for n in x.shape)
-    wtype = x.dtype if weight is None else weight.dtype
-    if wtype not in (x.dtype, torch.float32):
-        raise TypeError(f"weight must be {x.dtype} or float32, got {wtype}")
+    """Device index, B, T, N and the type of the weights."""
+    dev = _index("x", x)
+    if x.dim() != 3 or not x.is_contiguous():
+        raise ValueError("x must be contiguous [B, T, N]")
+    B, T, N = x.shape
+    first = weight if weight is not None else bias
+    wtype = x.dtype if first is None else first.dtype
+    if wtype is not x.dtype and wtype is not torch.float32:
+        raise TypeError(f"weight and bias must be {x.dtype} or float32, got {wtype}")
     if weight is not None:
-        _need("weight", weight, wtype, (N,), x.device)
+        _need("weight", weight, wtype, (N,), dev)
     if bias is not None:
-        wtype = wtype if weight is not None else bias.dtype
-        if wtype not in (x.dtype, torch.float32):
-            raise TypeError(f"bias must be {x.dtype} or float32, got {wtype}")
-        _need("bias", bias, wtype, (N,), x.device)
-    return B, T, N, wtype
+        _need("bias", bias, wtype, (N,), dev)
+    return dev, B, T, N, wtype
 
 
 def layer_norm(x, weight=None, bias=None, *, eps=1e-5, lengths=None, want_stats=False,
@@ -179,18 +192,19 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, lengths=None, want_stats=
     """Layer norm over the last axis of x [B, T, N].  weight, bias [N] in x's type or float32
     (None: ones, zeros).  With want_stats, (y, mean [B, T], rstd [B, T]), which
     layer_norm_grad takes; those two carry no gradient."""
+    dev, B, T, N, wtype = _norm_shape(x, weight, bias)
     if _tracked(x, weight, bias):
-        y, mean, rstd = _LayerNorm.apply(x, weight, bias, float(eps), lengths, check_status)
+        y, mean, rstd = _LayerNorm.apply(x, weight, bias, float(eps), lengths, wtype, check_status)
         return (y, mean, rstd) if want_stats else y
-    B, T, N, wtype = _norm_shape(x, weight, bias)
-    _lengths(lengths, B, x.device)
+    _lengths(lengths, B, dev)
     y = torch.empty_like(x)
-    mean = torch.empty((B, T), dtype=torch.float32, device=x.device) if want_stats else None
-    rstd = torch.empty_like(mean) if want_stats else None
-    st = _Status("semicrf_layer_norm", check_status, x.device)
-    st.check(_native.load().semicrf_layer_norm(
+    mean = rstd = None
+    if want_stats:
+        mean, rstd = (torch.empty((B, T), dtype=torch.float32, device=x.device) for _ in range(2))
+    word = _status(check_status, x.device)
+    _check("semicrf_layer_norm", _native.load().semicrf_layer_norm(
         x.data_ptr(), _TYPES[x.dtype], _ptr(weight), _ptr(bias), _TYPES[wtype], _ptr(lengths), B, T,
-        N, eps, _stream(x.device), y.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(st.word)))
+        N, eps, _raw_stream(dev), y.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(word)), word)
     return (y, mean, rstd) if want_stats else y
 
 
@@ -199,29 +213,29 @@ def layer_norm_grad(grad_out, x, weight, mean, rstd, *, lengths=None, want_param
     """Gradients of layer_norm from the mean and rstd it left: a dict with grad_x [B, T, N] and,
     unless want_params is False, grad_weight and grad_bias [N] in the weight's type (x's where
     weight is None)."""
-    B, T, N, wtype = _norm_shape(x, weight, None)
+    dev, B, T, N, wtype = _norm_shape(x, weight, None)
     return _norm_grad(grad_out, x, weight, wtype, mean, rstd, lengths, want_params, workspace,
-                      check_status, B, T, N)
+                      check_status, dev, B, T, N)
 
 
 def _norm_grad(grad_out, x, weight, wtype, mean, rstd, lengths, want_params, workspace,
-               check_status, B, T, N):
-    dev = x.device
+               check_status, dev, B, T, N):
     _need("grad_out", grad_out, x.dtype, x.shape, dev)
     _need("mean", mean, torch.float32, (B, T), dev)
     _need("rstd", rstd, torch.float32, (B, T), dev)
     _lengths(lengths, B, dev)
     lib = _native.load()
     n = lib.semicrf_layer_norm_grad_bytes(_TYPES[x.dtype], B, T, N)
-    ws = _workspace("semicrf_layer_norm_grad", n, dev, workspace)
+    ws = _workspace("semicrf_layer_norm_grad", n, x.device, workspace)
     gx = torch.empty_like(x)
-    gw = torch.empty(N, dtype=wtype, device=dev) if want_params else None
-    gb = torch.empty(N, dtype=wtype, device=dev) if want_params else None
-    st = _Status("semicrf_layer_norm_grad", check_status, dev)
-    st.check(lib.semicrf_layer_norm_grad(
+    gw = gb = None
+    if want_params:
+        gw, gb = (torch.empty(N, dtype=wtype, device=x.device) for _ in range(2))
+    word = _status(check_status, x.device)
+    _check("semicrf_layer_norm_grad", lib.semicrf_layer_norm_grad(
         grad_out.data_ptr(), x.data_ptr(), _TYPES[x.dtype], _ptr(weight), _TYPES[wtype],
-        mean.data_ptr(), rstd.data_ptr(), _ptr(lengths), B, T, N, _stream(dev), ws.data_ptr(), n,
-        gx.data_ptr(), _ptr(gw), _ptr(gb), _ptr(st.word)))
+        mean.data_ptr(), rstd.data_ptr(), _ptr(lengths), B, T, N, _raw_stream(dev), ws.data_ptr(), n,
+        gx.data_ptr(), _ptr(gw), _ptr(gb), _ptr(word)), word)
     out = {"grad_x": gx}
     if want_params:
         out.update(grad_weight=gw, grad_bias=gb)
@@ -230,8 +244,8 @@ def _norm_grad(grad_out, x, weight, wtype, mean, rstd, lengths, want_params, wor
 
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, eps, lengths, check_status):
-        ctx.wtype = _norm_shape(x, weight, bias)[3]
+    def forward(ctx, x, weight, bias, eps, lengths, wtype, check_status):
+        ctx.wtype = wtype
         y, mean, rstd = layer_norm(x, weight, bias, eps=eps, lengths=lengths, want_stats=True,
                                    check_status=check_status)
         ctx.save_for_backward(x, weight, mean, rstd, lengths)
@@ -244,40 +258,41 @@ class _LayerNorm(torch.autograd.Function):
         need_w, need_b = ctx.needs_input_grad[1:3]
         B, T, N = x.shape
         d = _norm_grad(g.contiguous(), x, weight, ctx.wtype, mean, rstd, lengths,
-                       need_w or need_b, None, False, B, T, N)
+                       need_w or need_b, None, False, x.get_device(), B, T, N)
         return (d["grad_x"], d.get("grad_weight") if need_w else None,
-                d.get("grad_bias") if need_b else None, None, None, None)
+                d.get("grad_bias") if need_b else None, None, None, None, None)
 
 
 # ---------------------------------------------------------------- attention
 
-def _attention(q, k, v, log_decay, scale, lengths, state, state_shape, T):
-    """The checked argument struct; q, k, v [B, T, H, D] (or [B, H, D] for one token)."""
-    dims = 3 if T is None else 4
-    for name, x in (("q", q), ("k", k), ("v", v)):
-        _need(name, x, None if name == "q" else q.dtype, device=q.device, dense=False)
-        if x.dim() != dims:
-            raise ValueError(f"{name} must have {dims} dimensions, got {list(x.shape)}")
-        if x.shape[-1] != 1 and x.stride(-1) != 1:
-            raise ValueError(f"the last axis of {name} must be dense")
-    B, (Hq, Dk), (Hk, Dv) = q.shape[0], q.shape[-2:], v.shape[-2:]
-    if k.shape[:-1] != v.shape[:-1] or k.shape[-1] != Dk or q.shape[:-2] != k.shape[:-2] or \
+def _attention(q, k, v, log_decay, scale, lengths, state, pool, dims):
+    """Device index and the checked argument struct; q, k, v [B, T, H, D] (dims 4), or [B, H, D] for
+    one token (dims 3) with states in a pool of `pool` rows."""
+    dev = _index("q", q)
+    try:
+        (B, *qt, Hq, Dk), (Bk, *kt, Hk, Dkk), (Bv, *vt, Hv, Dv) = q.shape, k.shape, v.shape
+    except (AttributeError, ValueError):
+        raise ValueError(f"q, k and v must be tensors of {dims} dimensions") from None
+    if len(qt) != dims - 3 or qt != kt or qt != vt or not B == Bk == Bv or Hk != Hv or Dk != Dkk or \
             Hk < 1 or Hq % Hk:
         raise ValueError(f"shape mismatch: q {list(q.shape)}, k {list(k.shape)}, v "
                          f"{list(v.shape)}; query heads must be a multiple of key heads")
-    _need("log_decay", log_decay, torch.float32, (Hq,), q.device)
-    _lengths(lengths, B, q.device)
+    if k.dtype is not q.dtype or v.dtype is not q.dtype:
+        raise TypeError(f"q, k and v must be of one type, got {q.dtype}, {k.dtype}, {v.dtype}")
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"k and v must be on cuda:{dev}")
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if qs[-1] != 1 and Dk != 1 or ks[-1] != 1 and Dk != 1 or vs[-1] != 1 and Dv != 1:
+        raise ValueError("the last axis of q, k and v must be dense")
+    _need("log_decay", log_decay, torch.float32, (Hq,), dev)
+    _lengths(lengths, B, dev)
     if state is not None:
-        _need("state", state, torch.float32, state_shape or (B, Hq, Dk, Dv), q.device)
-    a = _native.Attention()
-    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    for s, x in ((a.q_stride, q), (a.k_stride, k), (a.v_stride, v)):
-        s[0], s[1], s[2] = x.stride(0), x.stride(1) if dims == 4 else 0, x.stride(-2)
-    a.lengths, a.log_decay, a.state = _ptr(lengths), log_decay.data_ptr(), _ptr(state)
-    a.scale = float(Dk) ** -0.5 if scale is None else float(scale)
-    a.dtype = _TYPES[q.dtype]
-    a.B, a.T, a.Hq, a.Hk, a.Dk, a.Dv = B, 1 if T is None else q.shape[1], Hq, Hk, Dk, Dv
-    return a
+        _need("state", state, torch.float32, (B if pool is None else pool, Hq, Dk, Dv), dev)
+    S = _native.Strides
+    return dev, _native.Attention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), S(qs[0], qs[-3], qs[-2]), S(ks[0], ks[-3], ks[-2]),
+        S(vs[0], vs[-3], vs[-2]), _ptr(lengths), log_decay.data_ptr(), _ptr(state),
+        Dk ** -0.5 if scale is None else scale, _TYPES[q.dtype], B, qt[0] if qt else 1, Hq, Hk, Dk, Dv)
 
 
 def decay_attention(q, k, v, log_decay, *, scale=None, lengths=None, state=None,
@@ -293,15 +308,15 @@ def decay_attention(q, k, v, log_decay, *, scale=None, lengths=None, state=None,
         o, end = _DecayAttention.apply(q, k, v, log_decay, scale, lengths, state, want_state,
                                        check_status)
         return (o, end) if want_state else o
-    a = _attention(q, k, v, log_decay, scale, lengths, state, None, 0)
-    dev, lib = q.device, _native.load()
+    dev, a = _attention(q, k, v, log_decay, scale, lengths, state, None, 4)
+    lib = _native.load()
     n = lib.semicrf_decay_attention_bytes(a, 0)
-    ws = _workspace("semicrf_decay_attention", n, dev, workspace)
-    out = torch.empty((a.B, a.T, a.Hq, a.Dv), dtype=q.dtype, device=dev)
-    end = torch.empty((a.B, a.Hq, a.Dk, a.Dv), dtype=torch.float32, device=dev) if want_state else None
-    st = _Status("semicrf_decay_attention", check_status, dev)
-    st.check(lib.semicrf_decay_attention(a, _stream(dev), ws.data_ptr(), n, out.data_ptr(),
-                                         _ptr(end), _ptr(st.word)))
+    ws = _workspace("semicrf_decay_attention", n, q.device, workspace)
+    out = q.new_empty((a.B, a.T, a.Hq, a.Dv))
+    end = q.new_empty((a.B, a.Hq, a.Dk, a.Dv), dtype=torch.float32) if want_state else None
+    word = _status(check_status, q.device)
+    _check("semicrf_decay_attention", lib.semicrf_decay_attention(
+        a, _raw_stream(dev), ws.data_ptr(), n, out.data_ptr(), _ptr(end), _ptr(word)), word)
     return (out, end) if want_state else out
 
 
@@ -310,19 +325,19 @@ def decay_attention_grad(grad_out, q, k, v, log_decay, *, scale=None, lengths=No
     """Gradients of decay_attention from those of its output, grad_out [B, T, Hq, Dv], and of its
     final state, grad_state [B, Hq, Dk, Dv] (None: 0): a dict with grad_q, grad_k, grad_v and,
     where an initial state is given, grad_state."""
-    a = _attention(q, k, v, log_decay, scale, lengths, state, None, 0)
-    dev, lib = q.device, _native.load()
+    dev, a = _attention(q, k, v, log_decay, scale, lengths, state, None, 4)
+    lib = _native.load()
     _need("grad_out", grad_out, q.dtype, (a.B, a.T, a.Hq, a.Dv), dev)
     if grad_state is not None:
         _need("grad_state", grad_state, torch.float32, (a.B, a.Hq, a.Dk, a.Dv), dev)
     n = lib.semicrf_decay_attention_bytes(a, 1)
-    ws = _workspace("semicrf_decay_attention_grad", n, dev, workspace)
-    gq, gk, gv = (torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k, v))
+    ws = _workspace("semicrf_decay_attention_grad", n, q.device, workspace)
+    gq, gk, gv = (x.new_empty(x.shape) for x in (q, k, v))
     gs = torch.empty_like(state) if state is not None else None
-    st = _Status("semicrf_decay_attention_grad", check_status, dev)
-    st.check(lib.semicrf_decay_attention_grad(
-        a, grad_out.data_ptr(), _ptr(grad_state), _stream(dev), ws.data_ptr(), n, gq.data_ptr(),
-        gk.data_ptr(), gv.data_ptr(), _ptr(gs), _ptr(st.word)))
+    word = _status(check_status, q.device)
+    _check("semicrf_decay_attention_grad", lib.semicrf_decay_attention_grad(
+        a, grad_out.data_ptr(), _ptr(grad_state), _raw_stream(dev), ws.data_ptr(), n, gq.data_ptr(),
+        gk.data_ptr(), gv.data_ptr(), _ptr(gs), _ptr(word)), word)
     out = {"grad_q": gq, "grad_k": gk, "grad_v": gv}
     if gs is not None:
         out["grad_state"] = gs
@@ -355,21 +370,20 @@ def decay_attention_step(q, k, v, log_decay, state, *, scale=None, slots=None,
     left alone).  Stream b uses row slots[b] (int32; None: row b).  A slot outside [0, pool) is
     idle: its output is 0.  Slots in use must be distinct.  Returns o [B, Hq, Dv]; carries no
     gradient."""
-    if state.dim() != 4:
-        raise ValueError("state must be [pool, Hq, Dk, Dv]")
-    pool = state.shape[0]
-    a = _attention(q, k, v, log_decay, scale, None, state,
-                   (pool, q.shape[-2], q.shape[-1], v.shape[-1]), None)
-    if slots is None:
-        if pool < a.B:
-            raise ValueError(f"a pool of {pool} states for {a.B} streams needs slots")
-    else:
-        _need("slots", slots, torch.int32, (a.B,), q.device)
+    try:
+        pool = state.shape[0]
+    except (AttributeError, IndexError):
+        raise ValueError("state must be [pool, Hq, Dk, Dv]") from None
+    dev, a = _attention(q, k, v, log_decay, scale, None, state, pool, 3)
+    if slots is not None:
+        _need("slots", slots, torch.int32, (a.B,), dev)
+    elif pool < a.B:
+        raise ValueError(f"a pool of {pool} states for {a.B} streams needs slots")
     if state_out is None:
         state_out = state
     else:
-        _need("state_out", state_out, torch.float32, state.shape, q.device)
-    out = torch.empty((a.B, a.Hq, a.Dv), dtype=q.dtype, device=q.device)
-    _native.check("semicrf_decay_attention_step", _native.load().semicrf_decay_attention_step(
-        a, _ptr(slots), pool, _stream(q.device), out.data_ptr(), state_out.data_ptr()))
+        _need("state_out", state_out, torch.float32, state.shape, dev)
+    out = q.new_empty((a.B, a.Hq, a.Dv))
+    _check("semicrf_decay_attention_step", _native.load().semicrf_decay_attention_step(
+        a, _ptr(slots), pool, _raw_stream(dev), out.data_ptr(), state_out.data_ptr()))
     return out
