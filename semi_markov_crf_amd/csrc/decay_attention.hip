@@ -37,6 +37,7 @@ namespace semicrf {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -126,16 +127,29 @@ __device__ __forceinline__ int step_row(int j) {
 template <class T>
 constexpr int lds_pitch(int width) { return width + (sizeof(T) == 4 ? 4 : 16); }
 
-// Parts of an fp32 fragment that add up to it: one in fp32, n in bfloat16 (8 bits each).
+// Parts of an fp32 fragment that add up to it: one in fp32, n in bfloat16 (8 bits each).  Two
+// elements at a time, as the conversion takes them.
 template <class T, int N>
 struct Parts {
     typename Mma<T>::Frag f[N];
-    __device__ __forceinline__ void set(int j, float x) {
+    __device__ __forceinline__ void set(int j, float x, float y) {
+        if constexpr (sizeof(T) == 4) {
+            f[0][j] = x;
+            f[0][j + 1] = y;
+        } else {
+            typedef float f32x2 __attribute__((ext_vector_type(2)));
+            f32x2 r = {x, y};
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const T h = (T)x;
-            f[n][j] = h;
-            x -= (float)h;
+            for (int n = 0; n < N; ++n) {
+                const bf16x2 h = __builtin_convertvector(r, bf16x2);
+                f[n][j] = h[0];
+                f[n][j + 1] = h[1];
+                if (n + 1 < N) {
+                    const uint32_t u = __builtin_bit_cast(uint32_t, h);
+                    r[0] -= __builtin_bit_cast(float, u << 16);
+                    r[1] -= __builtin_bit_cast(float, u & 0xffff0000u);
+                }
+            }
         }
     }
 };
@@ -275,10 +289,10 @@ constexpr int sweep_occupancy() { return P == 128 ? 2 : sizeof(T) == 2 ? 3 : 4; 
 // factor rounded once would bend every old contribution the same way.
 struct Decay {
     float f;
-    bool near1;
+    int near1;               // the same in every lane
     __device__ __forceinline__ void set(float g, int m) {
         f = m == 0 ? 1.0f : expf(g * (float)m);
-        near1 = f > 0.5f;
+        near1 = __builtin_amdgcn_readfirstlane(f > 0.5f);
         if (near1) f = m == 0 ? 0.0f : expm1f(g * (float)m);
     }
 };
@@ -319,13 +333,21 @@ struct State {
                 }
     }
     __device__ __forceinline__ void decay(Decay d) {
+        if (d.near1) {
 #pragma unroll
-        for (int t = 0; t < ST; ++t)
+            for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int v = 0; v < VT; ++v)
+                for (int v = 0; v < VT; ++v)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    s[t][v][r] = d.near1 ? fmaf(s[t][v][r], d.f, s[t][v][r]) : s[t][v][r] * d.f;
+                    for (int r = 0; r < 4; ++r) s[t][v][r] = fmaf(s[t][v][r], d.f, s[t][v][r]);
+        } else {
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int v = 0; v < VT; ++v)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[t][v][r] *= d.f;
+        }
     }
     // S += sum_j w_j b_j c_j^T over one product step from row k0; `c` the columns' fragments
     __device__ __forceinline__ void update(const T* bbuf, int ld, int k0,
@@ -334,7 +356,7 @@ struct State {
 #pragma unroll
         for (int v = 0; v < VT; ++v)
 #pragma unroll
-            for (int j = 0; j < E; ++j) p[v].set(j, (float)c[v][j] * w[j]);
+            for (int j = 0; j < E; j += 2) p[v].set(j, (float)c[v][j] * w[j], (float)c[v][j + 1] * w[j + 1]);
 #pragma unroll
         for (int t = 0; t < ST; ++t) {
             const auto a = frag_col(bbuf, ld, k0, 16 * t);
@@ -589,6 +611,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
     const float g16 = power(g2, 16);
     Update<T, C> up;
     up.set(g, g2, w.su, w.e);
+    wait_loads();
     for (int t0 = t_begin; t0 < t_end; t0 += C) {
         const int m = min(C, t_end - t0);
         __syncthreads();
@@ -606,7 +629,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
 #pragma unroll
         for (int n0 = 0; n0 < IT * (IT + 1) / 2; n0 += NW) {
             const int n = n0 + wave;
-            if (n < IT * (IT + 1) / 2) {
+            if (n0 + NW <= IT * (IT + 1) / 2 || n < IT * (IT + 1) / 2) {
                 const int it = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, jt = n - it * (it + 1) / 2;
                 f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -635,7 +658,8 @@ k_attn_sweep(const Sweeps<N> set, int group) {
 #pragma unroll
             for (int v = 0; v < VT; ++v)
 #pragma unroll
-                for (int j = 0; j < E; ++j) p[v].set(j, S.s[kb * St::TPK + j / 4][v][j % 4]);
+                for (int j = 0; j < E; j += 2)
+                    p[v].set(j, S.s[kb * St::TPK + j / 4][v][j % 4], S.s[kb * St::TPK + j / 4][v][j % 4 + 1]);
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const auto a = frag_ordered<T>(sa, Tl::LD, 16 * it, kb * KS);
@@ -672,6 +696,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
             __builtin_amdgcn_sched_barrier(0);
         }
         const int col = wave * VT * 16 + 4 * gr;
+        wait_loads();
         if (w.out32) store_rows<float, FAST, IT, VT>(w, (float*)w.out + out0, t0, m, L, col, acc);
         else store_rows<T, FAST, IT, VT>(w, (T*)w.out + out0, t0, m, L, col, acc);
     }

@@ -58,6 +58,11 @@ __device__ __forceinline__ void store_piece(T* __restrict__ p, int valid,
     }
 }
 
+// Loads and stores are counted together, in order.  A loop that fetches its next input, then stores
+// its output, would wait at its top for the stores too (the first round has none to allow for).
+// Waiting for the fetch before the loop and before the stores leaves the stores in flight.
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
+
 // A piece as it lies in memory; what is past `valid` elements is zero.
 template <class T>
 __device__ __forceinline__ raw_piece load_raw(const T* __restrict__ p, int valid) {
