@@ -476,15 +476,26 @@ k_attn_state(const Sweeps<N> set, int group) {
 }
 
 // Start of every segment from the segments' own states, in place, in order; the state after
-// the last position to `out`.  grid (ceil(D / 256), H, B), D = Da Dc
-__global__ __launch_bounds__(256) void k_attn_scan(float* local, const float* init, float* out,
-                                                   const int32_t* lengths, const float* log_decay,
-                                                   int T, int H, int seg, int nseg, int D) {
-    const int i = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
+// the last position to `out`.  One or two states: blockIdx.y = state * H + head.
+// grid (ceil(D / 256), states * H, B), D = Da Dc
+struct Scan {
+    float* local[2];
+    const float* init[2];
+    float* out[2];
+    const int32_t* lengths;
+    const float* log_decay;
+    int T, H, seg, nseg, D;
+};
+__global__ __launch_bounds__(256) void k_attn_scan(const Scan a) {
+    const int i = blockIdx.x * 256 + threadIdx.x, which = blockIdx.y / a.H, h = blockIdx.y % a.H, b = blockIdx.z;
+    const int T = a.T, H = a.H, seg = a.seg, nseg = a.nseg, D = a.D;
+    float* const local = a.local[which];
+    const float* const init = a.init[which];
+    float* const out = a.out[which];
     if (i >= D) return;
     const size_t bh = (size_t)b * H + h;
-    const int L = seq_length(lengths, b, T, nullptr);
-    const double g = log_decay[h];
+    const int L = seq_length(a.lengths, b, T, nullptr);
+    const double g = a.log_decay[h];
     float cur = init ? init[bh * D + i] : 0.0f;
     const float full = (float)exp(g * seg);
     float* p = local + bh * nseg * D + i;
@@ -707,17 +718,42 @@ k_attn_sweep(const Sweeps<N> set, int group) {
     }
 }
 
-// out[row, hk, :] = sum over the group's query heads, in order.  One element a thread.
+// Sums over the query heads of a group, in order: out[row, hk, :] = sum of x[row, hk, 0 .. group).
+// blockIdx.y: 0 sums dk, 1 sums dv.  One piece of a row a thread.
+struct GroupSum {
+    const float* x[2];
+    void* out[2];
+    int D[2];
+    long heads;              // rows * Hk
+    int group;
+};
 template <class T>
-__global__ __launch_bounds__(256) void k_attn_group(const float* x, T* out, long n, int group, int D) {
+__global__ __launch_bounds__(256) void k_attn_group(const GroupSum a) {
+    constexpr int V = 4;
+    const int which = blockIdx.y, D = a.D[which], pieces = (D + V - 1) / V;
     const long i = (long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    const long head = i / D;
-    const int j = (int)(i - head * D);
-    const float* p = x + head * group * D + j;
-    float s = 0.0f;
-    for (int q = 0; q < group; ++q) s += p[(long)q * D];
-    out[i] = (T)s;
+    const long head = i / pieces;
+    if (head >= a.heads) return;
+    const int c = (int)(i - head * pieces) * V;
+    const float* p = a.x[which] + head * a.group * D + c;
+    float s[V] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q = 0; q < a.group; ++q) {
+        float x[V];
+        load_piece<float>(p + (long)q * D, D - c, x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] += x[j];
+    }
+    T* out = (T*)a.out[which] + head * D + c;
+    T y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = (T)s[j];
+    if (D - c >= V) {
+        __builtin_memcpy(out, y, sizeof(y));
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (c + j < D) out[j] = y[j];
+    }
 }
 
 // ------------------------------------------------------------------ one token
@@ -785,16 +821,33 @@ int sweep_slots(const semicrf_attention& p) {
     return 256 * (P == 128 ? 1 : P == 64 ? (f32 ? 4 : 3) : (f32 ? 8 : 5));
 }
 
-// Positions per segment: as many segments as fill the device once with all sweeps of the launch,
-// none shorter than 512.
-int segment(const semicrf_attention& p, int sweeps) {
-    const int C = chunk_of(p);
-    long n = sweep_slots(p) / ((long)p.B * p.Hq * sweeps);
-    const long most = p.T / 512;
-    if (n > most) n = most;
-    if (n < 1) n = 1;
-    const long len = (p.T + n - 1) / n;
-    return (int)((len + C - 1) / C * C);
+// Positions per segment.  Segments shorten the chain of chunks that one workgroup takes in order, at
+// the price of the pass over the states, its launches and the join.  The times are modelled in
+// units of one chunk of the sweep where a compute unit has one workgroup (2 us at width 64, 64
+// bfloat16 or 32 fp32 positions); with w workgroups a unit it takes 0.4 + 0.6 w, the state's pass 0.4
+// of that, launches and prologues 6 (9 with gradients), the join 0.06 a segment.  Measured, one
+// segment against the choice: 1 x 3,000 positions, 2 heads, bfloat16 99 and 19 us; 8 x 800, 8 heads 32
+// and 28 us, but its gradients 34 and (4 segments) 46 us: one is kept.
+int segment(const semicrf_attention& p, bool grad) {
+    const int C = chunk_of(p), sweeps = grad ? 3 : 1, states = grad ? 2 : 1, group = p.Hq / p.Hk;
+    const long bh = (long)p.B * p.Hq, n = ((long)p.T + C - 1) / C;
+    // workgroups go to the chiplets in turn: as many units (place()) as run at once on each of them
+    const long most = CHIPLETS * (sweep_slots(p) / CHIPLETS / (group * sweeps)) / ((long)p.B * p.Hk);
+    auto load = [](long workgroups) {
+        const double w = (double)workgroups / 256;
+        return w > 1.0 ? 0.4 + 0.6 * w : 1.0;
+    };
+    long best = 1;
+    double cost = n * load(bh * sweeps);
+    for (long k = 2; k <= most && k <= n; ++k) {
+        const long len = (n + k - 1) / k;
+        const double c = len * (load(bh * k * sweeps) + 0.4 * load(bh * k * states)) + (grad ? 9 : 6) + 0.06 * k;
+        if (c < cost) {
+            cost = c;
+            best = k;
+        }
+    }
+    return (int)((n + best - 1) / best * C);
 }
 
 struct AttnLayout {
@@ -804,7 +857,7 @@ struct AttnLayout {
 
 AttnLayout attn_layout(const semicrf_attention& p, bool grad) {
     AttnLayout l{};
-    l.seg = segment(p, grad ? 3 : 1);
+    l.seg = segment(p, grad);
     l.nseg = (p.T + l.seg - 1) / l.seg;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -905,11 +958,10 @@ hipError_t run_sweep(const semicrf_attention& p, const Sweeps<N>& set, hipStream
     });
 }
 
-hipError_t run_scan(const semicrf_attention& p, const AttnLayout& l, float* local, const float* init,
-                    float* out, hipStream_t stream) {
-    const int D = p.Dk * p.Dv;
-    hipLaunchKernelGGL(k_attn_scan, dim3((D + 255) / 256, p.Hq, p.B), dim3(256), 0, stream, local, init,
-                       out, p.lengths, p.log_decay, p.T, p.Hq, l.seg, l.nseg, D);
+hipError_t run_scan(const semicrf_attention& p, const AttnLayout& l, Scan s, int states, hipStream_t stream) {
+    s.lengths = p.lengths; s.log_decay = p.log_decay;
+    s.T = p.T; s.H = p.Hq; s.seg = l.seg; s.nseg = l.nseg; s.D = p.Dk * p.Dv;
+    hipLaunchKernelGGL(k_attn_scan, dim3((s.D + 255) / 256, states * p.Hq, p.B), dim3(256), 0, stream, s);
     return hipGetLastError();
 }
 
@@ -939,7 +991,7 @@ hipError_t launch_decay_attention(const AttnArgs& a, void* ws, hipStream_t strea
     if (l.nseg > 1) {
         w.local = (float*)((char*)ws + l.S);
         TRY(run_state(p, Sweeps<1>{{w}}, stream));
-        TRY(run_scan(p, l, w.local, p.state, a.state_out, stream));
+        TRY(run_scan(p, l, Scan{{w.local}, {p.state}, {a.state_out}}, 1, stream));
         w.state = w.local;
         w.state_nseg = l.nseg;
     } else {
@@ -968,8 +1020,7 @@ hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t 
         f.b = k; f.c = v; f.Da = p.Dk; f.Dc = p.Dv; f.local = S;
         r.b = q; r.c = g; r.Da = p.Dk; r.Dc = p.Dv; r.local = R;
         TRY(run_state(p, Sweeps<2>{{f, r}}, stream));
-        TRY(run_scan(p, l, S, p.state, nullptr, stream));
-        TRY(run_scan(p, l, R, a.grad_state_out, a.grad_state, stream));
+        TRY(run_scan(p, l, Scan{{S, R}, {p.state, a.grad_state_out}, {nullptr, a.grad_state}}, 2, stream));
         f.state = S;
         r.state = R;
     }
@@ -988,20 +1039,13 @@ hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t 
     r.state_out = nullptr;
     TRY(run_sweep(p, Sweeps<3>{{dv, r, f}}, stream));
     if (group > 1) {
-        const long rows = (long)p.B * p.T * p.Hk;
-        auto sum = [&](const float* x, void* out, int D) {
-            const long n = rows * D;
-            const dim3 grid((unsigned)((n + 255) / 256));
-            if (p.dtype == SEMICRF_F32)
-                hipLaunchKernelGGL((k_attn_group<float>), grid, dim3(256), 0, stream, x, (float*)out, n,
-                                   group, D);
-            else
-                hipLaunchKernelGGL((k_attn_group<bf16>), grid, dim3(256), 0, stream, x, (bf16*)out, n,
-                                   group, D);
-            return hipGetLastError();
-        };
-        TRY(sum((const float*)((char*)ws + l.gk), a.grad_k, p.Dk));
-        TRY(sum((const float*)((char*)ws + l.gv), a.grad_v, p.Dv));
+        GroupSum s{{(const float*)((char*)ws + l.gk), (const float*)((char*)ws + l.gv)},
+                   {a.grad_k, a.grad_v}, {p.Dk, p.Dv}, (long)p.B * p.T * p.Hk, group};
+        const long n = s.heads * (((p.Dk > p.Dv ? p.Dk : p.Dv) + 3) / 4);
+        const dim3 grid((unsigned)((n + 255) / 256), 2);
+        if (p.dtype == SEMICRF_F32) hipLaunchKernelGGL((k_attn_group<float>), grid, dim3(256), 0, stream, s);
+        else hipLaunchKernelGGL((k_attn_group<bf16>), grid, dim3(256), 0, stream, s);
+        TRY(hipGetLastError());
     }
     return hipSuccess;
 }

@@ -45,7 +45,7 @@ int check_shape(const semicrf_attention* p) {
         return SEMICRF_ERR_INVALID;
     const int rc = check_rows(p->B, p->T, 1);
     if (rc) return rc;
-    if (p->Dk > ATTN_MAX_D || p->Dv > ATTN_MAX_D || p->B >= 65536 || p->Hq >= 65536)
+    if (p->Dk > ATTN_MAX_D || p->Dv > ATTN_MAX_D || p->B >= 65536 || p->Hq >= 32768)
         return SEMICRF_ERR_UNSUPPORTED;
     return SEMICRF_OK;
 }
