@@ -297,6 +297,13 @@ struct Decay {
     }
 };
 
+// With e = 1 every weight of the update has a factor gamma.  A power of two near 1 / gamma, at most
+// 2^60, is kept in the state while it lies in registers, so that the low parts of c times its
+// weight do not underflow.
+__device__ __forceinline__ float state_scale(float g2, int e) {
+    return e ? __builtin_amdgcn_exp2f(fminf(60.0f, fmaxf(-60.0f, rintf(-g2)))) : 1.0f;
+}
+
 // State tiles of a wavefront: all rows, its own columns.
 template <class T, int P>
 struct State {
@@ -310,7 +317,7 @@ struct State {
     __device__ __forceinline__ int row(int t, int r) const {
         return 16 * t + 4 * ((threadIdx.x & 63) >> 4) + r;
     }
-    __device__ __forceinline__ void load(const float* p, int Da, int Dc, bool transposed) {
+    __device__ __forceinline__ void load(const float* p, int Da, int Dc, bool transposed, float scale) {
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -318,10 +325,10 @@ struct State {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = row(t, r), j = col(v);
-                    s[t][v][r] = p && i < Da && j < Dc ? p[transposed ? j * Da + i : i * Dc + j] : 0.0f;
+                    s[t][v][r] = p && i < Da && j < Dc ? p[transposed ? j * Da + i : i * Dc + j] * scale : 0.0f;
                 }
     }
-    __device__ __forceinline__ void store(float* p, int Da, int Dc, bool transposed) const {
+    __device__ __forceinline__ void store(float* p, int Da, int Dc, bool transposed, float scale) const {
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -329,7 +336,7 @@ struct State {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = row(t, r), j = col(v);
-                    if (i < Da && j < Dc) p[transposed ? j * Da + i : i * Dc + j] = s[t][v][r];
+                    if (i < Da && j < Dc) p[transposed ? j * Da + i : i * Dc + j] = s[t][v][r] * scale;
                 }
     }
     __device__ __forceinline__ void decay(Decay d) {
@@ -436,16 +443,16 @@ k_attn_state(const Sweeps<N> set, int group) {
     const int seg = at.seg, h = at.h, b = at.b;
     const int L = __builtin_amdgcn_readfirstlane(seq_length(w.lengths, b, w.T, w.status));
     const int t_begin = seg * w.seg, t_end = min(L, t_begin + w.seg);
-    const float g = w.log_decay[h], g2 = g * (float)LOG2E;
+    const float g = w.log_decay[h], g2 = g * (float)LOG2E, sigma = state_scale(g2, w.e), su = w.su * sigma;
     const T* pb = role_base<T>(w.b, b, h);
     const T* pc = role_base<T>(w.c, b, h);
     Tl tb, tc;
     tb.load(w.b, pb, w.Da, t_begin, min(C, t_end - t_begin), L, w.reverse);
     tc.load(w.c, pc, w.Dc, t_begin, min(C, t_end - t_begin), L, w.reverse);
     St S;
-    S.load(nullptr, 0, 0, false);
+    S.load(nullptr, 0, 0, false, 1.0f);
     Update<T, C> up;
-    up.set(g, g2, w.su, w.e);
+    up.set(g, g2, su, w.e);
     for (int t0 = t_begin; t0 < t_end; t0 += C) {
         const int m = min(C, t_end - t0);
         __syncthreads();
@@ -471,8 +478,8 @@ k_attn_state(const Sweeps<N> set, int group) {
         }
     }
     if (t_end > t_begin && (t_end - t_begin) % C)
-        update_rest<T, P, C>(S, sb, sc, (t_end - t_begin) % C, g, g2, w.su, w.e);
-    S.store(w.local + (((size_t)b * w.H + h) * w.nseg + seg) * w.Da * w.Dc, w.Da, w.Dc, false);
+        update_rest<T, P, C>(S, sb, sc, (t_end - t_begin) % C, g, g2, su, w.e);
+    S.store(w.local + (((size_t)b * w.H + h) * w.nseg + seg) * w.Da * w.Dc, w.Da, w.Dc, false, 1.0f / sigma);
 }
 
 // Start of every segment from the segments' own states, in place, in order; the state after
@@ -582,7 +589,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
     const int gr = lane >> 4, r16 = lane & 15;
     const int L = __builtin_amdgcn_readfirstlane(seq_length(w.lengths, b, w.T, w.status));
     const int t_begin = seg * w.seg, t_last = min(w.T, t_begin + w.seg), t_end = min(L, t_last);
-    const float g = w.log_decay[h], g2 = g * (float)LOG2E;
+    const float g = w.log_decay[h], g2 = g * (float)LOG2E, sigma = state_scale(g2, w.e), su = w.su * sigma;
     const size_t bh = (size_t)b * w.H + h;
     const size_t D = (size_t)w.Da * w.Dc;
     const size_t out0 = (size_t)b * w.T * w.H * w.Dc + (size_t)h * w.Dc;
@@ -605,7 +612,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
         }
     St S;
     S.load(w.state ? w.state + (bh * w.state_nseg + (w.state_nseg > 1 ? seg : 0)) * D : nullptr, w.Da,
-           w.Dc, w.transposed);
+           w.Dc, w.transposed, sigma);
     // masked products above the diagonal stay zero
     for (int i = threadIdx.x; i < C * LDM; i += NT) sm[i] = (T)0.0f;
     // scale gamma^(i-j) in a tile of products (rows j = 4 gr + r, column i = r16): on the
@@ -618,10 +625,10 @@ k_attn_sweep(const Sweeps<N> set, int group) {
         below[r] = w.scale * power(g2, 16 + d);
     }
 #pragma unroll
-    for (int it = 0; it < IT; ++it) inter[it] = w.si * power(g2, 16 * it + r16 + 1 - w.e);
+    for (int it = 0; it < IT; ++it) inter[it] = w.si / sigma * power(g2, 16 * it + r16 + 1 - w.e);
     const float g16 = power(g2, 16);
     Update<T, C> up;
-    up.set(g, g2, w.su, w.e);
+    up.set(g, g2, su, w.e);
     wait_loads();
     for (int t0 = t_begin; t0 < t_end; t0 += C) {
         const int m = min(C, t_end - t0);
@@ -713,8 +720,8 @@ k_attn_sweep(const Sweeps<N> set, int group) {
     }
     if (w.state_out) {
         if (t_end > t_begin && (t_end - t_begin) % C)
-            update_rest<T, P, C>(S, sb, sc, (t_end - t_begin) % C, g, g2, w.su, w.e);
-        S.store(w.state_out + bh * D, w.Da, w.Dc, w.transposed);
+            update_rest<T, P, C>(S, sb, sc, (t_end - t_begin) % C, g, g2, su, w.e);
+        S.store(w.state_out + bh * D, w.Da, w.Dc, w.transposed, 1.0f / sigma);
     }
 }
 
