@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
 //
 // counts says how many items of each tile have each digit of the pass; the first pass counts in
 // k_grad_begin.
-// Up to 64 tiles every scatter workgroup adds the counts up by itself and they lie tile by tile;
+// In tiles, beyond what one workgroup sorts.  Up to 64 tiles every scatter workgroup adds the counts up by itself and they lie tile by tile;
 // beyond, k_sort_scan does it once, digit by digit.
 constexpr int BINS = 256, SCAN_TILES = 64, TILE = 1024, SORT_NT = 256, PER = TILE / SORT_NT;
 
@@ -136,18 +136,20 @@ __global__ __launch_bounds__(256) void k_sort_count(const SortArgs s) {
     count_tile(key, from, s.n, s.shift, s.counts + (size_t)threadIdx.x * s.by_digit + (size_t)blockIdx.x * s.by_tile);
 }
 
-// Workgroups 0 .. ntiles - 1 count the first digit of a tile; the others clear the gradient's
-// `bytes` (rows of tokens that do not appear stay 0).
+// Clears `bytes` of the gradient (rows of tokens that do not appear stay 0): workgroup `block` of
+// `blocks`.
+__device__ __forceinline__ void clear_share(void* p, size_t bytes, int block, int blocks) {
+    char* out = (char*)p;
+    const size_t pieces = bytes / 16, step = (size_t)blocks * blockDim.x;
+    const raw_piece zero = {0, 0, 0, 0};
+    const size_t first = (size_t)block * blockDim.x + threadIdx.x;
+    for (size_t i = first; i < pieces; i += step) *(loose_piece*)(out + i * 16) = zero;
+    if (first < bytes - pieces * 16) out[pieces * 16 + first] = 0;
+}
+
+// Workgroups 0 .. ntiles - 1 count the first digit of a tile; the others clear the gradient.
 __global__ __launch_bounds__(256) void k_grad_begin(const EmbedArgs a, const SortArgs s, size_t bytes) {
-    if (blockIdx.x >= (unsigned)s.ntiles) {
-        char* out = (char*)a.out;
-        const size_t pieces = bytes / 16, step = (size_t)(gridDim.x - s.ntiles) * 256;
-        const raw_piece zero = {0, 0, 0, 0};
-        const size_t first = (size_t)(blockIdx.x - s.ntiles) * 256 + threadIdx.x;
-        for (size_t i = first; i < pieces; i += step) *(loose_piece*)(out + i * 16) = zero;
-        if (first < bytes - pieces * 16) out[pieces * 16 + first] = 0;
-        return;
-    }
+    if (blockIdx.x >= (unsigned)s.ntiles) return clear_share(a.out, bytes, blockIdx.x - s.ntiles, gridDim.x - s.ntiles);
     uint32_t key[PER];
     unsigned from[PER];
 #pragma unroll
@@ -156,6 +158,114 @@ __global__ __launch_bounds__(256) void k_grad_begin(const EmbedArgs a, const Sor
 #pragma unroll
     for (int p = 0; p < PER; ++p) key[p] = min(key[p], (uint32_t)a.V);
     count_tile(key, from, s.n, 0, s.counts + (size_t)threadIdx.x * s.by_digit + (size_t)blockIdx.x * s.by_tile);
+}
+
+// Ranks of a wavefront's items among its items of the same digit, 64 at a time: the lanes with the
+// same digit find each other with one ballot a bit, the lowest of them takes their places from
+// the wavefront's running count `run` [BINS].
+template <int N>
+__device__ __forceinline__ void rank_items(const uint32_t (&key)[N], const bool (&live)[N], int shift, int* run,
+                                           int (&rank)[N]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        const uint32_t d = (key[p] >> shift) & (BINS - 1);
+        uint64_t same = __ballot(live[p]);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            const bool bit = (d >> b) & 1;
+            const uint64_t m = __ballot(bit);
+            same &= bit ? m : ~m;
+        }
+        const int before = __popcll(same & ((1ull << lane) - 1));
+        int start = 0;
+        if (live[p]) start = run[d];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (live[p] && before == 0) run[d] = start + __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        rank[p] = start + before;
+    }
+}
+
+// Up to 4,096 positions: workgroup 0 sorts them all in LDS, a pass after the other, while the others
+// clear the gradient (310 positions, two digits: 12.5 us in one launch against 15.3 in four; 16,384 this way
+// would take 37 us against 28, its LDS keeping the clearing workgroups out).
+constexpr int ONE_NT = 1024, ONE_N = 4, ONE_MAX = ONE_N * ONE_NT;
+template <int N>
+__global__ __launch_bounds__(ONE_NT) void k_grad_sort_one(const EmbedArgs a, int n, int passes, uint32_t* keys_out,
+                                                          int* pos_out, size_t bytes) {
+    if (blockIdx.x > 0) return clear_share(a.out, bytes, blockIdx.x - 1, gridDim.x - 1);
+    constexpr int NW = ONE_NT / 64;
+    __shared__ uint32_t keys[N * ONE_NT];
+    __shared__ int pos[N * ONE_NT];
+    __shared__ int run[NW][BINS];
+    __shared__ int wsum[4];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    uint32_t key[N];
+    unsigned from[N];
+    bool live[N];
+    int rank[N];
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        from[p] = w * N * 64 + p * 64 + lane;
+        live[p] = from[p] < (unsigned)n;
+    }
+    load_keys<N>(a, from, n, key);
+#pragma unroll
+    for (int p = 0; p < N; ++p) key[p] = min(key[p], (uint32_t)a.V);
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = 8 * pass;
+        for (int i = tid; i < NW * BINS; i += ONE_NT) (&run[0][0])[i] = 0;
+        __syncthreads();
+        rank_items<N>(key, live, shift, run[w], rank);
+        __syncthreads();
+        // start of each digit, then of each wavefront's share of it
+        int total = 0, sum = 0;
+        if (tid < BINS) {
+            for (int i = 0; i < NW; ++i) total += run[i][tid];
+            sum = total;
+            for (int off = 1; off < 64; off <<= 1) {
+                const int t = __shfl_up(sum, off, 64);
+                if (lane >= off) sum += t;
+            }
+            if (lane == 63) wsum[w] = sum;
+        }
+        __syncthreads();
+        if (tid < BINS) {
+            int at = sum - total;
+            for (int i = 0; i < w; ++i) at += wsum[i];
+            for (int i = 0; i < NW; ++i) {
+                const int v = run[i][tid];
+                run[i][tid] = at;
+                at += v;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < N; ++p)
+            if (live[p]) {
+                const int to = run[w][(key[p] >> shift) & (BINS - 1)] + rank[p];
+                keys[to] = key[p];
+                pos[to] = (int)from[p];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+            const int i = w * N * 64 + p * 64 + lane;
+            if (live[p]) {
+                key[p] = keys[i];
+                from[p] = pos[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        const int i = w * N * 64 + p * 64 + lane;
+        if (live[p]) {
+            keys_out[i] = key[p];
+            pos_out[i] = (int)from[p];
+        }
+    }
 }
 
 // exclusive scan of one digit's counts over the tiles; totals [BINS].  grid BINS, block 256
@@ -183,9 +293,7 @@ __global__ __launch_bounds__(256) void k_sort_scan(int* counts, int ntiles, int*
     if (threadIdx.x == 0) totals[blockIdx.x] = carry;
 }
 
-// Stable scatter of one tile.  A wavefront takes PER * 64 consecutive items, 64 at a time: the
-// lanes with the same digit find each other with one ballot a bit, the lowest of them takes
-// their places from the wavefront's running count.
+// Stable scatter of one tile.  A wavefront takes PER * 64 consecutive items.
 __global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, const SortArgs s) {
     __shared__ int run[SORT_NT / 64][BINS];
     __shared__ int wsum[4];
@@ -196,8 +304,12 @@ __global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, con
     uint32_t key[PER];
     unsigned from[PER];
     int rank[PER];
+    bool live[PER];
 #pragma unroll
-    for (int p = 0; p < PER; ++p) from[p] = base + p * 64 + lane;
+    for (int p = 0; p < PER; ++p) {
+        from[p] = base + p * 64 + lane;
+        live[p] = from[p] < (unsigned)n;
+    }
     if (s.keys) {
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
@@ -228,25 +340,7 @@ __global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, con
             }
         }
     }
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-        const int i = base + p * 64 + lane;
-        const uint32_t d = (key[p] >> s.shift) & (BINS - 1);
-        uint64_t same = __ballot(i < n);
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            const bool bit = (d >> b) & 1;
-            const uint64_t m = __ballot(bit);
-            same &= bit ? m : ~m;
-        }
-        const int before = __popcll(same & ((1ull << lane) - 1));
-        int start = 0;
-        if (i < n) start = run[w][d];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (i < n && before == 0) run[w][d] = start + __popcll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        rank[p] = start + before;
-    }
+    rank_items<PER>(key, live, s.shift, run[w], rank);
     // digit start = items of smaller digits + this digit's items in earlier tiles, wavefronts
     int sum = total;
     for (int off = 1; off < 64; off <<= 1) {
@@ -265,8 +359,7 @@ __global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, con
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-        const int i = base + p * 64 + lane;
-        if (i < n) {
+        if (live[p]) {
             const int to = run[w][(key[p] >> s.shift) & (BINS - 1)] + rank[p];
             s.keys_out[to] = key[p];
             s.pos_out[to] = from[p];
@@ -421,7 +514,7 @@ GradLayout grad_layout(int B, int T, int V, int N, int es) {
     // rows per chunk: about 2,048 wavefronts over the chunks and column slabs fill the device; longer
     // chunks leave fewer partial rows
     const long slabs = ((long)N * es + 1023) / 1024;
-    l.R = 16;
+    l.R = 8;
     while (l.R < 256 && l.n * slabs / l.R > 2048) l.R *= 2;
     l.nchunks = (l.n + l.R - 1) / l.R;
     size_t off = 0;
@@ -460,7 +553,9 @@ hipError_t run_embed(const EmbedArgs& a, hipStream_t stream) {
         return hipGetLastError();
     };
     if (np <= 4) return go(std::integral_constant<int, 4>());
+    if (np <= 8) return go(std::integral_constant<int, 8>());
     if (np <= 16) return go(std::integral_constant<int, 16>());
+    if (np <= 32) return go(std::integral_constant<int, 32>());
     return go(std::integral_constant<int, 64>());
 }
 
@@ -477,21 +572,32 @@ hipError_t run_embed_grad(const EmbedArgs& a, char* ws, hipStream_t stream) {
     s.by_digit = scan ? l.ntiles : 1;
     s.by_tile = scan ? 1 : BINS;
     const size_t fill = bytes / (256 * 64) + 1;    // four pieces a thread, up to 4,096 workgroups
-    hipLaunchKernelGGL(k_grad_begin, dim3(l.ntiles + (unsigned)(fill < 4096 ? fill : 4096)), dim3(256), 0,
-                       stream, a, s, bytes);
-    for (int p = 0; p < l.passes; ++p) {
-        s.shift = 8 * p;
-        if (p > 0) hipLaunchKernelGGL(k_sort_count, dim3(l.ntiles), dim3(256), 0, stream, s);
-        if (scan) {
-            s.totals = (const int*)(ws + l.totals);
-            hipLaunchKernelGGL(k_sort_scan, dim3(BINS), dim3(256), 0, stream, s.counts, l.ntiles,
-                               (int*)(ws + l.totals));
-        }
-        s.keys_out = (uint32_t*)(ws + l.key[p & 1]);
-        s.pos_out = (int*)(ws + l.pos[p & 1]);
-        hipLaunchKernelGGL(k_sort_scatter, dim3(l.ntiles), dim3(SORT_NT), 0, stream, a, s);
+    if (l.n <= ONE_MAX) {
+        s.keys_out = (uint32_t*)(ws + l.key[0]);
+        s.pos_out = (int*)(ws + l.pos[0]);
+        const size_t share = bytes / (ONE_NT * 64) + 1;
+        const dim3 grid(1 + (unsigned)(share < 1024 ? share : 1024)), block(ONE_NT);
+        hipLaunchKernelGGL((k_grad_sort_one<ONE_N>), grid, block, 0, stream, a, l.n, l.passes, s.keys_out,
+                           s.pos_out, bytes);
         s.keys = s.keys_out;
         s.pos = s.pos_out;
+    } else {
+        hipLaunchKernelGGL(k_grad_begin, dim3(l.ntiles + (unsigned)(fill < 4096 ? fill : 4096)), dim3(256), 0,
+                           stream, a, s, bytes);
+        for (int p = 0; p < l.passes; ++p) {
+            s.shift = 8 * p;
+            if (p > 0) hipLaunchKernelGGL(k_sort_count, dim3(l.ntiles), dim3(256), 0, stream, s);
+            if (scan) {
+                s.totals = (const int*)(ws + l.totals);
+                hipLaunchKernelGGL(k_sort_scan, dim3(BINS), dim3(256), 0, stream, s.counts, l.ntiles,
+                                   (int*)(ws + l.totals));
+            }
+            s.keys_out = (uint32_t*)(ws + l.key[p & 1]);
+            s.pos_out = (int*)(ws + l.pos[p & 1]);
+            hipLaunchKernelGGL(k_sort_scatter, dim3(l.ntiles), dim3(SORT_NT), 0, stream, a, s);
+            s.keys = s.keys_out;
+            s.pos = s.pos_out;
+        }
     }
     float* part = (float*)(ws + l.part);
     hipLaunchKernelGGL((k_grad_chunks<T>), dim3((l.nchunks + 3) / 4, (a.N + 64 * V - 1) / (64 * V)),
