@@ -94,6 +94,7 @@ EMBED = [  # B, T, V, N, typ, token type, lengths
     (2, 20000, 6, 16, "bf16", np.int32, "ragged"),     # runs over hundreds of chunks
     (3, 4100, 2, 70, "f32", np.int32, "ragged"),
     (1, 40, 4, 1030, "bf16", np.int32, "full"),
+    (2, 40000, 300, 9, "f32", np.int32, "ragged"),     # counts scanned by a launch of their own
 ]
 
 
