@@ -222,7 +222,7 @@ __device__ __forceinline__ float power(float g2, int n) {
 //   Otherwise element by element.
 template <class T, int P, int C, int NT, bool FAST>
 struct Tile {
-    static constexpr int V = Piece<T>::V, PPR = P / V, LD = lds_pitch<T>(P), RPS = NT / PPR;
+    static constexpr int V = 16 / sizeof(T), PPR = P / V, LD = lds_pitch<T>(P), RPS = NT / PPR;
     static constexpr int NP = C / RPS;
     static_assert(NT % PPR == 0 && C % RPS == 0, "pieces per thread");
     u32x4 x[NP];
@@ -746,7 +746,7 @@ __global__ __launch_bounds__(256) void k_attn_group(const GroupSum a) {
     float s[V] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int q = 0; q < a.group; ++q) {
         float x[V];
-        load_piece<float>(p + (long)q * D, D - c, x);
+        load_elements<float>(p + (long)q * D, 0, D - c, x);
 #pragma unroll
         for (int j = 0; j < V; ++j) s[j] += x[j];
     }
@@ -794,14 +794,14 @@ __global__ __launch_bounds__(256) void k_attn_step(const semicrf_attention p, co
     const size_t base = ((size_t)slot * p.Hq + h) * Dk * Dv;
     for (int r = grp; r < Dk; r += ng) {
         float s[4];
-        load_piece<float>(p.state + base + (size_t)r * Dv + c, Dv - c, s);
+        load_elements<float>(p.state + base + (size_t)r * Dv, c, Dv, s);
         const float kr = sk[r], qr = sq[r];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             s[i] = fmaf(s[i], gamma, kr * vv[i]);
             acc[i] = fmaf(qr, s[i], acc[i]);
         }
-        store_piece<float>(state_out + base + (size_t)r * Dv + c, Dv - c, s);
+        store_elements(state_out + base + (size_t)r * Dv, c, Dv, s);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[tid * 4 + i] = acc[i];

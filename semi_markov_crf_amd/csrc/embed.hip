@@ -57,9 +57,10 @@ __device__ __forceinline__ void load_keys(const EmbedArgs& a, const unsigned (&a
 }
 
 // G lanes a row, U rows a lane group, a group's rows 256 / G apart.
-template <class T, int G, int U, bool STREAM>
+template <class T, int G, int U, bool STREAM, bool NARROW>
 __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
-    constexpr int V = Piece<T>::V, RPB = 256 / G;
+    using Pc = Piece<T, NARROW>;
+    constexpr int V = Pc::V, RPB = 256 / G;
     const int N = a.N, lane = threadIdx.x % G;
     const unsigned n = (unsigned)a.B * a.T;
     const unsigned i0 = blockIdx.x * RPB * U + threadIdx.x / G;
@@ -68,12 +69,13 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) at[u] = i0 + u * RPB;
     load_keys<U>(a, at, n, key);
-    for (int c = lane * V; c < N; c += G * V) {
+    for (int i = lane; i * V < N; i += G) {
+        const Pc pc(i, N);
         raw_piece x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool known = key[u] < (uint32_t)a.V;
-            x[u] = load_raw<T>((const T*)a.table + (size_t)(known ? key[u] : 0) * N + c, known ? N - c : 0);
+            x[u] = load_raw((const T*)a.table + (size_t)(known ? key[u] : 0) * N, pc, N);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -83,7 +85,7 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
             unpack<T>(x[u], y);
 #pragma unroll
             for (int j = 0; j < V; ++j) y[j] = key[u] < (uint32_t)a.V ? y[j] * a.scale : fill;
-            store_piece<T, STREAM>((T*)a.out + (size_t)at[u] * N + c, N - c, y);
+            store_piece<T, STREAM>((T*)a.out + (size_t)at[u] * N, pc, N, y);
         }
     }
 }
@@ -368,21 +370,23 @@ __global__ __launch_bounds__(SORT_NT) void k_sort_scatter(const EmbedArgs a, con
 }
 
 // ------------------------------------------------------------------ sums over runs
-// One wavefront adds the rows of one chunk over 64 pieces of columns, U rows on their way at a
-// time.  Partial rows: part[chunk][0] = the run that comes from the chunk before,
+// G lanes add the rows of one chunk over G pieces of columns, U rows on their way at a time; G is 64
+// but for narrow rows.  Partial rows: part[chunk][0] = the run that comes from the chunk before,
 // part[chunk][1] = the run that starts here and goes on.
-// grid (ceil(nchunks / 4), column slabs), block 256
-template <class T>
+// grid (ceil(nchunks / (256 / G)), column slabs), block 256
+template <class T, int G, bool NARROW>
 __global__ __launch_bounds__(256) void k_grad_chunks(const EmbedArgs a, const uint32_t* keys,
                                                      const int* pos, int n, int R, int nchunks,
                                                      float* part) {
-    constexpr int V = Piece<T>::V, U = 8;
-    const int N = a.N, lane = threadIdx.x & 63;
-    const int chunk = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+    using Pc = Piece<T, NARROW>;
+    constexpr int V = Pc::V, U = 8;
+    const int N = a.N, lane = threadIdx.x & (G - 1);
+    int chunk = blockIdx.x * (256 / G) + threadIdx.x / G;
+    if constexpr (G == 64) chunk = __builtin_amdgcn_readfirstlane(chunk);
     if (chunk >= nchunks) return;
-    const int c = (blockIdx.y * 64 + lane) * V;
+    const Pc pc(blockIdx.y * G + lane, N);
     const int r0 = chunk * R, r1 = min(n, r0 + R);
-    const T* g = (const T*)a.grad_out + c;
+    const T* g = (const T*)a.grad_out;
     const uint32_t key_before = r0 > 0 ? keys[r0 - 1] : ~0u, key_after = r1 < n ? keys[r1] : ~0u;
     float acc[V];
 #pragma unroll
@@ -392,42 +396,44 @@ __global__ __launch_bounds__(256) void k_grad_chunks(const EmbedArgs a, const ui
     bool from_before = key_before == cur;
     auto flush = [&](bool goes_on) {
         if (from_before || goes_on) {
-            float* p = part + ((size_t)chunk * 2 + (from_before ? 0 : 1)) * N + c;
-#pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                const float x[4] = {acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-                store_piece<float>(p + i, N - c - i, x);
-            }
+            if (pc.skip < V) store_elements(part + ((size_t)chunk * 2 + (from_before ? 0 : 1)) * N, pc.at, N, acc);
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] *= a.scale;
-            store_piece<T>((T*)a.out + (size_t)cur * N + c, N - c, acc);
+            store_piece<T>((T*)a.out + (size_t)cur * N, pc, N, acc);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
         from_before = false;
     };
-    for (int b0 = r0; b0 < r1; b0 += 64) {
+    for (int b0 = r0; b0 < r1; b0 += G) {
         // every lane keeps one row's key and position; row r of the block is read from lane r
-        const int m = min(r1 - b0, 64);
+        const int m = min(r1 - b0, G);
         const uint32_t my_key = lane < m ? keys[b0 + lane] : (uint32_t)a.V;
         const int my_pos = lane < m ? pos[b0 + lane] : 0;
-        const int live = __popcll(__ballot(my_key < (uint32_t)a.V));
-        auto row_of = [&](int r) {
-            return load_raw<T>(g + (size_t)(unsigned)__builtin_amdgcn_readlane(my_pos, r) * N, N - c);
+        const uint64_t mask = __ballot(my_key < (uint32_t)a.V);
+        const int live = G == 64 ? __popcll(mask)
+                                 : __popcll((mask >> (threadIdx.x & 63 & ~(G - 1))) & ((1ull << (G & 63)) - 1));
+        auto from_lane = [&](int v, int r) {
+            return G == 64 ? __builtin_amdgcn_readlane(v, r) : __shfl(v, r & (G - 1), G);
         };
         raw_piece x[U], y[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (u < live) x[u] = row_of(u);
+        for (int u = 0; u < U; ++u) {
+            const T* row = g + (size_t)(unsigned)from_lane(my_pos, u) * N;
+            if (u < live) x[u] = load_raw(row, pc, N);
+        }
         for (int r = 0; r < live; r += U) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r + U + u < live) y[u] = row_of(r + U + u);
+            for (int u = 0; u < U; ++u) {
+                const int q = r + U + u;
+                const T* row = g + (size_t)(unsigned)from_lane(my_pos, q & (G - 1)) * N;
+                if (q < live) y[u] = load_raw(row, pc, N);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                const uint32_t key = (uint32_t)from_lane((int)my_key, (r + u) & (G - 1));
                 if (r + u < live) {
-                    const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)my_key, r + u);
                     if (key != cur) {
                         flush(false);
                         cur = key;
@@ -473,13 +479,13 @@ __global__ __launch_bounds__(512) void k_grad_join(const EmbedArgs a, const uint
     const int per = (m + GR - 1) / GR;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < N) {
-        if (grp == 0) load_piece<float>(part + ((size_t)chunk * 2 + 1) * N + c, N - c, v);
+        if (grp == 0) load_elements(part + ((size_t)chunk * 2 + 1) * N, c, N, v);
         const int q1 = min(m, (grp + 1) * per);
-        const float* p = part + (size_t)(chunk + 1) * 2 * N + c;
+        const float* p = part + (size_t)(chunk + 1) * 2 * N;
         for (int q = grp * per; q < q1; q += U) {
             float x[U][4];
 #pragma unroll
-            for (int u = 0; u < U; ++u) load_piece<float>(p + (size_t)(q + u) * 2 * N, q + u < q1 ? N - c : 0, x[u]);
+            for (int u = 0; u < U; ++u) load_elements(p + (size_t)(q + u) * 2 * N, c, q + u < q1 ? N : 0, x[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -512,10 +518,10 @@ GradLayout grad_layout(int B, int T, int V, int N, int es) {
     while (((long)V >> bits) != 0) ++bits;
     l.passes = (bits + 7) / 8;
     // rows per chunk: about 2,048 wavefronts over the chunks and column slabs fill the device; longer
-    // chunks leave fewer partial rows
-    const long slabs = ((long)N * es + 1023) / 1024;
+    // chunks leave fewer partial rows.  A narrow row takes a part of a wavefront.
+    const long np = ((long)N * es + 15) / 16, G = np <= 8 ? 8 : np <= 16 ? 16 : np <= 32 ? 32 : 64;
     l.R = 8;
-    while (l.R < 256 && l.n * slabs / l.R > 2048) l.R *= 2;
+    while (l.R < 256 && l.n * ((np + G - 1) / G) * G / 64 / l.R > 2048) l.R *= 2;
     l.nchunks = (l.n + l.R - 1) / l.R;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -536,7 +542,7 @@ GradLayout grad_layout(int B, int T, int V, int N, int es) {
 
 template <class T>
 hipError_t run_embed(const EmbedArgs& a, hipStream_t stream) {
-    constexpr int V = Piece<T>::V;
+    constexpr int V = 16 / sizeof(T);
     const long n = (long)a.B * a.T;
     const int np = (a.N + V - 1) / V;
     // Outputs past the memory-side cache (256 MB) are written as a stream: what reads them finds
@@ -548,8 +554,9 @@ hipError_t run_embed(const EmbedArgs& a, hipStream_t stream) {
         constexpr int G = decltype(g)::value, U = 2;
         const long per = (256 / G) * U;
         const dim3 grid((unsigned)((n + per - 1) / per)), block(256);
-        if (stream_out) hipLaunchKernelGGL((k_embed<T, G, U, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((k_embed<T, G, U, false>), grid, block, 0, stream, a);
+        if (a.N < V) hipLaunchKernelGGL((k_embed<T, 4, U, false, true>), grid, block, 0, stream, a);
+        else if (stream_out) hipLaunchKernelGGL((k_embed<T, G, U, true, false>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((k_embed<T, G, U, false, false>), grid, block, 0, stream, a);
         return hipGetLastError();
     };
     if (np <= 4) return go(std::integral_constant<int, 4>());
@@ -561,7 +568,7 @@ hipError_t run_embed(const EmbedArgs& a, hipStream_t stream) {
 
 template <class T>
 hipError_t run_embed_grad(const EmbedArgs& a, char* ws, hipStream_t stream) {
-    constexpr int V = Piece<T>::V;
+    constexpr int V = 16 / sizeof(T);
     const GradLayout l = grad_layout(a.B, a.T, a.V, a.N, sizeof(T));
     const size_t bytes = (size_t)a.V * a.N * sizeof(T);
     SortArgs s{};
@@ -600,8 +607,21 @@ hipError_t run_embed_grad(const EmbedArgs& a, char* ws, hipStream_t stream) {
         }
     }
     float* part = (float*)(ws + l.part);
-    hipLaunchKernelGGL((k_grad_chunks<T>), dim3((l.nchunks + 3) / 4, (a.N + 64 * V - 1) / (64 * V)),
-                       dim3(256), 0, stream, a, s.keys, s.pos, l.n, l.R, l.nchunks, part);
+    auto chunks = [&](auto g) {
+        constexpr int G = decltype(g)::value, CPB = 256 / G;
+        const dim3 grid((l.nchunks + CPB - 1) / CPB, (a.N + G * V - 1) / (G * V));
+        if (a.N < V)
+            hipLaunchKernelGGL((k_grad_chunks<T, 8, true>), grid, dim3(256), 0, stream, a, s.keys, s.pos, l.n, l.R,
+                               l.nchunks, part);
+        else
+            hipLaunchKernelGGL((k_grad_chunks<T, G, false>), grid, dim3(256), 0, stream, a, s.keys, s.pos, l.n, l.R,
+                               l.nchunks, part);
+    };
+    const int np = (a.N + V - 1) / V;
+    if (np <= 8) chunks(std::integral_constant<int, 8>());
+    else if (np <= 16) chunks(std::integral_constant<int, 16>());
+    else if (np <= 32) chunks(std::integral_constant<int, 32>());
+    else chunks(std::integral_constant<int, 64>());
     if (l.nchunks > 1) {
         auto join = [&](auto cl) {
             constexpr int CL = decltype(cl)::value;

@@ -12,49 +12,88 @@ namespace semicrf {
 
 using bf16 = __bf16;
 
-// A row of N elements is taken in pieces of 16 bytes.  Global loads and stores of 16 bytes
-// need no 16-byte alignment on gfx950, so rows of any width take the same path; only the
-// last piece of a row whose width is no multiple of V goes element by element.
-template <class T>
+// A row of N elements is taken in pieces of 16 bytes, V elements.  Global loads and stores of 16
+// bytes need no 16-byte alignment on gfx950, so rows of any width take the same path: where N is
+// no multiple of V the last piece starts early, at N - V, and its first `skip` elements are the
+// piece before's too (loaded and stored twice with the same values, added up once).  A lane past
+// the row's pieces holds the last one with skip = V.  NARROW: N < V, element by element.
+template <class T, bool NARROW = false>
 struct Piece {
     static constexpr int V = 16 / sizeof(T);
-};
-
-template <class T>
-__device__ __forceinline__ void load_piece(const T* __restrict__ p, int valid,
-                                           float (&x)[Piece<T>::V]) {
-    constexpr int V = Piece<T>::V;
-    if (valid >= V) {
-        T t[V];
-        __builtin_memcpy(t, p, 16);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = (float)t[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = i < valid ? (float)p[i] : 0.0f;
+    int at, skip;
+    __device__ __forceinline__ Piece(int i, int N) {
+        const int c = i * V;
+        at = NARROW ? 0 : min(c, N - V);
+        skip = NARROW ? (c < N ? 0 : V) : min(c - at, V);
     }
-}
+};
 
 typedef uint32_t raw_piece __attribute__((ext_vector_type(4)));
 typedef raw_piece loose_piece __attribute__((aligned(1)));
 
-// STREAM: the store does not keep its line in the caches.
-template <class T, bool STREAM = false>
-__device__ __forceinline__ void store_piece(T* __restrict__ p, int valid,
-                                            const float (&x)[Piece<T>::V]) {
-    constexpr int V = Piece<T>::V;
-    if (valid >= V) {
+template <class T, bool NARROW>
+__device__ __forceinline__ raw_piece load_raw(const T* __restrict__ row, const Piece<T, NARROW>& p, int N) {
+    if constexpr (!NARROW) {
+        return *(const loose_piece*)(row + p.at);
+    } else {
+        constexpr int V = 16 / sizeof(T);
         T t[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = (T)x[i];
+        for (int i = 0; i < V; ++i) t[i] = i < N ? row[i] : (T)0.0f;
+        raw_piece x;
+        __builtin_memcpy(&x, t, 16);
+        return x;
+    }
+}
+template <class T>
+__device__ __forceinline__ void unpack(const raw_piece& r, float (&x)[16 / sizeof(T)]) {
+    T t[16 / sizeof(T)];
+    __builtin_memcpy(t, &r, 16);
+#pragma unroll
+    for (int i = 0; i < 16 / (int)sizeof(T); ++i) x[i] = (float)t[i];
+}
+// STREAM: the store does not keep its line in the caches.
+template <class T, bool STREAM = false, bool NARROW>
+__device__ __forceinline__ void store_piece(T* __restrict__ row, const Piece<T, NARROW>& p, int N,
+                                            const float (&x)[16 / sizeof(T)]) {
+    constexpr int V = 16 / sizeof(T);
+    T t[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] = (T)x[i];
+    if (p.skip == V) return;
+    if constexpr (!NARROW) {
         raw_piece r;
         __builtin_memcpy(&r, t, 16);
-        if constexpr (STREAM) __builtin_nontemporal_store(r, (loose_piece*)p);
-        else *(loose_piece*)p = r;
+        if constexpr (STREAM) __builtin_nontemporal_store(r, (loose_piece*)(row + p.at));
+        else *(loose_piece*)(row + p.at) = r;
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i < valid) p[i] = (T)x[i];
+            if (i < N) row[i] = t[i];
+    }
+}
+
+// V elements of type W from element `at` of a row, zeros past N
+template <class W, int V>
+__device__ __forceinline__ void load_elements(const W* __restrict__ row, int at, int N, float (&x)[V]) {
+    W t[V];
+    if (at + V <= N) {
+        __builtin_memcpy(t, row + at, sizeof(t));
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = (float)t[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = at + i < N ? (float)row[at + i] : 0.0f;
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_elements(float* __restrict__ row, int at, int N, const float (&x)[V]) {
+    if (at + V <= N) {
+        __builtin_memcpy(row + at, x, sizeof(x));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (at + i < N) row[at + i] = x[i];
     }
 }
 
@@ -62,29 +101,6 @@ __device__ __forceinline__ void store_piece(T* __restrict__ p, int valid,
 // its output, would wait at its top for the stores too (the first round has none to allow for).
 // Waiting for the fetch before the loop and before the stores leaves the stores in flight.
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
-
-// A piece as it lies in memory; what is past `valid` elements is zero.
-template <class T>
-__device__ __forceinline__ raw_piece load_raw(const T* __restrict__ p, int valid) {
-    constexpr int V = Piece<T>::V;
-    raw_piece x = {0, 0, 0, 0};
-    if (valid >= V) {
-        __builtin_memcpy(&x, p, 16);
-    } else if (valid > 0) {
-        T t[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = i < valid ? p[i] : (T)0.0f;
-        __builtin_memcpy(&x, t, 16);
-    }
-    return x;
-}
-template <class T>
-__device__ __forceinline__ void unpack(const raw_piece& r, float (&x)[Piece<T>::V]) {
-    T t[Piece<T>::V];
-    __builtin_memcpy(t, &r, 16);
-#pragma unroll
-    for (int i = 0; i < Piece<T>::V; ++i) x[i] = (float)t[i];
-}
 
 // Length of sequence b, clamped to [0, T]; a length outside raises the caller's status word.
 __device__ __forceinline__ int seq_length(const int32_t* __restrict__ lengths, int b, int T,

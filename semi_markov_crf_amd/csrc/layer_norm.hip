@@ -46,75 +46,79 @@ __device__ __forceinline__ bool row_valid(const NormArgs& a, unsigned row) {
     return (int)(row - b * (unsigned)a.T) < seq_length(a.lengths, b, a.T, a.status);
 }
 
+// Whether element i of a lane's piece is its own.
+template <class T, bool NARROW>
+__device__ __forceinline__ bool counted(const Piece<T, NARROW>& p, int i, int N) {
+    return i >= p.skip && (!NARROW || i < N);
+}
+
 // V weights from column c in the element type W of theirs
 template <class W, int V>
 __device__ __forceinline__ void load_weights(const void* p, int c, int N, float dflt,
                                              float (&w)[V]) {
-    if (!p) {
+    if (p) {
+        load_elements<W, V>((const W*)p, c, N, w);
+    } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) w[i] = dflt;
-        return;
-    }
-    constexpr int VW = Piece<W>::V;
-#pragma unroll
-    for (int i = 0; i < V; i += VW) {
-        float x[VW];
-        load_piece<W>((const W*)p + c + i, N - c - i, x);
-#pragma unroll
-        for (int j = 0; j < VW && i + j < V; ++j) w[i + j] = x[j];
     }
 }
 
 // One pass over the rows of a workgroup: the next row is on its way while this one is summed, and
 // the weights stay in registers.
-template <class T, class W, int G, int KP, int NT>
+//
+// MODE: rows fill the lanes' pieces exactly (G * KP * V elements), or not, or are narrower than one.
+enum { EXACT, MASKED, NARROWER };
+
+template <class T, class W, int G, int KP, int NT, int MODE>
 __global__ __launch_bounds__(NT) void k_layer_norm(const NormArgs a) {
-    constexpr int V = Piece<T>::V, RPB = NT / G;
+    using Pc = Piece<T, MODE == NARROWER>;
+    constexpr int V = Pc::V, RPB = NT / G;
     __shared__ float red[2 * (G > 64 ? G / 64 : 1)];
     int slot = 0;
-    const int N = a.N, lane = threadIdx.x % G;
+    const int N = MODE == EXACT ? G * KP * V : a.N, lane = threadIdx.x % G;
     const unsigned rows = (unsigned)a.B * a.T, step = gridDim.x * RPB;
     unsigned row = blockIdx.x * RPB + threadIdx.x / G;
     raw_piece x[KP];
-    bool ok = row < rows && row_valid(a, row);
+    bool ok;
+    auto fetch = [&](unsigned at) {
+        ok = at < rows && row_valid(a, at);
+        if (!ok) return;
+        const T* from = (const T*)a.x + (size_t)at * N;
 #pragma unroll
-    for (int k = 0; k < KP; ++k) {
-        const int c = (k * G + lane) * V;
-        x[k] = load_raw<T>((const T*)a.x + (size_t)(ok ? row : 0) * N + c, ok ? N - c : 0);
-    }
+        for (int k = 0; k < KP; ++k) x[k] = load_raw(from, Pc(k * G + lane, N), N);
+    };
+#pragma unroll
+    for (int k = 0; k < KP; ++k) x[k] = raw_piece{0, 0, 0, 0};
+    fetch(row);
     float w[KP][V], b[KP][V];
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
-        load_weights<W, V>(a.weight, (k * G + lane) * V, N, 1.0f, w[k]);
-        load_weights<W, V>(a.bias, (k * G + lane) * V, N, 0.0f, b[k]);
+        const Pc pc(k * G + lane, N);
+        load_weights<W, V>(a.weight, pc.at, N, 1.0f, w[k]);
+        load_weights<W, V>(a.bias, pc.at, N, 0.0f, b[k]);
     }
     for (unsigned r0 = blockIdx.x * RPB; r0 < rows; r0 += step, row += step) {
         float v[KP][V];
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
+            const Pc pc(k * G + lane, N);
             unpack<T>(x[k], v[k]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) s += v[k][i];
+            for (int i = 0; i < V; ++i) s += counted(pc, i, N) ? v[k][i] : 0.0f;
         }
         const bool now = ok, in = row < rows;
-        if (r0 + step < rows) {
-            ok = row + step < rows && row_valid(a, row + step);
-#pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const int c = (k * G + lane) * V;
-                x[k] = load_raw<T>((const T*)a.x + (size_t)(ok ? row + step : 0) * N + c, ok ? N - c : 0);
-            }
-        }
+        if (r0 + step < rows) fetch(row + step);
         const float mean = row_sum<G>(s, red, slot) / (float)N;
         s = 0.0f;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            const int c = (k * G + lane) * V;
+            const Pc pc(k * G + lane, N);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 v[k][i] -= mean;
-                s += c + i < N ? v[k][i] * v[k][i] : 0.0f;
+                s += counted(pc, i, N) ? v[k][i] * v[k][i] : 0.0f;
             }
         }
         const float var = row_sum<G>(s, red, slot) / (float)N;
@@ -127,48 +131,50 @@ __global__ __launch_bounds__(NT) void k_layer_norm(const NormArgs a) {
         T* y = (T*)a.y + (size_t)row * N;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            const int c = (k * G + lane) * V;
-            if (c >= N) break;
 #pragma unroll
             for (int i = 0; i < V; ++i) v[k][i] = now ? fmaf(v[k][i] * r, w[k][i], b[k][i]) : 0.0f;
-            store_piece<T>(y + c, N - c, v[k]);
+            store_piece<T>(y, Pc(k * G + lane, N), N, v[k]);
         }
     }
 }
 
-template <class T, class W, int G, int KP, int NT>
+template <class T, class W, int G, int KP, int NT, int MODE>
 __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float* part) {
-    constexpr int V = Piece<T>::V, RPB = NT / G;
+    using Pc = Piece<T, MODE == NARROWER>;
+    constexpr int V = Pc::V, RPB = NT / G;
     __shared__ float red[2 * (G > 64 ? G / 64 : 1)];
     __shared__ float join[RPB > 1 ? (RPB - 1) * G * V * 2 : 1];
     int slot = 0;
-    const int N = a.N, lane = threadIdx.x % G, sub = threadIdx.x / G;
+    const int N = MODE == EXACT ? G * KP * V : a.N, lane = threadIdx.x % G, sub = threadIdx.x / G;
     const unsigned rows = (unsigned)a.B * a.T;
     const float inv = 1.0f / (float)N;
     float w[KP][V], dw[KP][V], db[KP][V];
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
-        load_weights<W, V>(a.weight, (k * G + lane) * V, N, 1.0f, w[k]);
+        load_weights<W, V>(a.weight, Pc(k * G + lane, N).at, N, 1.0f, w[k]);
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
     }
     const unsigned step = gridDim.x * RPB;
     unsigned row = blockIdx.x * RPB + sub;
     raw_piece xr[KP], gr[KP];
-    float mean_r, rstd_r;
+    float mean_r = 0.0f, rstd_r = 0.0f;
     bool ok;
     auto fetch = [&](unsigned at) {            // the next row is on its way while one is summed
         ok = at < rows && row_valid(a, at);
-        const size_t first = (size_t)(ok ? at : 0) * N;
+        if (!ok) return;
+        const size_t first = (size_t)at * N;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            const int c = (k * G + lane) * V;
-            xr[k] = load_raw<T>((const T*)a.x + first + c, ok ? N - c : 0);
-            gr[k] = load_raw<T>((const T*)a.grad_out + first + c, ok ? N - c : 0);
+            const Pc pc(k * G + lane, N);
+            xr[k] = load_raw((const T*)a.x + first, pc, N);
+            gr[k] = load_raw((const T*)a.grad_out + first, pc, N);
         }
-        mean_r = ok ? a.mean_in[at] : 0.0f;
-        rstd_r = ok ? a.rstd_in[at] : 0.0f;
+        mean_r = a.mean_in[at];
+        rstd_r = a.rstd_in[at];
     };
+#pragma unroll
+    for (int k = 0; k < KP; ++k) xr[k] = gr[k] = raw_piece{0, 0, 0, 0};
     fetch(row);
     for (unsigned r0 = blockIdx.x * RPB; r0 < rows; r0 += step, row += step) {
         const bool in = row < rows, now = ok;
@@ -181,29 +187,31 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
             unpack<T>(gr[k], dy[k]);
         }
         if (r0 + step < rows) fetch(row + step);
+        if (now) {
 #pragma unroll
-        for (int k = 0; k < KP; ++k)
+            for (int k = 0; k < KP; ++k) {
+                const Pc pc(k * G + lane, N);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                h[k][i] = (h[k][i] - mean) * r;
-                const float t = dy[k][i] * w[k][i];
-                sg += t;
-                sgh += t * h[k][i];
-                dw[k][i] += dy[k][i] * h[k][i];
-                db[k][i] += dy[k][i];
+                for (int i = 0; i < V; ++i) {
+                    h[k][i] = (h[k][i] - mean) * r;
+                    const float t = counted(pc, i, N) ? dy[k][i] * w[k][i] : 0.0f;
+                    sg += t;
+                    sgh += t * h[k][i];
+                    dw[k][i] += dy[k][i] * h[k][i];
+                    db[k][i] += dy[k][i];
+                }
             }
+        }
         sg = row_sum<G>(sg, red, slot) * inv;
         sgh = row_sum<G>(sgh, red, slot) * inv;
         if (!in) continue;
         T* dx = (T*)a.grad_x + (size_t)row * N;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            const int c = (k * G + lane) * V;
-            if (c >= N) break;
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 dy[k][i] = now ? r * (dy[k][i] * w[k][i] - sg - h[k][i] * sgh) : 0.0f;
-            store_piece<T>(dx + c, N - c, dy[k]);
+            store_piece<T>(dx, Pc(k * G + lane, N), N, dy[k]);
         }
     }
     // join the row groups of the workgroup in order, then one partial row [2][N]
@@ -232,12 +240,12 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
                 }
         }
         if (sub == 0) {
-            const int c = (k * G + lane) * V;
+            const Pc pc(k * G + lane, N);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (c + i < N) {
-                    out[c + i] = dw[k][i];
-                    out[N + c + i] = db[k][i];
+                if (counted(pc, i, N)) {
+                    out[pc.at + i] = dw[k][i];
+                    out[N + pc.at + i] = db[k][i];
                 }
         }
     }
@@ -278,7 +286,7 @@ struct Shape2 {
 };
 Shape2 norm_shape(int N, int V) {
     const int np = (N + V - 1) / V;
-    int G = 8;
+    int G = 2;
     while (G < 64 && G < np) G *= 2;
     if (np > 2 * 64) G = 256;
     if (np > 2 * 256) G = 1024;
@@ -295,25 +303,33 @@ int norm_wgs(long rows, int G, int NT, int waves) {
 constexpr int norm_threads(int G) { return G > 256 ? G : 256; }
 // The gradient runs at 4 wavefronts a SIMD: the row on its way hides the latency, and every
 // workgroup leaves a partial row (400,000 rows of 512 bfloat16, with the partials' sum: 238 us
-// at 4, 299 at 6, 267 at 8; workgroups of 512 threads 326 at 4).
-constexpr int GRAD_WAVES = 4;
+// at 4, 299 at 6, 267 at 8; workgroups of 512 threads 326 at 4).  Narrow rows leave little and have
+// little on its way: 8.
+constexpr int norm_grad_waves(int G) { return G < 32 ? 8 : 4; }
 
+// Calls f with the shape's G, KP and MODE.
 template <class F>
 hipError_t with_shape(int N, int V, F&& f) {
     const Shape2 s = norm_shape(N, V);
-#define CASE(g, kp) \
-    if (s.G == g && s.KP == kp) return f(std::integral_constant<int, g>(), std::integral_constant<int, kp>())
-    CASE(8, 1); CASE(16, 1); CASE(32, 1); CASE(64, 1); CASE(64, 2); CASE(256, 1); CASE(256, 2);
-    CASE(1024, 1); CASE(1024, 2); CASE(1024, 4); CASE(1024, 8);
+    using I = std::integral_constant<int, MASKED>;
+    if (N < V) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>(), std::integral_constant<int, NARROWER>());
+#define CASE(g, kp)                                                                                                  \
+    if (s.G == g && s.KP == kp) {                                                                                    \
+        std::integral_constant<int, g> gg;                                                                           \
+        std::integral_constant<int, kp> kk;                                                                          \
+        return N == g * kp * V ? f(gg, kk, std::integral_constant<int, EXACT>()) : f(gg, kk, I());                   \
+    }
+    CASE(2, 1) CASE(4, 1) CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(64, 1) CASE(64, 2) CASE(256, 1) CASE(256, 2)
+    CASE(1024, 1) CASE(1024, 2) CASE(1024, 4) CASE(1024, 8)
 #undef CASE
     return hipErrorInvalidValue;
 }
 
 template <class T, class W>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
-    return with_shape(a.N, Piece<T>::V, [&](auto g, auto kp) {
+    return with_shape(a.N, 16 / (int)sizeof(T), [&](auto g, auto kp, auto mode) {
         constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = norm_threads(G);
-        hipLaunchKernelGGL((k_layer_norm<T, W, G, KP, NT>), dim3(norm_wgs((long)a.B * a.T, G, NT, 8)),
+        hipLaunchKernelGGL((k_layer_norm<T, W, G, KP, NT, decltype(mode)::value>), dim3(norm_wgs((long)a.B * a.T, G, NT, 8)),
                            dim3(NT), 0, stream, a);
         return hipGetLastError();
     });
@@ -321,10 +337,10 @@ hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
 
 template <class T, class W>
 hipError_t run_norm_grad(const NormArgs& a, float* part, hipStream_t stream) {
-    return with_shape(a.N, Piece<T>::V, [&](auto g, auto kp) {
+    return with_shape(a.N, 16 / (int)sizeof(T), [&](auto g, auto kp, auto mode) {
         constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = norm_threads(G);
-        const int nwg = norm_wgs((long)a.B * a.T, G, NT, GRAD_WAVES);
-        hipLaunchKernelGGL((k_layer_norm_grad<T, W, G, KP, NT>), dim3(nwg), dim3(NT), 0, stream, a,
+        const int nwg = norm_wgs((long)a.B * a.T, G, NT, norm_grad_waves(G));
+        hipLaunchKernelGGL((k_layer_norm_grad<T, W, G, KP, NT, decltype(mode)::value>), dim3(nwg), dim3(NT), 0, stream, a,
                            part);
         if (a.grad_weight || a.grad_bias)
             hipLaunchKernelGGL((k_norm_partials<W>), dim3((2 * a.N + 15) / 16), dim3(256), 0, stream,
@@ -343,7 +359,7 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
 size_t layer_norm_grad_bytes(int B, int T, int N, int dtype) {
     const int V = dtype == SEMICRF_F32 ? 4 : 8;
     const Shape2 s = norm_shape(N, V);
-    return (size_t)norm_wgs((long)B * T, s.G, norm_threads(s.G), GRAD_WAVES) * 2 * N * sizeof(float);
+    return (size_t)norm_wgs((long)B * T, s.G, norm_threads(s.G), norm_grad_waves(s.G)) * 2 * N * sizeof(float);
 }
 
 hipError_t launch_layer_norm_grad(const NormArgs& a, void* ws, hipStream_t stream) {
