@@ -451,57 +451,73 @@ __global__ __launch_bounds__(256) void k_grad_chunks(const EmbedArgs a, const ui
     flush(key_after == cur);
 }
 
-// The run that starts in this chunk and goes on: its partial rows, in order.  CL lanes take four
-// columns each, the workgroup's 512 / CL groups consecutive shares of the partial rows.
-// grid (nchunks, ceil(N / (4 CL))), block 512
+// The runs that start in a chunk and go on: their partial rows, in order.  A workgroup looks at `per`
+// chunks (at most 64, a lane each) and takes the runs it finds one by one; CL lanes take four
+// columns each, the 512 / CL groups consecutive shares of the partial rows.
+// grid (ceil(nchunks / per), ceil(N / (4 CL))), block 512
 template <class T, int CL>
 __global__ __launch_bounds__(512) void k_grad_join(const EmbedArgs a, const uint32_t* keys, int n,
-                                                   int R, int nchunks, const float* part) {
+                                                   int R, int nchunks, int per, const float* part) {
     constexpr int GR = 512 / CL, U = 8;
     __shared__ float s[GR][CL][4];
-    const int chunk = blockIdx.x, N = a.N;
-    const int r0 = chunk * R, r1 = r0 + R;
-    if (r1 >= n) return;
-    const uint32_t key = keys[r1], last_key = keys[r1 - 1], before = r0 > 0 ? keys[r0 - 1] : ~0u;
-    // only a run that starts here and goes on: an earlier start is joined by its first chunk
-    if (last_key != key || key >= (uint32_t)a.V || before == key) return;
-    // the first row past the run: chunk ends first, then inside one
-    int lo = chunk + 1, hi = nchunks;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        const int e = min(n, (mid + 1) * R) - 1;
-        if (keys[e] == key) lo = mid + 1; else hi = mid;
-    }
-    // chunk lo (if any) ends with another key: the run reaches into it if its first row has the key
-    const int last = lo < nchunks && keys[lo * R] == key ? lo : lo - 1;
-    const int m = last - chunk;                // partial rows after the first
+    const int N = a.N, lane64 = threadIdx.x & 63, c0 = blockIdx.x * per;
     const int lane = threadIdx.x % CL, grp = threadIdx.x / CL, c = (blockIdx.y * CL + lane) * 4;
-    const int per = (m + GR - 1) / GR;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < N) {
-        if (grp == 0) load_elements(part + ((size_t)chunk * 2 + 1) * N, c, N, v);
-        const int q1 = min(m, (grp + 1) * per);
-        const float* p = part + (size_t)(chunk + 1) * 2 * N;
-        for (int q = grp * per; q < q1; q += U) {
-            float x[U][4];
-#pragma unroll
-            for (int u = 0; u < U; ++u) load_elements(p + (size_t)(q + u) * 2 * N, c, q + u < q1 ? N : 0, x[u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += x[u][i];
+    // only a run that starts in its chunk and goes on: an earlier start is joined by its first chunk
+    bool starts = false;
+    uint32_t my_key = 0;
+    {
+        const int chunk = c0 + lane64, r0 = chunk * R, r1 = r0 + R;
+        if (lane64 < per && chunk < nchunks && r1 < n) {
+            my_key = keys[r1];
+            const uint32_t last = keys[r1 - 1], before = r0 > 0 ? keys[r0 - 1] : ~0u;
+            starts = last == my_key && my_key < (uint32_t)a.V && before != my_key;
         }
     }
+    // the same in every wavefront
+    for (uint64_t found = __ballot(starts); found; found &= found - 1) {
+        const int i = __builtin_ctzll(found), chunk = c0 + i;
+        const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)my_key, i);
+        // chunks lo .. hi - 1 may end with the key, those before lo do: 64 of them asked at a time
+        int lo = chunk + 1, hi = nchunks;
+        while (lo < hi) {
+            const int step = (hi - lo + 63) / 64, q = lo + (lane64 + 1) * step - 1;
+            const bool has = q < hi && keys[min(n, (q + 1) * R) - 1] == key;
+            const int yes = __popcll(__ballot(has));
+            lo += yes * step;
+            hi = min(hi, lo + step - 1);
+        }
+        // chunk lo (if any) ends with another key: the run reaches into it if its first row has the key
+        const int last = lo < nchunks && keys[lo * R] == key ? lo : lo - 1;
+        const int m = last - chunk;            // partial rows after the first
+        const int share = (m + GR - 1) / GR;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (c < N) {
+            if (grp == 0) load_elements(part + ((size_t)chunk * 2 + 1) * N, c, N, v);
+            const int q1 = min(m, (grp + 1) * share);
+            const float* p = part + (size_t)(chunk + 1) * 2 * N;
+            for (int q = grp * share; q < q1; q += U) {
+                float x[U][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[grp][lane][i] = v[i];
-    __syncthreads();
-    if (grp == 0 && c < N) {
-        for (int q = 1; q < GR; ++q)
+                for (int u = 0; u < U; ++u) load_elements(p + (size_t)(q + u) * 2 * N, c, q + u < q1 ? N : 0, x[u]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += s[q][lane][i];
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < N) ((T*)a.out)[(size_t)key * N + c + i] = (T)(v[i] * a.scale);
+                    for (int j = 0; j < 4; ++j) v[j] += x[u][j];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[grp][lane][j] = v[j];
+        __syncthreads();
+        if (grp == 0 && c < N) {
+#pragma unroll 8
+            for (int q = 1; q < GR; ++q)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += s[q][lane][j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < N) ((T*)a.out)[(size_t)key * N + c + j] = (T)(v[j] * a.scale);
+        }
     }
 }
 
@@ -518,10 +534,12 @@ GradLayout grad_layout(int B, int T, int V, int N, int es) {
     while (((long)V >> bits) != 0) ++bits;
     l.passes = (bits + 7) / 8;
     // rows per chunk: about 2,048 wavefronts over the chunks and column slabs fill the device; longer
-    // chunks leave fewer partial rows.  A narrow row takes a part of a wavefront.
+    // chunks leave fewer partial rows.  A narrow row takes a part of a wavefront; its chunks are at most
+    // 8,192, so that the join has no more to do than the sums (400,000 rows, sums + join: 17 + 18 us
+    // for 16 float32 columns, 13 + 28 with 16,384 chunks, 29 + 11 with 4,096).
     const long np = ((long)N * es + 15) / 16, G = np <= 8 ? 8 : np <= 16 ? 16 : np <= 32 ? 32 : 64;
     l.R = 8;
-    while (l.R < 256 && l.n * ((np + G - 1) / G) * G / 64 / l.R > 2048) l.R *= 2;
+    while (l.R < 256 && (l.n * ((np + G - 1) / G) * G / 64 / l.R > 2048 || l.n / l.R > 8192)) l.R *= 2;
     l.nchunks = (l.n + l.R - 1) / l.R;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -625,11 +643,17 @@ hipError_t run_embed_grad(const EmbedArgs& a, char* ws, hipStream_t stream) {
     if (l.nchunks > 1) {
         auto join = [&](auto cl) {
             constexpr int CL = decltype(cl)::value;
-            hipLaunchKernelGGL((k_grad_join<T, CL>), dim3(l.nchunks, (a.N + 4 * CL - 1) / (4 * CL)), dim3(512),
-                               0, stream, a, s.keys, l.n, l.R, l.nchunks, part);
+            const int slabs = (a.N + 4 * CL - 1) / (4 * CL);
+            // about 2,048 workgroups: most chunks have no run, and one that has keeps its workgroup for
+            // 5 us (12,500 chunks, each a workgroup: 93 us; 1,024 workgroups 70; 2,048 as here 28)
+            const long want = ((long)l.nchunks * slabs + 2047) / 2048;
+            const int per = (int)(want < 64 ? want : 64);
+            hipLaunchKernelGGL((k_grad_join<T, CL>), dim3((l.nchunks + per - 1) / per, slabs), dim3(512), 0, stream, a,
+                               s.keys, l.n, l.R, l.nchunks, per, part);
         };
         // narrow rows leave more groups for the partial rows
         if (a.N <= 64) join(std::integral_constant<int, 16>());
+        else if (a.N <= 128) join(std::integral_constant<int, 32>());
         else if (a.N <= 256) join(std::integral_constant<int, 64>());
         else join(std::integral_constant<int, 256>());
     }

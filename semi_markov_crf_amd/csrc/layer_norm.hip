@@ -46,7 +46,8 @@ __device__ __forceinline__ bool row_valid(const NormArgs& a, unsigned row) {
     return (int)(row - b * (unsigned)a.T) < seq_length(a.lengths, b, a.T, a.status);
 }
 
-// Whether element i of a lane's piece is its own.
+// Whether element i of a lane's piece is its own.  Sums take the others times 0: they hold elements
+// of the same row, so one that is not finite is in the sum either way.
 template <class T, bool NARROW>
 __device__ __forceinline__ bool counted(const Piece<T, NARROW>& p, int i, int N) {
     return i >= p.skip && (!NARROW || i < N);
@@ -91,36 +92,35 @@ __global__ __launch_bounds__(NT) void k_layer_norm(const NormArgs a) {
 #pragma unroll
     for (int k = 0; k < KP; ++k) x[k] = raw_piece{0, 0, 0, 0};
     fetch(row);
-    float w[KP][V], b[KP][V];
+    float w[KP][V], b[KP][V], own[KP][V];
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
         const Pc pc(k * G + lane, N);
         load_weights<W, V>(a.weight, pc.at, N, 1.0f, w[k]);
         load_weights<W, V>(a.bias, pc.at, N, 0.0f, b[k]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) own[k][i] = counted(pc, i, N) ? 1.0f : 0.0f;
     }
     for (unsigned r0 = blockIdx.x * RPB; r0 < rows; r0 += step, row += step) {
         float v[KP][V];
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            const Pc pc(k * G + lane, N);
             unpack<T>(x[k], v[k]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) s += counted(pc, i, N) ? v[k][i] : 0.0f;
+            for (int i = 0; i < V; ++i) s = MODE == EXACT ? s + v[k][i] : fmaf(v[k][i], own[k][i], s);
         }
         const bool now = ok, in = row < rows;
         if (r0 + step < rows) fetch(row + step);
         const float mean = row_sum<G>(s, red, slot) / (float)N;
         s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KP; ++k) {
-            const Pc pc(k * G + lane, N);
+        for (int k = 0; k < KP; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 v[k][i] -= mean;
-                s += counted(pc, i, N) ? v[k][i] * v[k][i] : 0.0f;
+                s = fmaf(v[k][i], MODE == EXACT ? v[k][i] : v[k][i] * own[k][i], s);
             }
-        }
         const float var = row_sum<G>(s, red, slot) / (float)N;
         const float r = 1.0f / sqrtf(var + a.eps);
         if (!in) continue;
@@ -148,12 +148,17 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
     const int N = MODE == EXACT ? G * KP * V : a.N, lane = threadIdx.x % G, sub = threadIdx.x / G;
     const unsigned rows = (unsigned)a.B * a.T;
     const float inv = 1.0f / (float)N;
-    float w[KP][V], dw[KP][V], db[KP][V];
+    // own: the weight where the element is the lane's own, else 0
+    float w[KP][V], own[KP][V], dw[KP][V], db[KP][V];
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
-        load_weights<W, V>(a.weight, Pc(k * G + lane, N).at, N, 1.0f, w[k]);
+        const Pc pc(k * G + lane, N);
+        load_weights<W, V>(a.weight, pc.at, N, 1.0f, w[k]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
+        for (int i = 0; i < V; ++i) {
+            own[k][i] = counted(pc, i, N) ? w[k][i] : 0.0f;
+            dw[k][i] = db[k][i] = 0.0f;
+        }
     }
     const unsigned step = gridDim.x * RPB;
     unsigned row = blockIdx.x * RPB + sub;
@@ -189,18 +194,16 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
         if (r0 + step < rows) fetch(row + step);
         if (now) {
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const Pc pc(k * G + lane, N);
+            for (int k = 0; k < KP; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     h[k][i] = (h[k][i] - mean) * r;
-                    const float t = counted(pc, i, N) ? dy[k][i] * w[k][i] : 0.0f;
+                    const float t = dy[k][i] * (MODE == EXACT ? w[k][i] : own[k][i]);
                     sg += t;
                     sgh += t * h[k][i];
                     dw[k][i] += dy[k][i] * h[k][i];
                     db[k][i] += dy[k][i];
                 }
-            }
         }
         sg = row_sum<G>(sg, red, slot) * inv;
         sgh = row_sum<G>(sgh, red, slot) * inv;
@@ -230,6 +233,7 @@ __global__ __launch_bounds__(NT) void k_layer_norm_grad(const NormArgs a, float*
             }
             __syncthreads();
             if (sub == 0)
+#pragma unroll 1                               // unrolled, it holds up to 512 registers
                 for (int q = 0; q < RPB - 1; ++q) {
                     const float* j = join + (q * G + lane) * V * 2;
 #pragma unroll
