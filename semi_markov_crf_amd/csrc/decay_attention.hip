@@ -214,23 +214,29 @@ __device__ __forceinline__ float power(float g2, int n) {
     return n == 0 ? 1.0f : __builtin_amdgcn_exp2f(g2 * (float)n);
 }
 
+// How a kernel reads its rows and what it leaves out.
+//   FULL: rows fill the padded width P exactly, by buffer descriptors.
+//   PART: by buffer descriptors; tiles of products past Da and columns past Dc are left out.
+//   LOOSE: rows of any width, stride and alignment, by pointers; the same left out.
+// A descriptor spans exactly the chunk's valid rows, less than 2^29 bytes, so that rows and columns
+// out of range read as zeros with no branch (bit 31 of the offset puts a column out of range); rows
+// are then whole pieces of 16 bytes from dword addresses.
+enum { FULL, PART, LOOSE };
+
 // A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces; a thread's
 // column piece is the same in all its rows.
-//   FAST: rows are whole pieces that do not overlap, and a chunk spans less than 2^29 bytes.  Loads
-//   go through a buffer descriptor over exactly the chunk's valid rows, so that rows and columns
-//   out of range read as zeros with no branch (bit 31 of the offset puts a column out of range).
-//   Otherwise element by element.
-template <class T, int P, int C, int NT, bool FAST>
+template <class T, int P, int C, int NT, int MODE>
 struct Tile {
     static constexpr int V = 16 / sizeof(T), PPR = P / V, LD = lds_pitch<T>(P), RPS = NT / PPR;
     static constexpr int NP = C / RPS;
     static_assert(NT % PPR == 0 && C % RPS == 0, "pieces per thread");
     u32x4 x[NP];
+    int shift;               // LOOSE: bits that the row's last piece starts early
 
     // m valid rows from sweep index t0 (position L - t0 - m is the lowest of a reversed chunk)
     __device__ __forceinline__ void load(const Role& w, const T* seq, int D, int t0, int m, int L, int reverse) {
         const int row0 = threadIdx.x / PPR, c = (threadIdx.x % PPR) * V;
-        if constexpr (FAST) {
+        if constexpr (MODE != LOOSE) {
             const int stb = (int)w.st * (int)sizeof(T);
             const T* base = seq + (long)(reverse ? L - t0 - m : t0) * w.st;
             const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
@@ -241,21 +247,34 @@ struct Tile {
 #pragma unroll
             for (int n = 0; n < NP; ++n) x[n] = __builtin_amdgcn_raw_buffer_load_b128(buf, off + n * RPS * step, 0, 0);
         } else {
+            // a last piece past the row's end is read from D - V on and shifted when it is put
+            const int at = D < V ? 0 : min(c, D - V);
+            shift = D < V ? 0 : (c - at) * 8 * (int)sizeof(T);
+            const long st = reverse ? -w.st : w.st;
+            const T* p = seq + (long)(reverse ? L - 1 - t0 : t0) * w.st + row0 * st + at;
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                const int row = row0 + n * RPS;
-                T e[V];
+            for (int n = 0; n < NP; ++n, p += RPS * st) {
+                x[n] = u32x4{0, 0, 0, 0};
+                if (row0 + n * RPS < m && c < D) {
+                    if (D >= V) {
+                        x[n] = *(const loose_piece*)p;
+                    } else {
+                        T e[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) e[i] = (T)0.0f;
-                if (row < m && c < D) {
-                    const T* p = seq + (long)(reverse ? L - 1 - t0 - row : t0 + row) * w.st + c;
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (c + i < D) e[i] = p[i];
+                        for (int i = 0; i < V; ++i) e[i] = i < D ? p[i] : (T)0.0f;
+                        __builtin_memcpy(&x[n], e, 16);
+                    }
                 }
-                __builtin_memcpy(&x[n], e, 16);
             }
         }
+    }
+    __device__ __forceinline__ u32x4 piece(int n) const {
+        if constexpr (MODE != LOOSE) return x[n];
+        const uint64_t lo = (uint64_t)x[n][1] << 32 | x[n][0], hi = (uint64_t)x[n][3] << 32 | x[n][2];
+        const int s = shift & 63;
+        const uint64_t l = shift & 64 ? hi : lo, h = shift & 64 ? 0 : hi;
+        const uint64_t a = l >> s | h << 1 << (63 - s), b = h >> s;
+        return shift < 128 ? u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)} : u32x4{0, 0, 0, 0};
     }
     // ORDERED: columns in the order of product steps
     template <bool ORDERED>
@@ -264,11 +283,12 @@ struct Tile {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             T* row = buf + (row0 + n * RPS) * LD;
+            const u32x4 y = piece(n);
             if constexpr (ORDERED && sizeof(T) == 2) {
-                *(u32x2*)(row + ordered<T>(c)) = u32x2{x[n][0], x[n][1]};
-                *(u32x2*)(row + ordered<T>(c + 4)) = u32x2{x[n][2], x[n][3]};
+                *(u32x2*)(row + ordered<T>(c)) = u32x2{y[0], y[1]};
+                *(u32x2*)(row + ordered<T>(c + 4)) = u32x2{y[2], y[3]};
             } else {
-                *(u32x4*)(row + c) = x[n];
+                *(u32x4*)(row + c) = y;
             }
         }
     }
@@ -356,8 +376,10 @@ struct State {
                     for (int r = 0; r < 4; ++r) s[t][v][r] *= d.f;
         }
     }
-    // S += sum_j w_j b_j c_j^T over one product step from row k0; `c` the columns' fragments
-    __device__ __forceinline__ void update(const T* bbuf, int ld, int k0,
+    // S += sum_j w_j b_j c_j^T over one product step from row k0; `c` the columns' fragments.  Rows
+    // of S from `rows` on are left out, 32 at a time.
+    template <int MODE>
+    __device__ __forceinline__ void update(const T* bbuf, int ld, int k0, int rows,
                                            const typename Mma<T>::Frag (&c)[VT], const float (&w)[E]) {
         Parts<T, update_parts<T>()> p[VT];
 #pragma unroll
@@ -365,13 +387,16 @@ struct State {
 #pragma unroll
             for (int j = 0; j < E; j += 2) p[v].set(j, (float)c[v][j] * w[j], (float)c[v][j + 1] * w[j + 1]);
 #pragma unroll
-        for (int t = 0; t < ST; ++t) {
-            const auto a = frag_col(bbuf, ld, k0, 16 * t);
+        for (int t0 = 0; t0 < ST; t0 += 2)
+            if (MODE == FULL || 16 * t0 < rows)
 #pragma unroll
-            for (int v = 0; v < VT; ++v)
+                for (int t = t0; t < t0 + 2; ++t) {
+                    const auto a = frag_col(bbuf, ld, k0, 16 * t);
 #pragma unroll
-                for (int n = 0; n < update_parts<T>(); ++n) s[t][v] = Mma<T>::mma(a, p[v].f[n], s[t][v]);
-        }
+                    for (int v = 0; v < VT; ++v)
+#pragma unroll
+                        for (int n = 0; n < update_parts<T>(); ++n) s[t][v] = Mma<T>::mma(a, p[v].f[n], s[t][v]);
+                }
     }
 };
 
@@ -425,17 +450,17 @@ __device__ __forceinline__ void update_rest(State<T, P>& S, const T* sb, const T
         for (int v = 0; v < VT; ++v) c[v] = frag_col(sc, LD, k0, ((threadIdx.x >> 6) * VT + v) * 16);
         float u[Mma<T>::E];
         update_weights<T>(g2, su, k0, m, e, u);
-        S.update(sb, LD, k0, c, u);
+        S.template update<FULL>(sb, LD, k0, P, c, u);
     }
 }
 
-template <class T, int P, int C, bool FAST, int N>
+template <class T, int P, int C, int MODE, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), P == 128 ? 2 : 4) void
 k_attn_state(const Sweeps<N> set, int group) {
     using M = Mma<T>;
     using St = State<T, P>;
     constexpr int NT = 64 * St::NW, VT = St::VT;
-    using Tl = Tile<T, P, C, NT, FAST>;
+    using Tl = Tile<T, P, C, NT, MODE>;
     __shared__ __align__(16) T sb[C * Tl::LD], sc[C * Tl::LD];
     Place at;
     if (!place(set.s[0], N, group, at)) return;
@@ -449,6 +474,8 @@ k_attn_state(const Sweeps<N> set, int group) {
     Tl tb, tc;
     tb.load(w.b, pb, w.Da, t_begin, min(C, t_end - t_begin), L, w.reverse);
     tc.load(w.c, pc, w.Dc, t_begin, min(C, t_end - t_begin), L, w.reverse);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool mine = MODE == FULL || wave * VT * 16 < w.Dc;     // columns of this wavefront
     St S;
     S.load(nullptr, 0, 0, false, 1.0f);
     Update<T, C> up;
@@ -464,17 +491,17 @@ k_attn_state(const Sweeps<N> set, int group) {
             tb.load(w.b, pb, w.Da, t0 + C, mn, L, w.reverse);
             tc.load(w.c, pc, w.Dc, t0 + C, mn, L, w.reverse);
         }
+        if (!mine) continue;
         if (m < C) up.skip();
         S.decay(up.d);
 #pragma unroll
         for (int k0 = 0; k0 < C; k0 += M::KS) {
             typename M::Frag c[VT];
 #pragma unroll
-            for (int v = 0; v < VT; ++v)
-                c[v] = frag_col(sc, Tl::LD, k0, ((threadIdx.x >> 6) * VT + v) * 16);
+            for (int v = 0; v < VT; ++v) c[v] = frag_col(sc, Tl::LD, k0, (wave * VT + v) * 16);
             float u[M::E];
             up.get(k0, u);
-            S.update(sb, Tl::LD, k0, c, u);
+            S.template update<MODE>(sb, Tl::LD, k0, w.Da, c, u);
         }
     }
     if (t_end > t_begin && (t_end - t_begin) % C)
@@ -538,12 +565,12 @@ __device__ __forceinline__ void store4(const __amdgpu_buffer_rsrc_t& buf, uint32
 
 // Rows i < m of a chunk from result tiles that hold column i = 16 it + r, rows (of the tile)
 // four consecutive output columns from `col`.
-template <class O, bool FAST, int IT, int VT>
+template <class O, int MODE, int IT, int VT>
 __device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m, int L, int col,
                                            const f32x4 (&acc)[IT][VT]) {
     const int r16 = threadIdx.x & 15;
     const long ost = (long)w.H * w.Dc;
-    if constexpr (FAST) {
+    if constexpr (MODE != LOOSE) {
         const int stb = (int)ost * (int)sizeof(O), step = w.reverse ? -stb : stb;
         O* base = seq + (long)(w.reverse ? L - t0 - m : t0) * ost;
         const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
@@ -563,22 +590,31 @@ __device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m
             if (i < m) {
                 O* p = seq + (long)(w.reverse ? L - 1 - t0 - i : t0 + i) * ost;
 #pragma unroll
-                for (int v = 0; v < VT; ++v)
+                for (int v = 0; v < VT; ++v) {
+                    const int c = col + 16 * v;
+                    O y[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (col + 16 * v + r < w.Dc) p[col + 16 * v + r] = (O)acc[it][v][r];
+                    for (int r = 0; r < 4; ++r) y[r] = (O)acc[it][v][r];
+                    if (c + 4 <= w.Dc) {
+                        __builtin_memcpy(p + c, y, sizeof(y));
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 3; ++r)
+                            if (c + r < w.Dc) p[c + r] = y[r];
+                    }
+                }
             }
         }
     }
 }
 
-template <class T, int P, int C, bool FAST, int N>
+template <class T, int P, int C, int MODE, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), (sweep_occupancy<T, P>())) void
 k_attn_sweep(const Sweeps<N> set, int group) {
     using M = Mma<T>;
     using St = State<T, P>;
     constexpr int NW = St::NW, NT = 64 * NW, VT = St::VT, IT = C / 16, KS = M::KS, E = M::E;
-    using Tl = Tile<T, P, C, NT, FAST>;
+    using Tl = Tile<T, P, C, NT, MODE>;
     constexpr int LDM = lds_pitch<T>(C);
     __shared__ __align__(16) T sa[C * Tl::LD], sb[C * Tl::LD], sc[C * Tl::LD], sm[C * LDM];
     Place at;
@@ -627,6 +663,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
 #pragma unroll
     for (int it = 0; it < IT; ++it) inter[it] = w.si / sigma * power(g2, 16 * it + r16 + 1 - w.e);
     const float g16 = power(g2, 16);
+    const bool mine = MODE == FULL || wave * VT * 16 < w.Dc;     // columns of this wavefront
     Update<T, C> up;
     up.set(g, g2, su, w.e);
     wait_loads();
@@ -651,8 +688,11 @@ k_attn_sweep(const Sweeps<N> set, int group) {
                 const int it = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, jt = n - it * (it + 1) / 2;
                 f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k0 = 0; k0 < P; k0 += KS)
-                    acc = M::mma(frag_row(sb, Tl::LD, 16 * jt, k0), frag_ordered<T>(sa, Tl::LD, 16 * it, k0), acc);
+                for (int k1 = 0; k1 < P; k1 += 32)
+                    if (MODE == FULL || k1 < w.Da)
+#pragma unroll
+                        for (int k0 = k1; k0 < k1 + 32; k0 += KS)
+                            acc = M::mma(frag_row(sb, Tl::LD, 16 * jt, k0), frag_ordered<T>(sa, Tl::LD, 16 * it, k0), acc);
                 const float step = it - jt <= 1 ? 1.0f : it - jt == 2 ? g16 : g16 * g16;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[r] *= jt < it ? below[r] * step : diag[r];
@@ -664,6 +704,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
             }
         }
         __syncthreads();
+        if (!mine) continue;
         // what the state gives each row; result tiles hold columns of c by rows
         f32x4 acc[IT][VT];
 #pragma unroll
@@ -672,6 +713,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
             for (int v = 0; v < VT; ++v) acc[it][v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int kb = 0; kb < P / KS; ++kb) {
+            if (MODE != FULL && kb * KS / 32 * 32 >= w.Da) break;
             Parts<T, state_parts<T>()> p[VT];
 #pragma unroll
             for (int v = 0; v < VT; ++v)
@@ -710,13 +752,13 @@ k_attn_sweep(const Sweeps<N> set, int group) {
             }
             float u[E];
             up.get(k0, u);
-            S.update(sb, Tl::LD, k0, c, u);
+            S.template update<MODE>(sb, Tl::LD, k0, w.Da, c, u);
             __builtin_amdgcn_sched_barrier(0);
         }
         const int col = wave * VT * 16 + 4 * gr;
         wait_loads();
-        if (w.out32) store_rows<float, FAST, IT, VT>(w, (float*)w.out + out0, t0, m, L, col, acc);
-        else store_rows<T, FAST, IT, VT>(w, (T*)w.out + out0, t0, m, L, col, acc);
+        if (w.out32) store_rows<float, MODE, IT, VT>(w, (float*)w.out + out0, t0, m, L, col, acc);
+        else store_rows<T, MODE, IT, VT>(w, (T*)w.out + out0, t0, m, L, col, acc);
     }
     if (w.state_out) {
         if (t_end > t_begin && (t_end - t_begin) % C)
@@ -914,8 +956,8 @@ Sweep base_sweep(const AttnArgs& a, const AttnLayout& l) {
 
 Role role(const void* p, const int64_t* s, int group) { return Role{p, (long)s[0], (long)s[1], (long)s[2], group}; }
 
-// Whether a role's rows can be read through buffer descriptors (Tile), addresses being whole
-// dwords, and whether the output's rows can be written so.
+// Whether a role's rows can be read through buffer descriptors, addresses being whole dwords, and
+// whether the output's rows can be written so.
 bool fast_role(const Role& r, int D, int es) {
     return (uintptr_t)r.p % 4 == 0 && r.sb * es % 4 == 0 && r.st * es % 4 == 0 && r.sh * es % 4 == 0 &&
            D * es % 16 == 0 && r.st >= D && r.st * es * 64 < (1l << 29);
@@ -938,10 +980,12 @@ hipError_t run_state(const semicrf_attention& p, const Sweeps<N>& set, hipStream
         const dim3 grid(sweep_grid(set.s[0], N, group)), block(64 * sweep_waves(P));
         bool fast = true;
         for (const Sweep& w : set.s) fast = fast && fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es);
-        if (fast)
-            hipLaunchKernelGGL((k_attn_state<T, P, C, true, N>), grid, block, 0, stream, set, group);
+        if (!fast)
+            hipLaunchKernelGGL((k_attn_state<T, P, C, LOOSE, N>), grid, block, 0, stream, set, group);
+        else if (p.Dk == P && p.Dv == P)
+            hipLaunchKernelGGL((k_attn_state<T, P, C, FULL, N>), grid, block, 0, stream, set, group);
         else
-            hipLaunchKernelGGL((k_attn_state<T, P, C, false, N>), grid, block, 0, stream, set, group);
+            hipLaunchKernelGGL((k_attn_state<T, P, C, PART, N>), grid, block, 0, stream, set, group);
         return hipGetLastError();
     });
 }
@@ -957,10 +1001,12 @@ hipError_t run_sweep(const semicrf_attention& p, const Sweeps<N>& set, hipStream
         for (const Sweep& w : set.s)
             fast = fast && fast_role(w.a, w.Da, es) && fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es) &&
                    fast_out(w, es);
-        if (fast)
-            hipLaunchKernelGGL((k_attn_sweep<T, P, C, true, N>), grid, block, 0, stream, set, group);
+        if (!fast)
+            hipLaunchKernelGGL((k_attn_sweep<T, P, C, LOOSE, N>), grid, block, 0, stream, set, group);
+        else if (p.Dk == P && p.Dv == P)
+            hipLaunchKernelGGL((k_attn_sweep<T, P, C, FULL, N>), grid, block, 0, stream, set, group);
         else
-            hipLaunchKernelGGL((k_attn_sweep<T, P, C, false, N>), grid, block, 0, stream, set, group);
+            hipLaunchKernelGGL((k_attn_sweep<T, P, C, PART, N>), grid, block, 0, stream, set, group);
         return hipGetLastError();
     });
 }
