@@ -378,25 +378,31 @@ struct State {
     }
     // S += sum_j w_j b_j c_j^T over one product step from row k0; `c` the columns' fragments.  Rows
     // of S from `rows` on are left out, 32 at a time.
-    template <int MODE>
-    __device__ __forceinline__ void update(const T* bbuf, int ld, int k0, int rows,
-                                           const typename Mma<T>::Frag (&c)[VT], const float (&w)[E]) {
+    struct Step {
+        typename Mma<T>::Frag a[ST];
         Parts<T, update_parts<T>()> p[VT];
+        __device__ __forceinline__ void prepare(const T* bbuf, int ld, int k0, const typename Mma<T>::Frag (&c)[VT],
+                                                const float (&w)[E]) {
 #pragma unroll
-        for (int v = 0; v < VT; ++v)
+            for (int t = 0; t < ST; ++t) a[t] = frag_col(bbuf, ld, k0, 16 * t);
 #pragma unroll
-            for (int j = 0; j < E; j += 2) p[v].set(j, (float)c[v][j] * w[j], (float)c[v][j + 1] * w[j + 1]);
+            for (int v = 0; v < VT; ++v)
 #pragma unroll
-        for (int t0 = 0; t0 < ST; t0 += 2)
+                for (int j = 0; j < E; j += 2) p[v].set(j, (float)c[v][j] * w[j], (float)c[v][j + 1] * w[j + 1]);
+        }
+    };
+    template <int MODE>
+    __device__ __forceinline__ void update(const Step& x, int rows) {
+        constexpr int TG = MODE == FULL ? ST : 2;
+#pragma unroll
+        for (int t0 = 0; t0 < ST; t0 += TG)
             if (MODE == FULL || 16 * t0 < rows)
 #pragma unroll
-                for (int t = t0; t < t0 + 2; ++t) {
-                    const auto a = frag_col(bbuf, ld, k0, 16 * t);
+                for (int n = 0; n < update_parts<T>(); ++n)
 #pragma unroll
-                    for (int v = 0; v < VT; ++v)
+                    for (int t = t0; t < t0 + TG; ++t)
 #pragma unroll
-                        for (int n = 0; n < update_parts<T>(); ++n) s[t][v] = Mma<T>::mma(a, p[v].f[n], s[t][v]);
-                }
+                        for (int v = 0; v < VT; ++v) s[t][v] = Mma<T>::mma(x.a[t], x.p[v].f[n], s[t][v]);
     }
 };
 
@@ -450,7 +456,9 @@ __device__ __forceinline__ void update_rest(State<T, P>& S, const T* sb, const T
         for (int v = 0; v < VT; ++v) c[v] = frag_col(sc, LD, k0, ((threadIdx.x >> 6) * VT + v) * 16);
         float u[Mma<T>::E];
         update_weights<T>(g2, su, k0, m, e, u);
-        S.template update<FULL>(sb, LD, k0, P, c, u);
+        typename State<T, P>::Step x;
+        x.prepare(sb, LD, k0, c, u);
+        S.template update<FULL>(x, P);
     }
 }
 
@@ -501,7 +509,11 @@ k_attn_state(const Sweeps<N> set, int group) {
             for (int v = 0; v < VT; ++v) c[v] = frag_col(sc, Tl::LD, k0, (wave * VT + v) * 16);
             float u[M::E];
             up.get(k0, u);
-            S.template update<MODE>(sb, Tl::LD, k0, w.Da, c, u);
+            typename St::Step x;
+            x.prepare(sb, Tl::LD, k0, c, u);
+            __builtin_amdgcn_sched_barrier(0);
+            S.template update<MODE>(x, w.Da);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (t_end > t_begin && (t_end - t_begin) % C)
@@ -720,14 +732,16 @@ k_attn_sweep(const Sweeps<N> set, int group) {
 #pragma unroll
                 for (int j = 0; j < E; j += 2)
                     p[v].set(j, S.s[kb * St::TPK + j / 4][v][j % 4], S.s[kb * St::TPK + j / 4][v][j % 4 + 1]);
+            typename M::Frag a[IT];
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const auto a = frag_ordered<T>(sa, Tl::LD, 16 * it, kb * KS);
+            for (int it = 0; it < IT; ++it) a[it] = frag_ordered<T>(sa, Tl::LD, 16 * it, kb * KS);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int v = 0; v < VT; ++v)
+            for (int n = 0; n < state_parts<T>(); ++n)
 #pragma unroll
-                    for (int n = 0; n < state_parts<T>(); ++n) acc[it][v] = M::mma(p[v].f[n], a, acc[it][v]);
-            }
+                for (int it = 0; it < IT; ++it)
+#pragma unroll
+                    for (int v = 0; v < VT; ++v) acc[it][v] = M::mma(p[v].f[n], a[it], acc[it][v]);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -744,15 +758,22 @@ k_attn_sweep(const Sweeps<N> set, int group) {
             typename M::Frag c[VT];
 #pragma unroll
             for (int v = 0; v < VT; ++v) c[v] = frag_col(sc, Tl::LD, k0, (wave * VT + v) * 16);
+            {
+                typename M::Frag a[IT];
 #pragma unroll
-            for (int it = k0 / 16; it < IT; ++it) {
-                const auto a = frag_ordered<T>(sm, LDM, 16 * it, k0);
+                for (int it = k0 / 16; it < IT; ++it) a[it] = frag_ordered<T>(sm, LDM, 16 * it, k0);
 #pragma unroll
-                for (int v = 0; v < VT; ++v) acc[it][v] = M::mma(c[v], a, acc[it][v]);
+                for (int it = k0 / 16; it < IT; ++it)
+#pragma unroll
+                    for (int v = 0; v < VT; ++v) acc[it][v] = M::mma(c[v], a[it], acc[it][v]);
             }
+            __builtin_amdgcn_sched_barrier(0);
             float u[E];
             up.get(k0, u);
-            S.template update<MODE>(sb, Tl::LD, k0, w.Da, c, u);
+            typename St::Step x;
+            x.prepare(sb, Tl::LD, k0, c, u);
+            __builtin_amdgcn_sched_barrier(0);
+            S.template update<MODE>(x, w.Da);
             __builtin_amdgcn_sched_barrier(0);
         }
         const int col = wave * VT * 16 + 4 * gr;
