@@ -369,6 +369,22 @@ def test_attention_and_its_gradient(crf, case):
     assert all((again[n] == d[n]).all() for n in d)
 
 
+# rows narrower than a 16-byte piece, one element past whole pieces, and next to wide ones
+NARROW_ATT = [
+    (2, 150, 2, 1, 3, 7, "bf16", "ragged", True),
+    (3, 70, 2, 2, 5, 100, "bf16", "ragged", False),
+    (2, 140, 3, 3, 2, 3, "f32", "ragged", True),
+    (2, 130, 2, 1, 9, 97, "bf16", "full", True),
+    (2, 1500, 2, 1, 33, 65, "f32", "ragged", True),
+    (2, 2000, 1, 1, 65, 33, "bf16", "ragged", True),
+]
+
+
+@pytest.mark.parametrize("case", NARROW_ATT, ids=[f"B{c[0]}T{c[1]}D{c[4]}_{c[5]}{c[6]}" for c in NARROW_ATT])
+def test_attention_rows_of_odd_widths(crf, case):
+    test_attention_and_its_gradient(crf, case)
+
+
 def test_attention_gradient_against_differences(crf):
     """The output is linear in each of q, k, v and the state: half the difference of two calls
     is the slope exactly, up to the rounding of the calls."""
