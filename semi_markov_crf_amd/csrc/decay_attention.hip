@@ -220,7 +220,9 @@ __device__ __forceinline__ float power(float g2, int n) {
 //   LOOSE: rows of any width, stride and alignment, by pointers; the same left out.
 // A descriptor spans exactly the chunk's valid rows, less than 2^29 bytes, so that rows and columns
 // out of range read as zeros with no branch (bit 31 of the offset puts a column out of range); rows
-// are then whole pieces of 16 bytes from dword addresses.
+// are then whole pieces of 16 bytes from dword addresses.  Measured in bfloat16: 32 x 800 positions,
+// 8 heads of 64 columns 36 us FULL, 42 PART, 52 LOOSE; 16 x 800 of 40 and 48 columns 36 PART, 47 LOOSE;
+// of 128 and 64 columns 53 PART against 62 when all 128 x 128 products are done.
 enum { FULL, PART, LOOSE };
 
 // A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces; a thread's
@@ -301,7 +303,8 @@ __device__ __forceinline__ const T* role_base(const Role& r, int b, int h) {
 
 // One wavefront for each 16 columns of the state.
 constexpr int sweep_waves(int P) { return P / 16; }
-// Wavefronts a SIMD that the sweep's registers are held to: as many as run without spills.
+// Wavefronts a SIMD that the sweep's registers are held to: as many as run with no more than a
+// dozen values spilled.
 template <class T, int P>
 constexpr int sweep_occupancy() { return P == 128 ? 2 : sizeof(T) == 2 ? 3 : 4; }
 
@@ -462,6 +465,10 @@ __device__ __forceinline__ void update_rest(State<T, P>& S, const T* sb, const T
     }
 }
 
+// The state of every segment alone, from zero: S = sum_j su gamma^(m-1-j+e) b_j c_j^T, a chunk at a
+// time.  Bound by HBM where segments are many: 4 x 100,000 positions, 8 heads of 64 columns, 0.82 GB
+// of bfloat16 in 175 us (4.7 TB/s).  fp32 takes the slower matrix instructions: 100,001 positions, 6
+// heads, both states of the gradients, 0.61 GB in 147 us (4.2 TB/s).
 template <class T, int P, int C, int MODE, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), P == 128 ? 2 : 4) void
 k_attn_state(const Sweeps<N> set, int group) {
@@ -522,7 +529,8 @@ k_attn_state(const Sweeps<N> set, int group) {
 }
 
 // Start of every segment from the segments' own states, in place, in order; the state after
-// the last position to `out`.  One or two states: blockIdx.y = state * H + head.
+// the last position to `out`.  One or two states: blockIdx.y = state * H + head.  Bound by the
+// latency of its loads, 16 segments at a time: 23 segments of 32 heads, 12 MB, 9 us.
 // grid (ceil(D / 256), states * H, B), D = Da Dc
 struct Scan {
     float* local[2];
@@ -620,6 +628,16 @@ __device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m
     }
 }
 
+// The sweep over every segment from its start.  A chunk: its rows go from registers to LDS (the next
+// chunk's loads leave at once), the masked products are shared out and exchanged through LDS, then
+// each wavefront has its columns to itself: the state's part, the chunk's own part, the update.  The
+// fragments of a product step are read and split ahead of its products (scheduling barriers keep
+// them there), and products that add to one tile are apart.
+// 4 x 100,000 positions, 8 heads of 64 columns in bfloat16: 1.64 GB in 385 us (4.3 TB/s), bound by
+// HBM; 32 x 800 positions, 8 heads on 256 workgroups: 35 us, bound by the latency of 13 chunks in
+// order, some 5,500 cycles each (LDS rows 700, masked products 1,200, state's part 700, own part
+// and update 1,500, loads and stores 1,200).  The three sweeps of the gradients in fp32, 100,001 positions, 6 heads:
+// 40 GFLOP of matrix instructions in 375 to 440 us, about 100 of the 155 TFLOP/s that a large product reaches.
 template <class T, int P, int C, int MODE, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), (sweep_occupancy<T, P>())) void
 k_attn_sweep(const Sweeps<N> set, int group) {
@@ -789,7 +807,8 @@ k_attn_sweep(const Sweeps<N> set, int group) {
 }
 
 // Sums over the query heads of a group, in order: out[row, hk, :] = sum of x[row, hk, 0 .. group).
-// blockIdx.y: 0 sums dk, 1 sums dv.  One piece of a row a thread.
+// blockIdx.y: 0 sums dk, 1 sums dv.  One piece of a row a thread.  Bound by memory: 25,600 rows of
+// 8 heads to 2, 64 columns, 118 MB in 17 us (6.9 TB/s: the sums' terms are still in the memory-side cache).
 struct GroupSum {
     const float* x[2];
     void* out[2];
@@ -827,6 +846,10 @@ __global__ __launch_bounds__(256) void k_attn_group(const GroupSum a) {
 }
 
 // ------------------------------------------------------------------ one token
+// S = gamma S + k v^T, o = scale q S: a state is read and written once, so HBM bounds a batch (256
+// streams, 16 heads of 128 x 128, 0.46 GB in 97 us, 4.8 TB/s) and the launch a single stream (8 heads
+// of 64 x 64 4.6 us).  A workgroup a head, so that one stream still spreads over compute units and no sum
+// leaves a workgroup.
 // grid (Hq, B), block 256: LR lanes take 4 columns each of a state row, 256 / LR row groups.
 template <class T>
 __global__ __launch_bounds__(256) void k_attn_step(const semicrf_attention p, const int32_t* slots,
@@ -896,8 +919,8 @@ int sweep_slots(const semicrf_attention& p) {
 // units of one chunk of the sweep where a compute unit has one workgroup (2 us at width 64, 64
 // bfloat16 or 32 fp32 positions); with w workgroups a unit it takes 0.4 + 0.6 w, the state's pass 0.4
 // of that, launches and prologues 6 (9 with gradients), the join 0.06 a segment.  Measured, one
-// segment against the choice: 1 x 3,000 positions, 2 heads, bfloat16 99 and 19 us; 8 x 800, 8 heads 32
-// and 28 us, but its gradients 34 and (4 segments) 46 us: one is kept.
+// segment against the choice: 1 x 3,000 positions, 2 heads, bfloat16 93 and 25 us; 8 x 800, 8 heads 32
+// and 30 us, fp32 57 and 44; but bfloat16 gradients 31 and (4 segments) 42 us: one is kept.
 int segment(const semicrf_attention& p, bool grad) {
     const int C = chunk_of(p), sweeps = grad ? 3 : 1, states = grad ? 2 : 1, group = p.Hq / p.Hk;
     const long bh = (long)p.B * p.Hq, n = ((long)p.T + C - 1) / C;

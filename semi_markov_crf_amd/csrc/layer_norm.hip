@@ -69,6 +69,10 @@ __device__ __forceinline__ void load_weights(const void* p, int c, int N, float 
 // the weights stay in registers.
 //
 // MODE: rows fill the lanes' pieces exactly (G * KP * V elements), or not, or are narrower than one.
+//
+// Forward, 25,600 ragged rows of 1,024 bfloat16: 92 MB in 17 us (5.4 TB/s).  128 rows of 333 float32:
+// 3.2 us, the launch.  Backward, 400,000 rows of 512 bfloat16: 1.23 GB in 221 us (5.6 TB/s), the sum of
+// 1,024 partial rows 6.6 us.
 enum { EXACT, MASKED, NARROWER };
 
 template <class T, class W, int G, int KP, int NT, int MODE>
@@ -306,8 +310,8 @@ int norm_wgs(long rows, int G, int NT, int waves) {
 }
 constexpr int norm_threads(int G) { return G > 256 ? G : 256; }
 // The gradient runs at 4 wavefronts a SIMD: the row on its way hides the latency, and every
-// workgroup leaves a partial row (400,000 rows of 512 bfloat16, with the partials' sum: 238 us
-// at 4, 299 at 6, 267 at 8; workgroups of 512 threads 326 at 4).  Narrow rows leave little and have
+// workgroup leaves a partial row (400,000 rows of 512 bfloat16, with the partials' sum: 228 us
+// at 4; 299 at 6 and 267 at 8 when it took 238 at 4, workgroups of 512 threads 326 at 4).  Narrow rows leave little and have
 // little on its way: 8.
 constexpr int norm_grad_waves(int G) { return G < 32 ? 8 : 4; }
 
