@@ -311,16 +311,18 @@ int norm_wgs(long rows, int G, int NT, int waves) {
 constexpr int norm_threads(int G) { return G > 256 ? G : 256; }
 // The gradient runs at 4 wavefronts a SIMD: the row on its way hides the latency, and every
 // workgroup leaves a partial row (400,000 rows of 512 bfloat16, with the partials' sum: 228 us
-// at 4; 299 at 6 and 267 at 8 when it took 238 at 4, workgroups of 512 threads 326 at 4).  Narrow rows leave little and have
-// little on its way: 8.
+// at 4; 299 at 6 and 267 at 8 when it took 238 at 4, workgroups of 512 threads 326 at 4).  Narrow
+// rows leave little and have little on its way: 8.
 constexpr int norm_grad_waves(int G) { return G < 32 ? 8 : 4; }
 
 // Calls f with the shape's G, KP and MODE.
-template <class F>
-hipError_t with_shape(int N, int V, F&& f) {
+template <int V, class F>
+hipError_t with_shape(int N, F&& f) {
     const Shape2 s = norm_shape(N, V);
     using I = std::integral_constant<int, MASKED>;
-    if (N < V) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>(), std::integral_constant<int, NARROWER>());
+    if (N < V)
+        return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>(),
+                 std::integral_constant<int, NARROWER>());
 #define CASE(g, kp)                                                                                                  \
     if (s.G == g && s.KP == kp) {                                                                                    \
         std::integral_constant<int, g> gg;                                                                           \
@@ -328,28 +330,29 @@ hipError_t with_shape(int N, int V, F&& f) {
         return N == g * kp * V ? f(gg, kk, std::integral_constant<int, EXACT>()) : f(gg, kk, I());                   \
     }
     CASE(2, 1) CASE(4, 1) CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(64, 1) CASE(64, 2) CASE(256, 1) CASE(256, 2)
-    CASE(1024, 1) CASE(1024, 2) CASE(1024, 4) CASE(1024, 8)
+    CASE(1024, 1) CASE(1024, 2) CASE(1024, 4)
+    if constexpr (V == 4) { CASE(1024, 8) }    // rows have at most 32,768 elements
 #undef CASE
     return hipErrorInvalidValue;
 }
 
 template <class T, class W>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
-    return with_shape(a.N, 16 / (int)sizeof(T), [&](auto g, auto kp, auto mode) {
+    return with_shape<16 / (int)sizeof(T)>(a.N, [&](auto g, auto kp, auto mode) {
         constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = norm_threads(G);
-        hipLaunchKernelGGL((k_layer_norm<T, W, G, KP, NT, decltype(mode)::value>), dim3(norm_wgs((long)a.B * a.T, G, NT, 8)),
-                           dim3(NT), 0, stream, a);
+        const int nwg = norm_wgs((long)a.B * a.T, G, NT, 8);
+        hipLaunchKernelGGL((k_layer_norm<T, W, G, KP, NT, decltype(mode)::value>), dim3(nwg), dim3(NT), 0, stream, a);
         return hipGetLastError();
     });
 }
 
 template <class T, class W>
 hipError_t run_norm_grad(const NormArgs& a, float* part, hipStream_t stream) {
-    return with_shape(a.N, 16 / (int)sizeof(T), [&](auto g, auto kp, auto mode) {
+    return with_shape<16 / (int)sizeof(T)>(a.N, [&](auto g, auto kp, auto mode) {
         constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = norm_threads(G);
         const int nwg = norm_wgs((long)a.B * a.T, G, NT, norm_grad_waves(G));
-        hipLaunchKernelGGL((k_layer_norm_grad<T, W, G, KP, NT, decltype(mode)::value>), dim3(nwg), dim3(NT), 0, stream, a,
-                           part);
+        hipLaunchKernelGGL((k_layer_norm_grad<T, W, G, KP, NT, decltype(mode)::value>), dim3(nwg), dim3(NT), 0, stream,
+                           a, part);
         if (a.grad_weight || a.grad_bias)
             hipLaunchKernelGGL((k_norm_partials<W>), dim3((2 * a.N + 15) / 16), dim3(256), 0, stream,
                                part, nwg, a.N, (W*)a.grad_weight, (W*)a.grad_bias);
