@@ -37,6 +37,7 @@ namespace semicrf {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -679,16 +680,27 @@ k_attn_sweep(const Sweeps<N> set, int group) {
     St S;
     S.load(w.state ? w.state + (bh * w.state_nseg + (w.state_nseg > 1 ? seg : 0)) * D : nullptr, w.Da,
            w.Dc, w.transposed, sigma);
-    // masked products above the diagonal stay zero
-    for (int i = threadIdx.x; i < C * LDM; i += NT) sm[i] = (T)0.0f;
-    // scale gamma^(i-j) in a tile of products (rows j = 4 gr + r, column i = r16): on the
-    // diagonal, and one tile off it
-    float diag[4], below[4], inter[IT];
+    // Weights of the masked products, scale gamma^(i-j) where i >= j.  BIG: three tiles of 32 x 32, a
+    // wavefront each; lanes hold column i = r32, rows j = 8 q + 4 h32 + r.  Otherwise in tiles of 16
+    // (rows j = 4 gr + r, column i = r16): on the diagonal, and one tile off it.
+    constexpr bool BIG = sizeof(T) == 2 && NW >= 4;
+    const int r32 = lane & 31, h32 = lane >> 5;
+    float own[BIG ? 16 : 1], diag[4], below[4], inter[IT];
+    if constexpr (BIG) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int d = r16 - 4 * gr - r;
-        diag[r] = d >= 0 ? w.scale * power(g2, d) : 0.0f;
-        below[r] = w.scale * power(g2, 16 + d);
+        for (int i = 0; i < 16; ++i) {
+            const int d = r32 - 8 * (i / 4) - 4 * h32 - i % 4 + (wave == 2 ? 32 : 0);
+            own[i] = d >= 0 ? w.scale * power(g2, d) : 0.0f;
+        }
+    } else {
+        // products above the diagonal stay zero
+        for (int i = threadIdx.x; i < C * LDM; i += NT) sm[i] = (T)0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int d = r16 - 4 * gr - r;
+            diag[r] = d >= 0 ? w.scale * power(g2, d) : 0.0f;
+            below[r] = w.scale * power(g2, 16 + d);
+        }
     }
 #pragma unroll
     for (int it = 0; it < IT; ++it) inter[it] = w.si / sigma * power(g2, 16 * it + r16 + 1 - w.e);
@@ -711,26 +723,50 @@ k_attn_sweep(const Sweeps<N> set, int group) {
             tc.load(w.c, pc, w.Dc, t0 + C, mn, L, w.reverse);
         }
         // masked products: the tiles on and below the diagonal, dealt out to the wavefronts
-#pragma unroll
-        for (int n0 = 0; n0 < IT * (IT + 1) / 2; n0 += NW) {
-            const int n = n0 + wave;
-            if (n0 + NW <= IT * (IT + 1) / 2 || n < IT * (IT + 1) / 2) {
-                const int it = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, jt = n - it * (it + 1) / 2;
-                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (BIG) {
+            if (wave < 3) {
+                const int it = wave > 0 ? 32 : 0, jt = wave == 1 ? 32 : 0;
+                const bf16* rb = (const bf16*)sb + (jt + r32) * Tl::LD + 4 * h32;
+                const bf16* ra = (const bf16*)sa + (it + r32) * Tl::LD + 8 * h32;
+                f32x16 acc = {};
 #pragma unroll
                 for (int k1 = 0; k1 < P; k1 += 32)
                     if (MODE == FULL || k1 < w.Da)
 #pragma unroll
-                        for (int k0 = k1; k0 < k1 + 32; k0 += KS)
-                            acc = M::mma(frag_row(sb, Tl::LD, 16 * jt, k0), frag_ordered<T>(sa, Tl::LD, 16 * it, k0), acc);
-                const float step = it - jt <= 1 ? 1.0f : it - jt == 2 ? g16 : g16 * g16;
+                        for (int s = 0; s < 2; ++s)
+                            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                __builtin_shufflevector(*(const bf16x4*)(rb + k1 + 8 * s), *(const bf16x4*)(rb + k1 + 8 * s + 16),
+                                                        0, 1, 2, 3, 4, 5, 6, 7),
+                                *(const bf16x8*)(ra + k1 + 16 * s), acc, 0, 0, 0);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] *= jt < it ? below[r] * step : diag[r];
-                T* to = sm + (16 * it + r16) * LDM + ordered<T>(16 * jt + 4 * gr);
-                if constexpr (sizeof(T) == 4)
-                    *(f32x4*)to = acc;
-                else
-                    *(bf16x4*)to = bf16x4{(bf16)acc[0], (bf16)acc[1], (bf16)acc[2], (bf16)acc[3]};
+                for (int q = 0; q < 4; ++q) {
+                    T* to = sm + (it + r32) * LDM + ordered<T>(jt + 8 * q + 4 * h32);
+                    *(bf16x4*)to = bf16x4{(bf16)(acc[4 * q] * own[4 * q]), (bf16)(acc[4 * q + 1] * own[4 * q + 1]),
+                                          (bf16)(acc[4 * q + 2] * own[4 * q + 2]), (bf16)(acc[4 * q + 3] * own[4 * q + 3])};
+                }
+            }
+        } else {
+#pragma unroll
+            for (int n0 = 0; n0 < IT * (IT + 1) / 2; n0 += NW) {
+                const int n = n0 + wave;
+                if (n0 + NW <= IT * (IT + 1) / 2 || n < IT * (IT + 1) / 2) {
+                    const int it = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, jt = n - it * (it + 1) / 2;
+                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k1 = 0; k1 < P; k1 += 32)
+                        if (MODE == FULL || k1 < w.Da)
+#pragma unroll
+                            for (int k0 = k1; k0 < k1 + 32; k0 += KS)
+                                acc = M::mma(frag_row(sb, Tl::LD, 16 * jt, k0), frag_ordered<T>(sa, Tl::LD, 16 * it, k0), acc);
+                    const float step = it - jt <= 1 ? 1.0f : it - jt == 2 ? g16 : g16 * g16;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[r] *= jt < it ? below[r] * step : diag[r];
+                    T* to = sm + (16 * it + r16) * LDM + ordered<T>(16 * jt + 4 * gr);
+                    if constexpr (sizeof(T) == 4)
+                        *(f32x4*)to = acc;
+                    else
+                        *(bf16x4*)to = bf16x4{(bf16)acc[0], (bf16)acc[1], (bf16)acc[2], (bf16)acc[3]};
+                }
             }
         }
         __syncthreads();
