@@ -223,7 +223,7 @@ __device__ __forceinline__ float power(float g2, int n) {
 // out of range read as zeros with no branch (bit 31 of the offset puts a column out of range); rows
 // are then whole pieces of 16 bytes from dword addresses.  Measured in bfloat16: 32 x 800 positions,
 // 8 heads of 64 columns 36 us FULL, 42 PART, 52 LOOSE; 16 x 800 of 40 and 48 columns 36 PART, 47 LOOSE;
-// of 128 and 64 columns 53 PART against 62 when all 128 x 128 products are done.
+// of 128 and 64 columns 53 PART, 62 when all 128 x 128 products are done.
 enum { FULL, PART, LOOSE };
 
 // A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces; a thread's
@@ -635,10 +635,11 @@ __device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m
 // fragments of a product step are read and split ahead of its products (scheduling barriers keep
 // them there), and products that add to one tile are apart.
 // 4 x 100,000 positions, 8 heads of 64 columns in bfloat16: 1.64 GB in 385 us (4.3 TB/s), bound by
-// HBM; 32 x 800 positions, 8 heads on 256 workgroups: 35 us, bound by the latency of 13 chunks in
-// order, some 5,500 cycles each (LDS rows 700, masked products 1,200, state's part 700, own part
-// and update 1,500, loads and stores 1,200).  The three sweeps of the gradients in fp32, 100,001 positions, 6 heads:
-// 40 GFLOP of matrix instructions in 375 to 440 us, about 100 of the 155 TFLOP/s that a large product reaches.
+// HBM; 32 x 800 positions, 8 heads on 256 workgroups: 34 us, bound by the latency of 13 chunks in
+// order, some 5,100 cycles each (rows into LDS 600, next loads 400, masked products 900, state's
+// part 700, own part and update 1,600, stores and the wait for loads 700).  The three sweeps of the
+// gradients in fp32, 100,001 positions, 6 heads: 40 GFLOP of matrix instructions in 375 to 440 us,
+// about 100 of the 155 TFLOP/s that a large product reaches.
 template <class T, int P, int C, int MODE, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), (sweep_occupancy<T, P>())) void
 k_attn_sweep(const Sweeps<N> set, int group) {
@@ -682,7 +683,8 @@ k_attn_sweep(const Sweeps<N> set, int group) {
            w.Dc, w.transposed, sigma);
     // Weights of the masked products, scale gamma^(i-j) where i >= j.  BIG: three tiles of 32 x 32, a
     // wavefront each; lanes hold column i = r32, rows j = 8 q + 4 h32 + r.  Otherwise in tiles of 16
-    // (rows j = 4 gr + r, column i = r16): on the diagonal, and one tile off it.
+    // (rows j = 4 gr + r, column i = r16): on the diagonal, and one tile off it.  16 x 800 positions, 8
+    // heads of 128 columns: 54.9 us against 56.7 in tiles of 16, the gradients 98.7 against 102.8.
     constexpr bool BIG = sizeof(T) == 2 && NW >= 4;
     const int r32 = lane & 31, h32 = lane >> 5;
     float own[BIG ? 16 : 1], diag[4], below[4], inter[IT];
@@ -735,8 +737,8 @@ k_attn_sweep(const Sweeps<N> set, int group) {
 #pragma unroll
                         for (int s = 0; s < 2; ++s)
                             acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                __builtin_shufflevector(*(const bf16x4*)(rb + k1 + 8 * s), *(const bf16x4*)(rb + k1 + 8 * s + 16),
-                                                        0, 1, 2, 3, 4, 5, 6, 7),
+                                __builtin_shufflevector(*(const bf16x4*)(rb + k1 + 8 * s),
+                                                        *(const bf16x4*)(rb + k1 + 8 * s + 16), 0, 1, 2, 3, 4, 5, 6, 7),
                                 *(const bf16x8*)(ra + k1 + 16 * s), acc, 0, 0, 0);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
