@@ -25,10 +25,11 @@
 // state, which stays in fp32 accumulators for the whole sweep) and all rows; the masked
 // products a.b^T of a chunk are shared out by rows and exchanged through LDS.
 //
-// Rounding (bfloat16): inputs are exact.  The masked products are rounded to bfloat16 once
-// before the second product, like the output.  The state is taken as the sum of two bfloat16
-// numbers (16 bits) when rows read it, and c scaled by its decay as the sum of three (24 bits)
-// when the state is updated, so that the state itself keeps fp32 accuracy.
+// Rounding (bfloat16): inputs are exact.  The masked products enter the second product, and the
+// state the rows that read it, as the sum of two bfloat16 numbers (16 bits): their error is 2^-8 of
+// the output's own rounding to 8 bits.  One number instead of two would add an error as large as
+// the output's.  c scaled by its decay is the sum of three (24 bits) when the state is updated, so
+// that the state itself keeps fp32 accuracy.
 #include "common.h"
 #include "encoder.h"
 
@@ -157,7 +158,21 @@ struct Parts {
 template <class T>
 constexpr int state_parts() { return sizeof(T) == 4 ? 1 : 2; }
 template <class T>
+constexpr int masked_parts() { return sizeof(T) == 4 ? 1 : 2; }
+template <class T>
 constexpr int update_parts() { return sizeof(T) == 4 ? 1 : 3; }
+
+// Four consecutive masked products as parts that add up to them, each part's array `stride`
+// elements after the one before.
+__device__ __forceinline__ void put_masked(float* to, int, f32x4 x) { *(f32x4*)to = x; }
+__device__ __forceinline__ void put_masked(bf16* to, int stride, f32x4 x) {
+    Parts<bf16, masked_parts<bf16>()> p;
+    p.set(0, x[0], x[1]);
+    p.set(2, x[2], x[3]);
+#pragma unroll
+    for (int n = 0; n < masked_parts<bf16>(); ++n)
+        *(bf16x4*)(to + n * stride) = __builtin_shufflevector(p.f[n], p.f[n], 0, 1, 2, 3);
+}
 
 // ------------------------------------------------------------------ a sweep
 struct Role {
@@ -305,9 +320,9 @@ __device__ __forceinline__ const T* role_base(const Role& r, int b, int h) {
 // One wavefront for each 16 columns of the state.
 constexpr int sweep_waves(int P) { return P / 16; }
 // Wavefronts a SIMD that the sweep's registers are held to: as many as run with no more than a
-// dozen values spilled.
+// dozen values spilled, and in bfloat16 of width 32 as the LDS lets run.
 template <class T, int P>
-constexpr int sweep_occupancy() { return P == 128 ? 2 : sizeof(T) == 2 ? 3 : 4; }
+constexpr int sweep_occupancy() { return P == 128 || (sizeof(T) == 2 && P == 32) ? 2 : sizeof(T) == 2 ? 3 : 4; }
 
 // gamma^m of the state.  Near 1 it is applied as S + (gamma^m - 1) S: over thousands of chunks a
 // factor rounded once would bend every old contribution the same way.
@@ -647,8 +662,8 @@ k_attn_sweep(const Sweeps<N> set, int group) {
     using St = State<T, P>;
     constexpr int NW = St::NW, NT = 64 * NW, VT = St::VT, IT = C / 16, KS = M::KS, E = M::E;
     using Tl = Tile<T, P, C, NT, MODE>;
-    constexpr int LDM = lds_pitch<T>(C);
-    __shared__ __align__(16) T sa[C * Tl::LD], sb[C * Tl::LD], sc[C * Tl::LD], sm[C * LDM];
+    constexpr int LDM = lds_pitch<T>(C), MP = masked_parts<T>();
+    __shared__ __align__(16) T sa[C * Tl::LD], sb[C * Tl::LD], sc[C * Tl::LD], sm[MP * C * LDM];
     Place at;
     if (!place(set.s[0], N, group, at)) return;
     const Sweep w = set.s[N == 1 ? 0 : at.sweep];
@@ -696,7 +711,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
         }
     } else {
         // products above the diagonal stay zero
-        for (int i = threadIdx.x; i < C * LDM; i += NT) sm[i] = (T)0.0f;
+        for (int i = threadIdx.x; i < MP * C * LDM; i += NT) sm[i] = (T)0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int d = r16 - 4 * gr - r;
@@ -743,31 +758,43 @@ k_attn_sweep(const Sweeps<N> set, int group) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     T* to = sm + (it + r32) * LDM + ordered<T>(jt + 8 * q + 4 * h32);
-                    *(bf16x4*)to = bf16x4{(bf16)(acc[4 * q] * own[4 * q]), (bf16)(acc[4 * q + 1] * own[4 * q + 1]),
-                                          (bf16)(acc[4 * q + 2] * own[4 * q + 2]), (bf16)(acc[4 * q + 3] * own[4 * q + 3])};
+                    put_masked(to, C * LDM, f32x4{acc[4 * q] * own[4 * q], acc[4 * q + 1] * own[4 * q + 1],
+                                                  acc[4 * q + 2] * own[4 * q + 2], acc[4 * q + 3] * own[4 * q + 3]});
                 }
             }
         } else {
+            // the products of all its tiles do not wait for one another
+            constexpr int NT2 = IT * (IT + 1) / 2, ROUNDS = (NT2 + NW - 1) / NW;
+            f32x4 acc[ROUNDS];
+            auto tile = [&](int n, int& it, int& jt) {
+                it = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3;
+                jt = n - it * (it + 1) / 2;
+            };
 #pragma unroll
-            for (int n0 = 0; n0 < IT * (IT + 1) / 2; n0 += NW) {
-                const int n = n0 + wave;
-                if (n0 + NW <= IT * (IT + 1) / 2 || n < IT * (IT + 1) / 2) {
-                    const int it = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, jt = n - it * (it + 1) / 2;
-                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < ROUNDS; ++k) {
+                const int n = k * NW + wave;
+                acc[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if ((k + 1) * NW <= NT2 || n < NT2) {
+                    int it, jt;
+                    tile(n, it, jt);
 #pragma unroll
                     for (int k1 = 0; k1 < P; k1 += 32)
                         if (MODE == FULL || k1 < w.Da)
 #pragma unroll
                             for (int k0 = k1; k0 < k1 + 32; k0 += KS)
-                                acc = M::mma(frag_row(sb, Tl::LD, 16 * jt, k0), frag_ordered<T>(sa, Tl::LD, 16 * it, k0), acc);
+                                acc[k] = M::mma(frag_row(sb, Tl::LD, 16 * jt, k0), frag_ordered<T>(sa, Tl::LD, 16 * it, k0), acc[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < ROUNDS; ++k) {
+                const int n = k * NW + wave;
+                if ((k + 1) * NW <= NT2 || n < NT2) {
+                    int it, jt;
+                    tile(n, it, jt);
                     const float step = it - jt <= 1 ? 1.0f : it - jt == 2 ? g16 : g16 * g16;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[r] *= jt < it ? below[r] * step : diag[r];
-                    T* to = sm + (16 * it + r16) * LDM + ordered<T>(16 * jt + 4 * gr);
-                    if constexpr (sizeof(T) == 4)
-                        *(f32x4*)to = acc;
-                    else
-                        *(bf16x4*)to = bf16x4{(bf16)acc[0], (bf16)acc[1], (bf16)acc[2], (bf16)acc[3]};
+                    for (int r = 0; r < 4; ++r) acc[k][r] *= jt < it ? below[r] * step : diag[r];
+                    put_masked(sm + (16 * it + r16) * LDM + ordered<T>(16 * jt + 4 * gr), C * LDM, acc[k]);
                 }
             }
         }
@@ -814,10 +841,11 @@ k_attn_sweep(const Sweeps<N> set, int group) {
             typename M::Frag c[VT];
 #pragma unroll
             for (int v = 0; v < VT; ++v) c[v] = frag_col(sc, Tl::LD, k0, (wave * VT + v) * 16);
-            {
+#pragma unroll
+            for (int n = 0; n < MP; ++n) {
                 typename M::Frag a[IT];
 #pragma unroll
-                for (int it = k0 / 16; it < IT; ++it) a[it] = frag_ordered<T>(sm, LDM, 16 * it, k0);
+                for (int it = k0 / 16; it < IT; ++it) a[it] = frag_ordered<T>(sm + n * C * LDM, LDM, 16 * it, k0);
 #pragma unroll
                 for (int it = k0 / 16; it < IT; ++it)
 #pragma unroll
@@ -945,11 +973,11 @@ int head_pad(const semicrf_attention& p) {
 int chunk_of(const semicrf_attention& p) { return p.dtype == SEMICRF_F32 ? 32 : 64; }
 
 // Workgroups of the sweep that run at once on 256 compute units, by registers (sweep_occupancy)
-// and, for bfloat16 of width 32, by LDS (28 KB of 160).
+// and, for bfloat16 of width 32, by LDS (38 KB of 160).
 int sweep_slots(const semicrf_attention& p) {
     const int P = head_pad(p);
     const bool f32 = p.dtype == SEMICRF_F32;
-    return 256 * (P == 128 ? 1 : P == 64 ? (f32 ? 4 : 3) : (f32 ? 8 : 5));
+    return 256 * (P == 128 ? 1 : P == 64 ? (f32 ? 4 : 3) : (f32 ? 8 : 4));
 }
 
 // Positions per segment.  Segments shorten the chain of chunks that one workgroup takes in order, at
