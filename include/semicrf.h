@@ -379,7 +379,8 @@ int semicrf_decay_attention_grad(const semicrf_attention* attention, const void*
  * same array; stream b uses row slots[b] (b itself where slots is NULL, then pool >= B).  A
  * slot outside [0, pool) marks an idle row: its output is 0 and no state is touched.  The
  * slots in [0, pool) must be distinct.  Rows of state_out that no slot names are left alone.
- * out [B, Hq, Dv]. */
+ * out [B, Hq, Dv].  Each token rounds the float32 state once, so a decay weaker than 2^-24 a token
+ * may be lost in the rounding. */
 int semicrf_decay_attention_step(const semicrf_attention* attention, const int32_t* slots,
                                  int pool, hipStream_t stream, void* out, float* state_out);
 

@@ -324,8 +324,8 @@ constexpr int sweep_waves(int P) { return P / 16; }
 template <class T, int P>
 constexpr int sweep_occupancy() { return P == 128 || (sizeof(T) == 2 && P == 32) ? 2 : sizeof(T) == 2 ? 3 : 4; }
 
-// gamma^m of the state.  Near 1 it is applied as S + (gamma^m - 1) S: over thousands of chunks a
-// factor rounded once would bend every old contribution the same way.
+// gamma^m of the state.  Near 1 it is applied as S + (gamma^m - 1) S: over thousands of chunks, or
+// of single tokens, a factor rounded once would bend every old contribution the same way.
 struct Decay {
     float f;
     int near1;               // the same in every lane
@@ -939,7 +939,8 @@ __global__ __launch_bounds__(256) void k_attn_step(const semicrf_attention p, co
     }
     __syncthreads();
     const int lr = tid & (LR - 1), grp = tid / LR, ng = 256 / LR, c = lr * 4;
-    const float gamma = expf(p.log_decay[h]);
+    Decay gamma;
+    gamma.set(p.log_decay[h], 1);
     float vv[4], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) vv[i] = c + i < Dv ? (float)v[c + i] : 0.0f;
@@ -950,7 +951,7 @@ __global__ __launch_bounds__(256) void k_attn_step(const semicrf_attention p, co
         const float kr = sk[r], qr = sq[r];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            s[i] = fmaf(s[i], gamma, kr * vv[i]);
+            s[i] = (gamma.near1 ? s[i] : 0.0f) + fmaf(s[i], gamma.f, kr * vv[i]);
             acc[i] = fmaf(qr, s[i], acc[i]);
         }
         store_elements(state_out + base + (size_t)r * Dv, c, Dv, s);

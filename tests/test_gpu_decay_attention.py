@@ -75,3 +75,43 @@ BF16 = [  # B, T, Hq, Hk, Dk, Dv, typ, lengths, initial state: every width, one 
 @pytest.mark.parametrize("case", BF16, ids=[name(c) for c in BF16])
 def test_bfloat16_is_as_exact_as_its_outputs(crf, case):  # noqa: F811
     check(crf, case)
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_a_long_stream_keeps_its_state(crf, typ):  # noqa: F811
+    """8,000 tokens one by one: the state follows the 64-bit recurrence and the sequence form.
+
+    A step rounds each element by at most u |s| and the decay forgets that as it forgets the rest.  In
+    float32, where k v has as many bits as the state, the errors are independent: those of
+    m = min(T, 1 / 2|log decay|) steps have a standard deviation of u / sqrt(3) sqrt(m) max|s|, and six
+    times u sqrt(m + 1) max|s| is ten of them.  An error of the decay itself would add up in one
+    direction, m times.  Products of bfloat16 numbers lie on a grid that is coarse beside an ulp of the
+    state; what is rounded there is the decay's share alone, alike from step to step, so only the sum
+    of all errors bounds them: u max|s| min(T, 1 / |log decay|)."""
+    import torch
+    B, T, H, Dk, Dv = 2, 8000, 6, 8, 12
+    rng = np.random.default_rng(8)
+    from test_gpu_encoder import host
+    r = lambda *s: host(dev(rng.standard_normal(s).astype(f32), typ))  # noqa: E731
+    q, k, v = r(B, T, H, Dk), r(B, T, H, Dk) * 0.125, r(B, T, H, Dv)
+    g = np.array([-2.0 ** -13, -3.3e-4, -1e-5, -1e-6, -3e-8, -0.2], f32)
+    st = (4 + rng.standard_normal((B, H, Dk, Dv))).astype(f32)
+    gamma = np.exp(g.astype(np.float64))[None, :, None, None]
+    s, top = st.astype(np.float64), np.abs(st).astype(np.float64)
+    for t in range(T):
+        s = gamma * s + k[:, t, :, :, None] * v[:, t, :, None, :]
+        top = np.maximum(top, np.abs(s))
+    a = np.abs(g.astype(np.float64))[None, :, None, None]
+    bound = 6 * U * np.sqrt(np.minimum(T, 0.5 / a) + 1) * top if typ == "f32" else \
+        U * (np.minimum(T, 1 / a) + 2) * top
+    qd, kd, vd = (dev(x.astype(f32), typ) for x in (q, k, v))
+    gd, state = dev(g), dev(st)
+    for t in range(T):
+        o = crf.decay_attention_step(qd[:, t], kd[:, t], vd[:, t], gd, state, scale=1.0)
+    torch.cuda.synchronize()
+    close(state, s, bound, "state")
+    want, end = crf.decay_attention(qd, kd, vd, gd, scale=1.0, state=dev(st), want_state=True)
+    close(end, s, bound, "state of the sequence form")
+    mag = (np.abs(q[:, -1, :, :, None]) * (bound + Dk * U * np.abs(s))).sum(2)
+    x = (q[:, -1, :, :, None] * s).sum(2)
+    close(o, x, mag + rounding(typ, x), "last output")
