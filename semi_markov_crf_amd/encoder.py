@@ -8,8 +8,9 @@ runs in the library's HIP kernels, on torch's current stream.
     decay_attention(q, k, v, log_decay)        -> o  [B, T, Hq, Dv] (and the final state)
     decay_attention_step(q, k, v, ..., state)  -> o  [B, Hq, Dv], one token a stream
 
-embed, layer_norm and decay_attention are differentiable; embed_grad, layer_norm_grad and
-decay_attention_grad are the gradients by themselves.  Tensors are float32 or bfloat16 on one
+embed, layer_norm and decay_attention are differentiable, once: a derivative of their gradients
+raises.  embed_grad, layer_norm_grad and decay_attention_grad are the gradients by themselves; they
+and decay_attention_step carry none.  Tensors are float32 or bfloat16 on one
 GPU.  lengths [B] int32 (0 <= lengths[b] <= T, None = T everywhere): what lies at t >= lengths[b]
 is not read and outputs are 0 there.  check_status=True waits for the call and raises when a
 length or a token was out of range.
@@ -20,6 +21,7 @@ from __future__ import annotations
 import torch
 
 from . import _native
+from ._autograd import first_order
 
 __all__ = ["embed", "embed_grad", "layer_norm", "layer_norm_grad", "decay_attention",
            "decay_attention_grad", "decay_attention_step"]
@@ -164,8 +166,9 @@ class _Embed(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         tokens, lengths = ctx.saved_tensors
-        return (None, embed_grad(tokens, g.contiguous(), ctx.V, scale=ctx.scale, lengths=lengths),
-                None, None, None)
+        grad = first_order("embed", lambda: embed_grad(tokens, g.contiguous(), ctx.V, scale=ctx.scale,
+                                                       lengths=lengths), g)
+        return None, grad, None, None, None
 
 
 # ---------------------------------------------------------------- layer norm
@@ -257,10 +260,14 @@ class _LayerNorm(torch.autograd.Function):
         x, weight, mean, rstd, lengths = ctx.saved_tensors
         need_w, need_b = ctx.needs_input_grad[1:3]
         B, T, N = x.shape
-        d = _norm_grad(g.contiguous(), x, weight, ctx.wtype, mean, rstd, lengths,
-                       need_w or need_b, None, False, x.get_device(), B, T, N)
-        return (d["grad_x"], d.get("grad_weight") if need_w else None,
-                d.get("grad_bias") if need_b else None, None, None, None, None)
+
+        def grads():
+            d = _norm_grad(g.contiguous(), x, weight, ctx.wtype, mean, rstd, lengths,
+                           need_w or need_b, None, False, x.get_device(), B, T, N)
+            return (d["grad_x"], d["grad_weight"] if need_w else None,
+                    d["grad_bias"] if need_b else None)
+
+        return *first_order("layer_norm", grads, g, x, weight), None, None, None, None
 
 
 # ---------------------------------------------------------------- attention
@@ -356,11 +363,15 @@ class _DecayAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g, g_state):
         q, k, v, log_decay, lengths, state = ctx.saved_tensors
-        d = decay_attention_grad(g.contiguous(), q, k, v, log_decay, scale=ctx.scale,
-                                 lengths=lengths, state=state,
-                                 grad_state=None if g_state is None else g_state.contiguous())
-        return (d["grad_q"], d["grad_k"], d["grad_v"], None, None, None, d.get("grad_state"), None,
-                None)
+
+        def grads():
+            d = decay_attention_grad(g.contiguous(), q, k, v, log_decay, scale=ctx.scale,
+                                     lengths=lengths, state=state,
+                                     grad_state=None if g_state is None else g_state.contiguous())
+            return d["grad_q"], d["grad_k"], d["grad_v"], d.get("grad_state")
+
+        gq, gk, gv, gs = first_order("decay_attention", grads, g, g_state, q, k, v, state)
+        return gq, gk, gv, None, None, None, gs, None, None
 
 
 def decay_attention_step(q, k, v, log_decay, state, *, scale=None, slots=None,
