@@ -25,6 +25,7 @@ from __future__ import annotations
 import torch
 
 from . import _native
+from ._autograd import first_order
 from ._native import OP_BACKWARD, OP_LOGZ, OP_PREFIX, OP_VITERBI, SemiCRFError
 from .encoder import (decay_attention, decay_attention_grad, decay_attention_step, embed,
                       embed_grad, layer_norm, layer_norm_grad)
@@ -290,15 +291,20 @@ class _LogPartition(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         em, lengths, trans, dur, ps, pe = ctx.saved_tensors
-        out = backward(em, lengths, trans, dur, proj_start=ps, proj_end=pe,
-                       grad_log_z=g.contiguous().float(), delta=ctx.delta, want_marginals=False)
-        return (out["grad_em"], None, out["grad_trans"], out["grad_dur"],
-                out.get("grad_proj_start") if ps is not None else None,
-                out.get("grad_proj_end") if pe is not None else None, None)
+
+        def grads():
+            out = backward(em, lengths, trans, dur, proj_start=ps, proj_end=pe,
+                           grad_log_z=g.contiguous().float(), delta=ctx.delta, want_marginals=False)
+            return (out["grad_em"], out["grad_trans"], out["grad_dur"],
+                    out["grad_proj_start"] if ps is not None else None,
+                    out["grad_proj_end"] if pe is not None else None)
+
+        gem, gtrans, gdur, gps, gpe = first_order("log_partition", grads, g, em, trans, dur, ps, pe)
+        return gem, None, gtrans, gdur, gps, gpe, None
 
 
 def log_partition(em, lengths, trans, dur, proj_start=None, proj_end=None,
                   delta: int = 0) -> torch.Tensor:
     """log Z [B] as a differentiable op (a drop-in CRF-layer loss term); the optional
-    boundary projections receive gradients too."""
+    boundary projections receive gradients too.  A derivative of its gradients raises."""
     return _LogPartition.apply(em, lengths, trans, dur, proj_start, proj_end, delta)

@@ -104,3 +104,24 @@ def test_a_gradient_linear_in_its_table_has_none(plain):
     (table,), f = cases()["embed"]
     g, = torch.autograd.grad(f(table).sum(), table, create_graph=True)
     assert not g.requires_grad
+
+
+def test_second_derivatives_of_log_partition_are_refused(monkeypatch):
+    """One position, segments of length one: log Z is the log-sum-exp of the emissions."""
+    import semi_markov_crf_amd as crf
+
+    def backward(em, lengths, trans, dur, *, proj_start, proj_end, grad_log_z, delta, want_marginals):
+        p = torch.softmax(em[:, 0], -1) * grad_log_z[:, None]
+        return {"grad_em": p[:, None], "grad_trans": torch.zeros_like(trans), "grad_dur": p.sum(0, keepdim=True)}
+
+    monkeypatch.setattr(crf, "logz", lambda em, *a, **kw: torch.logsumexp(em[:, 0], -1))
+    monkeypatch.setattr(crf, "backward", backward)
+    torch.manual_seed(1)
+    em = torch.randn(2, 1, 3, requires_grad=True)
+    lengths, trans, dur = torch.ones(2, dtype=torch.int32), torch.zeros(3, 3), torch.zeros(1, 3)
+    first, = torch.autograd.grad(crf.log_partition(em, lengths, trans, dur).sum(), em)
+    assert torch.allclose(first[:, 0], torch.softmax(em[:, 0], -1))
+    again, = torch.autograd.grad(crf.log_partition(em, lengths, trans, dur).sum(), em, create_graph=True)
+    assert torch.equal(first, again)
+    with pytest.raises(RuntimeError, match="log_partition has no second derivatives"):
+        torch.autograd.grad((again ** 2).sum() + (em ** 2).sum(), em)
