@@ -8,9 +8,9 @@ runs in the library's HIP kernels, on torch's current stream.
     decay_attention(q, k, v, log_decay)        -> o  [B, T, Hq, Dv] (and the final state)
     decay_attention_step(q, k, v, ..., state)  -> o  [B, Hq, Dv], one token a stream
 
-embed, layer_norm and decay_attention are differentiable, once: a derivative of their gradients
-raises.  embed_grad, layer_norm_grad and decay_attention_grad are the gradients by themselves; they
-and decay_attention_step carry none.  Tensors are float32 or bfloat16 on one
+embed, layer_norm and decay_attention are differentiable, once and backward: a derivative of their
+gradients and a forward-mode tangent raise.  embed_grad, layer_norm_grad and decay_attention_grad are the
+gradients by themselves; they and decay_attention_step carry none.  Tensors are float32 or bfloat16 on one
 GPU.  lengths [B] int32 (0 <= lengths[b] <= T, None = T everywhere): what lies at t >= lengths[b]
 is not read and outputs are 0 there.  check_status=True waits for the call and raises when a
 length or a token was out of range.
@@ -19,6 +19,7 @@ length or a token was out of range.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native
 from ._autograd import first_order
@@ -96,11 +97,14 @@ def _check(fn, rc, word=None):
 
 
 def _tracked(*tensors):
+    """Whether a call goes through its autograd function: one of its inputs wants a gradient, or
+    carries a forward-mode tangent, which the function refuses."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 return True
-    return False
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 # ---------------------------------------------------------------- embedding
@@ -309,7 +313,7 @@ def decay_attention(q, k, v, log_decay, *, scale=None, lengths=None, state=None,
     multiple of Hk, Dk and Dv up to 128; log_decay [Hq] float32, a constant; scale Dk**-0.5 by
     default; state [B, Hq, Dk, Dv] float32 before the first position (None: 0).  Returns o
     [B, T, Hq, Dv], and with want_state also the state after each sequence's last position."""
-    if log_decay.requires_grad and torch.is_grad_enabled():
+    if _tracked(log_decay):
         raise ValueError("log_decay is a constant of the head: it has no gradient")
     if _tracked(q, k, v, state):
         o, end = _DecayAttention.apply(q, k, v, log_decay, scale, lengths, state, want_state,

@@ -125,3 +125,23 @@ def test_second_derivatives_of_log_partition_are_refused(monkeypatch):
     assert torch.equal(first, again)
     with pytest.raises(RuntimeError, match="log_partition has no second derivatives"):
         torch.autograd.grad((again ** 2).sum() + (em ** 2).sum(), em)
+
+
+@pytest.mark.parametrize("name", ["embed", "layer_norm", "decay_attention"])
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_is_refused(plain, monkeypatch, name, grad):
+    """A dual input raises, with gradients on or off: its tangent is not dropped.  The calls go by
+    _tracked, and what it sends to the autograd function is refused there."""
+    import torch.autograd.forward_ad as fwd
+    args, f = cases()[name]
+    args = [a.detach() for a in args]
+    with torch.set_grad_enabled(grad):
+        assert not encoder._tracked(*args, None)
+        with fwd.dual_level():
+            assert not encoder._tracked(*args, None)
+            for i in range(len(args)):
+                dual = [fwd.make_dual(a, torch.ones_like(a)) if j == i else a for j, a in enumerate(args)]
+                assert encoder._tracked(*dual, None)
+                with pytest.raises(RuntimeError, match="forward"):
+                    f(*dual)
+        assert not encoder._tracked(*args, None)

@@ -115,3 +115,22 @@ def test_a_long_stream_keeps_its_state(crf, typ):  # noqa: F811
     mag = (np.abs(q[:, -1, :, :, None]) * (bound + Dk * U * np.abs(s))).sum(2)
     x = (q[:, -1, :, :, None] * s).sum(2)
     close(o, x, mag + rounding(typ, x), "last output")
+
+
+def test_forward_mode_is_refused(crf):  # noqa: F811
+    import torch
+    import torch.autograd.forward_ad as fwd
+    x = torch.randn(1, 3, 8, device="cuda")
+    tok = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    g = torch.zeros(2, device="cuda")
+    with fwd.dual_level():
+        d = fwd.make_dual(x, torch.ones_like(x))
+        h, p = (a.unflatten(-1, (2, 4)) for a in (d, x))
+        dg = fwd.make_dual(g, torch.ones_like(g))
+        for err, f in ((RuntimeError, lambda: crf.embed(tok, d[0])), (RuntimeError, lambda: crf.layer_norm(d)),
+                       (RuntimeError, lambda: crf.decay_attention(p, h, p, g)),
+                       (ValueError, lambda: crf.decay_attention(p, p, p, dg))):
+            with pytest.raises(err):
+                f()
+        crf.layer_norm(x)
+        crf.decay_attention(p, p, p, g)
