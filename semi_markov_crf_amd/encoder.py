@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import _native
 from ._autograd import first_order
@@ -384,7 +385,8 @@ def decay_attention_step(q, k, v, log_decay, state, *, scale=None, slots=None,
     [pool, Hq, Dk, Dv] float32, updated in place (or written to state_out, whose other rows are
     left alone).  Stream b uses row slots[b] (int32; None: row b).  A slot outside [0, pool) is
     idle: its output is 0.  Slots in use must be distinct.  Returns o [B, Hq, Dv]; carries no
-    gradient."""
+    gradient, and refuses to overwrite a state that wants one.  Autograd sees the write as that of
+    any in-place operation."""
     try:
         pool = state.shape[0]
     except (AttributeError, IndexError):
@@ -398,7 +400,10 @@ def decay_attention_step(q, k, v, log_decay, state, *, scale=None, slots=None,
         state_out = state
     else:
         _need("state_out", state_out, torch.float32, state.shape, dev)
+    if state_out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("the state that is written requires a gradient, which a step does not carry")
     out = q.new_empty((a.B, a.Hq, a.Dv))
     _check("semicrf_decay_attention_step", _native.load().semicrf_decay_attention_step(
         a, _ptr(slots), pool, _raw_stream(dev), out.data_ptr(), state_out.data_ptr()))
+    increment_version(state_out)
     return out

@@ -145,3 +145,50 @@ def test_forward_mode_is_refused(plain, monkeypatch, name, grad):
                 with pytest.raises(RuntimeError, match="forward"):
                     f(*dual)
         assert not encoder._tracked(*args, None)
+
+
+@pytest.fixture
+def step(monkeypatch):
+    """decay_attention_step on CPU tensors: the library's call writes a one into the state."""
+    import types
+
+    def call(a, slots, pool, stream, out, state_out):
+        call.state.data[0, 0, 0, 0] = 1.0          # .data: like a kernel's write, unseen by autograd
+        return 0
+
+    a = types.SimpleNamespace(B=2, Hq=2, Dv=5)
+    monkeypatch.setattr(encoder, "_attention", lambda *args: (-1, a))
+    monkeypatch.setattr(encoder, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(encoder._native, "load", lambda: types.SimpleNamespace(semicrf_decay_attention_step=call))
+    monkeypatch.setattr(encoder, "_need", lambda *args: None)
+
+    def run(state, state_out=None):
+        call.state = state if state_out is None else state_out
+        return encoder.decay_attention_step(torch.zeros(2, 2, 4), None, None, None, state, state_out=state_out)
+    return run
+
+
+@pytest.mark.parametrize("apart", [False, True])
+def test_a_step_counts_as_an_in_place_write(plain, step, apart):
+    """A state that decay_attention keeps for its backward pass and a step then overwrites: backward
+    raises, as after any in-place operation."""
+    torch.manual_seed(2)
+    q, k, v = (torch.randn(2, 3, 2, d, requires_grad=True) for d in (4, 4, 5))
+    state, other = torch.randn(2, 2, 4, 5), torch.randn(2, 2, 4, 5)
+    o = encoder._DecayAttention.apply(q, k, v, torch.tensor([-0.1, -1.0]), 0.5, None, state, False, False)[0]
+    step(other, state) if apart else step(state)
+    assert float(state[0, 0, 0, 0]) == 1.0
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()
+
+
+def test_a_step_refuses_a_state_that_wants_a_gradient(step):
+    state = torch.randn(2, 2, 4, 5, requires_grad=True)
+    for call in (lambda: step(state), lambda: step(state.detach(), state)):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+    with torch.no_grad():
+        step(state)
+    step(state, state.detach().clone())              # only read
+    with torch.inference_mode():                      # such tensors count no versions
+        step(torch.randn(2, 2, 4, 5))

@@ -134,3 +134,22 @@ def test_forward_mode_is_refused(crf):  # noqa: F811
                 f()
         crf.layer_norm(x)
         crf.decay_attention(p, p, p, g)
+
+
+def test_a_step_counts_as_an_in_place_write(crf):  # noqa: F811
+    import torch
+    torch.manual_seed(2)
+    q, k, v = (torch.randn(2, 3, 2, 8, device="cuda", requires_grad=True) for _ in range(3))
+    g, state = torch.tensor([-0.1, -1.0], device="cuda"), torch.randn(2, 2, 8, 8, device="cuda")
+    o = crf.decay_attention(q, k, v, g, state=state)
+    one = [x[:, 0].detach() for x in (q, k, v)]
+    crf.decay_attention_step(*one, g, state.clone())
+    crf.decay_attention_step(*one, g, state)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()
+    state.requires_grad_()
+    with pytest.raises(ValueError):
+        crf.decay_attention_step(*one, g, state)
+    with torch.inference_mode():
+        crf.decay_attention_step(*one, g, torch.zeros(2, 2, 8, 8, device="cuda"))
+    torch.cuda.synchronize()
