@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch  # noqa: F401  (must precede the dlopen below, see module docstring)
+import torch  # must precede the dlopen below, see module docstring
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsemicrf.so")
 
@@ -119,6 +119,16 @@ def load() -> ctypes.CDLL:
             f.argtypes = args
         _lib = lib
     return _lib
+
+
+def call(dev: int, name: str, *args):
+    """The library's function `name`, with GPU `dev` current: a default stream is a null handle, which
+    stands for that of the current GPU, whichever the arrays are on."""
+    f = getattr(load(), name)
+    if torch.cuda.current_device() == dev:
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
 
 
 def status_string(status: int) -> str:

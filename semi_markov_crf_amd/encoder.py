@@ -90,7 +90,9 @@ def _status(want, device):
     return torch.zeros(1, dtype=torch.int32, device=device) if want else None
 
 
-def _check(fn, rc, word=None):
+def _run(fn, dev, word, *args):
+    """A call of the library on GPU `dev`, whose status word (or None) is `word`."""
+    rc = _native.call(dev, fn, *args)
     if rc:
         raise _native.SemiCRFError(fn, rc)
     if word is not None and int(word.item()):
@@ -134,9 +136,8 @@ def embed(tokens, table, *, scale=1.0, lengths=None, check_status=False) -> torc
     V, N = table.shape
     out = table.new_empty((B, T, N))
     word = _status(check_status, table.device)
-    _check("semicrf_embed", _native.load().semicrf_embed(
-        tokens.data_ptr(), bits, _ptr(lengths), table.data_ptr(), _TYPES[table.dtype], B, T, V, N,
-        scale, _raw_stream(dev), out.data_ptr(), _ptr(word)), word)
+    _run("semicrf_embed", dev, word, tokens.data_ptr(), bits, _ptr(lengths), table.data_ptr(),
+         _TYPES[table.dtype], B, T, V, N, scale, _raw_stream(dev), out.data_ptr(), _ptr(word))
     return out
 
 
@@ -154,9 +155,9 @@ def embed_grad(tokens, grad_out, V, *, scale=1.0, lengths=None, workspace=None,
     ws = _workspace("semicrf_embed_grad", n, grad_out.device, workspace)
     out = grad_out.new_empty((V, N))
     word = _status(check_status, grad_out.device)
-    _check("semicrf_embed_grad", lib.semicrf_embed_grad(
-        tokens.data_ptr(), bits, _ptr(lengths), grad_out.data_ptr(), typ, B, T, V, N, scale,
-        _raw_stream(dev), ws.data_ptr(), n, out.data_ptr(), _ptr(word)), word)
+    _run("semicrf_embed_grad", dev, word, tokens.data_ptr(), bits, _ptr(lengths),
+         grad_out.data_ptr(), typ, B, T, V, N, scale, _raw_stream(dev), ws.data_ptr(), n,
+         out.data_ptr(), _ptr(word))
     return out
 
 
@@ -210,9 +211,9 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, lengths=None, want_stats=
     if want_stats:
         mean, rstd = (torch.empty((B, T), dtype=torch.float32, device=x.device) for _ in range(2))
     word = _status(check_status, x.device)
-    _check("semicrf_layer_norm", _native.load().semicrf_layer_norm(
-        x.data_ptr(), _TYPES[x.dtype], _ptr(weight), _ptr(bias), _TYPES[wtype], _ptr(lengths), B, T,
-        N, eps, _raw_stream(dev), y.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(word)), word)
+    _run("semicrf_layer_norm", dev, word, x.data_ptr(), _TYPES[x.dtype], _ptr(weight),
+         _ptr(bias), _TYPES[wtype], _ptr(lengths), B, T, N, eps, _raw_stream(dev), y.data_ptr(),
+         _ptr(mean), _ptr(rstd), _ptr(word))
     return (y, mean, rstd) if want_stats else y
 
 
@@ -240,10 +241,10 @@ def _norm_grad(grad_out, x, weight, wtype, mean, rstd, lengths, want_params, wor
     if want_params:
         gw, gb = (torch.empty(N, dtype=wtype, device=x.device) for _ in range(2))
     word = _status(check_status, x.device)
-    _check("semicrf_layer_norm_grad", lib.semicrf_layer_norm_grad(
-        grad_out.data_ptr(), x.data_ptr(), _TYPES[x.dtype], _ptr(weight), _TYPES[wtype],
-        mean.data_ptr(), rstd.data_ptr(), _ptr(lengths), B, T, N, _raw_stream(dev), ws.data_ptr(), n,
-        gx.data_ptr(), _ptr(gw), _ptr(gb), _ptr(word)), word)
+    _run("semicrf_layer_norm_grad", dev, word, grad_out.data_ptr(), x.data_ptr(),
+         _TYPES[x.dtype], _ptr(weight), _TYPES[wtype], mean.data_ptr(), rstd.data_ptr(),
+         _ptr(lengths), B, T, N, _raw_stream(dev), ws.data_ptr(), n, gx.data_ptr(), _ptr(gw),
+         _ptr(gb), _ptr(word))
     out = {"grad_x": gx}
     if want_params:
         out.update(grad_weight=gw, grad_bias=gb)
@@ -327,8 +328,8 @@ def decay_attention(q, k, v, log_decay, *, scale=None, lengths=None, state=None,
     out = q.new_empty((a.B, a.T, a.Hq, a.Dv))
     end = q.new_empty((a.B, a.Hq, a.Dk, a.Dv), dtype=torch.float32) if want_state else None
     word = _status(check_status, q.device)
-    _check("semicrf_decay_attention", lib.semicrf_decay_attention(
-        a, _raw_stream(dev), ws.data_ptr(), n, out.data_ptr(), _ptr(end), _ptr(word)), word)
+    _run("semicrf_decay_attention", dev, word, a, _raw_stream(dev), ws.data_ptr(), n,
+         out.data_ptr(), _ptr(end), _ptr(word))
     return (out, end) if want_state else out
 
 
@@ -347,9 +348,9 @@ def decay_attention_grad(grad_out, q, k, v, log_decay, *, scale=None, lengths=No
     gq, gk, gv = (x.new_empty(x.shape) for x in (q, k, v))
     gs = torch.empty_like(state) if state is not None else None
     word = _status(check_status, q.device)
-    _check("semicrf_decay_attention_grad", lib.semicrf_decay_attention_grad(
-        a, grad_out.data_ptr(), _ptr(grad_state), _raw_stream(dev), ws.data_ptr(), n, gq.data_ptr(),
-        gk.data_ptr(), gv.data_ptr(), _ptr(gs), _ptr(word)), word)
+    _run("semicrf_decay_attention_grad", dev, word, a, grad_out.data_ptr(), _ptr(grad_state),
+         _raw_stream(dev), ws.data_ptr(), n, gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
+         _ptr(gs), _ptr(word))
     out = {"grad_q": gq, "grad_k": gk, "grad_v": gv}
     if gs is not None:
         out["grad_state"] = gs
@@ -403,7 +404,7 @@ def decay_attention_step(q, k, v, log_decay, state, *, scale=None, slots=None,
     if state_out.requires_grad and torch.is_grad_enabled():
         raise ValueError("the state that is written requires a gradient, which a step does not carry")
     out = q.new_empty((a.B, a.Hq, a.Dv))
-    _check("semicrf_decay_attention_step", _native.load().semicrf_decay_attention_step(
-        a, _ptr(slots), pool, _raw_stream(dev), out.data_ptr(), state_out.data_ptr()))
+    _run("semicrf_decay_attention_step", dev, None, a, _ptr(slots), pool, _raw_stream(dev),
+         out.data_ptr(), state_out.data_ptr())
     increment_version(state_out)
     return out

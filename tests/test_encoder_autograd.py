@@ -159,7 +159,7 @@ def step(monkeypatch):
     a = types.SimpleNamespace(B=2, Hq=2, Dv=5)
     monkeypatch.setattr(encoder, "_attention", lambda *args: (-1, a))
     monkeypatch.setattr(encoder, "_raw_stream", lambda dev: 0)
-    monkeypatch.setattr(encoder._native, "load", lambda: types.SimpleNamespace(semicrf_decay_attention_step=call))
+    monkeypatch.setattr(encoder._native, "call", lambda dev, name, *args: call(*args))
     monkeypatch.setattr(encoder, "_need", lambda *args: None)
 
     def run(state, state_out=None):
