@@ -61,8 +61,8 @@ def prefix(em, lengths, *, workspace=None, check_status=False) -> torch.Tensor:
     B, T, C = (int(v) for v in em.shape)
     ws, n = _workspace(OP_PREFIX, B, T, C, 1, 0, em.device, workspace)
     S = torch.empty((B, T + 1, C), dtype=torch.float64, device=em.device)
-    rc = _native.load().semicrf_prefix(em.data_ptr(), lengths.data_ptr(), B, T, C,
-                                       _stream(em.device), ws.data_ptr(), n, S.data_ptr())
+    rc = _native.call(em.device.index, "semicrf_prefix", em.data_ptr(), lengths.data_ptr(), B, T,
+                      C, _stream(em.device), ws.data_ptr(), n, S.data_ptr())
     _native.check("semicrf_prefix", rc)
     _maybe_check(ws, check_status, "semicrf_prefix")
     return S
@@ -104,8 +104,8 @@ def _stream(device):
 
 def read_status(workspace: torch.Tensor) -> int:
     """Device status flag of the last call that used ``workspace`` (synchronises)."""
-    return int(_native.load().semicrf_read_status(workspace.data_ptr(),
-                                                  _stream(workspace.device)))
+    return int(_native.call(workspace.device.index, "semicrf_read_status", workspace.data_ptr(),
+                            _stream(workspace.device)))
 
 
 def _maybe_check(workspace, check_status, fn):
@@ -155,9 +155,9 @@ def logz(em, lengths, trans, dur, *, proj_start=None, proj_end=None, delta=0, wo
     sb, sr = _seams(B, em.device, want_seams)
     opt = _options(proj_start=_ptr(ps), proj_end=_ptr(pe), seam_bound=_ptr(sb),
                    seam_repairs=_ptr(sr), seam_tolerance=float(seam_tolerance) or None)
-    rc = _native.load().semicrf_logz_ex(em.data_ptr(), lengths.data_ptr(), trans.data_ptr(),
-                                        dur.data_ptr(), B, T, C, K, delta, _stream(em.device),
-                                        ws.data_ptr(), n, out.data_ptr(), opt)
+    rc = _native.call(em.device.index, "semicrf_logz_ex", em.data_ptr(), lengths.data_ptr(),
+                      trans.data_ptr(), dur.data_ptr(), B, T, C, K, delta, _stream(em.device),
+                      ws.data_ptr(), n, out.data_ptr(), opt)
     _native.check("semicrf_logz", rc)
     _maybe_check(ws, check_status, "semicrf_logz")
     return (out, sb, sr) if want_seams else out
@@ -196,10 +196,11 @@ def backward(em, lengths, trans, dur, *, proj_start=None, proj_end=None, grad_lo
                    grad_proj_end=_ptr(gpe), boundary=_ptr(bnd), node_mass=_ptr(nm),
                    seam_bound=_ptr(sb), seam_repairs=_ptr(sr),
                    seam_tolerance=float(seam_tolerance) or None)
-    rc = _native.load().semicrf_backward_ex(
-        em.data_ptr(), lengths.data_ptr(), trans.data_ptr(), dur.data_ptr(), B, T, C, K, delta,
-        _stream(dev), ws.data_ptr(), n, _ptr(grad_log_z), grad_em.data_ptr(),
-        grad_trans.data_ptr(), grad_dur.data_ptr(), _ptr(mu), lz.data_ptr(), opt)
+    rc = _native.call(
+        dev.index, "semicrf_backward_ex", em.data_ptr(), lengths.data_ptr(), trans.data_ptr(),
+        dur.data_ptr(), B, T, C, K, delta, _stream(dev), ws.data_ptr(), n, _ptr(grad_log_z),
+        grad_em.data_ptr(), grad_trans.data_ptr(), grad_dur.data_ptr(), _ptr(mu), lz.data_ptr(),
+        opt)
     _native.check("semicrf_backward", rc)
     _maybe_check(ws, check_status, "semicrf_backward")
     out = {"grad_em": grad_em, "grad_trans": grad_trans, "grad_dur": grad_dur,
@@ -242,8 +243,8 @@ def nll(em, lengths, trans, dur, gold_labels, gold_seg_start, *, proj_start=None
     gpe = torch.empty_like(em) if want_p else None
     opt = _options(proj_start=_ptr(ps), proj_end=_ptr(pe), grad_proj_start=_ptr(gps),
                    grad_proj_end=_ptr(gpe))
-    rc = _native.load().semicrf_nll(
-        em.data_ptr(), lengths.data_ptr(), trans.data_ptr(), dur.data_ptr(),
+    rc = _native.call(
+        dev.index, "semicrf_nll", em.data_ptr(), lengths.data_ptr(), trans.data_ptr(), dur.data_ptr(),
         gold_labels.data_ptr(), gold_seg_start.data_ptr(), B, T, C, K, delta, _stream(dev),
         ws.data_ptr(), n, _ptr(grad_nll), out.data_ptr(), grad_em.data_ptr(),
         grad_trans.data_ptr(), grad_dur.data_ptr(), opt)
@@ -269,10 +270,9 @@ def viterbi(em, lengths, trans, dur, *, proj_start=None, proj_end=None, workspac
     sb, sr = _seams(B, dev, want_seams)
     opt = _options(proj_start=_ptr(ps), proj_end=_ptr(pe), seam_bound=_ptr(sb),
                    seam_repairs=_ptr(sr), seam_tolerance=float(seam_tolerance) or None)
-    rc = _native.load().semicrf_viterbi_ex(em.data_ptr(), lengths.data_ptr(), trans.data_ptr(),
-                                           dur.data_ptr(), B, T, C, K, _stream(dev),
-                                           ws.data_ptr(), n, score.data_ptr(), labels.data_ptr(),
-                                           seg.data_ptr(), opt)
+    rc = _native.call(dev.index, "semicrf_viterbi_ex", em.data_ptr(), lengths.data_ptr(),
+                      trans.data_ptr(), dur.data_ptr(), B, T, C, K, _stream(dev), ws.data_ptr(), n,
+                      score.data_ptr(), labels.data_ptr(), seg.data_ptr(), opt)
     _native.check("semicrf_viterbi", rc)
     _maybe_check(ws, check_status, "semicrf_viterbi")
     if want_seams:

@@ -82,6 +82,21 @@ def test_encoder_operators(calls):
                        "semicrf_decay_attention", "semicrf_decay_attention_grad", "semicrf_decay_attention_step"])
 
 
+def test_crf(calls):
+    em, lengths, trans, dur = array(2, 3, 4), array(2, dtype=torch.int32), array(4, 4), array(5, 4)
+    gold, seg = array(2, 3, dtype=torch.int32), array(2, 3, dtype=torch.uint8)
+    ws = torch.empty(1 << 13, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:]
+    with torch.no_grad():
+        crf.prefix(em, lengths, workspace=ws)
+        crf.logz(em, lengths, trans, dur, workspace=ws, check_status=True)
+        crf.backward(em, lengths, trans, dur, workspace=ws)
+        crf.nll(em, lengths, trans, dur, gold, seg, workspace=ws)
+        crf.viterbi(em, lengths, trans, dur, workspace=ws)
+    only_there(calls, ["semicrf_prefix", "semicrf_logz_ex", "semicrf_read_status", "semicrf_backward_ex",
+                       "semicrf_nll", "semicrf_viterbi_ex"])
+
+
 def test_the_current_device_stays_where_it_is(monkeypatch):
     """No switch where the arrays' GPU is current."""
     monkeypatch.setattr(_native, "load", lambda: types.SimpleNamespace(f=lambda *a: a))
