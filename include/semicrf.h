@@ -298,8 +298,8 @@ int semicrf_read_status(const void* workspace, hipStream_t stream);
  *    whatever it holds, and outputs are 0 there.
  *  - status: NULL, or a device word the caller has cleared; the call sets bit 0 in it when a
  *    length, or a token, was out of range.
- *  - B * T and V are below 2^30, B below 2^16 and Hq below 2^15 for the attention calls (else
- *    SEMICRF_ERR_UNSUPPORTED).  Arrays need the alignment of their elements only. */
+ *  - B * T, V and the N of embed are below 2^30, B below 2^16 and Hq below 2^15 for the
+ *    attention calls (else SEMICRF_ERR_UNSUPPORTED).  Arrays need the alignment of their elements only. */
 typedef enum { SEMICRF_F32 = 0, SEMICRF_BF16 = 1 } semicrf_dtype;
 
 /* out[b, t, :] = scale * table[tokens[b, t], :].  tokens [B, T] int32 or int64 (token_bits 32

@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
     constexpr int V = Pc::V, RPB = 256 / G;
     const int N = a.N, lane = threadIdx.x % G;
     const unsigned n = (unsigned)a.B * a.T;
-    const unsigned i0 = blockIdx.x * RPB * U + threadIdx.x / G;
+    const unsigned i0 = a.first + blockIdx.x * RPB * U + threadIdx.x / G;
     unsigned at[U];
     uint32_t key[U];
 #pragma unroll
@@ -576,11 +576,17 @@ hipError_t run_embed(const EmbedArgs& a, hipStream_t stream) {
     const bool stream_out = (size_t)n * a.N * sizeof(T) > (size_t)256 << 20;
     auto go = [&](auto g) {
         constexpr int G = decltype(g)::value, U = 2;
-        const long per = (256 / G) * U;
-        const dim3 grid((unsigned)((n + per - 1) / per)), block(256);
-        if (a.N < V) hipLaunchKernelGGL((k_embed<T, 4, U, false, true>), grid, block, 0, stream, a);
-        else if (stream_out) hipLaunchKernelGGL((k_embed<T, G, U, true, false>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((k_embed<T, G, U, false, false>), grid, block, 0, stream, a);
+        const long per = (256 / G) * U, most = per << 22;    // a launch holds less than 2^32 threads
+        const dim3 block(256);
+        EmbedArgs part = a;
+        for (long first = 0; first < n; first += most) {
+            part.first = (unsigned)first;
+            const long rows = n - first < most ? n - first : most;
+            const dim3 grid((unsigned)((rows + per - 1) / per));
+            if (a.N < V) hipLaunchKernelGGL((k_embed<T, 4, U, false, true>), grid, block, 0, stream, part);
+            else if (stream_out) hipLaunchKernelGGL((k_embed<T, G, U, true, false>), grid, block, 0, stream, part);
+            else hipLaunchKernelGGL((k_embed<T, G, U, false, false>), grid, block, 0, stream, part);
+        }
         return hipGetLastError();
     };
     if (np <= 4) return go(std::integral_constant<int, 4>());

@@ -120,6 +120,7 @@ struct EmbedArgs {
     const void* table;       // embed
     const void* grad_out;    // embed_grad
     int dtype, B, T, V, N;
+    unsigned first;          // embed: first row of a launch
     float scale;
     void* out;               // y, or the gradient of the table
     int32_t* status;

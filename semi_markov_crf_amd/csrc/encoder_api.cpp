@@ -29,7 +29,7 @@ int check_embed(const void* tokens, int token_bits, int dtype, int B, int T, int
         return SEMICRF_ERR_INVALID;
     const int rc = check_rows(B, T, N);
     if (rc) return rc;
-    return V < MAX_ROWS ? SEMICRF_OK : SEMICRF_ERR_UNSUPPORTED;
+    return V < MAX_ROWS && N < MAX_ROWS ? SEMICRF_OK : SEMICRF_ERR_UNSUPPORTED;
 }
 
 int check_norm(const void* x, int dtype, int wdtype, int B, int T, int N) {
