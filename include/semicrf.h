@@ -310,7 +310,7 @@ int semicrf_embed(const void* tokens, int token_bits, const int32_t* lengths, co
 
 /* grad_table[v, :] = scale * sum of grad_out[b, t, :] over the positions with token v (0 for a
  * token that does not appear; a token outside [0, V) counts for nothing).  Positions are
- * sorted by token and each row's sum has a fixed order.  Workspace:
+ * sorted by token and each row's sum has a fixed order.  N <= 2^23.  Workspace:
  * semicrf_embed_grad_bytes, 256-byte aligned. */
 size_t semicrf_embed_grad_bytes(int dtype, int B, int T, int V, int N);
 int semicrf_embed_grad(const void* tokens, int token_bits, const int32_t* lengths,

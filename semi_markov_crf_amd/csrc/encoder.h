@@ -125,6 +125,7 @@ struct EmbedArgs {
     void* out;               // y, or the gradient of the table
     int32_t* status;
 };
+constexpr int EMBED_GRAD_MAX_N = 1 << 23;      // slabs of columns are the second grid dimension, below 2^16
 hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream);
 size_t embed_grad_bytes(int B, int T, int V, int N, int dtype);
 hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream);

@@ -74,7 +74,7 @@ int semicrf_embed(const void* tokens, int token_bits, const int32_t* lengths, co
 }
 
 size_t semicrf_embed_grad_bytes(int dtype, int B, int T, int V, int N) {
-    if (!type_ok(dtype) || check_rows(B, T, N) || V < 1 || V >= MAX_ROWS) return 0;
+    if (!type_ok(dtype) || check_rows(B, T, N) || V < 1 || V >= MAX_ROWS || N > EMBED_GRAD_MAX_N) return 0;
     return embed_grad_bytes(B, T, V, N, dtype);
 }
 
@@ -84,6 +84,7 @@ int semicrf_embed_grad(const void* tokens, int token_bits, const int32_t* length
                        void* grad_table, int32_t* status) {
     int rc = check_embed(tokens, token_bits, dtype, B, T, V, N);
     if (rc) return rc;
+    if (N > EMBED_GRAD_MAX_N) return SEMICRF_ERR_UNSUPPORTED;
     if (!grad_out || !grad_table) return SEMICRF_ERR_INVALID;
     if ((rc = check_ws(workspace, workspace_bytes, embed_grad_bytes(B, T, V, N, dtype)))) return rc;
     EmbedArgs a{};
