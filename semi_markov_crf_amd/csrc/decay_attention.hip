@@ -183,7 +183,8 @@ struct Role {
 
 struct Sweep {
     Role a, b, c;
-    int B, T, H, Da, Dc;     // H: query heads
+    int B0, B1;              // sequences of a launch
+    int T, H, Da, Dc;        // H: query heads
     const int32_t* lengths;
     const float* log_decay;
     float scale, si, su;
@@ -222,8 +223,8 @@ __device__ __forceinline__ bool place(const Sweep& w, int sweeps, int group, Pla
     p.seg = u % w.nseg;
     u /= w.nseg;
     p.h = u % hk * group + m % group;
-    p.b = u / hk;
-    return p.b < w.B;
+    p.b = w.B0 + u / hk;
+    return p.b < w.B1;
 }
 
 __device__ __forceinline__ float power(float g2, int n) {
@@ -879,7 +880,7 @@ struct GroupSum {
     const float* x[2];
     void* out[2];
     int D[2];
-    long heads;              // rows * Hk
+    long first, end;         // heads of a launch, of rows * Hk
     int group;
 };
 template <class T>
@@ -887,9 +888,9 @@ __global__ __launch_bounds__(256) void k_attn_group(const GroupSum a) {
     constexpr int V = 4;
     const int which = blockIdx.y, D = a.D[which], pieces = (D + V - 1) / V;
     const long i = (long)blockIdx.x * 256 + threadIdx.x;
-    const long head = i / pieces;
-    if (head >= a.heads) return;
-    const int c = (int)(i - head * pieces) * V;
+    const long head = a.first + i / pieces;
+    if (head >= a.end) return;
+    const int c = (int)(i % pieces) * V;
     const float* p = a.x[which] + head * a.group * D + c;
     float s[V] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int q = 0; q < a.group; ++q) {
@@ -1056,7 +1057,7 @@ hipError_t with_kernel(const semicrf_attention& p, F&& f) {
 Sweep base_sweep(const AttnArgs& a, const AttnLayout& l) {
     const semicrf_attention& p = a.p;
     Sweep w{};
-    w.B = p.B; w.T = p.T; w.H = p.Hq;
+    w.T = p.T; w.H = p.Hq;
     w.lengths = p.lengths;
     w.log_decay = p.log_decay;
     w.scale = p.scale;
@@ -1077,9 +1078,23 @@ bool fast_out(const Sweep& w, int es) {
     return (uintptr_t)w.out % 4 == 0 && w.Dc % 4 == 0 && (long)w.H * w.Dc * (w.out32 ? 4 : es) * 64 < (1l << 29);
 }
 
-unsigned sweep_grid(const Sweep& w, int sweeps, int group) {
-    const long units = (long)w.B * (w.H / group) * w.nseg;
-    return (unsigned)((units + CHIPLETS - 1) / CHIPLETS * CHIPLETS * sweeps * group);
+// Launches over all sequences, as many at a time as a grid of less than 2^32 threads holds:
+// f(set, workgroups).
+template <int N, class F>
+hipError_t by_sequences(const semicrf_attention& p, Sweeps<N> set, int threads, F&& f) {
+    const long group = p.Hq / p.Hk, units = (long)p.Hk * set.s[0].nseg;      // of a sequence
+    const long most = (1l << 32) / threads / (N * group) / CHIPLETS * CHIPLETS - CHIPLETS, step = most / units;
+    for (long b = 0; b < p.B; b += step) {
+        const long end = b + step < p.B ? b + step : p.B;
+        for (Sweep& w : set.s) {
+            w.B0 = (int)b;
+            w.B1 = (int)end;
+        }
+        f(set, (unsigned)(((end - b) * units + CHIPLETS - 1) / CHIPLETS * CHIPLETS * N * group));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <int N>
@@ -1087,17 +1102,17 @@ hipError_t run_state(const semicrf_attention& p, const Sweeps<N>& set, hipStream
     return with_kernel(p, [&](auto t, auto pp, auto cc) {
         using T = decltype(t);
         constexpr int P = decltype(pp)::value, C = decltype(cc)::value, es = sizeof(T);
-        const int group = p.Hq / p.Hk;
-        const dim3 grid(sweep_grid(set.s[0], N, group)), block(64 * sweep_waves(P));
+        const int group = p.Hq / p.Hk, threads = 64 * sweep_waves(P);
         bool fast = true;
         for (const Sweep& w : set.s) fast = fast && fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es);
-        if (!fast)
-            hipLaunchKernelGGL((k_attn_state<T, P, C, LOOSE, N>), grid, block, 0, stream, set, group);
-        else if (p.Dk == P && p.Dv == P)
-            hipLaunchKernelGGL((k_attn_state<T, P, C, FULL, N>), grid, block, 0, stream, set, group);
-        else
-            hipLaunchKernelGGL((k_attn_state<T, P, C, PART, N>), grid, block, 0, stream, set, group);
-        return hipGetLastError();
+        return by_sequences(p, set, threads, [&](const Sweeps<N>& part, unsigned grid) {
+            if (!fast)
+                hipLaunchKernelGGL((k_attn_state<T, P, C, LOOSE, N>), grid, threads, 0, stream, part, group);
+            else if (p.Dk == P && p.Dv == P)
+                hipLaunchKernelGGL((k_attn_state<T, P, C, FULL, N>), grid, threads, 0, stream, part, group);
+            else
+                hipLaunchKernelGGL((k_attn_state<T, P, C, PART, N>), grid, threads, 0, stream, part, group);
+        });
     });
 }
 
@@ -1106,19 +1121,19 @@ hipError_t run_sweep(const semicrf_attention& p, const Sweeps<N>& set, hipStream
     return with_kernel(p, [&](auto t, auto pp, auto cc) {
         using T = decltype(t);
         constexpr int P = decltype(pp)::value, C = decltype(cc)::value, es = sizeof(T);
-        const int group = p.Hq / p.Hk;
-        const dim3 grid(sweep_grid(set.s[0], N, group)), block(64 * sweep_waves(P));
+        const int group = p.Hq / p.Hk, threads = 64 * sweep_waves(P);
         bool fast = true;
         for (const Sweep& w : set.s)
             fast = fast && fast_role(w.a, w.Da, es) && fast_role(w.b, w.Da, es) && fast_role(w.c, w.Dc, es) &&
                    fast_out(w, es);
-        if (!fast)
-            hipLaunchKernelGGL((k_attn_sweep<T, P, C, LOOSE, N>), grid, block, 0, stream, set, group);
-        else if (p.Dk == P && p.Dv == P)
-            hipLaunchKernelGGL((k_attn_sweep<T, P, C, FULL, N>), grid, block, 0, stream, set, group);
-        else
-            hipLaunchKernelGGL((k_attn_sweep<T, P, C, PART, N>), grid, block, 0, stream, set, group);
-        return hipGetLastError();
+        return by_sequences(p, set, threads, [&](const Sweeps<N>& part, unsigned grid) {
+            if (!fast)
+                hipLaunchKernelGGL((k_attn_sweep<T, P, C, LOOSE, N>), grid, threads, 0, stream, part, group);
+            else if (p.Dk == P && p.Dv == P)
+                hipLaunchKernelGGL((k_attn_sweep<T, P, C, FULL, N>), grid, threads, 0, stream, part, group);
+            else
+                hipLaunchKernelGGL((k_attn_sweep<T, P, C, PART, N>), grid, threads, 0, stream, part, group);
+        });
     });
 }
 
@@ -1204,12 +1219,16 @@ hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t 
     TRY(run_sweep(p, Sweeps<3>{{dv, r, f}}, stream));
     if (group > 1) {
         GroupSum s{{(const float*)((char*)ws + l.gk), (const float*)((char*)ws + l.gv)},
-                   {a.grad_k, a.grad_v}, {p.Dk, p.Dv}, (long)p.B * p.T * p.Hk, group};
-        const long n = s.heads * (((p.Dk > p.Dv ? p.Dk : p.Dv) + 3) / 4);
-        const dim3 grid((unsigned)((n + 255) / 256), 2);
-        if (p.dtype == SEMICRF_F32) hipLaunchKernelGGL((k_attn_group<float>), grid, dim3(256), 0, stream, s);
-        else hipLaunchKernelGGL((k_attn_group<bf16>), grid, dim3(256), 0, stream, s);
-        TRY(hipGetLastError());
+                   {a.grad_k, a.grad_v}, {p.Dk, p.Dv}, 0, 0, group};
+        const long heads = (long)p.B * p.T * p.Hk, pieces = ((p.Dk > p.Dv ? p.Dk : p.Dv) + 3) / 4;
+        const long most = (1l << 31) / pieces;           // a launch holds less than 2^32 threads
+        for (; s.first < heads; s.first = s.end) {
+            s.end = s.first + most < heads ? s.first + most : heads;
+            const dim3 grid((unsigned)(((s.end - s.first) * pieces + 255) / 256), 2);
+            if (p.dtype == SEMICRF_F32) hipLaunchKernelGGL((k_attn_group<float>), grid, dim3(256), 0, stream, s);
+            else hipLaunchKernelGGL((k_attn_group<bf16>), grid, dim3(256), 0, stream, s);
+            TRY(hipGetLastError());
+        }
     }
     return hipSuccess;
 }
