@@ -545,6 +545,17 @@ k_attn_state(const Sweeps<N> set, int group) {
     S.store(w.local + (((size_t)b * w.H + h) * w.nseg + seg) * w.Da * w.Dc, w.Da, w.Dc, false, 1.0f / sigma);
 }
 
+// As Decay, of the many positions of a segment
+struct Decay64 {
+    float f;
+    bool near1;
+    __device__ __forceinline__ Decay64(double g, int m) {
+        const double e = m == 0 ? 1.0 : exp(g * m);
+        near1 = e > 0.5;
+        f = (float)(m == 0 ? 0.0 : near1 ? expm1(g * m) : e);
+    }
+};
+
 // Start of every segment from the segments' own states, in place, in order; the state after
 // the last position to `out`.  One or two states: blockIdx.y = state * H + head.  Bound by the
 // latency of its loads, 16 segments at a time: 23 segments of 32 heads, 12 MB, 9 us.
@@ -568,7 +579,7 @@ __global__ __launch_bounds__(256) void k_attn_scan(const Scan a) {
     const int L = seq_length(a.lengths, b, T, nullptr);
     const double g = a.log_decay[h];
     float cur = init ? init[bh * D + i] : 0.0f;
-    const float full = (float)exp(g * seg);
+    const Decay64 full(g, seg);
     float* p = local + bh * nseg * D + i;
     // the loads do not wait for one another: U at a time
     constexpr int U = 16;
@@ -582,8 +593,8 @@ __global__ __launch_bounds__(256) void k_attn_scan(const Scan a) {
             if (s >= nseg) break;
             p[(size_t)s * D] = cur;
             const int m = min(seg, max(0, L - s * seg));
-            const float f = m == seg ? full : m == 0 ? 1.0f : (float)exp(g * m);
-            cur = fmaf(cur, f, own[n]);
+            const Decay64 d = m == seg ? full : Decay64(g, m);
+            cur = (d.near1 ? cur : 0.0f) + fmaf(cur, d.f, own[n]);
         }
     }
     if (out) out[bh * D + i] = cur;

@@ -153,3 +153,33 @@ def test_a_step_counts_as_an_in_place_write(crf):  # noqa: F811
     with torch.inference_mode():
         crf.decay_attention_step(*one, g, torch.zeros(2, 2, 8, 8, device="cuda"))
     torch.cuda.synchronize()
+
+
+def segments(crf, B, T, Hq, Hk, Dk, Dv, typ, grad=False):  # noqa: F811
+    """Segments that a call is cut into, from the states that its workspace holds."""
+    a = crf._native.Attention()
+    a.dtype, a.B, a.T, a.Hq, a.Hk, a.Dk, a.Dv = int(typ == "bf16"), B, T, Hq, Hk, Dk, Dv
+    n = crf._native.load().semicrf_decay_attention_bytes(a, int(grad))
+    if grad and Hq > Hk:
+        n -= sum(-(-B * T * Hq * 4 * D // 256) * 256 for D in (Dk, Dv))
+    return max(1, n // (1 + grad) // (B * Hq * Dk * Dv * 4))
+
+
+def test_segments_join_without_drift(crf):  # noqa: F811
+    """A state that only decays, over a hundred segments and more: every join rounds it once, errors of
+    independent sign (as in test_a_long_stream_keeps_its_state), and exp(log decay * segment) adds
+    nothing of one sign.  grad_state is the same sum backward."""
+    import torch
+    B, T, H, D = 1, 100_000, 8, 16
+    rng = np.random.default_rng(11)
+    n = min(segments(crf, B, T, H, H, D, D, "f32", grad) for grad in (False, True))
+    assert n >= 40
+    g = -np.exp2(rng.uniform(-24, -17, H)).astype(f32)
+    st = rng.standard_normal((B, H, D, D)).astype(f32)
+    want = st * np.exp(g.astype(np.float64) * T)[None, :, None, None]
+    bound = 6 * U * np.sqrt(max(segments(crf, B, T, H, H, D, D, "f32", x) for x in (False, True)) + 1)
+    zero = torch.zeros(B, T, H, D, device="cuda")
+    _, end = crf.decay_attention(zero, zero, zero, dev(g), state=dev(st), want_state=True)
+    close(end, want, bound * np.abs(want), "state")
+    d = crf.decay_attention_grad(zero, zero, zero, zero, dev(g), state=dev(st), grad_state=dev(st))
+    close(d["grad_state"], want, bound * np.abs(want), "grad_state")
