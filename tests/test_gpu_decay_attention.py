@@ -183,3 +183,25 @@ def test_segments_join_without_drift(crf):  # noqa: F811
     close(end, want, bound * np.abs(want), "state")
     d = crf.decay_attention_grad(zero, zero, zero, zero, dev(g), state=dev(st), grad_state=dev(st))
     close(d["grad_state"], want, bound * np.abs(want), "grad_state")
+
+
+def test_float32_rounds_a_long_memory_once_a_chunk(crf):  # noqa: F811
+    """Time constants of 8,192 positions, where the state is the sum of many chunks.  Rounding a number
+    gives a relative error of 0.42 u on average (u / sqrt(3), less over a binade).  If each chunk of 32
+    rounds the state once, what the decay leaves of the errors is 0.42 u sqrt(8192 / 64) = 4.7 u of it;
+    joins of segments add 1.5 u, a product of 64 terms 2.4 u, weights about 1 u: 5.6 u in all, of the
+    result as of the state.  9 u is half as much again; one rounding for every product of a chunk
+    would give 14 u and more."""
+    from test_gpu_encoder import host
+    B, T, H, D = 1, 20_000, 2, 64
+    rng = np.random.default_rng(13)
+    q, k, v, do = (host(dev(rng.standard_normal((B, T, H, D)).astype(f32))) for _ in range(4))
+    g = np.array([-2.0 ** -13, -1.25 * 2.0 ** -13], f32)
+    a = [dev(x.astype(f32)) for x in (q, k, v)] + [dev(g)]
+    got = {"out": crf.decay_attention(*a, scale=1.0), **crf.decay_attention_grad(dev(do.astype(f32)), *a, scale=1.0)}
+    want = dict(zip(("grad_q", "grad_k", "grad_v"), ref.attention_grad(do, q, k, v, g, 1.0, [T])))
+    want["out"] = ref.attention(q, k, v, g, 1.0, [T])[0]
+    for n, x in want.items():
+        off = np.linalg.norm(host(got[n]) - x) / np.linalg.norm(x)
+        print(f"{n}: {off / U:.2f} u", flush=True)
+        assert off <= 9 * U, (n, off / U)
