@@ -205,3 +205,56 @@ def test_float32_rounds_a_long_memory_once_a_chunk(crf):  # noqa: F811
         off = np.linalg.norm(host(got[n]) - x) / np.linalg.norm(x)
         print(f"{n}: {off / U:.2f} u", flush=True)
         assert off <= 9 * U, (n, off / U)
+
+
+# rows that fill the padded width, cut into segments of several chunks: B, T, Hq, Hk, D, typ
+LONG = [
+    (2, 9000, 4, 2, 64, "f32"), (2, 9000, 4, 2, 64, "bf16"),
+    (2, 9000, 4, 2, 32, "f32"), (2, 9000, 4, 2, 32, "bf16"),
+    (2, 9000, 2, 1, 128, "f32"), (2, 9000, 2, 1, 128, "bf16"),
+    (1, 9000, 4, 4, 64, "bf16"), (1, 9000, 8, 1, 64, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=[f"B{c[0]}T{c[1]}H{c[2]}_{c[3]}D{c[4]}{c[5]}" for c in LONG])
+def test_segments_of_several_chunks(crf, case):  # noqa: F811
+    """Slow heads among them one that keeps everything, ragged lengths, initial and final states.
+    Element by element within `tol`; and the norm of all errors of an array, which a lost part of the
+    state or of the masked products would raise, although sums over thousands of positions leave
+    `tol` wide:
+      * rounding to bfloat16 gives 0.42 w of the result on average (w / sqrt(3), less over a binade);
+        5 % more leave room for a third of it besides;
+      * in float32, 9 u as in test_float32_rounds_a_long_memory_once_a_chunk.  A head without decay rounds
+        its growing state T / 32 times, the same as 140 times at its final size: 5 u; a product of 128
+        terms 3.4 u; joins and weights 1.8 u: 6.3 u in all."""
+    import encoder_ref64 as ref64
+    from test_gpu_encoder import host
+    B, T, Hq, Hk, D, typ = case
+    for grad in (False, True):
+        n, C = segments(crf, B, T, Hq, Hk, D, D, typ, grad), 64 if typ == "bf16" else 32
+        print(f"\n[decay_attention {case}: {n} segments]", flush=True)
+        assert n >= 4 and -(-T // C) / n > 2
+    rng = np.random.default_rng(T + D)
+    r = lambda *s: host(dev(rng.standard_normal(s).astype(f32), typ))  # noqa: E731
+    q, k, v, do = r(B, T, Hq, D), r(B, T, Hk, D), r(B, T, Hk, D), r(B, T, Hq, D)
+    g = np.resize(np.array([0.0, -2.0 ** -12, -2.0 ** -6, -0.5], f32), Hq)
+    st, gs = (rng.standard_normal((B, Hq, D, D)).astype(f32) for _ in range(2))
+    lengths = np.array([T, T * 2 // 3 + 7], np.int32)[:B]
+    scale, ln = 0.25, dev(lengths)
+    a = [dev(poison(x.copy(), lengths).astype(f32), typ) for x in (q, k, v)] + [dev(g)]
+    got = dict(zip(("o", "state"), crf.decay_attention(*a, scale=scale, lengths=ln, state=dev(st), want_state=True)))
+    want = dict(zip(got, ref64.attention(q, k, v, g, scale, lengths, st, "cuda")))
+    p = ref.absolute(do, q, k, v, st, gs)
+    mag = dict(zip(got, ref64.attention(p[1], p[2], p[3], g, scale, lengths, p[4], "cuda")))
+    got.update(crf.decay_attention_grad(dev(poison(do.copy(), lengths).astype(f32), typ), *a, scale=scale, lengths=ln,
+                                        state=dev(st), grad_state=dev(gs)))
+    grads = ("grad_q", "grad_k", "grad_v", "grad_state")
+    want.update(zip(grads, ref64.attention_grad(do, q, k, v, g, scale, lengths, st, gs, "cuda")))
+    mag.update(zip(grads, ref64.attention_grad(p[0], p[1], p[2], p[3], g, scale, lengths, p[4], p[5], "cuda")))
+    for n, x in want.items():
+        t = "f32" if "state" in n else typ
+        off = np.linalg.norm(host(got[n]) - x) / np.linalg.norm(x)
+        print(f"{n}: {off / (W if t == 'bf16' else U):.2f} of its unit", flush=True)
+        close(got[n], x, tol(t, T, D + Hq // Hk, x, mag[n]), n)
+        if t == typ:
+            assert off <= (1.05 * 0.425 * W if t == "bf16" else 9 * U), (n, off)
