@@ -7,7 +7,8 @@ result adds up.
     in test_gpu_encoder.py);
   * in bfloat16 the masked products and the state are sums of two bfloat16 numbers when they are
     multiplied: w^2 of each term, 1.1 w^2 mag in all;
-  * the output is rounded once: w |result| in bfloat16.
+  * the output is rounded once: w |result| in bfloat16;
+  * below 2^-126 float32 is rounded to multiples of 2^-149: an output's own rounding is 2^-150 at least.
 """
 
 import numpy as np
@@ -24,7 +25,8 @@ f32 = np.float32
 def tol(typ, T, D, want, mag):
     """Of a result that is rounded to `typ`: D terms of a product, 64 positions of a chunk twice,
     a chain of chunks."""
-    return ((D + 2 * 64 + T // 32 + 64) * U + (1.1 * W ** 2 if typ == "bf16" else 0)) * mag + rounding(typ, want)
+    return ((D + 2 * 64 + T // 32 + 64) * U + (1.1 * W ** 2 if typ == "bf16" else 0)) * mag + \
+        np.maximum(rounding(typ, want), 2.0 ** -150)
 
 
 def check(crf, case, seed=0, g=None, scale=0.25):  # noqa: F811
@@ -258,3 +260,15 @@ def test_segments_of_several_chunks(crf, case):  # noqa: F811
         close(got[n], x, tol(t, T, D + Hq // Hk, x, mag[n]), n)
         if t == typ:
             assert off <= (1.05 * 0.425 * W if t == "bf16" else 9 * U), (n, off)
+
+
+STRONG = [(2, 200, 6, 6, 32, 32, "bf16", "ragged", True), (2, 150, 6, 3, 64, 64, "bf16", "full", True),
+          (2, 70, 6, 6, 128, 128, "bf16", "ragged", True), (2, 200, 6, 3, 39, 20, "bf16", "full", True),
+          (2, 150, 6, 6, 64, 64, "f32", "full", True)]
+
+
+@pytest.mark.parametrize("case", STRONG, ids=[name(c) for c in STRONG])
+def test_strong_decays(crf, case):  # noqa: F811
+    """gamma from 0 and e^-80 to 1.  The gradient of the initial state is of order gamma, down to 10^-35,
+    and as exact as any: the low parts of what is added to it must not underflow."""
+    check(crf, case, g=[-np.inf, -80.0, -30.0, -12.0, -1e-6, 0.0])
