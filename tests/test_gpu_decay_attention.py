@@ -272,3 +272,13 @@ def test_strong_decays(crf, case):  # noqa: F811
     """gamma from 0 and e^-80 to 1.  The gradient of the initial state is of order gamma, down to 10^-35,
     and as exact as any: the low parts of what is added to it must not underflow."""
     check(crf, case, g=[-np.inf, -80.0, -30.0, -12.0, -1e-6, 0.0])
+
+
+SHARED = [(2, 200, 16, 1, 128, 128, "bf16", "ragged", True), (2, 100, 16, 1, 64, 64, "f32", "ragged", True),
+          (2, 130, 33, 1, 64, 64, "bf16", "full", True), (2, 90, 12, 1, 128, 100, "f32", "full", False),
+          (1, 1500, 34, 2, 32, 32, "bf16", "full", True)]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=[name(c) for c in SHARED])
+def test_many_query_heads_on_one(crf, case):  # noqa: F811
+    check(crf, case)
