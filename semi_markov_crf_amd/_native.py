@@ -121,11 +121,16 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+# the current device; torch.cuda.current_device first asks whether torch is initialised, which it is where
+# there are arrays, and single-token calls are host-bound
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def call(dev: int, name: str, *args):
     """The library's function `name`, with GPU `dev` current: a default stream is a null handle, which
     stands for that of the current GPU, whichever the arrays are on."""
-    f = getattr(load(), name)
-    if torch.cuda.current_device() == dev:
+    f = getattr(_lib or load(), name)
+    if _current_device() == dev:
         return f(*args)
     with torch.cuda.device(dev):
         return f(*args)

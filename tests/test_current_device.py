@@ -48,8 +48,10 @@ def calls(monkeypatch):
     def on_host(make):
         return lambda *a, device=None, **kw: make(*a, **kw).as_subclass(Array)
 
-    monkeypatch.setattr(_native, "load", lambda lib=Lib(): lib)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    lib = Lib()
+    monkeypatch.setattr(_native, "load", lambda: lib)
+    monkeypatch.setattr(_native, "_lib", lib)
+    monkeypatch.setattr(_native, "_current_device", lambda: now[0])
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=0))
     monkeypatch.setattr(encoder, "_raw_stream", lambda index: 0)
@@ -99,7 +101,7 @@ def test_crf(calls):
 
 def test_the_current_device_stays_where_it_is(monkeypatch):
     """No switch where the arrays' GPU is current."""
-    monkeypatch.setattr(_native, "load", lambda: types.SimpleNamespace(f=lambda *a: a))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_native, "_lib", types.SimpleNamespace(f=lambda *a: a))
+    monkeypatch.setattr(_native, "_current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "device", lambda index: pytest.fail("switched"))
     assert _native.call(0, "f", 3, 4) == (3, 4)
