@@ -27,7 +27,8 @@
  *    workspace.  The library allocates no device memory and keeps no pointer or
  *    other state after a call returns.  Calls on different streams with distinct
  *    workspaces may run concurrently.
- *  - Execution: all work is enqueued on `stream`; no call synchronises the host.
+ *  - Execution: all work is enqueued on `stream`; no call synchronises the host.  The
+ *    arrays and `stream` belong to the current device (NULL is its default stream).
  *    Outputs are valid once the stream reaches that point.  Results are bitwise
  *    reproducible for the same inputs, shapes and checkpoint interval (fixed-order
  *    reductions, no floating-point atomics).

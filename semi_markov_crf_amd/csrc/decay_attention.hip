@@ -244,8 +244,8 @@ __device__ __forceinline__ float power(float g2, int n) {
 // A descriptor spans exactly the chunk's valid rows, less than 2^29 bytes, so that rows and columns
 // out of range read as zeros with no branch (bit 31 of the offset puts a column out of range); rows
 // are then whole pieces of 16 bytes from dword addresses.  Measured in bfloat16: 32 x 800 positions,
-// 8 heads of 64 columns 36 us FULL, 42 PART, 52 LOOSE; 16 x 800 of 40 and 48 columns 36 PART, 47 LOOSE;
-// of 128 and 64 columns 53 PART, 62 when all 128 x 128 products are done.
+// 8 heads of 64 columns 34 us FULL, 44 LOOSE; 16 x 800 of 40 and 48 columns 33 PART, 41 LOOSE; of 128
+// and 64 columns 48 PART, 51 FULL with 128 and 128.
 enum { FULL, PART, LOOSE };
 
 // A chunk's rows of one role on their way from memory to LDS, in 16-byte pieces; a thread's
@@ -515,7 +515,7 @@ __device__ __forceinline__ void update_rest(State<T, P>& S, const T* sb, const T
 // The state of every segment alone, from zero: S = sum_j su gamma^(m-1-j+e) b_j c_j^T, a chunk at a
 // time.  Bound by HBM where segments are many: 4 x 100,000 positions, 8 heads of 64 columns, 0.82 GB
 // of bfloat16 in 175 us (4.7 TB/s).  fp32 takes the slower matrix instructions: 100,001 positions, 6
-// heads, both states of the gradients, 0.61 GB in 147 us (4.2 TB/s).
+// heads, both states of the gradients, 0.61 GB in 152 us (4.0 TB/s).
 template <class T, int P, int C, int MODE, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), P == 128 ? 2 : 4) void
 k_attn_state(const Sweeps<N> set, int group) {
@@ -592,7 +592,7 @@ struct Decay64 {
 
 // Start of every segment from the segments' own states, in place, in order; the state after
 // the last position to `out`.  One or two states: blockIdx.y = state * H + head.  Bound by the
-// latency of its loads, 16 segments at a time: 23 segments of 32 heads, 12 MB, 9 us.
+// latency of its loads, 16 segments at a time: 23 segments of 32 heads, 12 MB, 9.5 us.
 // grid (ceil(D / 256), states * H, B), D = Da Dc
 struct Scan {
     float* local[2];
@@ -695,12 +695,13 @@ __device__ __forceinline__ void store_rows(const Sweep& w, O* seq, int t0, int m
 // each wavefront has its columns to itself: the state's part, the chunk's own part, the update.  The
 // fragments of a product step are read and split ahead of its products (scheduling barriers keep
 // them there), and products that add to one tile are apart.
-// 4 x 100,000 positions, 8 heads of 64 columns in bfloat16: 1.64 GB in 385 us (4.3 TB/s), bound by
-// HBM; 32 x 800 positions, 8 heads on 256 workgroups: 34 us, bound by the latency of 13 chunks in
-// order, some 5,100 cycles each (rows into LDS 600, next loads 400, masked products 900, state's
-// part 700, own part and update 1,600, stores and the wait for loads 700).  The three sweeps of the
-// gradients in fp32, 100,001 positions, 6 heads: 40 GFLOP of matrix instructions in 375 to 440 us,
-// about 100 of the 155 TFLOP/s that a large product reaches.
+// Medians of a few calls after a start: 4 x 100,000 positions, 8 heads of 64 columns in bfloat16:
+// 1.64 GB in 397 us (4.1 TB/s), bound by HBM; 32 x 800 positions, 8 heads on 256 workgroups: 36 us (34
+// in many calls), bound by the latency of 13 chunks in order, some 5,500 cycles each (rows into LDS
+// 650, next loads 450, masked products 1,000, state's part 650, own part and update 1,800, stores and
+// the wait for loads 750).  The three sweeps of the gradients in fp32, 100,001 positions, 6 heads: 40
+// GFLOP of matrix instructions in 476 us (387 to 552), 84 of the 155 TFLOP/s that a large product
+// reaches.
 template <class T, int P, int C, int MODE, int N>
 __global__ __launch_bounds__(64 * sweep_waves(P), (sweep_occupancy<T, P>())) void
 k_attn_sweep(const Sweeps<N> set, int group) {
@@ -745,7 +746,7 @@ k_attn_sweep(const Sweeps<N> set, int group) {
     // Weights of the masked products, scale gamma^(i-j) where i >= j.  BIG: three tiles of 32 x 32, a
     // wavefront each; lanes hold column i = r32, rows j = 8 q + 4 h32 + r.  Otherwise in tiles of 16
     // (rows j = 4 gr + r, column i = r16): on the diagonal, and one tile off it.  16 x 800 positions, 8
-    // heads of 128 columns: 54.9 us against 56.7 in tiles of 16, the gradients 98.7 against 102.8.
+    // heads of 128 columns: 50.5 us against 52.8 in tiles of 16, the gradients 99.9 against 104.7.
     constexpr bool BIG = sizeof(T) == 2 && NW >= 4;
     const int r32 = lane & 31, h32 = lane >> 5;
     float own[BIG ? 16 : 1], diag[4], below[4], inter[IT];
@@ -963,8 +964,8 @@ __global__ __launch_bounds__(256) void k_attn_group(const GroupSum a) {
 
 // ------------------------------------------------------------------ one token
 // S = gamma S + k v^T, o = scale q S: a state is read and written once, so HBM bounds a batch (256
-// streams, 16 heads of 128 x 128, 0.46 GB in 97 us, 4.8 TB/s) and the launch a single stream (8 heads
-// of 64 x 64 4.6 us).  A workgroup a head, so that one stream still spreads over compute units and no sum
+// streams, 16 heads of 128 x 128, 0.46 GB in 98 us, 4.7 TB/s) and the launch a single stream (8 heads
+// of 64 x 64 4.9 us).  A workgroup a head, so that one stream still spreads over compute units and no sum
 // leaves a workgroup.
 // grid (Hq, B), block 256: LR lanes take 4 columns each of a state row, 256 / LR row groups.
 template <class T>
@@ -1035,9 +1036,13 @@ int sweep_slots(const semicrf_attention& p) {
 // the price of the pass over the states, its launches and the join.  The times are modelled in
 // units of one chunk of the sweep where a compute unit has one workgroup (2 us at width 64, 64
 // bfloat16 or 32 fp32 positions); with w workgroups a unit it takes 0.4 + 0.6 w, the state's pass 0.4
-// of that, launches and prologues 6 (9 with gradients), the join 0.06 a segment.  Measured, one
-// segment against the choice: 1 x 3,000 positions, 2 heads, bfloat16 93 and 25 us; 8 x 800, 8 heads 32
-// and 30 us, fp32 57 and 44; but bfloat16 gradients 31 and (4 segments) 42 us: one is kept.
+// of that, launches and prologues 6 (9 with gradients), the join 0.06 a segment.  Measured at width
+// 64, one segment against the choice: 1 x 3,000 positions, 2 heads, bfloat16 94 and 24 us; 8 x 800, 8
+// heads 31 and 30 us, fp32 57 and 44; but bfloat16 gradients 32 and (4 segments) 44 us: one is kept.
+// The constants are those of width 64 at widths 32 and 128 too.  The members of a unit are to run at
+// once on one chiplet; more query heads on one than it holds (gradients: from 11 at width 128, from
+// 33 at width 64 in bfloat16) get one segment: 100,000 positions, 16 heads on one of 128 columns, 11.3 ms,
+// in four segments 3.6.
 int segment(const semicrf_attention& p, bool grad) {
     const int C = chunk_of(p), sweeps = grad ? 3 : 1, states = grad ? 2 : 1, group = p.Hq / p.Hk;
     const long bh = (long)p.B * p.Hq, n = ((long)p.T + C - 1) / C;

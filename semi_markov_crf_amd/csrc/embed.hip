@@ -9,7 +9,9 @@
 // wavefront adds the rows of its chunk into registers, run by run.  A run inside one chunk is
 // written to dW at once; a run that crosses chunk borders leaves one partial row a chunk, and
 // k_grad_join adds those in order.  So a token that fills the whole batch and 50,000 tokens
-// that appear once cost the same reads, and the same inputs give the same bits.
+// that appear once cost the same reads, and the same inputs give the same bits.  Beyond 2 million
+// positions the partial rows of such a token grow with the batch (one a 256 positions), and one
+// workgroup a column slab adds them up.
 #include "common.h"
 #include "encoder.h"
 
@@ -541,8 +543,9 @@ GradLayout grad_layout(int B, int T, int V, int N, int es) {
     l.passes = (bits + 7) / 8;
     // rows per chunk: about 2,048 wavefronts over the chunks and column slabs fill the device; longer
     // chunks leave fewer partial rows.  A narrow row takes a part of a wavefront; its chunks are at most
-    // 8,192, so that the join has no more to do than the sums (400,000 rows, sums + join: 17 + 18 us
-    // for 16 float32 columns, 13 + 28 with 16,384 chunks, 29 + 11 with 4,096).
+    // 8,192 up to 2 million positions (256 rows a chunk at most), so that the join has no more to do than
+    // the sums (400,000 rows, sums + join: 17 + 18 us for 16 float32 columns, 13 + 28 with 16,384
+    // chunks, 29 + 11 with 4,096).
     const long np = ((long)N * es + 15) / 16, G = np <= 8 ? 8 : np <= 16 ? 16 : np <= 32 ? 32 : 64;
     l.R = 8;
     while (l.R < 256 && (l.n * ((np + G - 1) / G) * G / 64 / l.R > 2048 || l.n / l.R > 8192)) l.R *= 2;
