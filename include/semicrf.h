@@ -385,6 +385,122 @@ int semicrf_decay_attention_grad(const semicrf_attention* attention, const void*
 int semicrf_decay_attention_step(const semicrf_attention* attention, const int32_t* slots,
                                  int pool, hipStream_t stream, void* out, float* state_out);
 
+/* ------------------------------------------------------------------ blocks and pretraining
+ * What an encoder block needs beside attention, and what it is trained on before there are
+ * segments.  Conventions as for the encoder operators. */
+
+/* Gated linear recurrence, a decay of its own for each position and channel:
+ *   s_t = log_decay[n] sig(r_t),  a_t = exp(s_t),  h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sig(i_t) x_t,
+ * sig(z) = 1 / (1 + exp(-z)), r the decay gate and i the input gate before their sigmoid, h_0 = `state`
+ * or 0.  log_decay [N] is meant to be finite and <= 0: above 0, 1 - a^2 is negative and outputs are NaN. */
+typedef struct semicrf_recurrence {
+    const void* x;               /* [B, T, N], as decay_gate and input_gate */
+    const void* decay_gate;
+    const void* input_gate;
+    int64_t x_stride[2];         /* elements between sequences and positions; the last axis */
+    int64_t decay_stride[2];     /* is dense */
+    int64_t input_stride[2];
+    const int32_t* lengths;      /* [B] or NULL */
+    const float* log_decay;      /* [N] */
+    const float* state;          /* [B, N] before the first position, or NULL for 0 */
+    int dtype;                   /* of x, the gates and the outputs shaped like them */
+    int B, T, N;                 /* B < 2^16, N <= 2^20 */
+} semicrf_recurrence;
+
+/* Whole sequences.  out [B, T, N] dense, 0 at padding; state_out [B, N] float32 after position
+ * lengths[b] - 1 (the state before the first where that is 0), or NULL; it may be the array `state`
+ * points to.  starts [B, ceil(T / SEMICRF_RECURRENCE_SPAN), N] float32, or NULL: the state before
+ * each span of positions, for the gradient (spans past the length are left as they are).
+ * Workspace: semicrf_gated_recurrence_bytes(recurrence, 0), 256-byte aligned. */
+#define SEMICRF_RECURRENCE_SPAN 16
+size_t semicrf_gated_recurrence_bytes(const semicrf_recurrence* recurrence, int grad);
+int semicrf_gated_recurrence(const semicrf_recurrence* recurrence, hipStream_t stream,
+                             void* workspace, size_t workspace_bytes, void* out, float* state_out,
+                             float* starts, int32_t* status);
+
+/* Gradients, of out (grad_out [B, T, N] dense) and of state_out (grad_state_out [B, N] float32, or
+ * NULL for 0), from the `starts` the forward call left.  grad_x, grad_decay_gate, grad_input_gate
+ * [B, T, N] dense, 0 at padding; grad_log_decay [N] float32, summed over all positions in a fixed
+ * order; grad_state [B, N] float32; the last two may be NULL.  A decay gate so far closed that 1 - a^2
+ * is below 2^-123 counts sqrt(1 - a^2) as a constant.  Workspace:
+ * semicrf_gated_recurrence_bytes(recurrence, 1). */
+int semicrf_gated_recurrence_grad(const semicrf_recurrence* recurrence, const float* starts,
+                                  const void* grad_out, const float* grad_state_out,
+                                  hipStream_t stream, void* workspace, size_t workspace_bytes,
+                                  void* grad_x, void* grad_decay_gate, void* grad_input_gate,
+                                  float* grad_log_decay, float* grad_state, int32_t* status);
+
+/* One token of B streams (recurrence->T is 1, lengths NULL, inputs [B, N]: the strides between
+ * positions are not looked at), on states kept in a pool: recurrence->state and state_out are [pool,
+ * N] float32 and may be the same array.  slots as in semicrf_decay_attention_step.  out [B, N]. */
+int semicrf_gated_recurrence_step(const semicrf_recurrence* recurrence, const int32_t* slots,
+                                  int pool, hipStream_t stream, void* out, float* state_out);
+
+/* The end of one block and the start of the next, on the residual stream x:
+ *   r = x + scale sig(gate) f(branch),   y = norm(r) weight + bias,
+ * f(o) = o, or norm(o) branch_weight + branch_bias where norm_branch is set.  norm(z) = (z - mean) rstd
+ * over the last axis with rstd = 1 / sqrt(mean (z - mean)^2 + eps); center = 0 takes mean as 0 (the
+ * root-mean-square norm), in both norms.  A NULL gate or scale is a factor of 1, a NULL weight ones,
+ * a NULL bias zeros. */
+typedef struct semicrf_residual {
+    const void* x;               /* [B, T, N] dense */
+    const void* branch;          /* [B, T, N] */
+    const void* gate;            /* [B, T, N] before its sigmoid, or NULL */
+    int64_t branch_stride[2];    /* elements between sequences and positions; the last axis */
+    int64_t gate_stride[2];      /* is dense */
+    const void* scale;           /* [N] of type wdtype, as the four below; each may be NULL */
+    const void* weight;
+    const void* bias;
+    const void* branch_weight;   /* looked at where norm_branch is set */
+    const void* branch_bias;
+    const int32_t* lengths;      /* [B] or NULL */
+    float eps;
+    int dtype, wdtype;           /* wdtype: dtype or SEMICRF_F32 */
+    int norm_branch, center;
+    int B, T, N;                 /* N <= 16384 */
+} semicrf_residual;
+
+/* r, y [B, T, N] dense, 0 at padding; y is the norm of r before its rounding.  stats [B, T, 4]
+ * float32 (mean and rstd of r, mean and rstd of the branch; 0 where there is none), or NULL.  Outputs
+ * may not overlap inputs. */
+int semicrf_residual_norm(const semicrf_residual* residual, hipStream_t stream, void* r, void* y,
+                          float* stats, int32_t* status);
+
+/* Gradients of r and y (grad_r, grad_y [B, T, N] dense; NULL for 0) from the stats of the forward
+ * call.  grad_x, grad_branch and, where there is a gate, grad_gate [B, T, N] dense; grad_params
+ * [5][N] of type wdtype, or NULL: the gradients of weight, bias, scale, branch_weight and
+ * branch_bias, summed over all rows in a fixed order (of those that are not there, as if they were).
+ * Workspace: semicrf_residual_norm_grad_bytes, 256-byte aligned. */
+size_t semicrf_residual_norm_grad_bytes(int dtype, int B, int T, int N);
+int semicrf_residual_norm_grad(const semicrf_residual* residual, const float* stats,
+                               const void* grad_r, const void* grad_y, hipStream_t stream,
+                               void* workspace, size_t workspace_bytes, void* grad_x,
+                               void* grad_branch, void* grad_gate, void* grad_params,
+                               int32_t* status);
+
+/* Negative log-likelihood of tokens over a vocabulary: with z_v = scale x[b, t] . table[v],
+ *   loss[b, t] = log sum_v exp(z_v) - z_target,
+ * x [B, T, N], table [V, N] (it may be the one semicrf_embed reads), targets [B, T] int32 or int64
+ * (target_bits 32 or 64), loss [B, T] float32.  A negative target marks a position with nothing to
+ * predict: its x is not read and its loss is 0.  A target of V or more gives NaN and the status bit.
+ * lse [B, T] float32, or NULL: the log sum, for the gradient (0 where there is nothing to predict).
+ * The scores are formed in pieces and never kept.  B * T and V up to 2^22, N <= 32768.  Workspace:
+ * semicrf_token_nll_bytes(..., 0), 256-byte aligned. */
+size_t semicrf_token_nll_bytes(int dtype, int B, int T, int V, int N, int grad);
+int semicrf_token_nll(const void* x, const void* table, int dtype, const void* targets,
+                      int target_bits, const int32_t* lengths, int B, int T, int V, int N,
+                      float scale, hipStream_t stream, void* workspace, size_t workspace_bytes,
+                      float* loss, float* lse, int32_t* status);
+
+/* Its gradients from those of loss (grad_loss [B, T] float32) and the lse of the forward call:
+ * grad_x [B, T, N] (0 where there is nothing to predict) and grad_table [V, N], both of type dtype; either
+ * may be NULL.  A target of V or more counts for nothing.  Workspace: semicrf_token_nll_bytes(..., 1). */
+int semicrf_token_nll_grad(const float* grad_loss, const void* x, const void* table, int dtype,
+                           const void* targets, int target_bits, const int32_t* lengths,
+                           const float* lse, int B, int T, int V, int N, float scale,
+                           hipStream_t stream, void* workspace, size_t workspace_bytes,
+                           void* grad_x, void* grad_table, int32_t* status);
+
 #ifdef __cplusplus
 }
 #endif

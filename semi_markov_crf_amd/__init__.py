@@ -17,7 +17,8 @@ takes optional boundary projections proj_start / proj_end [B, T, C] float32: a
 segment [s, e) of label c gains proj_start[b, s, c] + proj_end[b, e-1, c].
 
 The operators of an encoder that makes the emissions (embedding, layer norm, decayed linear
-attention, each with its gradient) are in ``encoder`` and are exported here too.
+attention, each with its gradient) are in ``encoder``, those of a block and of pretraining (gated
+recurrence, residual norm, token loss) in ``blocks``; both are exported here too.
 """
 
 from __future__ import annotations
@@ -27,6 +28,8 @@ import torch
 from . import _native
 from ._autograd import first_order
 from ._native import OP_BACKWARD, OP_LOGZ, OP_PREFIX, OP_VITERBI, SemiCRFError
+from .blocks import (gated_recurrence, gated_recurrence_grad, gated_recurrence_step,
+                     residual_norm, residual_norm_grad, token_nll, token_nll_grad)
 from .encoder import (decay_attention, decay_attention_grad, decay_attention_step, embed,
                       embed_grad, layer_norm, layer_norm_grad)
 
@@ -34,7 +37,9 @@ __all__ = ["prefix", "logz", "backward", "viterbi", "nll", "log_partition", "wor
            "checkpoint_interval", "default_interval", "read_status", "SemiCRFError",
            "OP_LOGZ", "OP_BACKWARD", "OP_VITERBI", "OP_PREFIX",
            "embed", "embed_grad", "layer_norm", "layer_norm_grad", "decay_attention",
-           "decay_attention_grad", "decay_attention_step"]
+           "decay_attention_grad", "decay_attention_step",
+           "gated_recurrence", "gated_recurrence_grad", "gated_recurrence_step", "residual_norm",
+           "residual_norm_grad", "token_nll", "token_nll_grad"]
 
 
 def checkpoint_interval(T: int, K: int, delta: int = 0) -> int:

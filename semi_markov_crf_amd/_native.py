@@ -21,7 +21,7 @@ STATUS_NAMES = {0: "SEMICRF_OK", 1: "SEMICRF_ERR_INVALID", 2: "SEMICRF_ERR_WORKS
                 5: "SEMICRF_ERR_UNIMPLEMENTED"}
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
-_c_float, Strides = ctypes.c_float, ctypes.c_int64 * 3
+_c_float, Strides, Strides2 = ctypes.c_float, ctypes.c_int64 * 3, ctypes.c_int64 * 2
 
 
 class Options(ctypes.Structure):
@@ -41,8 +41,25 @@ class Attention(ctypes.Structure):
                 ("Dv", _c_int)]
 
 
+class Recurrence(ctypes.Structure):
+    """struct semicrf_recurrence (include/semicrf.h), field for field."""
+    _fields_ = [("x", _vp), ("decay_gate", _vp), ("input_gate", _vp), ("x_stride", Strides2),
+                ("decay_stride", Strides2), ("input_stride", Strides2), ("lengths", _vp),
+                ("log_decay", _vp), ("state", _vp), ("dtype", _c_int), ("B", _c_int),
+                ("T", _c_int), ("N", _c_int)]
+
+
+class Residual(ctypes.Structure):
+    """struct semicrf_residual (include/semicrf.h), field for field."""
+    _fields_ = [("x", _vp), ("branch", _vp), ("gate", _vp), ("branch_stride", Strides2),
+                ("gate_stride", Strides2), ("scale", _vp), ("weight", _vp), ("bias", _vp),
+                ("branch_weight", _vp), ("branch_bias", _vp), ("lengths", _vp), ("eps", _c_float),
+                ("dtype", _c_int), ("wdtype", _c_int), ("norm_branch", _c_int),
+                ("center", _c_int), ("B", _c_int), ("T", _c_int), ("N", _c_int)]
+
+
 _opt = ctypes.POINTER(Options)
-_att = ctypes.POINTER(Attention)
+_att, _rec, _res = (ctypes.POINTER(s) for s in (Attention, Recurrence, Residual))
 
 # the problem statement's argument lists: (emissions, lengths, trans, dur, B, T, C, K, ...)
 _LOGZ = [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_size, _vp]
@@ -83,7 +100,23 @@ SIGNATURES = {
     "semicrf_decay_attention_grad": (_c_int, [_att, _vp, _vp, _vp, _vp, _c_size, _vp, _vp, _vp,
                                               _vp, _vp]),
     "semicrf_decay_attention_step": (_c_int, [_att, _vp, _c_int, _vp, _vp, _vp]),
+    "semicrf_gated_recurrence_bytes": (_c_size, [_rec, _c_int]),
+    "semicrf_gated_recurrence": (_c_int, [_rec, _vp, _vp, _c_size, _vp, _vp, _vp, _vp]),
+    "semicrf_gated_recurrence_grad": (_c_int, [_rec, _vp, _vp, _vp, _vp, _vp, _c_size, _vp, _vp,
+                                               _vp, _vp, _vp, _vp]),
+    "semicrf_gated_recurrence_step": (_c_int, [_rec, _vp, _c_int, _vp, _vp, _vp]),
+    "semicrf_residual_norm": (_c_int, [_res, _vp, _vp, _vp, _vp, _vp]),
+    "semicrf_residual_norm_grad_bytes": (_c_size, [_c_int] * 4),
+    "semicrf_residual_norm_grad": (_c_int, [_res, _vp, _vp, _vp, _vp, _vp, _c_size, _vp, _vp, _vp,
+                                            _vp, _vp]),
+    "semicrf_token_nll_bytes": (_c_size, [_c_int] * 6),
+    "semicrf_token_nll": (_c_int, [_vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
+                                   _c_int, _c_float, _vp, _vp, _c_size, _vp, _vp, _vp]),
+    "semicrf_token_nll_grad": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _c_int,
+                                        _c_int, _c_int, _c_int, _c_float, _vp, _vp, _c_size, _vp,
+                                        _vp, _vp]),
 }
+RECURRENCE_SPAN = 16
 STATIC_SCRATCH_BYTES = 32 << 20
 STAGES = {"logz": 2, "backward": 5, "viterbi": 3}
 

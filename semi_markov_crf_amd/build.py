@@ -42,7 +42,8 @@ SOURCES = ["api.cpp", "sweep_cfg.cpp", "scan.hip", "sweep_lse_mirror.hip", "swee
            "sweep_round_proj.hip", "sweep_round_proj_log.hip", "marginals.hip", "gold.hip", "viterbi.hip", "seam.hip",
            "sweep_xk_lse.hip", "sweep_xk_maxplus.hip"]
 # the encoder operators: NaN and infinities in their inputs reach their outputs
-ENCODER_SOURCES = ["encoder_api.cpp", "embed.hip", "layer_norm.hip", "decay_attention.hip"]
+ENCODER_SOURCES = ["encoder_api.cpp", "embed.hip", "layer_norm.hip", "decay_attention.hip",
+                   "recurrence.hip", "residual_norm.hip", "token_nll.hip"]
 
 
 def _compile(src: str) -> str:

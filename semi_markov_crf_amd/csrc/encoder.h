@@ -1,5 +1,5 @@
-// Shared by the encoder operators (embedding, layer norm, decayed linear attention): element
-// types, 16-byte pieces of rows, and the interfaces between encoder_api.cpp and the kernels.
+// Shared by the encoder operators (embedding, layer norm, decayed linear attention, gated
+// recurrence, residual norm, token loss): element types, 16-byte pieces of rows, and the interfaces between encoder_api.cpp and the kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -161,5 +161,53 @@ hipError_t launch_decay_attention(const AttnArgs& a, void* ws, hipStream_t strea
 hipError_t launch_decay_attention_grad(const AttnArgs& a, void* ws, hipStream_t stream);
 hipError_t launch_decay_attention_step(const semicrf_attention& p, const int32_t* slots, int pool,
                                        void* out, float* state_out, hipStream_t stream);
+
+struct RecArgs {
+    semicrf_recurrence p;
+    const float* starts_in;
+    const void* grad_out;
+    const float* grad_state_out;
+    void* out;               // h
+    float *state_out, *starts;
+    void *grad_x, *grad_decay, *grad_input;
+    float *grad_log_decay, *grad_state;
+    int32_t* status;
+};
+constexpr int REC_MAX_N = 1 << 20;
+size_t gated_recurrence_bytes(const semicrf_recurrence& p, bool grad);
+hipError_t launch_gated_recurrence(const RecArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_gated_recurrence_grad(const RecArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_gated_recurrence_step(const semicrf_recurrence& p, const int32_t* slots, int pool,
+                                        void* out, float* state_out, hipStream_t stream);
+
+struct ResArgs {
+    semicrf_residual p;
+    void *r, *y;
+    float* stats;
+    const float* stats_in;
+    const void *grad_r, *grad_y;
+    void *grad_x, *grad_branch, *grad_gate, *grad_params;
+    int32_t* status;
+};
+constexpr int RES_MAX_N = 16384;
+hipError_t launch_residual_norm(const ResArgs& a, hipStream_t stream);
+size_t residual_norm_grad_bytes(int B, int T, int N, int dtype);
+hipError_t launch_residual_norm_grad(const ResArgs& a, void* ws, hipStream_t stream);
+
+struct NllArgs {
+    const void *x, *table, *targets;
+    const int32_t* lengths;
+    const float *grad_loss, *lse_in;
+    int dtype, target_bits, B, T, V, N;
+    float scale;
+    float *loss, *lse;
+    void *grad_x, *grad_table;
+    int32_t* status;
+};
+constexpr long NLL_MAX_ROWS = 1l << 22;        // of x and of the table: 256 rows of a transposed copy span less than 2^32 bytes
+constexpr int NLL_MAX_N = 32768;
+size_t token_nll_bytes(int dtype, int B, int T, int V, int N, bool grad);
+hipError_t launch_token_nll(const NllArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_token_nll_grad(const NllArgs& a, void* ws, hipStream_t stream);
 
 }  // namespace semicrf

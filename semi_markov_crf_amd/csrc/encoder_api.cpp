@@ -56,6 +56,40 @@ int check_attention(const semicrf_attention* p) {
     return p->q && p->k && p->v && p->log_decay ? SEMICRF_OK : SEMICRF_ERR_INVALID;
 }
 
+int check_recurrence_shape(const semicrf_recurrence* p) {
+    if (!p || !type_ok(p->dtype)) return SEMICRF_ERR_INVALID;
+    const int rc = check_rows(p->B, p->T, p->N);
+    if (rc) return rc;
+    return p->N <= REC_MAX_N && p->B < 65536 ? SEMICRF_OK : SEMICRF_ERR_UNSUPPORTED;
+}
+
+int check_recurrence(const semicrf_recurrence* p) {
+    const int rc = check_recurrence_shape(p);
+    if (rc) return rc;
+    return p->x && p->decay_gate && p->input_gate && p->log_decay ? SEMICRF_OK : SEMICRF_ERR_INVALID;
+}
+
+int check_residual(const semicrf_residual* p) {
+    if (!p || !p->branch || !(p->eps >= 0.0f)) return SEMICRF_ERR_INVALID;
+    const int rc = check_norm(p->x, p->dtype, p->wdtype, p->B, p->T, p->N);
+    if (rc) return rc;
+    return p->N <= RES_MAX_N ? SEMICRF_OK : SEMICRF_ERR_UNSUPPORTED;
+}
+
+int check_nll_shape(int dtype, int B, int T, int V, int N) {
+    if (!type_ok(dtype) || V < 1) return SEMICRF_ERR_INVALID;
+    const int rc = check_rows(B, T, N);
+    if (rc) return rc;
+    return (long)B * T <= NLL_MAX_ROWS && V <= NLL_MAX_ROWS && N <= NLL_MAX_N ? SEMICRF_OK : SEMICRF_ERR_UNSUPPORTED;
+}
+
+int check_nll(const void* x, const void* table, const void* targets, int target_bits, int dtype, int B,
+              int T, int V, int N, float scale) {
+    if (!x || !table || !targets || (target_bits != 32 && target_bits != 64) || !(scale - scale == 0.0f))
+        return SEMICRF_ERR_INVALID;
+    return check_nll_shape(dtype, B, T, V, N);
+}
+
 }  // namespace
 
 extern "C" {
@@ -167,6 +201,115 @@ int semicrf_decay_attention_step(const semicrf_attention* attention, const int32
         (!slots && pool < attention->B))
         return SEMICRF_ERR_INVALID;
     return done(launch_decay_attention_step(*attention, slots, pool, out, state_out, stream));
+}
+
+size_t semicrf_gated_recurrence_bytes(const semicrf_recurrence* recurrence, int grad) {
+    return check_recurrence_shape(recurrence) ? 0 : gated_recurrence_bytes(*recurrence, grad != 0);
+}
+
+int semicrf_gated_recurrence(const semicrf_recurrence* recurrence, hipStream_t stream,
+                             void* workspace, size_t workspace_bytes, void* out, float* state_out,
+                             float* starts, int32_t* status) {
+    int rc = check_recurrence(recurrence);
+    if (rc) return rc;
+    if (!out) return SEMICRF_ERR_INVALID;
+    if ((rc = check_ws(workspace, workspace_bytes, gated_recurrence_bytes(*recurrence, false)))) return rc;
+    RecArgs a{};
+    a.p = *recurrence; a.out = out; a.state_out = state_out; a.starts = starts; a.status = status;
+    return done(launch_gated_recurrence(a, workspace, stream));
+}
+
+int semicrf_gated_recurrence_grad(const semicrf_recurrence* recurrence, const float* starts,
+                                  const void* grad_out, const float* grad_state_out,
+                                  hipStream_t stream, void* workspace, size_t workspace_bytes,
+                                  void* grad_x, void* grad_decay_gate, void* grad_input_gate,
+                                  float* grad_log_decay, float* grad_state, int32_t* status) {
+    int rc = check_recurrence(recurrence);
+    if (rc) return rc;
+    if (!starts || !grad_out || !grad_x || !grad_decay_gate || !grad_input_gate) return SEMICRF_ERR_INVALID;
+    if ((rc = check_ws(workspace, workspace_bytes, gated_recurrence_bytes(*recurrence, true)))) return rc;
+    RecArgs a{};
+    a.p = *recurrence; a.starts_in = starts; a.grad_out = grad_out; a.grad_state_out = grad_state_out;
+    a.grad_x = grad_x; a.grad_decay = grad_decay_gate; a.grad_input = grad_input_gate;
+    a.grad_log_decay = grad_log_decay; a.grad_state = grad_state; a.status = status;
+    return done(launch_gated_recurrence_grad(a, workspace, stream));
+}
+
+int semicrf_gated_recurrence_step(const semicrf_recurrence* recurrence, const int32_t* slots,
+                                  int pool, hipStream_t stream, void* out, float* state_out) {
+    const int rc = check_recurrence(recurrence);
+    if (rc) return rc;
+    if (!out || !state_out || !recurrence->state || recurrence->T != 1 || recurrence->lengths || pool < 1 ||
+        (!slots && pool < recurrence->B))
+        return SEMICRF_ERR_INVALID;
+    return done(launch_gated_recurrence_step(*recurrence, slots, pool, out, state_out, stream));
+}
+
+int semicrf_residual_norm(const semicrf_residual* residual, hipStream_t stream, void* r, void* y,
+                          float* stats, int32_t* status) {
+    const int rc = check_residual(residual);
+    if (rc) return rc;
+    if (!r || !y) return SEMICRF_ERR_INVALID;
+    ResArgs a{};
+    a.p = *residual; a.r = r; a.y = y; a.stats = stats; a.status = status;
+    return done(launch_residual_norm(a, stream));
+}
+
+size_t semicrf_residual_norm_grad_bytes(int dtype, int B, int T, int N) {
+    if (!type_ok(dtype) || check_rows(B, T, N) || N > RES_MAX_N) return 0;
+    return residual_norm_grad_bytes(B, T, N, dtype);
+}
+
+int semicrf_residual_norm_grad(const semicrf_residual* residual, const float* stats,
+                               const void* grad_r, const void* grad_y, hipStream_t stream,
+                               void* workspace, size_t workspace_bytes, void* grad_x,
+                               void* grad_branch, void* grad_gate, void* grad_params,
+                               int32_t* status) {
+    int rc = check_residual(residual);
+    if (rc) return rc;
+    if (!stats || !grad_x || !grad_branch || (residual->gate && !grad_gate)) return SEMICRF_ERR_INVALID;
+    const size_t need = residual_norm_grad_bytes(residual->B, residual->T, residual->N, residual->dtype);
+    if ((rc = check_ws(workspace, workspace_bytes, need))) return rc;
+    ResArgs a{};
+    a.p = *residual; a.stats_in = stats; a.grad_r = grad_r; a.grad_y = grad_y; a.grad_x = grad_x;
+    a.grad_branch = grad_branch; a.grad_gate = grad_gate; a.grad_params = grad_params; a.status = status;
+    return done(launch_residual_norm_grad(a, workspace, stream));
+}
+
+size_t semicrf_token_nll_bytes(int dtype, int B, int T, int V, int N, int grad) {
+    return check_nll_shape(dtype, B, T, V, N) ? 0 : token_nll_bytes(dtype, B, T, V, N, grad != 0);
+}
+
+int semicrf_token_nll(const void* x, const void* table, int dtype, const void* targets,
+                      int target_bits, const int32_t* lengths, int B, int T, int V, int N,
+                      float scale, hipStream_t stream, void* workspace, size_t workspace_bytes,
+                      float* loss, float* lse, int32_t* status) {
+    int rc = check_nll(x, table, targets, target_bits, dtype, B, T, V, N, scale);
+    if (rc) return rc;
+    if (!loss) return SEMICRF_ERR_INVALID;
+    if ((rc = check_ws(workspace, workspace_bytes, token_nll_bytes(dtype, B, T, V, N, false)))) return rc;
+    NllArgs a{};
+    a.x = x; a.table = table; a.targets = targets; a.target_bits = target_bits; a.lengths = lengths;
+    a.dtype = dtype; a.B = B; a.T = T; a.V = V; a.N = N; a.scale = scale;
+    a.loss = loss; a.lse = lse; a.status = status;
+    return done(launch_token_nll(a, workspace, stream));
+}
+
+int semicrf_token_nll_grad(const float* grad_loss, const void* x, const void* table, int dtype,
+                           const void* targets, int target_bits, const int32_t* lengths,
+                           const float* lse, int B, int T, int V, int N, float scale,
+                           hipStream_t stream, void* workspace, size_t workspace_bytes,
+                           void* grad_x, void* grad_table, int32_t* status) {
+    int rc = check_nll(x, table, targets, target_bits, dtype, B, T, V, N, scale);
+    if (rc) return rc;
+    if (!grad_loss || !lse || (!grad_x && !grad_table)) return SEMICRF_ERR_INVALID;
+    if ((rc = check_ws(workspace, workspace_bytes, token_nll_bytes(dtype, B, T, V, N, true)))) return rc;
+    NllArgs a{};
+    a.x = x; a.table = table; a.targets = targets; a.target_bits = target_bits; a.lengths = lengths;
+    a.grad_loss = grad_loss; a.lse_in = lse;
+    a.dtype = dtype; a.B = B; a.T = T; a.V = V; a.N = N; a.scale = scale;
+    a.grad_x = grad_x; a.grad_table = grad_table; a.status = status;
+    return done(launch_token_nll_grad(a, workspace, stream));
 }
 
 }  // extern "C"

@@ -15,54 +15,17 @@
 // order (no atomics: the same inputs give the same bits).
 #include "common.h"
 #include "encoder.h"
+#include "norm_rows.h"
 
 namespace semicrf {
 
 namespace {
-
-// Sum over the G lanes of a row (G <= 64: inside a wavefront; else the whole workgroup of G
-// threads, through `red`, which alternates between two slots so one barrier is enough).
-template <int G>
-__device__ __forceinline__ float row_sum(float v, float* red, int& slot) {
-    if constexpr (G <= 64) {
-        return group_reduce<G>(v, OpSum());
-    } else {
-        v = group_reduce<64>(v, OpSum());
-        float* s = red + slot * (G / 64);
-        slot ^= 1;
-        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-        __syncthreads();
-        float t = 0.0f;
-#pragma unroll
-        for (int i = 0; i < G / 64; ++i) t += s[i];
-        return t;
-    }
-}
 
 // Row -> t < length of its sequence.  Rows are numbered b * T + t, below 2^30.
 __device__ __forceinline__ bool row_valid(const NormArgs& a, unsigned row) {
     if (!a.lengths) return true;
     const unsigned b = row / (unsigned)a.T;
     return (int)(row - b * (unsigned)a.T) < seq_length(a.lengths, b, a.T, a.status);
-}
-
-// Whether element i of a lane's piece is its own.  Sums take the others times 0: they hold elements
-// of the same row, so one that is not finite is in the sum either way.
-template <class T, bool NARROW>
-__device__ __forceinline__ bool counted(const Piece<T, NARROW>& p, int i, int N) {
-    return i >= p.skip && (!NARROW || i < N);
-}
-
-// V weights from column c in the element type W of theirs
-template <class W, int V>
-__device__ __forceinline__ void load_weights(const void* p, int c, int N, float dflt,
-                                             float (&w)[V]) {
-    if (p) {
-        load_elements<W, V>((const W*)p, c, N, w);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) w[i] = dflt;
-    }
 }
 
 // One pass over the rows of a workgroup: the next row is on its way while this one is summed, and
@@ -73,8 +36,6 @@ __device__ __forceinline__ void load_weights(const void* p, int c, int N, float 
 // Forward, 25,600 ragged rows of 1,024 bfloat16: 92 MB in 17 us (5.4 TB/s).  128 rows of 333 float32:
 // 3.2 us, the launch.  Backward, 400,000 rows of 512 bfloat16: 1.23 GB in 221 us (5.6 TB/s), the sum of
 // 1,024 partial rows 6.6 us.
-enum { EXACT, MASKED, NARROWER };
-
 template <class T, class W, int G, int KP, int NT, int MODE>
 __global__ __launch_bounds__(NT) void k_layer_norm(const NormArgs a) {
     using Pc = Piece<T, MODE == NARROWER>;
