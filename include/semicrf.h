@@ -397,8 +397,8 @@ typedef struct semicrf_recurrence {
     const void* x;               /* [B, T, N], as decay_gate and input_gate */
     const void* decay_gate;
     const void* input_gate;
-    int64_t x_stride[2];         /* elements between sequences and positions; the last axis */
-    int64_t decay_stride[2];     /* is dense */
+    int64_t x_stride[2];         /* elements between sequences and positions (the second from 0 */
+    int64_t decay_stride[2];     /* to 2^25 - 1 where T > 1); the last axis is dense */
     int64_t input_stride[2];
     const int32_t* lengths;      /* [B] or NULL */
     const float* log_decay;      /* [N] */

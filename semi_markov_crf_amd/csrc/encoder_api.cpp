@@ -60,6 +60,10 @@ int check_recurrence_shape(const semicrf_recurrence* p) {
     if (!p || !type_ok(p->dtype)) return SEMICRF_ERR_INVALID;
     const int rc = check_rows(p->B, p->T, p->N);
     if (rc) return rc;
+    // 16 positions of a row are addressed by 32 bits
+    const int64_t s[3] = {p->x_stride[1], p->decay_stride[1], p->input_stride[1]};
+    for (int i = 0; i < 3; ++i)
+        if (p->T > 1 && (s[i] < 0 || s[i] >= 1 << 25)) return SEMICRF_ERR_UNSUPPORTED;
     return p->N <= REC_MAX_N && p->B < 65536 ? SEMICRF_OK : SEMICRF_ERR_UNSUPPORTED;
 }
 
@@ -213,7 +217,9 @@ int semicrf_gated_recurrence(const semicrf_recurrence* recurrence, hipStream_t s
     int rc = check_recurrence(recurrence);
     if (rc) return rc;
     if (!out) return SEMICRF_ERR_INVALID;
-    if ((rc = check_ws(workspace, workspace_bytes, gated_recurrence_bytes(*recurrence, false)))) return rc;
+    const size_t need = gated_recurrence_bytes(*recurrence, false);
+    if (!need) return SEMICRF_ERR_UNSUPPORTED;
+    if ((rc = check_ws(workspace, workspace_bytes, need))) return rc;
     RecArgs a{};
     a.p = *recurrence; a.out = out; a.state_out = state_out; a.starts = starts; a.status = status;
     return done(launch_gated_recurrence(a, workspace, stream));
@@ -227,7 +233,9 @@ int semicrf_gated_recurrence_grad(const semicrf_recurrence* recurrence, const fl
     int rc = check_recurrence(recurrence);
     if (rc) return rc;
     if (!starts || !grad_out || !grad_x || !grad_decay_gate || !grad_input_gate) return SEMICRF_ERR_INVALID;
-    if ((rc = check_ws(workspace, workspace_bytes, gated_recurrence_bytes(*recurrence, true)))) return rc;
+    const size_t need = gated_recurrence_bytes(*recurrence, true);
+    if (!need) return SEMICRF_ERR_UNSUPPORTED;
+    if ((rc = check_ws(workspace, workspace_bytes, need))) return rc;
     RecArgs a{};
     a.p = *recurrence; a.starts_in = starts; a.grad_out = grad_out; a.grad_state_out = grad_state_out;
     a.grad_x = grad_x; a.grad_decay = grad_decay_gate; a.grad_input = grad_input_gate;

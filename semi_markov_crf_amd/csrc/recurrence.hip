@@ -20,7 +20,7 @@ namespace {
 constexpr int SPAN = SEMICRF_RECURRENCE_SPAN;
 
 // expm1 for s <= 0, and exp(s).  Below -1/4 the difference costs at most two bits; above, five terms
-// of the series leave s^6 / 5040 < 2^-24.
+// of the series leave s^6 / 5040 < 2^-24.  WEAK: s is above -1/4.
 __device__ __forceinline__ float expm1_neg(float s, float& e) {
     float p = fmaf(s, 1.0f / 720.0f, 1.0f / 120.0f);
     p = fmaf(s, p, 1.0f / 24.0f);
@@ -42,94 +42,557 @@ __device__ __forceinline__ const T* row(const void* p, const int64_t (&stride)[2
     return (const T*)p + b * stride[0] + t * stride[1];
 }
 
-// grid (ceil(N / 64), B), block 64: a channel a thread
-template <class T>
-__global__ __launch_bounds__(64) void k_recurrence(const RecArgs a) {
-    const semicrf_recurrence& p = a.p;
-    const int n = blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
-    const int L = seq_length(p.lengths, b, p.T, a.status);
-    if (n >= p.N) return;
-    const float lam = p.log_decay[n];
-    float h = p.state ? p.state[(size_t)b * p.N + n] : 0.0f;
-    const size_t spans = (p.T + SPAN - 1) / SPAN;
-    for (int t = 0; t < p.T; ++t) {
-        T* out = (T*)a.out + ((size_t)b * p.T + t) * p.N + n;
-        if (t >= L) {
-            *out = (T)0.0f;
-            continue;
-        }
-        if (a.starts && t % SPAN == 0) a.starts[((size_t)b * spans + t / SPAN) * p.N + n] = h;
-        const float x = (float)row<T>(p.x, p.x_stride, b, t)[n];
-        const float r = (float)row<T>(p.decay_gate, p.decay_stride, b, t)[n];
-        const float i = (float)row<T>(p.input_gate, p.input_stride, b, t)[n];
-        const float m = expm1_neg(lam * sigmoid(r));
-        h = fmaf(m, h, root(-m * (m + 2.0f)) * (sigmoid(i) * x)) + h;
-        *out = (T)h;
-    }
-    if (a.state_out) a.state_out[(size_t)b * p.N + n] = h;
+// ------------------------------------------------------------------ elements of a lane
+// A wavefront takes a span of 16 positions of 16 CH channels: lane 16 q + l holds CH neighbouring
+// channels at positions 4 q .. 4 q + 3.  Where N is no multiple of CH the last lanes start early, at
+// N - CH, and compute channels that a neighbour has too.
+constexpr int POS = 4, LANES = 16;
+
+template <class T, int CH>
+struct Raw {
+    T v[CH];
+};
+template <class T, int CH>
+__device__ __forceinline__ Raw<T, CH> load(const T* base, unsigned at) {
+    Raw<T, CH> r;
+    __builtin_memcpy(&r, (const char*)base + at * (unsigned)sizeof(T), sizeof(r));
+    return r;
+}
+// Positions past the length: a gate that is closed for good keeps the state, whatever else is there
+template <class T, int CH>
+__device__ __forceinline__ void close(Raw<T, CH> (&r)[POS], int first, int count) {
+#pragma unroll
+    for (int i = 0; i < POS; ++i)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (first + i >= count) r[i].v[c] = (T)-__builtin_inff();
+}
+template <class T, int CH>
+__device__ __forceinline__ void store(T* base, unsigned at, const float (&x)[CH]) {
+    Raw<T, CH> r;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) r.v[c] = (T)x[c];
+    __builtin_memcpy((char*)base + at * (unsigned)sizeof(T), &r, sizeof(r));
 }
 
-// the same grid; part [B][N]: the sequence's share of the gradient of log_decay
-template <class T>
-__global__ __launch_bounds__(64) void k_recurrence_grad(const RecArgs a, float* part) {
-    const semicrf_recurrence& p = a.p;
-    const int n = blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
-    const int L = seq_length(p.lengths, b, p.T, a.status);
-    if (n >= p.N) return;
-    const float lam = p.log_decay[n];
-    const size_t spans = (p.T + SPAN - 1) / SPAN, at = (size_t)b * p.T * p.N + n;
-    float e = a.grad_state_out ? a.grad_state_out[(size_t)b * p.N + n] : 0.0f, dlam = 0.0f;
-    for (int j = (int)spans - 1; j >= 0; --j) {
-        const int t0 = j * SPAN;
-        float h[SPAN], m[SPAN], av[SPAN];
-        if (t0 < L) h[0] = a.starts_in[((size_t)b * spans + j) * p.N + n];
-#pragma unroll
-        for (int k = 0; k < SPAN; ++k) {
-            const int t = t0 + k;
-            m[k] = 0.0f;
-            float bu = 0.0f;
-            if (t < L) {
-                m[k] = expm1_neg(lam * sigmoid((float)row<T>(p.decay_gate, p.decay_stride, b, t)[n]), av[k]);
-                bu = root(-m[k] * (m[k] + 2.0f)) * sigmoid((float)row<T>(p.input_gate, p.input_stride, b, t)[n]) *
-                     (float)row<T>(p.x, p.x_stride, b, t)[n];
-            }
-            if (k + 1 < SPAN) h[k + 1] = fmaf(m[k], h[k], bu) + h[k];
-        }
-#pragma unroll
-        for (int k = SPAN - 1; k >= 0; --k) {
-            const int t = t0 + k;
-            if (t >= p.T) continue;
-            const size_t o = at + (size_t)t * p.N;
-            float dx = 0.0f, dr = 0.0f, di = 0.0f;
-            if (t < L) {
-                float sr, qr, si, qi;
-                sigmoids((float)row<T>(p.decay_gate, p.decay_stride, b, t)[n], sr, qr);
-                sigmoids((float)row<T>(p.input_gate, p.input_stride, b, t)[n], si, qi);
-                const float x = (float)row<T>(p.x, p.x_stride, b, t)[n], s = lam * sr, u = si * x;
-                const float bb = -m[k] * (m[k] + 2.0f), ib = bb > 0x1p-123f ? __builtin_amdgcn_rsqf(bb) : 0.0f;
-                e += (float)((const T*)a.grad_out)[o];
-                const float ds = e * av[k] * (h[k] - av[k] * ib * u), du = e * root(bb);
-                dx = du * si;
-                di = du * u * qi;
-                dr = ds * s * qr;
-                dlam += ds * sr;
-                e = fmaf(m[k], e, e);
-            }
-            ((T*)a.grad_x)[o] = (T)dx;
-            ((T*)a.grad_decay)[o] = (T)dr;
-            ((T*)a.grad_input)[o] = (T)di;
-        }
-    }
-    if (a.grad_state) a.grad_state[(size_t)b * p.N + n] = e;
-    part[(size_t)b * p.N + n] = dlam;
+// ------------------------------------------------------------------ joins
+// The state goes through a stretch of positions as h + (M h + H), M = (product of the a) - 1 and H what
+// the stretch makes of 0.
+struct Map {
+    float M, H;
+};
+__device__ __forceinline__ Map then(Map a, Map b) {          // a first
+    return {a.M + fmaf(b.M, a.M, b.M), a.H + fmaf(b.M, a.H, b.H)};
+}
+__device__ __forceinline__ float apply(Map a, float h) { return h + fmaf(a.M, h, a.H); }
+
+// Of the four rows of 16 lanes: each pair's even one (or odd one), the lower half's value (or the upper)
+template <int ODD>
+__device__ __forceinline__ float of_pair(float v) {
+    const int i = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, (int)__builtin_amdgcn_permlane16_swap(i, i, false, false)[ODD]);
+}
+template <int UPPER>
+__device__ __forceinline__ float of_half(float v) {
+    const int i = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, (int)__builtin_amdgcn_permlane32_swap(i, i, false, false)[UPPER]);
 }
 
-__global__ __launch_bounds__(64) void k_recurrence_partials(const float* part, int rows, int N, float* out) {
-    const int n = blockIdx.x * 64 + threadIdx.x;
-    if (n >= N) return;
+// Maps of the four rows, in order of position (REVERSED: from the last): what comes before the lane's
+// row, and all four.
+template <bool REVERSED>
+__device__ __forceinline__ void join_rows(Map own, Map& before, Map& all) {
+    constexpr int FIRST = REVERSED ? 1 : 0;
+    const int q = (threadIdx.x & 63) / LANES;
+    const bool second = (q & 1) != FIRST, later = (q >> 1) != FIRST;
+    const Map first{of_pair<FIRST>(own.M), of_pair<FIRST>(own.H)};
+    const Map pair = then(first, Map{of_pair<!FIRST>(own.M), of_pair<!FIRST>(own.H)});
+    const Map half{of_half<FIRST>(pair.M), of_half<FIRST>(pair.H)};
+    all = then(half, Map{of_half<!FIRST>(pair.M), of_half<!FIRST>(pair.H)});
+    const Map m{second ? first.M : 0.0f, second ? first.H : 0.0f};
+    const Map n = then(half, m);
+    before = Map{later ? n.M : m.M, later ? n.H : m.H};
+}
+
+// ------------------------------------------------------------------ tiles in order
+// A tile is W spans, a span a wavefront; a chain is the tiles of 16 CH channels of a sequence.  Every tile
+// finds its map by itself and then needs the state it starts from.  A workgroup serves one chain and takes
+// its tiles in order by a ticket, so that whoever waits waits for tiles that are at work already or done.
+// (One ticket for all chains costs 24 ns a tile, on one after another: more than the tile's bytes.)
+// Tile k publishes its map, and the last of each GROUP tiles the state it ends with; tile k reads the
+// state of the group before and the maps since, and joins them in order: the same additions on every
+// call.  A publication is one 8-byte store, with a pattern that no map has as "not there yet".
+constexpr int GROUP = 16;
+constexpr unsigned long long EMPTY = ~0ull;
+
+struct Chain {
+    unsigned long long* words;   // [sequence x columns][tiles][channels of a tile]: maps
+    unsigned long long* states;  // [sequence x columns][groups][channels of a tile]: (0, state)
+    unsigned* tickets;           // [sequence x columns][TICKET], or NULL where a chain is one tile
+    int tiles, groups, cols;
+    unsigned chains;
+};
+constexpr int TICKET = 32;       // a line each
+
+__device__ __forceinline__ unsigned long long pack(Map m) {
+    if (m.M != m.M) m.M = __builtin_nanf("");            // never the pattern of EMPTY
+    return ((unsigned long long)__float_as_uint(m.H) << 32) | __float_as_uint(m.M);
+}
+__device__ __forceinline__ Map unpack_map(unsigned long long v) {
+    return {__uint_as_float((unsigned)v), __uint_as_float((unsigned)(v >> 32))};
+}
+__device__ __forceinline__ void publish(unsigned long long* p, unsigned long long v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ unsigned long long peek(const unsigned long long* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The next n <= U words of each lane, once all of them are there.  The wait ends: what is waited for
+// is held by a workgroup that waits for earlier tiles only.
+template <int U>
+__device__ __forceinline__ void await(const unsigned long long* p, size_t stride, int n,
+                                      unsigned long long (&v)[U]) {
+    for (;;) {
+        bool missing = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            v[u] = u < n ? peek(p + u * stride) : 0;
+            missing |= v[u] == EMPTY;
+        }
+        if (!__any(missing)) return;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+// What a workgroup shares while it joins its spans and finds the state it starts from
+template <int CW, int W>
+struct Shared {
+    Map part[W][CW];             // maps of the spans, in the order in which the state goes through them
+    Map look[W][CW];             // maps of a wavefront's share of the tiles since the last group
+    float base[CW];              // the state at the end of the last group
+    float start[W][CW];          // the state each span starts from
+    unsigned slot;
+};
+
+// The state before each span of tile k of chain `seq`, into sh.start: `order` is the wavefront's place in
+// part, `first` the state before tile 0 at a channel.  A lane takes whole channels here.  Call after a
+// barrier that follows the writes of part.
+template <int CW, int W, class F>
+__device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, long seq, int k, bool last, int order,
+                                            F&& first) {
+    constexpr int U = (GROUP + W - 1) / W, PER = (CW + 63) / 64;
+    const int lane = threadIdx.x & 63;
+    const int g = k / GROUP, j = k - g * GROUP;
+    float h[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) h[i] = g == 0 && lane + i * 64 < CW ? first(lane + i * 64) : 0.0f;
+    if (W > 1 && ch.tickets) {                         // one span: one tile
+        unsigned long long* words = ch.words + (size_t)seq * ch.tiles * CW;
+        unsigned long long* states = ch.states + (size_t)seq * ch.groups * CW;
+        // the first state is read before anything is published: the last tile may overwrite it after that
+#pragma unroll
+        for (int i = 0; i < PER; ++i) asm volatile("" : "+v"(h[i]));
+        Map own[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int c = lane + i * 64;
+            own[i] = Map{0.0f, 0.0f};
+            if (CW % 64 && c >= CW) continue;
+            if (order == 0 && !last) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) own[i] = then(own[i], sh.part[w][c]);
+                if (j < GROUP - 1) publish(words + (size_t)k * CW + c, pack(own[i]));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int c = lane + i * 64;
+            if (CW % 64 && c >= CW) continue;
+            unsigned long long v[U];
+            const int n = min(U, j - order * U);
+            Map m{0.0f, 0.0f};
+            if (n > 0) await(words + (size_t)(g * GROUP + order * U) * CW + c, CW, n, v);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < n) m = then(m, unpack_map(v[u]));
+            sh.look[order][c] = m;
+            if (order == W - 1 && g > 0) {
+                unsigned long long s[1];
+                await(states + (size_t)(g - 1) * CW + c, 0, 1, s);
+                sh.base[c] = unpack_map(s[0]).H;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int c = lane + i * 64;
+            if (CW % 64 && c >= CW) continue;
+            if (g > 0) h[i] = sh.base[c];
+#pragma unroll
+            for (int w = 0; w < W; ++w) h[i] = apply(sh.look[w][c], h[i]);
+            if (order == 0 && !last && j == GROUP - 1)
+                publish(states + (size_t)g * CW + c, pack(Map{0.0f, apply(own[i], h[i])}));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int c = lane + i * 64;
+        if (CW % 64 && c >= CW) continue;
+#pragma unroll
+        for (int w = 0; w < W - 1; ++w)
+            if (w < order) h[i] = apply(sh.part[w][c], h[i]);
+        sh.start[order][c] = h[i];
+    }
+    // read by the same wavefront only
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__global__ __launch_bounds__(256) void k_recurrence_clear(unsigned long long* p, size_t n, unsigned* tickets,
+                                                          size_t m) {
+    const size_t at = blockIdx.x * 256ul + threadIdx.x, step = gridDim.x * 256ul;
+    for (size_t i = at; i < n; i += step) p[i] = EMPTY;
+    for (size_t i = at; i < m; i += step) tickets[i] = 0;
+}
+
+// The workgroup's tiles, one after another.  The next ticket is drawn while a tile is worked on.
+// work(chain, tile, pass) calls pass() before its last barrier.
+template <class F>
+__device__ __forceinline__ void each_tile(const Chain& ch, unsigned& slot, F&& work) {
+    const unsigned seq = blockIdx.x % ch.chains;
+    unsigned* ticket = ch.tickets + (size_t)seq * TICKET;
+    int k = 0;
+    if (ch.tickets) {
+        if (threadIdx.x == 0) slot = atomicAdd(ticket, 1u);
+        __syncthreads();
+        k = __builtin_amdgcn_readfirstlane((int)slot);
+    }
+    while (k < ch.tiles) {
+        unsigned next = ch.tiles;
+        if (ch.tickets && threadIdx.x == 0) next = atomicAdd(ticket, 1u);
+        work(seq, k, [&] {
+            if (threadIdx.x == 0) slot = next;
+        });
+        k = __builtin_amdgcn_readfirstlane((int)slot);
+    }
+}
+
+// Where a tile lies
+struct Place {
+    int b, col, L, last, t0, count;
+};
+template <int W, bool REVERSED>
+__device__ __forceinline__ Place place(const semicrf_recurrence& p, const Chain& ch, unsigned seq, int k, int wave,
+                                       int32_t* status) {
+    Place o;
+    o.b = (int)(seq / ch.cols);
+    o.col = (int)(seq - o.b * ch.cols);
+    o.L = __builtin_amdgcn_readfirstlane(seq_length(p.lengths, o.b, p.T, status));
+    o.last = o.L > 0 ? (o.L - 1) / (W * SPAN) : 0;
+    const int tile = REVERSED && k <= o.last ? o.last - k : k;     // tiles of padding come last
+    o.t0 = (tile * W + wave) * SPAN;
+    o.count = max(0, min(SPAN, o.L - o.t0));
+    return o;
+}
+
+// Forward.  Reads x and the gates once: the positions' m and b u stay in registers while the state before
+// them is found.
+template <class T, int CH, int W>
+__global__ __launch_bounds__(64 * W, W == 1 ? 2 : 4) void k_recurrence(const RecArgs a, const Chain ch) {
+    constexpr int CW = CH * LANES;
+    __shared__ Shared<CW, W> sh;
+    const semicrf_recurrence& p = a.p;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane / LANES, l = lane % LANES;
+    const int spans = (p.T + SPAN - 1) / SPAN;
+    each_tile(ch, sh.slot, [&](unsigned seq, int k, auto pass) __attribute__((always_inline)) {
+        const Place o = place<W, false>(p, ch, seq, k, wave, a.status);
+        const unsigned n = min((o.col * LANES + l) * CH, p.N - CH);
+        const bool mine = (o.col * LANES + l) * CH < p.N;
+        T* out = (T*)a.out + ((size_t)o.b * p.T + o.t0) * p.N;
+        if (k > o.last) {                             // all padding
+            const float zero[CH] = {};
+            if (mine)
+                for (int i = q; i < SPAN && o.t0 + i < p.T; i += 4) store<T, CH>(out, i * p.N + n, zero);
+            __syncthreads();                            // all have read the ticket
+            pass();
+            __syncthreads();
+            return;
+        }
+        float m[POS][CH], bu[POS][CH], sum[CH], H[CH];
+        if (o.count > 0) {
+            Raw<T, CH> x[POS], r[POS], g[POS];
+            const T* px = row<T>(p.x, p.x_stride, o.b, o.t0);
+            const T* pr = row<T>(p.decay_gate, p.decay_stride, o.b, o.t0);
+            const T* pg = row<T>(p.input_gate, p.input_stride, o.b, o.t0);
+#pragma unroll
+            for (int i = 0; i < POS; ++i) {
+                const unsigned at = min(q * POS + i, o.count - 1);
+                x[i] = load<T, CH>(px, at * (unsigned)p.x_stride[1] + n);
+                r[i] = load<T, CH>(pr, at * (unsigned)p.decay_stride[1] + n);
+                g[i] = load<T, CH>(pg, at * (unsigned)p.input_stride[1] + n);
+            }
+            const Raw<float, CH> lam = load<float, CH>(p.log_decay, n);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) sum[c] = H[c] = 0.0f;
+            __builtin_amdgcn_sched_barrier(0);          // the loads first, then a few elements at a time
+            if (o.count < SPAN) close(r, q * POS, o.count);
+#pragma unroll
+            for (int i = 0; i < POS; ++i) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const float s = lam.v[c] * sigmoid((float)r[i].v[c]);
+                    m[i][c] = expm1_neg(s);
+                    bu[i][c] = root(-m[i][c] * (m[i][c] + 2.0f)) * (sigmoid((float)g[i].v[c]) * (float)x[i].v[c]);
+                    sum[c] += s;
+                    H[c] += fmaf(m[i][c], H[c], bu[i][c]);
+                    if (c % 2) __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                sum[c] = H[c] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < POS; ++i) m[i][c] = bu[i][c] = 0.0f;
+            }
+        }
+        Map before[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            Map all;
+            join_rows<false>(Map{expm1_neg(sum[c]), H[c]}, before[c], all);
+            if (q == 0) sh.part[wave][l * CH + c] = all;
+        }
+        __syncthreads();
+        find_starts(ch, sh, seq, k, k == o.last, wave, [&](int c) {
+            const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
+            return p.state ? p.state[(size_t)o.b * p.N + at] : 0.0f;
+        });
+        if (mine) {
+            float h[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) h[c] = sh.start[wave][l * CH + c];
+            if (a.starts && o.count > 0 && q == 0)
+                store<float, CH>(a.starts + ((size_t)o.b * spans + o.t0 / SPAN) * p.N, n, h);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) h[c] = apply(before[c], h[c]);
+#pragma unroll
+            for (int i = 0; i < POS; ++i) {
+                float y[CH];
+                const int at = q * POS + i;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    h[c] += fmaf(m[i][c], h[c], bu[i][c]);
+                    y[c] = at < o.count ? h[c] : 0.0f;
+                }
+                if (o.t0 + at < p.T) store<T, CH>(out, at * p.N + n, y);
+            }
+            if (a.state_out && k == o.last && wave == W - 1 && q == 3)
+                store<float, CH>(a.state_out + (size_t)o.b * p.N, n, h);
+        }
+        pass();
+        __syncthreads();                                // before the next tile's part
+    });
+}
+
+// Backward, from the last tile to the first.  What later positions pass on to earlier ones, f_t = a_t (g_t +
+// f_{t+1}), goes through a tile as h does in the forward pass.  Before a position's f is known its
+// factors of it are: with e = g + f the gradient of h,
+//   dx = e kx,  di = e ki,  dr = e kr,  dlog_decay += e kl
+// kx = b sig(i), ki = kx x (1 - sig i), kl = a (h' - a u / b) sig(r), kr = kl log_decay (1 - sig r); h' runs
+// forward from the span's stored start.  dpart [tile x sequence][N]: the tile's share of dlog_decay.
+template <class T, int CH, int W>
+__global__ __launch_bounds__(64 * W, 2) void k_recurrence_grad(const RecArgs a, const Chain ch, float* dpart) {
+    constexpr int CW = CH * LANES;
+    __shared__ Shared<CW, W> sh;
+    __shared__ float dl[W][CW];
+    const semicrf_recurrence& p = a.p;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane / LANES, l = lane % LANES;
+    const int spans = (p.T + SPAN - 1) / SPAN;
+    each_tile(ch, sh.slot, [&](unsigned seq, int k, auto pass) __attribute__((always_inline)) {
+        const Place o = place<W, true>(p, ch, seq, k, wave, a.status);
+        const unsigned n = min((o.col * LANES + l) * CH, p.N - CH);
+        const bool mine = (o.col * LANES + l) * CH < p.N;
+        const size_t at0 = ((size_t)o.b * p.T + o.t0) * p.N;
+        T *gx = (T*)a.grad_x + at0, *gr = (T*)a.grad_decay + at0, *gi = (T*)a.grad_input + at0;
+        float* dout = dpart + ((size_t)(o.t0 / (W * SPAN)) * p.B + o.b) * p.N;
+        if (k > o.last) {
+            const float zero[CH] = {};
+            if (mine) {
+                for (int i = q; i < SPAN && o.t0 + i < p.T; i += 4) {
+                    store<T, CH>(gx, i * p.N + n, zero);
+                    store<T, CH>(gr, i * p.N + n, zero);
+                    store<T, CH>(gi, i * p.N + n, zero);
+                }
+                if (wave == 0 && q == 0) store<float, CH>(dout, n, zero);
+            }
+            __syncthreads();                            // all have read the ticket
+            pass();
+            __syncthreads();
+            return;
+        }
+        float m[POS][CH], kx[POS][CH], ki[POS][CH], kr[POS][CH], kl[POS][CH], M[CH], F[CH];
+        Raw<T, CH> d[POS];
+        if (o.count > 0) {
+            Raw<T, CH> x[POS], r[POS], g[POS];
+            const T* px = row<T>(p.x, p.x_stride, o.b, o.t0);
+            const T* pr = row<T>(p.decay_gate, p.decay_stride, o.b, o.t0);
+            const T* pg = row<T>(p.input_gate, p.input_stride, o.b, o.t0);
+            const T* po = (const T*)a.grad_out + at0;
+#pragma unroll
+            for (int i = 0; i < POS; ++i) {
+                const unsigned at = min(q * POS + i, o.count - 1);
+                x[i] = load<T, CH>(px, at * (unsigned)p.x_stride[1] + n);
+                r[i] = load<T, CH>(pr, at * (unsigned)p.decay_stride[1] + n);
+                g[i] = load<T, CH>(pg, at * (unsigned)p.input_stride[1] + n);
+                d[i] = load<T, CH>(po, at * (unsigned)p.N + n);
+            }
+            const Raw<float, CH> lam = load<float, CH>(p.log_decay, n);
+            const Raw<float, CH> first = load<float, CH>(a.starts_in + ((size_t)o.b * spans + o.t0 / SPAN) * p.N, n);
+            __builtin_amdgcn_sched_barrier(0);
+            if (o.count < SPAN) {
+                close(r, q * POS, o.count);
+#pragma unroll
+                for (int i = 0; i < POS; ++i)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        if (q * POS + i >= o.count) d[i].v[c] = (T)0.0f;
+            }
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                float sum = 0.0f, H = 0.0f, bu[POS], av[POS], aub[POS], sr[POS], qr[POS];
+#pragma unroll
+                for (int i = 0; i < POS; ++i) {
+                    float si, qi;
+                    sigmoids((float)r[i].v[c], sr[i], qr[i]);
+                    sigmoids((float)g[i].v[c], si, qi);
+                    const float s = lam.v[c] * sr[i], mm = m[i][c] = expm1_neg(s, av[i]);
+                    const float bb = -mm * (mm + 2.0f), bv = root(bb);
+                    const float ib = bb > 0x1p-123f ? __builtin_amdgcn_rsqf(bb) : 0.0f;
+                    const float xv = (float)x[i].v[c], u = si * xv;
+                    bu[i] = bv * u;
+                    sum += s;
+                    H += fmaf(m[i][c], H, bu[i]);
+                    aub[i] = av[i] * ib * u;
+                    kx[i][c] = bv * si;
+                    ki[i][c] = kx[i][c] * xv * qi;
+                }
+                M[c] = expm1_neg(sum);
+                Map before, all;
+                join_rows<false>(Map{M[c], H}, before, all);
+                float h = apply(before, first.v[c]);
+#pragma unroll
+                for (int i = 0; i < POS; ++i) {
+                    kl[i][c] = av[i] * (h - aub[i]) * sr[i];
+                    kr[i][c] = kl[i][c] * lam.v[c] * qr[i];
+                    h += fmaf(m[i][c], h, bu[i]);
+                }
+                float f = 0.0f;
+#pragma unroll
+                for (int i = POS - 1; i >= 0; --i) {
+                    const float e = f + (float)d[i].v[c];
+                    f = fmaf(m[i][c], e, e);
+                    // held until f is known: not moved to where they are used, with what they are made of
+                    asm volatile("" : "+v"(m[i][c]), "+v"(kx[i][c]), "+v"(ki[i][c]), "+v"(kl[i][c]), "+v"(kr[i][c]));
+                }
+                F[c] = f;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                M[c] = F[c] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < POS; ++i) {
+                    m[i][c] = kx[i][c] = ki[i][c] = kr[i][c] = kl[i][c] = 0.0f;
+                    d[i].v[c] = (T)0.0f;
+                }
+            }
+        }
+        Map before[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            Map all;
+            join_rows<true>(Map{M[c], F[c]}, before[c], all);
+            if (q == 0) sh.part[W - 1 - wave][l * CH + c] = all;
+        }
+        __syncthreads();
+        find_starts(ch, sh, seq, k, k == o.last, W - 1 - wave, [&](int c) {
+            const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
+            return a.grad_state_out ? a.grad_state_out[(size_t)o.b * p.N + at] : 0.0f;
+        });
+        float f[CH], dlam[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            f[c] = apply(before[c], sh.start[W - 1 - wave][l * CH + c]);
+            dlam[c] = 0.0f;
+        }
+#pragma unroll
+        for (int i = POS - 1; i >= 0; --i) {
+            float dx[CH], dr[CH], di[CH];
+            const int at = q * POS + i;
+            const bool in = at < o.count;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const float e = f[c] + (float)d[i].v[c];
+                dx[c] = in ? e * kx[i][c] : 0.0f;
+                di[c] = in ? e * ki[i][c] : 0.0f;
+                dr[c] = in ? e * kr[i][c] : 0.0f;
+                dlam[c] += in ? e * kl[i][c] : 0.0f;
+                f[c] = fmaf(m[i][c], e, e);
+            }
+            if (mine && o.t0 + at < p.T) {
+                store<T, CH>(gx, at * p.N + n, dx);
+                store<T, CH>(gr, at * p.N + n, dr);
+                store<T, CH>(gi, at * p.N + n, di);
+            }
+        }
+        if (mine && a.grad_state && k == o.last && wave == 0 && q == 0)
+            store<float, CH>(a.grad_state + (size_t)o.b * p.N, n, f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            dlam[c] = of_pair<0>(dlam[c]) + of_pair<1>(dlam[c]);
+            dlam[c] = of_half<0>(dlam[c]) + of_half<1>(dlam[c]);
+            if (q == 0) dl[wave][l * CH + c] = dlam[c];
+        }
+        pass();
+        __syncthreads();
+        if (wave == 0 && q == 0 && mine) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int w = 1; w < W; ++w) dlam[c] += dl[w][l * CH + c];
+            store<float, CH>(dout, n, dlam);
+        }
+    });
+}
+
+// grid (ceil(N / 16)), block 1024: 16 columns, 64 groups of partial rows, joined in order
+__global__ __launch_bounds__(1024) void k_recurrence_partials(const float* part, long rows, int N, float* out) {
+    __shared__ float s[64][17];
+    const int n = blockIdx.x * 16 + (threadIdx.x & 15), grp = threadIdx.x >> 4;
+    const long per = (rows + 63) / 64, r1 = min(rows, (grp + 1) * per);
     float v = 0.0f;
-    for (int r = 0; r < rows; ++r) v += part[(size_t)r * N + n];
-    out[n] = v;
+    if (n < N) {
+        constexpr int U = 8;                            // loads in flight
+        for (long r = grp * per; r < r1; r += U) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = r + u < r1 ? part[(r + u) * N + n] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) v += x[u];
+        }
+    }
+    s[grp][threadIdx.x & 15] = v;
+    __syncthreads();
+    if (grp == 0 && n < N) {
+        for (int i = 1; i < 64; ++i) v += s[i][threadIdx.x];
+        out[n] = v;
+    }
 }
 
 // One token: grid (ceil(N / 256), B).
@@ -154,27 +617,98 @@ __global__ __launch_bounds__(256) void k_recurrence_step(const semicrf_recurrenc
     out[o] = (T)h;
 }
 
+// ------------------------------------------------------------------ host
+constexpr int WIDE = 8, WIDE_GRAD = 8;       // wavefronts a workgroup
+constexpr int SERVE = 2048;                  // workgroups of a launch
+
+// How a call is laid out: channels a lane, wavefronts a workgroup, and the workspace
+struct Plan {
+    int CH, W;
+    Chain chain;
+    int grid;
+    bool fits;
+    size_t words, states, ticket, part, total;
+};
+
+Plan make_plan(const semicrf_recurrence& p, bool grad) {
+    Plan q{};
+    q.CH = p.N < 4 ? 1 : 4;
+    q.W = p.T <= SPAN ? 1 : grad ? WIDE_GRAD : WIDE;
+    Chain& c = q.chain;
+    c.tiles = (p.T + q.W * SPAN - 1) / (q.W * SPAN);
+    c.groups = (c.tiles + GROUP - 1) / GROUP;
+    c.cols = (p.N + LANES * q.CH - 1) / (LANES * q.CH);
+    const long seqs = (long)p.B * c.cols;
+    q.fits = seqs < (1l << 22);          // launches hold less than 2^32 threads
+    c.chains = (unsigned)seqs;
+    // enough workgroups on a chain that all of them together fill the GPU a few times over (chains of
+    // short sequences end early)
+    long serve = (SERVE + seqs - 1) / seqs;
+    serve = serve < c.tiles ? serve : c.tiles;
+    q.grid = (int)(seqs * serve);
+    size_t at = 0;
+    auto region = [&](size_t bytes) {
+        const size_t r = at;
+        at += (bytes + 255) / 256 * 256;
+        return r;
+    };
+    q.ticket = region(c.tiles > 1 ? seqs * TICKET * sizeof(unsigned) : 1);
+    if (c.tiles > 1) {
+        q.words = region(seqs * c.tiles * q.CH * LANES * 8);
+        q.states = region(seqs * c.groups * q.CH * LANES * 8);
+    }
+    if (grad) q.part = region((size_t)c.tiles * p.B * p.N * sizeof(float));
+    q.total = at;
+    return q;
+}
+
+// Binds the plan to its workspace and clears what tiles wait for
+void prepare(Plan& q, void* ws, hipStream_t stream) {
+    if (q.chain.tiles == 1) return;
+    char* w = (char*)ws;
+    q.chain.tickets = (unsigned*)(w + q.ticket);
+    q.chain.words = (unsigned long long*)(w + q.words);
+    q.chain.states = (unsigned long long*)(w + q.states);
+    const size_t n = (size_t)q.chain.chains * (q.chain.tiles + q.chain.groups) * q.CH * LANES;
+    const size_t blocks = (n + 2047) / 2048;
+    hipLaunchKernelGGL(k_recurrence_clear, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream,
+                       q.chain.words, n, q.chain.tickets, (size_t)q.chain.chains * TICKET);
+}
+
 }  // namespace
 
 size_t gated_recurrence_bytes(const semicrf_recurrence& p, bool grad) {
-    return grad ? ((size_t)p.B * p.N * sizeof(float) + 255) / 256 * 256 : 256;
+    const Plan q = make_plan(p, grad);
+    return q.fits ? q.total : 0;
 }
 
-hipError_t launch_gated_recurrence(const RecArgs& a, void*, hipStream_t stream) {
-    const dim3 grid((a.p.N + 63) / 64, a.p.B);
-    if (a.p.dtype == SEMICRF_F32) hipLaunchKernelGGL(k_recurrence<float>, grid, dim3(64), 0, stream, a);
-    else hipLaunchKernelGGL(k_recurrence<bf16>, grid, dim3(64), 0, stream, a);
+hipError_t launch_gated_recurrence(const RecArgs& a, void* ws, hipStream_t stream) {
+    Plan q = make_plan(a.p, false);
+    prepare(q, ws, stream);
+#define RUN(T, CH)                                                                                                       if (q.W == 1)                                                                                                            hipLaunchKernelGGL((k_recurrence<T, CH, 1>), dim3(q.grid), dim3(64), 0, stream, a, q.chain);                     else                                                                                                                     hipLaunchKernelGGL((k_recurrence<T, CH, WIDE>), dim3(q.grid), dim3(64 * WIDE), 0, stream, a, q.chain);
+    if (a.p.dtype == SEMICRF_F32) {
+        if (q.CH == 4) { RUN(float, 4) } else { RUN(float, 1) }
+    } else {
+        if (q.CH == 4) { RUN(bf16, 4) } else { RUN(bf16, 1) }
+    }
+#undef RUN
     return hipGetLastError();
 }
 
 hipError_t launch_gated_recurrence_grad(const RecArgs& a, void* ws, hipStream_t stream) {
-    const dim3 grid((a.p.N + 63) / 64, a.p.B);
-    float* part = (float*)ws;
-    if (a.p.dtype == SEMICRF_F32) hipLaunchKernelGGL(k_recurrence_grad<float>, grid, dim3(64), 0, stream, a, part);
-    else hipLaunchKernelGGL(k_recurrence_grad<bf16>, grid, dim3(64), 0, stream, a, part);
+    Plan q = make_plan(a.p, true);
+    prepare(q, ws, stream);
+    float* part = (float*)((char*)ws + q.part);
+#define RUN(T, CH)                                                                                                       if (q.W == 1)                                                                                                            hipLaunchKernelGGL((k_recurrence_grad<T, CH, 1>), dim3(q.grid), dim3(64), 0, stream, a, q.chain, part);          else                                                                                                                     hipLaunchKernelGGL((k_recurrence_grad<T, CH, WIDE_GRAD>), dim3(q.grid), dim3(64 * WIDE_GRAD), 0, stream, a, q.chain,                              part);
+    if (a.p.dtype == SEMICRF_F32) {
+        if (q.CH == 4) { RUN(float, 4) } else { RUN(float, 1) }
+    } else {
+        if (q.CH == 4) { RUN(bf16, 4) } else { RUN(bf16, 1) }
+    }
+#undef RUN
     if (a.grad_log_decay)
-        hipLaunchKernelGGL(k_recurrence_partials, dim3(grid.x), dim3(64), 0, stream, part, a.p.B, a.p.N,
-                           a.grad_log_decay);
+        hipLaunchKernelGGL(k_recurrence_partials, dim3((a.p.N + 15) / 16), dim3(1024), 0, stream, part,
+                           (long)q.chain.tiles * a.p.B, a.p.N, a.grad_log_decay);
     return hipGetLastError();
 }
 
