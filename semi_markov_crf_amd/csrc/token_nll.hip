@@ -8,11 +8,11 @@
 // tiles, so that masked positions and padding cost nothing; their number stays on the GPU, and the
 // grids are fixed: a workgroup takes tiles until none is left.
 //
-// Three products, one core: a tile of BA x BB results over rows of A and B that are both dense along
-// the contracted axis, 128 bytes of each row a step, through LDS.
-//   scores    A = W,   B = x        the log sum (k_nll_scores<false>), p in pieces of the vocabulary (<true>)
-//   dx        A = W^T, B = p
-//   dW        A = x^T, B = p^T
+// Three products, one core: a tile of BA x BB results, 128 bytes of the contracted axis a step, through
+// two stages of LDS that are filled without passing through registers.
+//   scores    A = W,            B = x            the log sum (k_nll_scores); p of a piece of words (k_nll_p)
+//   dx        A = W by columns, B = p
+//   dW        A = x by columns, B = p by columns
 // Scores are summed and exponentiated in registers; a lane holds scores of the same rows of x for all
 // tiles of the vocabulary it sees, so that maximum and sum run along without an exchange.
 //
@@ -58,69 +58,141 @@ __device__ __forceinline__ f32x4 mma(const float*, raw_piece a, raw_piece b, f32
     return c;
 }
 
-// A tile: BA rows of A, BB rows of B, WA x WB wavefronts.  A step's rows lie in LDS 128 bytes apart;
-// 16-byte chunk c of row r lies at place c ^ (r mod 8), so that the 16 rows a fragment is read
-// from fall on different banks.
-template <class T, int BA_, int BB_, int WA_, int WB_>
+// Four columns of 16 lanes of an LDS tile of rows of the contracted axis, as a fragment: lane 16 g + r gets
+// column r, rows 8 g .. 8 g + 7 of the step half (the order of a fragment read along a row).  The transposing
+// read gives lane 16 g + i the i-th column of the 4 x 16 block whose row j is what lanes 16 g + 4 j .. + 3
+// point at.
+typedef __fp16 half4 __attribute__((__vector_size__(8)));
+typedef __attribute__((address_space(3))) half4 LdsHalf4;
+
+// How an operand lies in memory: ROWS: dense along the contracted axis, a step takes 128 bytes of each row;
+// COLUMNS: dense along the other axis, a step takes 64 (fp16) or 32 (fp32) rows of as many elements as the
+// tile has.  In LDS a step's bytes keep that form; 16-byte chunks are permuted within a row so that the
+// lanes of a read fall on different banks.
+enum Form { ROWS, COLUMNS };
+
+template <class T>
+__device__ __forceinline__ int column_swizzle(int k) {
+    return sizeof(T) == 2 ? (k & 3) * 2 : (k >> 2 & 3) * 4;
+}
+
+// One operand of a tile: SIZE rows (or columns) shared out to NW wavefronts
+template <class T, Form F, int SIZE, int NW>
+struct Operand {
+    static constexpr int ELEMENTS = STEP / sizeof(T);            // of the contracted axis a step
+    static constexpr int CHUNKS = F == ROWS ? STEP / 16 : SIZE * (int)sizeof(T) / 16;   // of a row in LDS
+    static constexpr int BYTES = SIZE * STEP, LOADS = BYTES / 1024 / NW;
+    const char* base;
+    size_t step;                                                 // bytes from one step to the next
+    unsigned at[LOADS];
+
+    // rows: how many of the tile's rows exist (ROWS), or bytes of a row from the tile's first column
+    // (COLUMNS); what lies beyond is taken as the last
+    __device__ __forceinline__ void point(const void* p, unsigned ld, int limit) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        base = (const char*)p;
+        step = F == ROWS ? STEP : (size_t)ELEMENTS * ld;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int chunk = (i * NW + wave) * 64 + lane, r = chunk / CHUNKS, c = chunk % CHUNKS;
+            if (F == ROWS) at[i] = (unsigned)min(r, limit - 1) * ld + (c ^ (r & 7)) * 16;
+            else at[i] = (unsigned)r * ld + min((c ^ column_swizzle<T>(r)) * 16, limit - 16);
+        }
+    }
+    __device__ __forceinline__ void fetch(int k, char* lds) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const char* from = base + k * step;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + at[i]),
+                                             (__attribute__((address_space(3))) void*)(lds + (i * NW + wave) * 1024),
+                                             16, 0, 0);
+    }
+    // Of half a step, the 16 rows (or columns) from `first`
+    __device__ __forceinline__ static raw_piece fragment(const char* lds, int first, int half) {
+        const int lane = threadIdx.x & 63, g = lane / 16, r = lane & 15;
+        if constexpr (F == ROWS) {
+            return *(const raw_piece*)(lds + (first + r) * STEP + (((half * 4 + g) ^ (r & 7)) * 16));
+        } else if constexpr (sizeof(T) == 2) {
+            const int k = half * 32 + 8 * g + (r >> 2), c = first / 8 + (r & 3) / 2, in = (r & 1) * 8;
+            const char* p = lds + k * (CHUNKS * 16) + in + (c ^ column_swizzle<T>(k)) * 16;
+            const half4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((LdsHalf4*)p);
+            const half4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((LdsHalf4*)(p + 4 * CHUNKS * 16));
+            return __builtin_bit_cast(raw_piece, __builtin_shufflevector(__builtin_bit_cast(f16x4, lo),
+                                                                         __builtin_bit_cast(f16x4, hi), 0, 1, 2, 3, 4,
+                                                                         5, 6, 7));
+        } else {
+            f32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = half * 16 + 4 * g + j, c = (first + r) / 4;
+                v[j] = *(const float*)(lds + k * (CHUNKS * 16) + (c ^ column_swizzle<T>(k)) * 16 + (r & 3) * 4);
+            }
+            return __builtin_bit_cast(raw_piece, v);
+        }
+    }
+};
+
+// All fetches are there, and all wavefronts have read what the next ones overwrite
+__device__ __forceinline__ void step_barrier() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// A tile: BA rows of A, BB rows of B, WA x WB wavefronts, two steps in LDS: one is multiplied while the
+// next is on its way.
+template <class T, Form FA, Form FB, int BA_, int BB_, int WA_, int WB_>
 struct Tile {
     static constexpr int BA = BA_, BB = BB_, WA = WA_, WB = WB_;
     static constexpr int NW = WA * WB, NT = 64 * NW, MA = BA / WA / 16, MB = BB / WB / 16;
-    static constexpr int LOADS_A = BA / 8 / NW, LOADS_B = BB / 8 / NW;
     static constexpr int STAGE = (BA + BB) * STEP;
+    using OpA = Operand<T, FA, BA, NW>;
+    using OpB = Operand<T, FB, BB, NW>;
 
     f32x4 acc[MA][MB];
+    OpA a;
+    OpB b;
+    int turn = 0;                        // which half of LDS the next step goes to
 
-    // acc = A . B over nk steps.  A and B point to the tile's first rows; rows of A past rowsA - 1 are
-    // taken as that one.
-    __device__ __forceinline__ void product(const char* A, unsigned lda, int rowsA, const char* B, unsigned ldb,
-                                            int nk, char* lds) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        const int wa = wave / WB, wb = wave % WB;
-        unsigned oa[LOADS_A], ob[LOADS_B];
-#pragma unroll
-        for (int i = 0; i < LOADS_A; ++i) {
-            const int r = (i * NW + wave) * 8 + lane / 8;
-            oa[i] = (unsigned)min(r, rowsA - 1) * lda + ((lane & 7) ^ (r & 7)) * 16;
-        }
-#pragma unroll
-        for (int i = 0; i < LOADS_B; ++i) {
-            const int r = (i * NW + wave) * 8 + lane / 8;
-            ob[i] = (unsigned)r * ldb + ((lane & 7) ^ (r & 7)) * 16;
-        }
+    __device__ __forceinline__ void fetch(int k, char* lds) {
+        a.fetch(k, lds + turn * STAGE);
+        b.fetch(k, lds + turn * STAGE + BA * STEP);
+        turn ^= 1;
+    }
+    // Points at a tile and fetches its first step; no other wavefront reads that half of LDS any more.
+    __device__ __forceinline__ void start(const void* pa, unsigned lda, int limit_a, const void* pb, unsigned ldb,
+                                          int limit_b, int k, char* lds) {
+        a.point(pa, lda, limit_a);
+        b.point(pb, ldb, limit_b);
+        fetch(k, lds);
+    }
+    // acc = A . B over steps k0 .. k1 - 1, of which the first was fetched; then next(), which may start
+    // another tile.
+    template <class Next>
+    __device__ __forceinline__ void product(int k0, int k1, char* lds, Next&& next) {
+        const int wave = threadIdx.x >> 6, wa = wave / WB, wb = wave % WB;
 #pragma unroll
         for (int i = 0; i < MA; ++i)
 #pragma unroll
             for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        raw_piece ra[LOADS_A], rb[LOADS_B];
-        const int to = (wave * 8 + lane / 8) * STEP + (lane & 7) * 16;
-        for (int k = 0; k < nk; ++k) {
-#pragma unroll
-            for (int i = 0; i < LOADS_A; ++i) ra[i] = *(const raw_piece*)(A + (size_t)k * STEP + oa[i]);
-#pragma unroll
-            for (int i = 0; i < LOADS_B; ++i) rb[i] = *(const raw_piece*)(B + (size_t)k * STEP + ob[i]);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < LOADS_A; ++i) *(raw_piece*)(lds + i * NW * 8 * STEP + to) = ra[i];
-#pragma unroll
-            for (int i = 0; i < LOADS_B; ++i) *(raw_piece*)(lds + BA * STEP + i * NW * 8 * STEP + to) = rb[i];
-            __syncthreads();
-            const int r = lane & 15;
+        for (int k = k0; k < k1; ++k) {
+            step_barrier();
+            const char* now = lds + (turn ^ 1) * STAGE;
+            if (k + 1 < k1) fetch(k + 1, lds);
+            else next();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int c = ((half * 4 + lane / 16) ^ (r & 7)) * 16;
-                raw_piece b[MB];
+                raw_piece fb[MB];
 #pragma unroll
                 for (int j = 0; j < MB; ++j)
-                    b[j] = *(const raw_piece*)(lds + (BA + wb * (BB / WB) + j * 16 + r) * STEP + c);
+                    fb[j] = OpB::fragment(now + BA * STEP, wb * (BB / WB) + j * 16, half);
 #pragma unroll
                 for (int i = 0; i < MA; ++i) {
-                    const raw_piece a = *(const raw_piece*)(lds + (wa * (BA / WA) + i * 16 + r) * STEP + c);
+                    const raw_piece fa = OpA::fragment(now, wa * (BA / WA) + i * 16, half);
 #pragma unroll
-                    for (int j = 0; j < MB; ++j) acc[i][j] = mma((const T*)nullptr, a, b[j], acc[i][j]);
+                    for (int j = 0; j < MB; ++j) acc[i][j] = mma((const T*)nullptr, fa, fb[j], acc[i][j]);
                 }
             }
         }
-        __syncthreads();
     }
 };
 
@@ -135,7 +207,7 @@ __device__ __forceinline__ int64_t target_at(const NllArgs& a, unsigned row) {
     return a.target_bits == 64 ? ((const int64_t*)a.targets)[row] : ((const int32_t*)a.targets)[row];
 }
 
-// Row -> whether it is listed; NaN: its target is out of range
+// Row -> whether it is listed; beyond: its target is out of range
 __device__ __forceinline__ bool listed(const NllArgs& a, unsigned row, bool& beyond, int& target) {
     const unsigned b = row / (unsigned)a.T, t = row - b * (unsigned)a.T;
     beyond = false;
@@ -148,7 +220,7 @@ __device__ __forceinline__ bool listed(const NllArgs& a, unsigned row, bool& bey
 
 constexpr int LIST = 4096, LIST_THREADS = 1024, LIST_EACH = LIST / LIST_THREADS;
 
-// counts[block] = listed rows of the block's 4,096; clears the control block
+// counts[block] = listed rows of the block's 4,096
 __global__ __launch_bounds__(LIST_THREADS) void k_nll_count(const NllArgs a, Control* ctl, int* counts) {
     __shared__ int s[LIST_THREADS / 64];
     const unsigned rows = (unsigned)a.B * a.T, first = blockIdx.x * (unsigned)LIST + threadIdx.x * LIST_EACH;
@@ -169,23 +241,26 @@ __global__ __launch_bounds__(LIST_THREADS) void k_nll_count(const NllArgs a, Con
     }
 }
 
-// What a listed row carries into the products
+// The listed rows in order, then the others from the end on, and what listed rows carry into the products
 struct Listed {
-    int* row;                // its place among all rows
+    int* row;                // place among all rows
     int* target;
-    float *lse, *grad;       // gradients only
-    int* place;              // [all rows] its number in the list, or -1 (gradients only)
+    float *lse, *grad;       // gradients only; lse in log2 units
 };
 
+// counts NULL: one workgroup, which also clears the control block
 template <bool GRAD>
 __global__ __launch_bounds__(LIST_THREADS) void k_nll_list(const NllArgs a, Control* ctl, const int* counts,
                                                            Listed list) {
     __shared__ int s[LIST_THREADS / 64], before[LIST_THREADS / 64];
+    __shared__ unsigned top;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const unsigned rows = (unsigned)a.B * a.T, first = blockIdx.x * (unsigned)LIST + threadIdx.x * LIST_EACH;
     int n = 0, prev = 0, target[LIST_EACH];
     bool is[LIST_EACH];
-    for (unsigned i = threadIdx.x; i < blockIdx.x; i += LIST_THREADS) prev += counts[i];
+    if (threadIdx.x == 0) top = 0;
+    if (counts)
+        for (unsigned i = threadIdx.x; i < blockIdx.x; i += LIST_THREADS) prev += counts[i];
     for (int off = 32; off >= 1; off >>= 1) prev += __shfl_xor(prev, off, 64);
 #pragma unroll
     for (int i = 0; i < LIST_EACH; ++i) {
@@ -193,11 +268,8 @@ __global__ __launch_bounds__(LIST_THREADS) void k_nll_list(const NllArgs a, Cont
         bool beyond = false;
         is[i] = row < rows && listed(a, row, beyond, target[i]);
         n += is[i];
-        if (row >= rows) continue;
         if (beyond && a.status) atomicOr(a.status, 1);
-        if (GRAD) {
-            if (!is[i]) list.place[row] = -1;
-        } else if (!is[i]) {
+        if (!GRAD && row < rows && !is[i]) {
             a.loss[row] = beyond ? __builtin_nanf("") : 0.0f;
             if (a.lse) a.lse[row] = 0.0f;
         }
@@ -219,14 +291,16 @@ __global__ __launch_bounds__(LIST_THREADS) void k_nll_list(const NllArgs a, Cont
 #pragma unroll
     for (int i = 0; i < LIST_EACH; ++i) {
         const unsigned row = first + i;
-        if (!is[i]) continue;
+        if (!is[i]) {
+            if (row < rows) list.row[rows - 1 - (row - at)] = (int)row;
+            continue;
+        }
         list.row[at] = (int)row;
         list.target[at] = target[i];
         if (GRAD) {
             const float g = a.grad_loss[row];
             list.lse[at] = a.lse_in[row] * LOG2EF;
             list.grad[at] = g;
-            list.place[row] = at;
             const unsigned bits = __float_as_uint(g) & 0x7fffffffu;
             if (bits < 0x7f800000u) most = max(most, bits);
         }
@@ -234,52 +308,32 @@ __global__ __launch_bounds__(LIST_THREADS) void k_nll_list(const NllArgs a, Cont
     }
     if (GRAD) {
         for (int off = 32; off >= 1; off >>= 1) most = max(most, (unsigned)__shfl_xor((int)most, off, 64));
-        if (lane == 0 && most) atomicMax(&ctl->max_g, most);
+        if (lane == 0 && most) atomicMax(&top, most);
+        __syncthreads();
+        if (counts && threadIdx.x == 0 && top) atomicMax(&ctl->max_g, top);
     }
-    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == LIST_THREADS - 1) ctl->rows = at;
+    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == LIST_THREADS - 1) {
+        ctl->rows = at;
+        if (!counts) {
+            ctl->max_x = ctl->max_w = 0;
+            ctl->max_g = top;
+        }
+    }
 }
 
 __host__ __device__ __forceinline__ int tiles(int rows, int tile) { return (rows + tile - 1) / tile; }
 
-// dst [rows][ld] = src rows (index: which; NULL: in order) of N elements, zeros beyond N and in rows
-// past the last up to a whole tile.  A wavefront a row.  max: the largest finite magnitude.
+// The largest finite magnitude of n elements, by blocks `first` .. of the grid's `blocks`
 template <class T>
-__global__ __launch_bounds__(256) void k_nll_rows(const T* src, const int* index, const Control* ctl, int rows, int N,
-                                                  T* dst, int ld, int pad) {
-    constexpr int V = 16 / sizeof(T);
-    if (ctl) rows = ctl->rows;
-    const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (r >= tiles(rows, pad) * pad) return;
-    T* to = dst + (size_t)r * ld;
-    const T* from = src + (size_t)(r < rows ? (index ? index[r] : r) : 0) * N;
-    for (int c = lane * V; c < ld; c += 64 * V) {
-        raw_piece x = {0, 0, 0, 0};
-        if (r < rows) {
-            if (c + V <= N) {
-                x = *(const loose_piece*)(from + c);
-            } else {
-                T t[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) t[i] = c + i < N ? from[c + i] : (T)0.0f;
-                __builtin_memcpy(&x, t, 16);
-            }
-        }
-        *(raw_piece*)(to + c) = x;
-    }
-}
-
-// The largest finite magnitude of `rows` rows of N elements: a fixed grid
-template <class T>
-__global__ __launch_bounds__(256) void k_nll_max(const T* src, const Control* ctl, long n, int N, unsigned* out) {
-    if (ctl) n = (long)ctl->rows * N;
+__device__ __forceinline__ unsigned largest(const T* src, long n, int block, int blocks) {
     constexpr int V = 16 / sizeof(T);
     unsigned most = 0;
     auto see = [&](float x) {
         const unsigned bits = __float_as_uint(x) & 0x7fffffffu;
         if (bits < 0x7f800000u) most = max(most, bits);
     };
-    const long step = (long)gridDim.x * 256 * V;
-    long i = ((long)blockIdx.x * 256 + threadIdx.x) * V;
+    const long step = (long)blocks * 256 * V;
+    long i = ((long)block * 256 + threadIdx.x) * V;
     for (; i + V <= n; i += step) {
         const raw_piece r = *(const loose_piece*)(src + i);
         float x[V];
@@ -288,8 +342,43 @@ __global__ __launch_bounds__(256) void k_nll_max(const T* src, const Control* ct
         for (int j = 0; j < V; ++j) see(x[j]);
     }
     for (; i < n; ++i) see((float)src[i]);
+    return most;
+}
+
+// max_x over the listed rows, max_w over the table: a quarter of the workgroups for x
+template <class T>
+__global__ __launch_bounds__(256) void k_nll_max(const NllArgs a, Control* ctl, const int* row) {
+    const int quarter = gridDim.x / 4, lane = threadIdx.x & 63;
+    const bool of_x = (int)blockIdx.x < quarter;
+    unsigned most = 0;
+    if (of_x) {
+        // a wavefront a row
+        constexpr int V = 16 / sizeof(T);
+        for (int r = blockIdx.x * 4 + (threadIdx.x >> 6); r < ctl->rows; r += quarter * 4) {
+            const T* from = (const T*)a.x + (size_t)row[r] * a.N;
+            for (int c = lane * V; c < a.N; c += 64 * V) {
+                if (c + V <= a.N) {
+                    float x[V];
+                    const raw_piece v = *(const loose_piece*)(from + c);
+                    unpack<T>(v, x);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const unsigned bits = __float_as_uint(x[j]) & 0x7fffffffu;
+                        if (bits < 0x7f800000u) most = max(most, bits);
+                    }
+                } else {
+                    for (int j = c; j < a.N; ++j) {
+                        const unsigned bits = __float_as_uint((float)from[j]) & 0x7fffffffu;
+                        if (bits < 0x7f800000u) most = max(most, bits);
+                    }
+                }
+            }
+        }
+    } else {
+        most = largest((const T*)a.table, (long)a.V * a.N, blockIdx.x - quarter, gridDim.x - quarter);
+    }
     for (int off = 32; off >= 1; off >>= 1) most = max(most, (unsigned)__shfl_xor((int)most, off, 64));
-    if ((threadIdx.x & 63) == 0 && most) atomicMax(out, most);
+    if (lane == 0 && most) atomicMax(of_x ? &ctl->max_x : &ctl->max_w, most);
 }
 
 // The power of two that brings a largest magnitude to [2^14, 2^15)
@@ -302,28 +391,75 @@ __device__ __forceinline__ float held_scale(unsigned bits) {
 // p's scale: |p| <= 1
 template <class H>
 constexpr float P_SCALE = sizeof(H) == 4 ? 1.0f : 32768.0f;
-
-// What the rows' gradients are divided by in p^T: the largest one
+// What the rows' gradients are divided by where x carries them into dW: the largest one
 __device__ __forceinline__ float grad_unit(unsigned bits) { return fmaxf(__uint_as_float(bits), 0x1p-120f); }
 
-// dst [N][ldd] = the transpose of src [rows][ld], scaled, zeros in columns past the rows up to a whole tile
-template <class T, class H>
-__global__ __launch_bounds__(256) void k_nll_transpose(const T* src, const Control* ctl, bool listed_rows, int rows,
-                                                       int N, int ld, const unsigned* most, H* dst, size_t ldd,
-                                                       int pad) {
-    __shared__ H s[64][64 + 8 / sizeof(H) * 1];
-    if (listed_rows) rows = ctl->rows;
-    const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
-    if (r0 >= tiles(rows, pad) * pad) return;
-    const float f = held_scale<H>(*most);
-    const int cx = threadIdx.x & 63, ry = threadIdx.x >> 6;
-    for (int r = ry; r < 64; r += 4) {
-        const bool in = r0 + r < rows && c0 + cx < N;
-        s[r][cx] = (H)(in ? (float)src[(size_t)(r0 + r) * ld + c0 + cx] * f : 0.0f);
+// What the products read, laid out once a call.  Rows of ld elements, zeros past N.
+struct Layout {
+    void* x;                 // [rows up to a whole tile][ld]: the listed rows
+    void* w;                 // the table, or its copy with rows of ld elements where the table's own are no
+                             // whole steps
+    void* xg;                // as x, times the row's gradient over the largest one (dW)
+    void* wh;                // [words up to whole pieces][ld] (dx)
+    int ld, words;           // rows of the copies of W
+    bool copy_w;
+};
+
+// Blocks of 64 rows by 64 columns: first those of x, then those of W; rows without a target get their zeros in grad_x
+template <class T, class H, bool GRAD>
+__global__ __launch_bounds__(256) void k_nll_lay(const NllArgs a, const Control* ctl, Listed list, Layout l,
+                                                 int x_blocks) {
+    constexpr int V = 16 / sizeof(T), ACROSS = 64 / V, DOWN = 256 / ACROSS;
+    const int cols = l.ld / 64, M = a.B * a.T, rows = ctl->rows, padded = tiles(rows, ROW_TILE) * ROW_TILE;
+    const bool of_x = (int)blockIdx.x < x_blocks;
+    const int block = of_x ? blockIdx.x : blockIdx.x - x_blocks;
+    const int c = block % cols * 64 + threadIdx.x % ACROSS * V, r0 = block / cols * 64;
+    if (of_x && r0 >= padded && !(GRAD && a.grad_x && r0 < M)) return;
+    float unit = 0.0f, sx = 1.0f, sw = 1.0f;
+    if (GRAD) {
+        unit = 1.0f / grad_unit(ctl->max_g);
+        sx = held_scale<H>(ctl->max_x);
+        sw = held_scale<H>(ctl->max_w);
     }
-    __syncthreads();
-    for (int c = ry; c < 64; c += 4)
-        if (c0 + c < N) dst[(size_t)(c0 + c) * ldd + r0 + cx] = s[cx][c];
+    for (int r = r0 + threadIdx.x / ACROSS; r < r0 + 64; r += DOWN) {
+        const int n = of_x ? rows : a.V;
+        raw_piece v = {0, 0, 0, 0};
+        if (r < n) {
+            const T* from = of_x ? (const T*)a.x + (size_t)list.row[r] * a.N : (const T*)a.table + (size_t)r * a.N;
+            if (c + V <= a.N) {
+                v = *(const loose_piece*)(from + c);
+            } else {
+                T t[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) t[i] = c + i < a.N ? from[c + i] : (T)0.0f;
+                __builtin_memcpy(&v, t, 16);
+            }
+        }
+        const size_t at = (size_t)r * l.ld + c;
+        auto held = [&](float f, void* to) {
+            float x[V];
+            H h[V];
+            unpack<T>(v, x);
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[i] = (H)(x[i] * f);
+            __builtin_memcpy((H*)to + at, h, sizeof(h));
+        };
+        if (of_x) {
+            if (r < padded) {
+                *(raw_piece*)((T*)l.x + at) = v;
+                if (GRAD && a.grad_table) held(r < rows ? list.grad[r] * unit * sx : 0.0f, l.xg);
+            }
+            if (GRAD && a.grad_x && r >= rows && r < M) {
+                T* to = (T*)a.grad_x + (size_t)list.row[r] * a.N;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (c + i < a.N) to[c + i] = (T)0.0f;
+            }
+        } else {
+            if (l.copy_w && r < l.words) *(raw_piece*)((T*)l.w + at) = v;
+            if (GRAD && sizeof(H) == 2 && a.grad_x && r < l.words) held(sw, l.wh);
+        }
+    }
 }
 
 // ------------------------------------------------------------------ scores
@@ -331,6 +467,12 @@ __global__ __launch_bounds__(256) void k_nll_transpose(const T* src, const Contr
 // cache each, and to which consecutive workgroups go in turn) takes consecutive numbers.
 __device__ __forceinline__ int ordered_block() {
     return (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;
+}
+// Tile number -> row tile and column tile: eight tiles of rows by all columns at a time
+__device__ __forceinline__ void in_groups(int tile, int rows, int cols, int& r, int& c) {
+    const int group = tile / (8 * cols), in = tile - group * 8 * cols, width = min(8, rows - group * 8);
+    r = group * 8 + in % width;
+    c = in / width;
 }
 
 // How many workgroups share the vocabulary of a tile of rows: the number that leaves the least for the
@@ -349,7 +491,7 @@ __device__ __forceinline__ int vocab_split(int mt, int vt, int wgs) {
 
 struct Scores {
     const char *w, *x;
-    unsigned ldw, ldx;       // bytes
+    unsigned ld;             // bytes
     int V, nk;
     float scale;             // to log2 units
 };
@@ -359,12 +501,20 @@ struct Scores {
 template <class T, class Tl>
 __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Control* ctl, const int* target,
                                                        float2* part, float* at_target) {
-    __shared__ __align__(16) char lds[Tl::STAGE];
-    const int mt = tiles(ctl->rows, Tl::BB), vt = tiles(p.V, Tl::BA), S = vocab_split(mt, vt, gridDim.x);
+    __shared__ __align__(16) char lds[2 * Tl::STAGE];
+    const int rows = __builtin_amdgcn_readfirstlane(ctl->rows);
+    const int mt = tiles(rows, Tl::BB), vt = tiles(p.V, Tl::BA), S = vocab_split(mt, vt, gridDim.x);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wa = wave / Tl::WB, wb = wave % Tl::WB;
-    for (int item = ordered_block(); item < mt * S; item += gridDim.x) {
-        const int m0 = item / S * Tl::BB, share = item % S;
-        const int col = wb * (Tl::BB / Tl::WB) + (lane & 15);
+    const int col = wb * (Tl::BB / Tl::WB) + (lane & 15);
+    Tl t;
+    auto start = [&](int item, int v) {
+        t.start(p.w + (size_t)v * Tl::BA * p.ld, p.ld, p.V - v * Tl::BA, p.x + (size_t)(item / S) * Tl::BB * p.ld, p.ld,
+                Tl::BB, 0, lds);
+    };
+    int item = ordered_block();
+    if (item < mt * S) start(item, item % S * vt / S);
+    for (; item < mt * S; item += gridDim.x) {
+        const int m0 = item / S * Tl::BB, v1 = (item % S + 1) * vt / S;
         float top[Tl::MB], sum[Tl::MB];
         int tgt[Tl::MB];
 #pragma unroll
@@ -372,31 +522,43 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Con
             top[j] = -__builtin_inff();
             sum[j] = 0.0f;
             const int m = m0 + col + j * 16;
-            tgt[j] = m < ctl->rows ? target[m] : -1;
+            tgt[j] = m < rows ? target[m] : -1;
         }
-        for (int v = share * vt / S; v < (share + 1) * vt / S; ++v) {
-            Tl t;
-            t.product(p.w + (size_t)v * Tl::BA * p.ldw, p.ldw, p.V - v * Tl::BA, p.x + (size_t)m0 * p.ldx, p.ldx, p.nk,
-                      lds);
+        for (int v = item % S * vt / S; v < v1; ++v) {
+            t.product(0, p.nk, lds, [&] {
+                const int next = item + gridDim.x;
+                if (v + 1 < v1) start(item, v + 1);
+                else if (next < mt * S) start(next, next % S * vt / S);
+            });
             const int first = v * Tl::BA + wa * (Tl::BA / Tl::WA) + lane / 16 * 4;
+            const bool whole = (v + 1) * Tl::BA <= p.V;
 #pragma unroll
             for (int j = 0; j < Tl::MB; ++j) {
-                float z[Tl::MA][4], most = top[j];
+                float most = top[j];
 #pragma unroll
-                for (int i = 0; i < Tl::MA; ++i)
+                for (int i = 0; i < Tl::MA; ++i) {
+                    f32x4& z = t.acc[i][j];
+                    z *= p.scale;
+                    if (!whole)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int at = first + i * 16 + k;
-                        z[i][k] = at < p.V ? t.acc[i][j][k] * p.scale : -__builtin_inff();
-                        most = fmaxf(most, z[i][k]);
-                        if (at == tgt[j]) at_target[m0 + col + j * 16] = z[i][k];
-                    }
+                        for (int k = 0; k < 4; ++k)
+                            if (first + i * 16 + k >= p.V) z[k] = -__builtin_inff();
+                    most = fmaxf(most, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+                }
+                const int hit = tgt[j] - first;          // the target is one of the lane's words
+                if (hit >= 0 && hit < Tl::MA * 16 && hit % 16 < 4) {
+#pragma unroll
+                    for (int i = 0; i < Tl::MA; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (hit == i * 16 + k) at_target[m0 + col + j * 16] = t.acc[i][j][k];
+                }
                 const float ref = most == -__builtin_inff() ? 0.0f : most;
                 float s = sum[j] * fast_exp2(top[j] - ref);
 #pragma unroll
                 for (int i = 0; i < Tl::MA; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) s += fast_exp2(z[i][k] - ref);
+                    for (int k = 0; k < 4; ++k) s += fast_exp2(t.acc[i][j][k] - ref);
                 sum[j] = s;
                 top[j] = most;
             }
@@ -436,41 +598,47 @@ __global__ __launch_bounds__(256) void k_nll_loss(const Control* ctl, const int*
 }
 
 // ------------------------------------------------------------------ gradients
-// p of a piece of the vocabulary, [rows][ldp] and its transpose [piece][ldt] times the row's gradient
-// over the largest one.  Zero for rows and words past the last.
+// p of a piece of the vocabulary, [rows up to a whole tile][ldp], times P_SCALE.  Zero for rows and words past
+// the last.
 template <class T, class H, class Tl>
 __global__ __launch_bounds__(Tl::NT) void k_nll_p(const Scores s, const Control* ctl, const int* target,
-                                                  const float* lse, const float* grad, int v0, int vt, H* p,
-                                                  size_t ldp, H* pt, size_t ldt) {
-    __shared__ __align__(16) char lds[Tl::STAGE];
-    const int rows = ctl->rows, mt = tiles(rows, ROW_TILE) * (ROW_TILE / Tl::BB);
+                                                  const float* lse, int v0, int vt, H* p, int ldp) {
+    __shared__ __align__(16) char lds[2 * Tl::STAGE];
+    const int rows = __builtin_amdgcn_readfirstlane(ctl->rows), mt = tiles(rows, ROW_TILE) * (ROW_TILE / Tl::BB);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wa = wave / Tl::WB, wb = wave % Tl::WB;
-    const float over = 1.0f / grad_unit(ctl->max_g);
-    for (int tile = ordered_block(); tile < mt * vt; tile += gridDim.x) {
-        // eight tiles of rows by all of the vocabulary at a time
-        const int group = tile / (8 * vt), in = tile - group * 8 * vt, width = min(8, mt - group * 8);
-        const int m0 = (group * 8 + in % width) * Tl::BB, v = in / width;
-        Tl t;
+    Tl t;
+    auto start = [&](int tile) {
+        int m, v;
+        in_groups(tile, mt, vt, m, v);
         const int w0 = min(v0 + v * Tl::BA, s.V - 1);         // pieces may end past the vocabulary
-        t.product(s.w + (size_t)w0 * s.ldw, s.ldw, s.V - w0, s.x + (size_t)m0 * s.ldx, s.ldx, s.nk, lds);
+        t.start(s.w + (size_t)w0 * s.ld, s.ld, s.V - w0, s.x + (size_t)m * Tl::BB * s.ld, s.ld, Tl::BB, 0, lds);
+    };
+    int tile = ordered_block();
+    if (tile < mt * vt) start(tile);
+    for (; tile < mt * vt; tile += gridDim.x) {
+        t.product(0, s.nk, lds, [&] {
+            if (tile + (int)gridDim.x < mt * vt) start(tile + gridDim.x);
+        });
+        int mi, v;
+        in_groups(tile, mt, vt, mi, v);
         const int first = v * Tl::BA + wa * (Tl::BA / Tl::WA) + lane / 16 * 4;
+        const bool whole = v0 + (v + 1) * Tl::BA <= s.V;
 #pragma unroll
         for (int j = 0; j < Tl::MB; ++j) {
-            const int m = m0 + wb * (Tl::BB / Tl::WB) + j * 16 + (lane & 15);
+            const int m = mi * Tl::BB + wb * (Tl::BB / Tl::WB) + j * 16 + (lane & 15);
             const bool in_rows = m < rows;
-            const float l = in_rows ? lse[m] : 0.0f, g = in_rows ? grad[m] * over : 0.0f;
-            const int tgt = in_rows ? target[m] - v0 : -1;
+            // a row past the last has an infinite log sum: its p is 0
+            const float l = in_rows ? lse[m] : __builtin_inff();
+            const int hit = (in_rows ? target[m] - v0 : -1) - first;
 #pragma unroll
             for (int i = 0; i < Tl::MA; ++i) {
                 H out[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int at = first + i * 16 + k;
                     float q = fast_exp2(fmaf(t.acc[i][j][k], s.scale, -l));
-                    if (at == tgt) q -= 1.0f;
-                    if (!in_rows || v0 + at >= s.V) q = 0.0f;
+                    if (hit == i * 16 + k) q -= 1.0f;
+                    if (!whole && v0 + first + i * 16 + k >= s.V) q = 0.0f;
                     out[k] = (H)(q * P_SCALE<H>);
-                    pt[(size_t)at * ldt + m] = (H)(in_rows ? q * g * P_SCALE<H> : 0.0f);
                 }
                 __builtin_memcpy(p + (size_t)m * ldp + first + i * 16, out, sizeof(out));
             }
@@ -478,101 +646,170 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_p(const Scores s, const Control*
     }
 }
 
-// How the contracted axis of dx is shared out: as many shares as fill the workgroups
-__device__ __forceinline__ int dx_split(int mt, int at, int wgs, int nk) {
-    return max(1, min(min(wgs / max(1, mt * at), nk), 16));
+// Where a product's results go.  Partial sums: out[share][row of B][ldo], fp32, added to where `add` is
+// set.  Final results (of one share): rows of N elements of type T, times the factors.
+struct Product {
+    const char *A, *B;
+    unsigned lda, ldb;       // bytes
+    int N;                   // columns of the result
+    int b_tiles, b_rows;     // dW: tiles of words, and words
+    int nk, split;           // dx: steps; dW: shares
+    bool add, last;          // dx: pieces before this one, none after it
+    float* part;
+    int ldo;
+    const int* row;          // dx: of a listed row
+    const float* grad;       // dx: the row's gradient
+    float scale;
+    void* out;
+};
+
+// How the contracted axis of dx is shared out: as many shares of at least eight steps as fill the workgroups
+__host__ __device__ __forceinline__ int dx_split(int mt, int at, int wgs, int nk) {
+    const int fill = wgs / (mt * at > 0 ? mt * at : 1), most = nk / 8 < 16 ? nk / 8 : 16;
+    const int s = fill < most ? fill : most;
+    return s < 1 ? 1 : s;
 }
 
-// out[share][row of B][ldo] (+)= A . B over a share of the contracted axis, fp32.  dx: the rows of B are
-// the listed ones, dW: the contracted axis is theirs.
-template <class H, class Tl, bool DX>
-__global__ __launch_bounds__(Tl::NT) void k_nll_product(const char* A, unsigned lda, int rowsA, const char* B,
-                                                        unsigned ldb, const Control* ctl, int bt, int nk, int S,
-                                                        bool add, float* out, int ldo) {
-    __shared__ __align__(16) char lds[Tl::STAGE];
-    const int padded = tiles(ctl->rows, ROW_TILE) * ROW_TILE, at = tiles(rowsA, Tl::BA);
-    if (DX) {
-        bt = padded / Tl::BB;
-        S = dx_split(bt, at, gridDim.x, nk);
-    } else {
-        nk = padded / (int)(STEP / sizeof(H));
-    }
+template <class T, class H, class Tl, bool DX>
+__global__ __launch_bounds__(Tl::NT) void k_nll_product(const Product p, const Control* ctl) {
+    __shared__ __align__(16) char lds[2 * Tl::STAGE];
+    const int rows = __builtin_amdgcn_readfirstlane(ctl->rows), padded = tiles(rows, ROW_TILE) * ROW_TILE;
+    const int at = tiles(p.N, Tl::BA), bt = DX ? padded / Tl::BB : p.b_tiles;
+    const int nk = DX ? p.nk : padded / (int)(STEP / sizeof(H));
+    const int S = DX ? dx_split(bt, at, gridDim.x, nk) : p.split;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wa = wave / Tl::WB, wb = wave % Tl::WB;
-    for (int item = ordered_block(); item < at * bt * S; item += gridDim.x) {
-        const int share = item / (at * bt), tile = item - share * at * bt;
-        const int group = tile / (8 * at), in = tile - group * 8 * at, width = min(8, bt - group * 8);
-        const int b0 = (group * 8 + in % width) * Tl::BB, a0 = in / width * Tl::BA;
-        const int k0 = (int)((long)share * nk / S), k1 = (int)((long)(share + 1) * nk / S);
-        Tl t;
-        t.product(A + (size_t)a0 * lda + (size_t)k0 * STEP, lda, rowsA - a0, B + (size_t)b0 * ldb + (size_t)k0 * STEP,
-                  ldb, k1 - k0, lds);
+    const int total = at * bt * S;
+    Tl t;
+    auto where = [&](int item, int& share, int& a0, int& b0, int& k0, int& k1) {
+        share = item / (at * bt);
+        int ai, bi;
+        in_groups(item - share * at * bt, bt, at, bi, ai);
+        a0 = ai * Tl::BA;
+        b0 = bi * Tl::BB;
+        k0 = (int)((long)share * nk / S);
+        k1 = (int)((long)(share + 1) * nk / S);
+    };
+    auto start = [&](int item) {
+        int share, a0, b0, k0, k1;
+        where(item, share, a0, b0, k0, k1);
+        if (k0 >= k1) return;
+        const int ca = (int)p.lda - a0 * (int)sizeof(H);
+        if (DX)
+            t.start(p.A + a0 * sizeof(H), p.lda, ca, p.B + (size_t)b0 * p.ldb, p.ldb, Tl::BB, k0, lds);
+        else
+            t.start(p.A + a0 * sizeof(H), p.lda, ca, p.B + b0 * sizeof(H), p.ldb, (int)p.ldb - b0 * (int)sizeof(H), k0,
+                    lds);
+    };
+    // the scales of the operands are taken out one at a time: their product may be out of range
+    const float back = 1.0f / held_scale<H>(DX ? ctl->max_w : ctl->max_x);
+    const bool direct = S == 1 && (!DX || (p.last && !p.add));
+    int item = ordered_block();
+    if (item < total) start(item);
+    for (; item < total; item += gridDim.x) {
+        int share, a0, b0, k0, k1;
+        where(item, share, a0, b0, k0, k1);
+        t.product(k0, k1, lds, [&] {
+            if (item + (int)gridDim.x < total) start(item + gridDim.x);
+        });
 #pragma unroll
         for (int j = 0; j < Tl::MB; ++j) {
             const int b = b0 + wb * (Tl::BB / Tl::WB) + j * 16 + (lane & 15);
-            float* row = out + ((size_t)share * bt * Tl::BB + b) * ldo;
+            const int a1 = a0 + wa * (Tl::BA / Tl::WA) + lane / 16 * 4;
+            if (direct) {
+                const bool in = b < (DX ? rows : p.b_rows);
+                const float g = DX ? (in ? p.grad[b] * p.scale : 0.0f) : grad_unit(ctl->max_g) * p.scale;
+                T* to = (T*)p.out + (size_t)(in ? (DX ? p.row[b] : b) : 0) * p.N;
 #pragma unroll
-            for (int i = 0; i < Tl::MA; ++i) {
-                const int a = a0 + wa * (Tl::BA / Tl::WA) + i * 16 + lane / 16 * 4;
-                if (a >= ldo) continue;              // ldo: N up to a multiple of 4
-                f32x4 x = t.acc[i][j];
-                if (add) x += *(const f32x4*)(row + a);
-                *(f32x4*)(row + a) = x;
+                for (int i = 0; i < Tl::MA; ++i) {
+                    const int a = a1 + i * 16;
+                    T v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = (T)(t.acc[i][j][k] * (1.0f / P_SCALE<H>) * back * g);
+                    if (!in) continue;
+                    if (a + 4 <= p.N) {
+                        __builtin_memcpy(to + a, v, sizeof(v));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (a + k < p.N) to[a + k] = v[k];
+                    }
+                }
+            } else {
+                float* to = p.part + ((size_t)share * bt * Tl::BB + b) * p.ldo;
+#pragma unroll
+                for (int i = 0; i < Tl::MA; ++i) {
+                    const int a = a1 + i * 16;
+                    if (a >= p.ldo) continue;              // ldo: N up to a multiple of 4
+                    f32x4 x = t.acc[i][j];
+                    if (DX && p.add) x += *(const f32x4*)(to + a);
+                    *(f32x4*)(to + a) = x;
+                }
             }
         }
     }
 }
 
-// A wavefront a row of x: zeros where it is not listed, else the shares' sum times the row's gradient
-template <class T, class H>
-__global__ __launch_bounds__(256) void k_nll_dx(const Control* ctl, const int* place, const float* grad, float scale,
-                                                const float* part, int ldo, int BA, int BB, int wgs, int nk, int rows,
-                                                int N, T* out) {
+// The shares' sums to results: a wavefront a row
+template <class T, class H, bool DX>
+__global__ __launch_bounds__(256) void k_nll_join(const Product p, const Control* ctl, int BA, int BB, int wgs) {
     const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (r >= rows) return;
-    const int i = place[r], bt = tiles(ctl->rows, ROW_TILE) * (ROW_TILE / BB);
-    T* to = out + (size_t)r * N;
-    if (i < 0) {
-        for (int c = lane; c < N; c += 64) to[c] = (T)0.0f;
-        return;
-    }
-    const int S = dx_split(bt, tiles(N, BA), wgs, nk);
-    const float back = 1.0f / held_scale<H>(ctl->max_w), g = grad[i] * scale;
-    for (int c = lane; c < N; c += 64) {
-        float v = 0.0f;
-        for (int s = 0; s < S; ++s) v += part[((size_t)s * bt * BB + i) * ldo + c];
-        to[c] = (T)(v * (1.0f / P_SCALE<H>) * back * g);
-    }
-}
-
-// A wavefront a word of a piece
-template <class T, class H>
-__global__ __launch_bounds__(256) void k_nll_dw(const Control* ctl, const float* part, int ldo, int piece, int S,
-                                                float scale, int words, int N, T* out) {
-    const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (r >= words) return;
-    const float back = 1.0f / held_scale<H>(ctl->max_x), g = grad_unit(ctl->max_g) * scale;
-    for (int c = lane; c < N; c += 64) {
-        float v = 0.0f;
-        for (int s = 0; s < S; ++s) v += part[((size_t)s * piece + r) * ldo + c];
-        out[(size_t)r * N + c] = (T)(v * (1.0f / P_SCALE<H>) * back * g);
+    const int bt = DX ? tiles(ctl->rows, ROW_TILE) * (ROW_TILE / BB) : p.b_tiles;
+    if (r >= (DX ? ctl->rows : p.b_rows)) return;
+    const int S = DX ? dx_split(bt, tiles(p.N, BA), wgs, p.nk) : p.split;
+    if (S == 1 && (!DX || !p.add)) return;               // written by the product itself
+    const float back = 1.0f / held_scale<H>(DX ? ctl->max_w : ctl->max_x);
+    const float g = (DX ? p.grad[r] : grad_unit(ctl->max_g)) * p.scale;
+    T* to = (T*)p.out + (size_t)(DX ? p.row[r] : r) * p.N;
+    const float* from = p.part + (size_t)r * p.ldo;
+    for (int c = lane * 4; c < p.N; c += 256) {
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < S; ++s) v += *(const f32x4*)(from + (size_t)s * bt * BB * p.ldo + c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c + k < p.N) to[c + k] = (T)(v[k] * (1.0f / P_SCALE<H>) * back * g);
     }
 }
 
 // ------------------------------------------------------------------ host
-template <class T> using Large = Tile<T, 256, 256, 2, 4>;
-template <class T> using Small = Tile<T, 128, 128, 2, 2>;
+// Three sizes of tile.  Each holds its workgroups' LDS: 1, 2 and 4 workgroups a CU.
+enum Size { LARGE, MEDIUM, SMALL };
+struct Config {
+    int tile, wgs;
+};
+constexpr Config CONFIG[3] = {{256, 256}, {128, 512}, {64, 1024}};
+template <class T, Form FA, Form FB> using Large = Tile<T, FA, FB, 256, 256, 2, 4>;
+template <class T, Form FA, Form FB> using Medium = Tile<T, FA, FB, 128, 128, 2, 2>;
+template <class T, Form FA, Form FB> using Small = Tile<T, FA, FB, 64, 64, 2, 2>;
 
 long up(long n, long m) { return (n + m - 1) / m * m; }
 
+// The size whose busiest workgroup is done first: rounds of tiles, times what a step of a tile takes with
+// the CU's workgroups at work (a large tile's as unit).  A contracted axis of nk steps may be shared out.
+Size pick(long a, long b, long nk, bool split) {
+    constexpr double step[3] = {1.0, 0.6, 0.4};
+    Size best = LARGE;
+    double least = 1e300;
+    for (int s = 0; s < 3; ++s) {
+        const long t = up(a, CONFIG[s].tile) / CONFIG[s].tile * (up(b, CONFIG[s].tile) / CONFIG[s].tile);
+        const long shares = split ? dx_split((int)(t < 1 << 20 ? t : 1 << 20), 1, CONFIG[s].wgs, (int)nk) : 1;
+        const double rounds = (double)((t * shares + CONFIG[s].wgs - 1) / CONFIG[s].wgs);
+        const double time = rounds * ((double)nk / shares + 2.0) * step[s];
+        if (time < least) {
+            least = time;
+            best = (Size)s;
+        }
+    }
+    return best;
+}
+
 // Everything a call lays out in its workspace
 struct Plan {
-    bool large, copy_w;
-    int wgs, BA, BB, WA;
-    long rows, padded, V, N, ld;       // ld: elements of a padded row of x (and of W)
+    bool copy_w;
+    Size scores, dx, dw;
+    long rows, padded, ld;       // ld: elements of a padded row of x and W
     long piece, pieces, vpad, ldo;
-    int dw_split;
-    size_t ctl, counts, list_row, list_target, list_lse, list_grad, place, x, w, part, score;
-    size_t xt, wt, p, pt, dx, dw, total;
+    int nk, nk_dx, dw_split;
+    size_t ctl, counts, row, target, lse, grad, x, w, part, score, xg, wh, p, dx_part, dw_part, total;
 };
 
 size_t region(size_t& at, size_t bytes) {
@@ -587,50 +824,47 @@ Plan make_plan(int dtype, int B, int T, int V, int N, bool grad, const void* tab
     const long e = dtype == SEMICRF_F32 ? 4 : 2;
     p.rows = (long)B * T;
     p.padded = up(p.rows, ROW_TILE);
-    p.V = V;
-    p.N = N;
-    p.ld = up(N, STEP / e);
-    p.large = tiles((int)p.rows, 256) * (long)tiles(V, 256) >= 256;
-    p.BA = p.BB = p.large ? 256 : 128;
-    p.WA = 2;
-    p.wgs = p.large ? 256 : 512;
-    p.copy_w = N * e % STEP != 0 || !table || (uintptr_t)table % 16;
+    p.ld = up(N, 64);
+    p.nk = (int)(up(N * e, STEP) / STEP);
+    p.copy_w = N % 64 || !table || (uintptr_t)table % 16 || (grad && e == 4);
+    p.scores = pick(V, p.rows, p.nk, false);
     size_t at = 0;
     p.ctl = region(at, sizeof(Control));
     p.counts = region(at, (size_t)up(p.rows, LIST) / LIST * 4);
-    p.list_row = region(at, p.padded * 4);
-    p.list_target = region(at, p.padded * 4);
+    p.row = region(at, p.padded * 4);
+    p.target = region(at, p.padded * 4);
     p.x = region(at, p.padded * p.ld * e);
+    p.vpad = V;
     if (!grad) {
-        const long items = p.padded / p.BB > 4l * p.wgs ? p.padded / p.BB : 4l * p.wgs;
-        p.part = region(at, items * p.WA * p.BB * sizeof(float2));
+        const Config c = CONFIG[p.scores];
+        const long items = p.padded / c.tile > 4l * c.wgs ? p.padded / c.tile : 4l * c.wgs;
+        p.part = region(at, items * 2 * c.tile * sizeof(float2));
         p.score = region(at, p.padded * 4);
     } else {
-        p.list_lse = region(at, p.padded * 4);
-        p.list_grad = region(at, p.padded * 4);
-        p.place = region(at, p.rows * 4);
+        p.lse = region(at, p.padded * 4);
+        p.grad = region(at, p.padded * 4);
         p.vpad = up(V, 256);
-        // pieces of the vocabulary: p and its transpose take at most 1 GB together, or one tile of words
-        const long most = (512l << 20) / (p.padded * e) / 256 * 256;
-        p.pieces = most < 256 ? p.vpad / 256 : tiles((int)p.vpad, (int)(most < p.vpad ? most : p.vpad));
+        // pieces of the vocabulary: p takes at most 1 GB, or one large tile of words
+        const long most = (1024l << 20) / (p.padded * e) / 256 * 256;
+        p.pieces = most < 256 ? p.vpad / 256 : (p.vpad + most - 1) / most;
         p.piece = up((p.vpad + p.pieces - 1) / p.pieces, 256);
-        p.pieces = (p.vpad + p.piece - 1) / p.piece;
+        p.pieces = (V + p.piece - 1) / p.piece;
         p.vpad = p.piece * p.pieces;
         p.ldo = up(N, 4);
-        const long nt = tiles(N, p.BA);
-        const long shares = p.wgs / ((p.piece / p.BB) * nt);
-        p.dw_split = (int)(shares < 1 ? 1 : shares > 16 ? 16 : shares);
-        const long k = p.padded * e / STEP;
-        if (p.dw_split > k) p.dw_split = (int)k;
-        p.xt = region(at, p.N * p.padded * e);
-        p.wt = region(at, p.N * p.vpad * e);
+        p.nk_dx = (int)(p.piece * e / STEP);
+        const long nk_dw = p.padded * e / STEP;
+        p.dx = pick(N, p.rows, p.nk_dx, true);
+        p.dw = pick(N, p.piece, nk_dw, true);
+        const Config cx = CONFIG[p.dx], cw = CONFIG[p.dw];
+        p.dw_split = dx_split((int)(p.piece / cw.tile), tiles(N, cw.tile), cw.wgs, (int)nk_dw);
+        p.xg = region(at, p.padded * p.ld * e);
+        p.wh = region(at, e == 2 ? p.vpad * p.ld * e : 0);
         p.p = region(at, p.padded * p.piece * e);
-        p.pt = region(at, p.padded * p.piece * e);
-        const long dx_rows = p.padded > p.wgs * p.BB / nt ? p.padded : p.wgs * p.BB / nt;
-        p.dx = region(at, dx_rows * p.ldo * 4);
-        p.dw = region(at, (size_t)p.dw_split * p.piece * p.ldo * 4);
+        const long nt = tiles(N, cx.tile), least = (long)cx.wgs / nt * cx.tile;
+        p.dx_part = region(at, (p.padded > least ? p.padded : least) * p.ldo * 4);
+        p.dw_part = region(at, p.dw_split > 1 ? (size_t)p.dw_split * p.piece * p.ldo * 4 : 0);
     }
-    p.w = region(at, p.copy_w ? (size_t)V * p.ld * e : 0);
+    p.w = region(at, p.copy_w ? (size_t)p.vpad * p.ld * e : 0);
     p.total = at;
     return p;
 }
@@ -638,96 +872,126 @@ Plan make_plan(int dtype, int B, int T, int V, int N, bool grad, const void* tab
 template <class P>
 P* in(void* ws, size_t at) { return (P*)((char*)ws + at); }
 
-// The listed rows and the padded copies of x and, where its rows are no whole steps, of W.
-template <class T, bool GRAD>
-Scores gather(const NllArgs& a, const Plan& p, const Listed& list, void* ws, hipStream_t stream) {
+// f(tile type) of a size
+template <class T, Form FA, Form FB, class F>
+void with_size(Size s, F&& f) {
+    if (s == LARGE) f((Large<T, FA, FB>*)nullptr);
+    else if (s == MEDIUM) f((Medium<T, FA, FB>*)nullptr);
+    else f((Small<T, FA, FB>*)nullptr);
+}
+
+// Lists the rows and lays out what the products read
+template <class T, class H, bool GRAD>
+Scores gather(const NllArgs& a, const Plan& p, const Listed& list, Layout& l, void* ws, hipStream_t stream) {
     Control* ctl = in<Control>(ws, p.ctl);
     int* counts = in<int>(ws, p.counts);
     const int blocks = (int)(up(p.rows, LIST) / LIST);
-    hipLaunchKernelGGL(k_nll_count, dim3(blocks), dim3(LIST_THREADS), 0, stream, a, ctl, counts);
-    hipLaunchKernelGGL(k_nll_list<GRAD>, dim3(blocks), dim3(LIST_THREADS), 0, stream, a, ctl, counts, list);
-    T* x = in<T>(ws, p.x);
-    hipLaunchKernelGGL(k_nll_rows<T>, dim3((unsigned)(p.padded / 4)), dim3(256), 0, stream, (const T*)a.x, list.row, ctl,
-                       0, a.N, x, (int)p.ld, ROW_TILE);
-    const T* w = (const T*)a.table;
-    if (p.copy_w) {
-        T* copy = in<T>(ws, p.w);
-        hipLaunchKernelGGL(k_nll_rows<T>, dim3((unsigned)((p.V + 3) / 4)), dim3(256), 0, stream, w, (const int*)nullptr,
-                           (const Control*)nullptr, a.V, a.N, copy, (int)p.ld, 1);
-        w = copy;
-    }
+    if (blocks > 1)
+        hipLaunchKernelGGL(k_nll_count, dim3(blocks), dim3(LIST_THREADS), 0, stream, a, ctl, counts);
+    hipLaunchKernelGGL(k_nll_list<GRAD>, dim3(blocks), dim3(LIST_THREADS), 0, stream, a, ctl,
+                       blocks > 1 ? counts : nullptr, list);
+    if (GRAD && sizeof(H) == 2)
+        hipLaunchKernelGGL(k_nll_max<T>, dim3(1024), dim3(256), 0, stream, a, ctl, list.row);
+    l.x = in<T>(ws, p.x);
+    l.w = p.copy_w ? in<T>(ws, p.w) : (void*)a.table;
+    l.ld = (int)p.ld;
+    l.words = (int)p.vpad;
+    l.copy_w = p.copy_w;
+    const unsigned cols = (unsigned)(p.ld / 64), x_blocks = (unsigned)(p.padded / 64) * cols;
+    const bool w_too = p.copy_w || (GRAD && a.grad_x);
+    const unsigned w_blocks = w_too ? (unsigned)((p.vpad + 63) / 64) * cols : 0;
+    hipLaunchKernelGGL((k_nll_lay<T, H, GRAD>), dim3(x_blocks + w_blocks), dim3(256), 0, stream, a, ctl, list, l,
+                       (int)x_blocks);
     Scores s{};
-    s.w = (const char*)w;
-    s.x = (const char*)x;
-    s.ldw = s.ldx = (unsigned)(p.ld * sizeof(T));
+    s.w = (const char*)l.w;
+    s.x = (const char*)l.x;
+    s.ld = (unsigned)(p.ld * sizeof(T));
     s.V = a.V;
-    s.nk = (int)(p.ld * sizeof(T) / STEP);
+    s.nk = p.nk;
     s.scale = a.scale * LOG2EF;
     return s;
 }
 
-template <class T, class Tl>
-hipError_t run_nll(const NllArgs& a, const Plan& p, void* ws, hipStream_t stream) {
-    Listed list{in<int>(ws, p.list_row), in<int>(ws, p.list_target), nullptr, nullptr, nullptr};
-    const Scores s = gather<T, false>(a, p, list, ws, stream);
+template <class T>
+hipError_t run_nll(const NllArgs& a, void* ws, hipStream_t stream) {
+    const Plan p = make_plan(a.dtype, a.B, a.T, a.V, a.N, false, a.table);
+    Listed list{in<int>(ws, p.row), in<int>(ws, p.target), nullptr, nullptr};
+    Layout l{};
+    const Scores s = gather<T, T, false>(a, p, list, l, ws, stream);
     const Control* ctl = in<Control>(ws, p.ctl);
     float2* part = in<float2>(ws, p.part);
     float* score = in<float>(ws, p.score);
-    hipLaunchKernelGGL((k_nll_scores<T, Tl>), dim3(p.wgs), dim3(Tl::NT), 0, stream, s, ctl, list.target, part, score);
-    hipLaunchKernelGGL(k_nll_loss, dim3((unsigned)((p.rows + 255) / 256)), dim3(256), 0, stream, ctl, list.row, part,
-                       score, a.V, p.BA, p.BB, p.WA, p.wgs, a.loss, a.lse);
+    with_size<T, ROWS, ROWS>(p.scores, [&](auto* t) {
+        using Tl = std::remove_pointer_t<decltype(t)>;
+        const int wgs = CONFIG[p.scores].wgs;
+        hipLaunchKernelGGL((k_nll_scores<T, Tl>), dim3(wgs), dim3(Tl::NT), 0, stream, s, ctl, list.target, part, score);
+        hipLaunchKernelGGL(k_nll_loss, dim3((unsigned)((p.rows + 255) / 256)), dim3(256), 0, stream, ctl, list.row, part,
+                           score, a.V, Tl::BA, Tl::BB, Tl::WA, wgs, a.loss, a.lse);
+    });
     return hipGetLastError();
 }
 
-template <class T, class Tl, class Tg>
-hipError_t run_nll_grad(const NllArgs& a, const Plan& p, void* ws, hipStream_t stream) {
+template <class T>
+hipError_t run_nll_grad(const NllArgs& a, void* ws, hipStream_t stream) {
     using H = typename Held<T>::type;
-    Listed list{in<int>(ws, p.list_row), in<int>(ws, p.list_target), in<float>(ws, p.list_lse),
-                in<float>(ws, p.list_grad), in<int>(ws, p.place)};
-    const Scores s = gather<T, true>(a, p, list, ws, stream);
-    Control* ctl = in<Control>(ws, p.ctl);
-    H *xt = in<H>(ws, p.xt), *wt = in<H>(ws, p.wt), *pp = in<H>(ws, p.p), *pt = in<H>(ws, p.pt);
-    float *dx = in<float>(ws, p.dx), *dw = in<float>(ws, p.dw);
-    const unsigned nb = (unsigned)((a.N + 63) / 64);
-    if (a.grad_table) {
-        if (sizeof(H) == 2)
-            hipLaunchKernelGGL(k_nll_max<T>, dim3(256), dim3(256), 0, stream, (const T*)s.x, ctl, 0l, (int)p.ld,
-                               &ctl->max_x);
-        hipLaunchKernelGGL((k_nll_transpose<T, H>), dim3((unsigned)(p.padded / 64), nb), dim3(256), 0, stream,
-                           (const T*)s.x, ctl, true, 0, a.N, (int)p.ld, &ctl->max_x, xt, (size_t)p.padded, ROW_TILE);
-    }
-    if (a.grad_x) {
-        if (sizeof(H) == 2)
-            hipLaunchKernelGGL(k_nll_max<T>, dim3(1024), dim3(256), 0, stream, (const T*)a.table, (const Control*)nullptr,
-                               (long)a.V * a.N, a.N, &ctl->max_w);
-        hipLaunchKernelGGL((k_nll_transpose<T, H>), dim3((unsigned)(p.vpad / 64), nb), dim3(256), 0, stream,
-                           (const T*)a.table, ctl, false, a.V, a.N, a.N, &ctl->max_w, wt, (size_t)p.vpad, (int)p.vpad);
-    }
-    const int nk_dx = (int)(p.piece * sizeof(H) / STEP);
+    const Plan p = make_plan(a.dtype, a.B, a.T, a.V, a.N, true, a.table);
+    Listed list{in<int>(ws, p.row), in<int>(ws, p.target), in<float>(ws, p.lse), in<float>(ws, p.grad)};
+    Layout l{};
+    l.xg = in<H>(ws, p.xg);
+    l.wh = sizeof(H) == 2 ? (void*)in<H>(ws, p.wh) : (void*)in<T>(ws, p.w);
+    const Scores s = gather<T, H, true>(a, p, list, l, ws, stream);
+    const Control* ctl = in<Control>(ws, p.ctl);
+    H* pp = in<H>(ws, p.p);
+    const int ldp = (int)p.piece;
     for (long i = 0; i < p.pieces; ++i) {
-        const int v0 = (int)(i * p.piece);
-        const int words = (int)(p.V - v0 < p.piece ? p.V - v0 : p.piece);
-        if (words <= 0) break;
-        hipLaunchKernelGGL((k_nll_p<T, H, Tl>), dim3(p.wgs), dim3(Tl::NT), 0, stream, s, ctl, list.target, list.lse,
-                           list.grad, v0, (int)(p.piece / Tl::BA), pp, (size_t)p.piece, pt, (size_t)p.padded);
+        const int v0 = (int)(i * p.piece), words = (int)(a.V - v0 < p.piece ? a.V - v0 : p.piece);
+        with_size<T, ROWS, ROWS>(p.scores, [&](auto* t) {
+            using Tl = std::remove_pointer_t<decltype(t)>;
+            hipLaunchKernelGGL((k_nll_p<T, H, Tl>), dim3(CONFIG[p.scores].wgs), dim3(Tl::NT), 0, stream, s, ctl,
+                               list.target, list.lse, v0, ldp / Tl::BA, pp, ldp);
+        });
+        Product q{};
+        q.B = (const char*)pp;
+        q.lda = (unsigned)(p.ld * sizeof(H));
+        q.ldb = (unsigned)(p.piece * sizeof(H));
+        q.N = a.N;
+        q.ldo = (int)p.ldo;
+        q.scale = a.scale;
         if (a.grad_x)
-            hipLaunchKernelGGL((k_nll_product<H, Tg, true>), dim3(p.wgs), dim3(Tg::NT), 0, stream,
-                               (const char*)(wt + v0), (unsigned)(p.vpad * sizeof(H)), a.N, (const char*)pp,
-                               (unsigned)(p.piece * sizeof(H)), ctl, 0, nk_dx, 0, i > 0, dx, (int)p.ldo);
-        if (a.grad_table) {
-            hipLaunchKernelGGL((k_nll_product<H, Tg, false>), dim3(p.wgs), dim3(Tg::NT), 0, stream, (const char*)xt,
-                               (unsigned)(p.padded * sizeof(H)), a.N, (const char*)pt,
-                               (unsigned)(p.padded * sizeof(H)), ctl, (int)(p.piece / Tg::BB), 0, p.dw_split, false, dw,
-                               (int)p.ldo);
-            hipLaunchKernelGGL((k_nll_dw<T, H>), dim3((unsigned)((words + 3) / 4)), dim3(256), 0, stream, ctl, dw,
-                               (int)p.ldo, (int)p.piece, p.dw_split, a.scale, words, a.N,
-                               (T*)a.grad_table + (size_t)v0 * a.N);
-        }
+            with_size<H, COLUMNS, ROWS>(p.dx, [&](auto* t) {
+                using Tl = std::remove_pointer_t<decltype(t)>;
+                const int wgs = CONFIG[p.dx].wgs;
+                Product d = q;
+                d.A = (const char*)((H*)l.wh + (size_t)v0 * p.ld);
+                d.nk = p.nk_dx;
+                d.add = i > 0;
+                d.last = i + 1 == p.pieces;
+                d.part = in<float>(ws, p.dx_part);
+                d.row = list.row;
+                d.grad = list.grad;
+                d.out = a.grad_x;
+                hipLaunchKernelGGL((k_nll_product<T, H, Tl, true>), dim3(wgs), dim3(Tl::NT), 0, stream, d, ctl);
+                if (d.last && (d.add || p.nk_dx >= 16))     // else there is one share, whatever the rows
+                    hipLaunchKernelGGL((k_nll_join<T, H, true>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0,
+                                       stream, d, ctl, Tl::BA, Tl::BB, wgs);
+            });
+        if (a.grad_table)
+            with_size<H, COLUMNS, COLUMNS>(p.dw, [&](auto* t) {
+                using Tl = std::remove_pointer_t<decltype(t)>;
+                Product d = q;
+                d.A = (const char*)l.xg;
+                d.b_tiles = ldp / Tl::BB;
+                d.b_rows = words;
+                d.split = p.dw_split;
+                d.part = in<float>(ws, p.dw_part);
+                d.out = (T*)a.grad_table + (size_t)v0 * a.N;
+                hipLaunchKernelGGL((k_nll_product<T, H, Tl, false>), dim3(CONFIG[p.dw].wgs), dim3(Tl::NT), 0, stream, d,
+                                   ctl);
+                if (d.split > 1)
+                    hipLaunchKernelGGL((k_nll_join<T, H, false>), dim3((unsigned)((words + 3) / 4)), dim3(256), 0,
+                                       stream, d, ctl, Tl::BA, Tl::BB, CONFIG[p.dw].wgs);
+            });
     }
-    if (a.grad_x)
-        hipLaunchKernelGGL((k_nll_dx<T, H>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0, stream, ctl, list.place,
-                           list.grad, a.scale, dx, (int)p.ldo, p.BA, p.BB, p.wgs, nk_dx, (int)p.rows, a.N,
-                           (T*)a.grad_x);
     return hipGetLastError();
 }
 
@@ -738,19 +1002,11 @@ size_t token_nll_bytes(int dtype, int B, int T, int V, int N, bool grad) {
 }
 
 hipError_t launch_token_nll(const NllArgs& a, void* ws, hipStream_t stream) {
-    const Plan p = make_plan(a.dtype, a.B, a.T, a.V, a.N, false, a.table);
-    if (a.dtype == SEMICRF_F32)
-        return p.large ? run_nll<float, Large<float>>(a, p, ws, stream) : run_nll<float, Small<float>>(a, p, ws, stream);
-    return p.large ? run_nll<bf16, Large<bf16>>(a, p, ws, stream) : run_nll<bf16, Small<bf16>>(a, p, ws, stream);
+    return a.dtype == SEMICRF_F32 ? run_nll<float>(a, ws, stream) : run_nll<bf16>(a, ws, stream);
 }
 
 hipError_t launch_token_nll_grad(const NllArgs& a, void* ws, hipStream_t stream) {
-    const Plan p = make_plan(a.dtype, a.B, a.T, a.V, a.N, true, a.table);
-    if (a.dtype == SEMICRF_F32)
-        return p.large ? run_nll_grad<float, Large<float>, Large<float>>(a, p, ws, stream)
-                       : run_nll_grad<float, Small<float>, Small<float>>(a, p, ws, stream);
-    return p.large ? run_nll_grad<bf16, Large<bf16>, Large<f16>>(a, p, ws, stream)
-                   : run_nll_grad<bf16, Small<bf16>, Small<f16>>(a, p, ws, stream);
+    return a.dtype == SEMICRF_F32 ? run_nll_grad<float>(a, ws, stream) : run_nll_grad<bf16>(a, ws, stream);
 }
 
 }  // namespace semicrf
