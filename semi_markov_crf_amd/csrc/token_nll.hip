@@ -99,14 +99,22 @@ struct Operand {
             else at[i] = (unsigned)r * ld + min((c ^ column_swizzle<T>(r)) * 16, limit - 16);
         }
     }
+    // To LDS directly, 1,024 bytes an instruction from the address in m0 on.  As assembly without results: the
+    // compiler would wait for such loads before any transposing read of LDS, whichever half of it they fill
+    // (the 25,088-word product of dW took 1,120 us so).  step_barrier() waits for them.
     __device__ __forceinline__ void fetch(int k, char* lds) const {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const char* from = base + k * step;
+        const unsigned to = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 1024;
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"          // m0 is reserved; nothing else here uses it
 #pragma unroll
         for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + at[i]),
-                                             (__attribute__((address_space(3))) void*)(lds + (i * NW + wave) * 1024),
-                                             16, 0, 0);
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                         :
+                         : "s"(to + i * NW * 1024), "v"(at[i]), "s"(from)
+                         : "memory", "m0");
+#pragma clang diagnostic pop
     }
     // Of half a step, the 16 rows (or columns) from `first`
     __device__ __forceinline__ static raw_piece fragment(const char* lds, int first, int half) {
@@ -158,18 +166,16 @@ struct Tile {
         b.fetch(k, lds + turn * STAGE + BA * STEP);
         turn ^= 1;
     }
-    // Points at a tile and fetches its first step; no other wavefront reads that half of LDS any more.
-    __device__ __forceinline__ void start(const void* pa, unsigned lda, int limit_a, const void* pb, unsigned ldb,
-                                          int limit_b, int k, char* lds) {
+    __device__ __forceinline__ void point(const void* pa, unsigned lda, int limit_a, const void* pb, unsigned ldb,
+                                          int limit_b) {
         a.point(pa, lda, limit_a);
         b.point(pb, ldb, limit_b);
-        fetch(k, lds);
     }
-    // acc = A . B over steps k0 .. k1 - 1, of which the first was fetched; then next(), which may start
-    // another tile.
+    // acc = A . B over steps k0 .. k1 - 1, of which the first was fetched.  next(k): points at the tile to
+    // come and sets k to its first step, which is fetched during the last one here; false: there is none.
     template <class Next>
     __device__ __forceinline__ void product(int k0, int k1, char* lds, Next&& next) {
-        const int wave = threadIdx.x >> 6, wa = wave / WB, wb = wave % WB;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wa = wave / WB, wb = wave % WB;
 #pragma unroll
         for (int i = 0; i < MA; ++i)
 #pragma unroll
@@ -177,8 +183,10 @@ struct Tile {
         for (int k = k0; k < k1; ++k) {
             step_barrier();
             const char* now = lds + (turn ^ 1) * STAGE;
-            if (k + 1 < k1) fetch(k + 1, lds);
-            else next();
+            int to = k + 1;
+            bool more = true;
+            if (to == k1) more = next(to);
+            if (more) fetch(to, lds);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 raw_piece fb[MB];
@@ -190,6 +198,18 @@ struct Tile {
                     const raw_piece fa = OpA::fragment(now, wa * (BA / WA) + i * 16, half);
 #pragma unroll
                     for (int j = 0; j < MB; ++j) acc[i][j] = mma((const T*)nullptr, fa, fb[j], acc[i][j]);
+                }
+            }
+            // In this order: the first two fragments of A and those of B, then a read ahead of each row of products
+            // (products of a step alone leave half of the matrix cores' time to waits for LDS).
+            if constexpr (sizeof(T) == 2) {
+                constexpr int RA = FA == ROWS ? 1 : 2, RB = FB == ROWS ? 1 : 2;
+                __builtin_amdgcn_sched_group_barrier(0x100, MB * RB + 2 * RA, 0);
+#pragma unroll
+                for (int i = 0; i < 2 * MA; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, MB, 0);
+                    if (i + 2 < 2 * MA) __builtin_amdgcn_sched_group_barrier(0x100, RA, 0);
+                    if (i >= MA - 1 - MB && i < MA - 1) __builtin_amdgcn_sched_group_barrier(0x100, RB, 0);
                 }
             }
         }
@@ -377,8 +397,16 @@ __global__ __launch_bounds__(256) void k_nll_max(const NllArgs a, Control* ctl, 
     } else {
         most = largest((const T*)a.table, (long)a.V * a.N, blockIdx.x - quarter, gridDim.x - quarter);
     }
+    // one atomic a workgroup at most: on one address they take some 20 ns each, one after another
+    __shared__ unsigned s[4];
     for (int off = 32; off >= 1; off >>= 1) most = max(most, (unsigned)__shfl_xor((int)most, off, 64));
-    if (lane == 0 && most) atomicMax(of_x ? &ctl->max_x : &ctl->max_w, most);
+    if (lane == 0) s[threadIdx.x >> 6] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        most = max(max(s[0], s[1]), max(s[2], s[3]));
+        unsigned* to = of_x ? &ctl->max_x : &ctl->max_w;
+        if (most > __hip_atomic_load(to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(to, most);
+    }
 }
 
 // The power of two that brings a largest magnitude to [2^14, 2^15)
@@ -451,9 +479,13 @@ __global__ __launch_bounds__(256) void k_nll_lay(const NllArgs a, const Control*
             }
             if (GRAD && a.grad_x && r >= rows && r < M) {
                 T* to = (T*)a.grad_x + (size_t)list.row[r] * a.N;
+                if (c + V <= a.N) {
+                    *(loose_piece*)(to + c) = raw_piece{0, 0, 0, 0};
+                } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i < a.N) to[c + i] = (T)0.0f;
+                    for (int i = 0; i < V; ++i)
+                        if (c + i < a.N) to[c + i] = (T)0.0f;
+                }
             }
         } else {
             if (l.copy_w && r < l.words) *(raw_piece*)((T*)l.w + at) = v;
@@ -507,28 +539,30 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Con
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wa = wave / Tl::WB, wb = wave % Tl::WB;
     const int col = wb * (Tl::BB / Tl::WB) + (lane & 15);
     Tl t;
-    auto start = [&](int item, int v) {
-        t.start(p.w + (size_t)v * Tl::BA * p.ld, p.ld, p.V - v * Tl::BA, p.x + (size_t)(item / S) * Tl::BB * p.ld, p.ld,
-                Tl::BB, 0, lds);
+    auto point = [&](int item, int v) {
+        t.point(p.w + (size_t)v * Tl::BA * p.ld, p.ld, p.V - v * Tl::BA, p.x + (size_t)(item / S) * Tl::BB * p.ld, p.ld,
+                Tl::BB);
     };
     int item = ordered_block();
-    if (item < mt * S) start(item, item % S * vt / S);
+    if (item < mt * S) {
+        point(item, item % S * vt / S);
+        t.fetch(0, lds);
+    }
     for (; item < mt * S; item += gridDim.x) {
         const int m0 = item / S * Tl::BB, v1 = (item % S + 1) * vt / S;
         float top[Tl::MB], sum[Tl::MB];
-        int tgt[Tl::MB];
 #pragma unroll
         for (int j = 0; j < Tl::MB; ++j) {
             top[j] = -__builtin_inff();
             sum[j] = 0.0f;
-            const int m = m0 + col + j * 16;
-            tgt[j] = m < rows ? target[m] : -1;
         }
         for (int v = item % S * vt / S; v < v1; ++v) {
-            t.product(0, p.nk, lds, [&] {
-                const int next = item + gridDim.x;
-                if (v + 1 < v1) start(item, v + 1);
-                else if (next < mt * S) start(next, next % S * vt / S);
+            t.product(0, p.nk, lds, [&](int& k) {
+                const int after = v + 1 < v1 ? item : item + (int)gridDim.x;
+                if (after >= mt * S) return false;
+                point(after, v + 1 < v1 ? v + 1 : after % S * vt / S);
+                k = 0;
+                return true;
             });
             const int first = v * Tl::BA + wa * (Tl::BA / Tl::WA) + lane / 16 * 4;
             const bool whole = (v + 1) * Tl::BA <= p.V;
@@ -545,13 +579,14 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Con
                             if (first + i * 16 + k >= p.V) z[k] = -__builtin_inff();
                     most = fmaxf(most, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
                 }
-                const int hit = tgt[j] - first;          // the target is one of the lane's words
+                const int m = m0 + col + j * 16;
+                const int hit = (m < rows ? target[m] : -1) - first;      // the target is one of the lane's words
                 if (hit >= 0 && hit < Tl::MA * 16 && hit % 16 < 4) {
 #pragma unroll
                     for (int i = 0; i < Tl::MA; ++i)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (hit == i * 16 + k) at_target[m0 + col + j * 16] = t.acc[i][j][k];
+                            if (hit == i * 16 + k) at_target[m] = t.acc[i][j][k];
                 }
                 const float ref = most == -__builtin_inff() ? 0.0f : most;
                 float s = sum[j] * fast_exp2(top[j] - ref);
@@ -607,17 +642,24 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_p(const Scores s, const Control*
     const int rows = __builtin_amdgcn_readfirstlane(ctl->rows), mt = tiles(rows, ROW_TILE) * (ROW_TILE / Tl::BB);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wa = wave / Tl::WB, wb = wave % Tl::WB;
     Tl t;
-    auto start = [&](int tile) {
+    auto point = [&](int tile) {
         int m, v;
         in_groups(tile, mt, vt, m, v);
         const int w0 = min(v0 + v * Tl::BA, s.V - 1);         // pieces may end past the vocabulary
-        t.start(s.w + (size_t)w0 * s.ld, s.ld, s.V - w0, s.x + (size_t)m * Tl::BB * s.ld, s.ld, Tl::BB, 0, lds);
+        t.point(s.w + (size_t)w0 * s.ld, s.ld, s.V - w0, s.x + (size_t)m * Tl::BB * s.ld, s.ld, Tl::BB);
     };
     int tile = ordered_block();
-    if (tile < mt * vt) start(tile);
+    if (tile < mt * vt) {
+        point(tile);
+        t.fetch(0, lds);
+    }
     for (; tile < mt * vt; tile += gridDim.x) {
-        t.product(0, s.nk, lds, [&] {
-            if (tile + (int)gridDim.x < mt * vt) start(tile + gridDim.x);
+        t.product(0, s.nk, lds, [&](int& k) {
+            const int after = tile + gridDim.x;
+            if (after >= mt * vt) return false;
+            point(after);
+            k = 0;
+            return true;
         });
         int mi, v;
         in_groups(tile, mt, vt, mi, v);
@@ -646,16 +688,17 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_p(const Scores s, const Control*
     }
 }
 
-// Where a product's results go.  Partial sums: out[share][row of B][ldo], fp32, added to where `add` is
-// set.  Final results (of one share): rows of N elements of type T, times the factors.
+// Where a product's results go: rows of N elements of type T times the factors, or, from tiles whose
+// contracted axis is shared out, partial sums in fp32 that k_nll_join adds.  dx over several pieces of the
+// vocabulary is added up in fp32 rows instead.
 struct Product {
     const char *A, *B;
     unsigned lda, ldb;       // bytes
     int N;                   // columns of the result
     int b_tiles, b_rows;     // dW: tiles of words, and words
-    int nk, split;           // dx: steps; dW: shares
-    bool add, last;          // dx: pieces before this one, none after it
-    float* part;
+    int nk;                  // dx: steps
+    bool pieces, add, last;  // dx: several pieces; some before this one; none after it
+    float* part;             // [share][tile][BB][BA], or [rows][ldo] over several pieces
     int ldo;
     const int* row;          // dx: of a listed row
     const float* grad;       // dx: the row's gradient
@@ -663,11 +706,24 @@ struct Product {
     void* out;
 };
 
-// How the contracted axis of dx is shared out: as many shares of at least eight steps as fill the workgroups
-__host__ __device__ __forceinline__ int dx_split(int mt, int at, int wgs, int nk) {
-    const int fill = wgs / (mt * at > 0 ? mt * at : 1), most = nk / 8 < 16 ? nk / 8 : 16;
-    const int s = fill < most ? fill : most;
-    return s < 1 ? 1 : s;
+// Tiles are taken whole, a round of all workgroups after the other; those of the last round, if they are
+// few, are shared out along the contracted axis, in shares of at least eight steps.
+struct Rounds {
+    int whole, rest, shares, total;      // whole tiles, tiles shared out, shares of each, items
+};
+__host__ __device__ __forceinline__ Rounds rounds(int tiles, int wgs, int nk, bool split) {
+    Rounds r{tiles, 0, 1, tiles};
+    const int rest = tiles % wgs;
+    if (!split || !rest) return r;
+    int s = wgs / rest;
+    if (s > nk / 8) s = nk / 8;
+    if (s > 16) s = 16;
+    if (s < 2) return r;
+    r.whole = tiles - rest;
+    r.rest = rest;
+    r.shares = s;
+    r.total = r.whole + rest * s;
+    return r;
 }
 
 template <class T, class H, class Tl, bool DX>
@@ -676,52 +732,66 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_product(const Product p, const C
     const int rows = __builtin_amdgcn_readfirstlane(ctl->rows), padded = tiles(rows, ROW_TILE) * ROW_TILE;
     const int at = tiles(p.N, Tl::BA), bt = DX ? padded / Tl::BB : p.b_tiles;
     const int nk = DX ? p.nk : padded / (int)(STEP / sizeof(H));
-    const int S = DX ? dx_split(bt, at, gridDim.x, nk) : p.split;
+    const Rounds rd = rounds(at * bt, gridDim.x, nk, !p.pieces);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wa = wave / Tl::WB, wb = wave % Tl::WB;
-    const int total = at * bt * S;
     Tl t;
-    auto where = [&](int item, int& share, int& a0, int& b0, int& k0, int& k1) {
-        share = item / (at * bt);
+    auto where = [&](int item, int& a0, int& b0, int& k0, int& k1) {
+        const int j = item - rd.whole, share = j / max(1, rd.rest);
         int ai, bi;
-        in_groups(item - share * at * bt, bt, at, bi, ai);
+        in_groups(j < 0 ? item : rd.whole + j - share * rd.rest, bt, at, bi, ai);
         a0 = ai * Tl::BA;
         b0 = bi * Tl::BB;
-        k0 = (int)((long)share * nk / S);
-        k1 = (int)((long)(share + 1) * nk / S);
+        k0 = j < 0 ? 0 : (int)((long)share * nk / rd.shares);
+        k1 = j < 0 ? nk : (int)((long)(share + 1) * nk / rd.shares);
     };
-    auto start = [&](int item) {
-        int share, a0, b0, k0, k1;
-        where(item, share, a0, b0, k0, k1);
-        if (k0 >= k1) return;
-        const int ca = (int)p.lda - a0 * (int)sizeof(H);
-        if (DX)
-            t.start(p.A + a0 * sizeof(H), p.lda, ca, p.B + (size_t)b0 * p.ldb, p.ldb, Tl::BB, k0, lds);
-        else
-            t.start(p.A + a0 * sizeof(H), p.lda, ca, p.B + b0 * sizeof(H), p.ldb, (int)p.ldb - b0 * (int)sizeof(H), k0,
-                    lds);
+    // whether an item has steps; its first
+    auto point = [&](int item, int& k) {
+        int a0, b0, k1;
+        where(item, a0, b0, k, k1);
+        if (k >= k1) return false;
+        t.point(p.A + a0 * sizeof(H), p.lda, (int)p.lda - a0 * (int)sizeof(H),
+                DX ? p.B + (size_t)b0 * p.ldb : p.B + b0 * sizeof(H), p.ldb,
+                DX ? Tl::BB : (int)p.ldb - b0 * (int)sizeof(H));
+        return true;
     };
     // the scales of the operands are taken out one at a time: their product may be out of range
     const float back = 1.0f / held_scale<H>(DX ? ctl->max_w : ctl->max_x);
-    const bool direct = S == 1 && (!DX || (p.last && !p.add));
-    int item = ordered_block();
-    if (item < total) start(item);
-    for (; item < total; item += gridDim.x) {
-        int share, a0, b0, k0, k1;
-        where(item, share, a0, b0, k0, k1);
-        t.product(k0, k1, lds, [&] {
-            if (item + (int)gridDim.x < total) start(item + gridDim.x);
-        });
+    int item = ordered_block(), k = 0;
+    if (item < rd.total && point(item, k)) t.fetch(k, lds);
+    for (; item < rd.total; item += gridDim.x) {
+        int a0, b0, k0, k1;
+        where(item, a0, b0, k0, k1);
+        auto next = [&](int& k) {
+            const int after = item + gridDim.x;
+            return after < rd.total && point(after, k);
+        };
+        t.product(k0, k1, lds, next);
+        if (k0 >= k1 && next(k)) t.fetch(k, lds);            // no listed rows
+        const int a1 = wa * (Tl::BA / Tl::WA) + lane / 16 * 4;
 #pragma unroll
         for (int j = 0; j < Tl::MB; ++j) {
-            const int b = b0 + wb * (Tl::BB / Tl::WB) + j * 16 + (lane & 15);
-            const int a1 = a0 + wa * (Tl::BA / Tl::WA) + lane / 16 * 4;
-            if (direct) {
+            const int b1 = wb * (Tl::BB / Tl::WB) + j * 16 + (lane & 15), b = b0 + b1;
+            if (item >= rd.whole) {
+                float* to = p.part + ((size_t)(item - rd.whole) * Tl::BB + b1) * Tl::BA;
+#pragma unroll
+                for (int i = 0; i < Tl::MA; ++i) *(f32x4*)(to + a1 + i * 16) = t.acc[i][j];
+            } else if (DX && p.pieces) {
+                float* to = p.part + (size_t)b * p.ldo;
+#pragma unroll
+                for (int i = 0; i < Tl::MA; ++i) {
+                    const int a = a0 + a1 + i * 16;
+                    if (a >= p.ldo) continue;              // ldo: N up to a multiple of 4
+                    f32x4 x = t.acc[i][j];
+                    if (p.add) x += *(const f32x4*)(to + a);
+                    *(f32x4*)(to + a) = x;
+                }
+            } else {
                 const bool in = b < (DX ? rows : p.b_rows);
                 const float g = DX ? (in ? p.grad[b] * p.scale : 0.0f) : grad_unit(ctl->max_g) * p.scale;
                 T* to = (T*)p.out + (size_t)(in ? (DX ? p.row[b] : b) : 0) * p.N;
 #pragma unroll
                 for (int i = 0; i < Tl::MA; ++i) {
-                    const int a = a1 + i * 16;
+                    const int a = a0 + a1 + i * 16;
                     T v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[k] = (T)(t.acc[i][j][k] * (1.0f / P_SCALE<H>) * back * g);
@@ -734,40 +804,43 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_product(const Product p, const C
                             if (a + k < p.N) to[a + k] = v[k];
                     }
                 }
-            } else {
-                float* to = p.part + ((size_t)share * bt * Tl::BB + b) * p.ldo;
-#pragma unroll
-                for (int i = 0; i < Tl::MA; ++i) {
-                    const int a = a1 + i * 16;
-                    if (a >= p.ldo) continue;              // ldo: N up to a multiple of 4
-                    f32x4 x = t.acc[i][j];
-                    if (DX && p.add) x += *(const f32x4*)(to + a);
-                    *(f32x4*)(to + a) = x;
-                }
             }
         }
     }
 }
 
-// The shares' sums to results: a wavefront a row
+// Partial sums to results, in the order of the shares.  Shared-out tiles: grid (tiles of a round, BB * BA /
+// 1024), four columns a thread.
 template <class T, class H, bool DX>
 __global__ __launch_bounds__(256) void k_nll_join(const Product p, const Control* ctl, int BA, int BB, int wgs) {
-    const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int bt = DX ? tiles(ctl->rows, ROW_TILE) * (ROW_TILE / BB) : p.b_tiles;
-    if (r >= (DX ? ctl->rows : p.b_rows)) return;
-    const int S = DX ? dx_split(bt, tiles(p.N, BA), wgs, p.nk) : p.split;
-    if (S == 1 && (!DX || !p.add)) return;               // written by the product itself
+    const int rows = ctl->rows, padded = tiles(rows, ROW_TILE) * ROW_TILE;
+    const int at = tiles(p.N, BA), bt = DX ? padded / BB : p.b_tiles;
+    const Rounds rd = rounds(at * bt, wgs, DX ? p.nk : padded / (int)(STEP / sizeof(H)), true);
+    if ((int)blockIdx.x >= rd.rest) return;
+    int ai, bi;
+    in_groups(rd.whole + blockIdx.x, bt, at, bi, ai);
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4, b = bi * BB + e / BA, a = ai * BA + e % BA;
+    if (b >= (DX ? rows : p.b_rows) || a >= p.N) return;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < rd.shares; ++s)
+        v += *(const f32x4*)(p.part + ((size_t)s * rd.rest + blockIdx.x) * BB * BA + e);
     const float back = 1.0f / held_scale<H>(DX ? ctl->max_w : ctl->max_x);
-    const float g = (DX ? p.grad[r] : grad_unit(ctl->max_g)) * p.scale;
-    T* to = (T*)p.out + (size_t)(DX ? p.row[r] : r) * p.N;
-    const float* from = p.part + (size_t)r * p.ldo;
-    for (int c = lane * 4; c < p.N; c += 256) {
-        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < S; ++s) v += *(const f32x4*)(from + (size_t)s * bt * BB * p.ldo + c);
+    const float g = (DX ? p.grad[b] : grad_unit(ctl->max_g)) * p.scale;
+    T* to = (T*)p.out + (size_t)(DX ? p.row[b] : b) * p.N + a;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (c + k < p.N) to[c + k] = (T)(v[k] * (1.0f / P_SCALE<H>) * back * g);
-    }
+    for (int k = 0; k < 4; ++k)
+        if (a + k < p.N) to[k] = (T)(v[k] * (1.0f / P_SCALE<H>) * back * g);
+}
+
+// dx over several pieces: a wavefront a listed row
+template <class T, class H>
+__global__ __launch_bounds__(256) void k_nll_dx(const Product p, const Control* ctl) {
+    const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (r >= ctl->rows) return;
+    const float back = 1.0f / held_scale<H>(ctl->max_w), g = p.grad[r] * p.scale;
+    T* to = (T*)p.out + (size_t)p.row[r] * p.N;
+    const float* from = p.part + (size_t)r * p.ldo;
+    for (int c = lane; c < p.N; c += 64) to[c] = (T)(from[c] * (1.0f / P_SCALE<H>) * back * g);
 }
 
 // ------------------------------------------------------------------ host
@@ -783,17 +856,17 @@ template <class T, Form FA, Form FB> using Small = Tile<T, FA, FB, 64, 64, 2, 2>
 
 long up(long n, long m) { return (n + m - 1) / m * m; }
 
-// The size whose busiest workgroup is done first: rounds of tiles, times what a step of a tile takes with
-// the CU's workgroups at work (a large tile's as unit).  A contracted axis of nk steps may be shared out.
+// The size whose busiest workgroup is done first: steps of the tiles and shares it takes, times what a step
+// takes with the CU's workgroups at work (a large tile's as unit).
 Size pick(long a, long b, long nk, bool split) {
     constexpr double step[3] = {1.0, 0.6, 0.4};
     Size best = LARGE;
     double least = 1e300;
     for (int s = 0; s < 3; ++s) {
         const long t = up(a, CONFIG[s].tile) / CONFIG[s].tile * (up(b, CONFIG[s].tile) / CONFIG[s].tile);
-        const long shares = split ? dx_split((int)(t < 1 << 20 ? t : 1 << 20), 1, CONFIG[s].wgs, (int)nk) : 1;
-        const double rounds = (double)((t * shares + CONFIG[s].wgs - 1) / CONFIG[s].wgs);
-        const double time = rounds * ((double)nk / shares + 2.0) * step[s];
+        const Rounds r = rounds((int)(t < 1l << 30 ? t : 1l << 30), CONFIG[s].wgs, (int)nk, split);
+        const double whole = (double)((r.whole + CONFIG[s].wgs - 1) / CONFIG[s].wgs);
+        const double time = step[s] * (whole * (nk + 2.0) + (r.rest ? (double)nk / r.shares + 2.0 : 0.0));
         if (time < least) {
             least = time;
             best = (Size)s;
@@ -808,7 +881,7 @@ struct Plan {
     Size scores, dx, dw;
     long rows, padded, ld;       // ld: elements of a padded row of x and W
     long piece, pieces, vpad, ldo;
-    int nk, nk_dx, dw_split;
+    int nk, nk_dx;
     size_t ctl, counts, row, target, lse, grad, x, w, part, score, xg, wh, p, dx_part, dw_part, total;
 };
 
@@ -844,25 +917,23 @@ Plan make_plan(int dtype, int B, int T, int V, int N, bool grad, const void* tab
         p.lse = region(at, p.padded * 4);
         p.grad = region(at, p.padded * 4);
         p.vpad = up(V, 256);
-        // pieces of the vocabulary: p takes at most 1 GB, or one large tile of words
-        const long most = (1024l << 20) / (p.padded * e) / 256 * 256;
+        // pieces of the vocabulary: p takes at most 2 GB, or one large tile of words
+        const long most = (2048l << 20) / (p.padded * e) / 256 * 256;
         p.pieces = most < 256 ? p.vpad / 256 : (p.vpad + most - 1) / most;
         p.piece = up((p.vpad + p.pieces - 1) / p.pieces, 256);
         p.pieces = (V + p.piece - 1) / p.piece;
         p.vpad = p.piece * p.pieces;
         p.ldo = up(N, 4);
         p.nk_dx = (int)(p.piece * e / STEP);
-        const long nk_dw = p.padded * e / STEP;
-        p.dx = pick(N, p.rows, p.nk_dx, true);
-        p.dw = pick(N, p.piece, nk_dw, true);
-        const Config cx = CONFIG[p.dx], cw = CONFIG[p.dw];
-        p.dw_split = dx_split((int)(p.piece / cw.tile), tiles(N, cw.tile), cw.wgs, (int)nk_dw);
+        p.dx = pick(N, p.rows, p.nk_dx, p.pieces == 1);
+        p.dw = pick(N, p.piece, p.padded * e / STEP, true);
         p.xg = region(at, p.padded * p.ld * e);
         p.wh = region(at, e == 2 ? p.vpad * p.ld * e : 0);
         p.p = region(at, p.padded * p.piece * e);
-        const long nt = tiles(N, cx.tile), least = (long)cx.wgs / nt * cx.tile;
-        p.dx_part = region(at, (p.padded > least ? p.padded : least) * p.ldo * 4);
-        p.dw_part = region(at, p.dw_split > 1 ? (size_t)p.dw_split * p.piece * p.ldo * 4 : 0);
+        // shares of the last round's tiles: at most one a workgroup
+        const Config cx = CONFIG[p.dx], cw = CONFIG[p.dw];
+        p.dx_part = region(at, p.pieces > 1 ? p.padded * p.ldo * 4 : (size_t)cx.wgs * cx.tile * cx.tile * 4);
+        p.dw_part = region(at, (size_t)cw.wgs * cw.tile * cw.tile * 4);
     }
     p.w = region(at, p.copy_w ? (size_t)p.vpad * p.ld * e : 0);
     p.total = at;
@@ -891,7 +962,7 @@ Scores gather(const NllArgs& a, const Plan& p, const Listed& list, Layout& l, vo
     hipLaunchKernelGGL(k_nll_list<GRAD>, dim3(blocks), dim3(LIST_THREADS), 0, stream, a, ctl,
                        blocks > 1 ? counts : nullptr, list);
     if (GRAD && sizeof(H) == 2)
-        hipLaunchKernelGGL(k_nll_max<T>, dim3(1024), dim3(256), 0, stream, a, ctl, list.row);
+        hipLaunchKernelGGL(k_nll_max<T>, dim3(2048), dim3(256), 0, stream, a, ctl, list.row);
     l.x = in<T>(ws, p.x);
     l.w = p.copy_w ? in<T>(ws, p.w) : (void*)a.table;
     l.ld = (int)p.ld;
@@ -964,6 +1035,7 @@ hipError_t run_nll_grad(const NllArgs& a, void* ws, hipStream_t stream) {
                 Product d = q;
                 d.A = (const char*)((H*)l.wh + (size_t)v0 * p.ld);
                 d.nk = p.nk_dx;
+                d.pieces = p.pieces > 1;
                 d.add = i > 0;
                 d.last = i + 1 == p.pieces;
                 d.part = in<float>(ws, p.dx_part);
@@ -971,25 +1043,28 @@ hipError_t run_nll_grad(const NllArgs& a, void* ws, hipStream_t stream) {
                 d.grad = list.grad;
                 d.out = a.grad_x;
                 hipLaunchKernelGGL((k_nll_product<T, H, Tl, true>), dim3(wgs), dim3(Tl::NT), 0, stream, d, ctl);
-                if (d.last && (d.add || p.nk_dx >= 16))     // else there is one share, whatever the rows
-                    hipLaunchKernelGGL((k_nll_join<T, H, true>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0,
-                                       stream, d, ctl, Tl::BA, Tl::BB, wgs);
+                if (!d.pieces && p.nk_dx >= 16)             // else no tile is shared out, whatever the rows
+                    hipLaunchKernelGGL((k_nll_join<T, H, true>), dim3(wgs, Tl::BA * Tl::BB / 1024), dim3(256), 0, stream,
+                                       d, ctl, Tl::BA, Tl::BB, wgs);
+                if (d.pieces && d.last)
+                    hipLaunchKernelGGL((k_nll_dx<T, H>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0, stream, d,
+                                       ctl);
             });
         if (a.grad_table)
             with_size<H, COLUMNS, COLUMNS>(p.dw, [&](auto* t) {
                 using Tl = std::remove_pointer_t<decltype(t)>;
+                const int wgs = CONFIG[p.dw].wgs;
                 Product d = q;
                 d.A = (const char*)l.xg;
                 d.b_tiles = ldp / Tl::BB;
                 d.b_rows = words;
-                d.split = p.dw_split;
                 d.part = in<float>(ws, p.dw_part);
                 d.out = (T*)a.grad_table + (size_t)v0 * a.N;
-                hipLaunchKernelGGL((k_nll_product<T, H, Tl, false>), dim3(CONFIG[p.dw].wgs), dim3(Tl::NT), 0, stream, d,
-                                   ctl);
-                if (d.split > 1)
-                    hipLaunchKernelGGL((k_nll_join<T, H, false>), dim3((unsigned)((words + 3) / 4)), dim3(256), 0,
-                                       stream, d, ctl, Tl::BA, Tl::BB, CONFIG[p.dw].wgs);
+                hipLaunchKernelGGL((k_nll_product<T, H, Tl, false>), dim3(wgs), dim3(Tl::NT), 0, stream, d, ctl);
+                const Rounds rd = rounds(tiles(a.N, Tl::BA) * d.b_tiles, wgs, (int)(p.padded * sizeof(H) / STEP), true);
+                if (rd.rest)                                // fewer rows may mean no shares, never more
+                    hipLaunchKernelGGL((k_nll_join<T, H, false>), dim3(rd.rest, Tl::BA * Tl::BB / 1024), dim3(256), 0,
+                                       stream, d, ctl, Tl::BA, Tl::BB, wgs);
             });
     }
     return hipGetLastError();
