@@ -20,6 +20,9 @@ namespace semicrf {
 
 namespace {
 
+// Pieces a lane up to which the weights stay in registers
+constexpr int HOLD = 2;
+
 // Two sums at once
 template <int G>
 __device__ __forceinline__ void row_sums(float& u, float& v, float* red, int& slot) {
@@ -63,20 +66,55 @@ __device__ __forceinline__ At locate(const semicrf_residual& p, unsigned row, un
     return at;
 }
 
-// The five vectors of weights from a column; what is not there is a factor of 1 or a term of 0.
+// V weights from a column as they lie in memory, which takes half the registers in bfloat16; where there
+// are none, a factor of 1 or a term of 0.
+template <class W, int V>
+struct Weights {
+    W t[V];
+    // Called in a loop: keeps the compiler from converting them once and holding the results
+    __device__ __forceinline__ void stay() {
+        constexpr int WORDS = V * sizeof(W) / 4;
+        uint32_t r[WORDS];
+        __builtin_memcpy(r, t, sizeof(r));
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(r[i]));
+        __builtin_memcpy(t, r, sizeof(r));
+    }
+    __device__ __forceinline__ void load(const void* p, int at, int N, float dflt) {
+        const W* w = (const W*)p;
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = (W)dflt;
+        if (!p) return;
+        if (at + V <= N) {
+            __builtin_memcpy(t, w + at, sizeof(t));
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (at + i < N) t[i] = w[at + i];
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const { return (float)t[i]; }
+};
 template <class W, int V>
 struct Params {
-    float w[V], b[V], c[V], p[V], q[V];
+    Weights<W, V> w, b, c, p, q;
+    __device__ __forceinline__ void stay() {
+        w.stay();
+        b.stay();
+        c.stay();
+        p.stay();
+        q.stay();
+    }
     __device__ __forceinline__ void load(const semicrf_residual& a, int at, bool post) {
-        load_weights<W, V>(a.weight, at, a.N, 1.0f, w);
-        load_weights<W, V>(a.bias, at, a.N, 0.0f, b);
-        load_weights<W, V>(a.scale, at, a.N, 1.0f, c);
-        load_weights<W, V>(post ? a.branch_weight : nullptr, at, a.N, 1.0f, p);
-        load_weights<W, V>(post ? a.branch_bias : nullptr, at, a.N, 0.0f, q);
+        w.load(a.weight, at, a.N, 1.0f);
+        b.load(a.bias, at, a.N, 0.0f);
+        c.load(a.scale, at, a.N, 1.0f);
+        p.load(post ? a.branch_weight : nullptr, at, a.N, 1.0f);
+        q.load(post ? a.branch_bias : nullptr, at, a.N, 0.0f);
     }
 };
 
-template <class T, class W, int G, int KP, int NT, int MODE>
+template <class T, class W, int G, int KP, int NT, int MODE, bool POST>
 __global__ __launch_bounds__(NT) void k_residual_norm(const ResArgs a) {
     using Pc = Piece<T, MODE == NARROWER>;
     constexpr int V = Pc::V, RPB = NT / G;
@@ -85,7 +123,7 @@ __global__ __launch_bounds__(NT) void k_residual_norm(const ResArgs a) {
     const semicrf_residual& p = a.p;
     const int N = MODE == EXACT ? G * KP * V : p.N, lane = threadIdx.x % G;
     const unsigned rows = (unsigned)p.B * p.T, step = gridDim.x * RPB;
-    const bool post = p.norm_branch, gated = p.gate;
+    const bool gated = p.gate;
     unsigned row = blockIdx.x * RPB + threadIdx.x / G;
     raw_piece xr[KP], br[KP], gr[KP];
     At at;
@@ -103,8 +141,10 @@ __global__ __launch_bounds__(NT) void k_residual_norm(const ResArgs a) {
 #pragma unroll
     for (int k = 0; k < KP; ++k) xr[k] = br[k] = gr[k] = raw_piece{0, 0, 0, 0};
     fetch(row);
-    Params<W, V> par[KP == 1 ? 1 : KP];
-    if constexpr (KP == 1) par[0].load(p, Pc(lane, N).at, post);
+    Params<W, V> par[KP];
+    if constexpr (KP <= HOLD)
+#pragma unroll
+        for (int k = 0; k < KP; ++k) par[k].load(p, Pc(k * G + lane, N).at, POST);
     for (unsigned r0 = blockIdx.x * RPB; r0 < rows; r0 += step, row += step) {
         const bool now = at.ok, in = row < rows;
         const size_t dense = (size_t)row * N;
@@ -112,14 +152,14 @@ __global__ __launch_bounds__(NT) void k_residual_norm(const ResArgs a) {
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
             const Pc pc(k * G + lane, N);
-            if constexpr (KP > 1) par[k].load(p, pc.at, post);
+            if constexpr (KP > HOLD) par[k].load(p, pc.at, POST);
 #pragma unroll
             for (int i = 0; i < V; ++i) own[k][i] = MODE == EXACT || counted(pc, i, N) ? 1.0f : 0.0f;
             unpack<T>(xr[k], x[k]);
             unpack<T>(br[k], f[k]);
         }
         float mean_o = 0.0f, rstd_o = 0.0f;
-        if (post) {
+        if constexpr (POST) {
             if (p.center) {
                 float s = 0.0f;
 #pragma unroll
@@ -189,8 +229,8 @@ __global__ __launch_bounds__(NT) void k_residual_norm(const ResArgs a) {
 }
 
 // part [workgroup][5][N]: the sums over the workgroup's rows, in the order of grad_params
-template <class T, class W, int G, int KP, int NT, int MODE>
-__global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, float* part) {
+template <class T, class W, int G, int KP, int NT, int MODE, bool POST>
+__global__ __launch_bounds__(NT, KP == 1 && !POST ? 3 : 1) void k_residual_norm_grad(const ResArgs a, float* part) {
     using Pc = Piece<T, MODE == NARROWER>;
     constexpr int V = Pc::V, RPB = NT / G;
     __shared__ float red[4 * (G > 64 ? G / 64 : 1)];
@@ -199,7 +239,7 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
     const semicrf_residual& p = a.p;
     const int N = MODE == EXACT ? G * KP * V : p.N, lane = threadIdx.x % G, sub = threadIdx.x / G;
     const unsigned rows = (unsigned)p.B * p.T, step = gridDim.x * RPB;
-    const bool post = p.norm_branch, gated = p.gate;
+    const bool gated = p.gate;
     const float inv = 1.0f / (float)N, cinv = p.center ? inv : 0.0f;
     unsigned row = blockIdx.x * RPB + sub;
     raw_piece xr[KP], br[KP], gr[KP], dr[KP], dy[KP];
@@ -207,7 +247,13 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
     At at;
     auto fetch = [&](unsigned i) {
         at = locate(p, i, rows, a.status);
-        if (!at.ok) return;
+        if (!at.ok) {                                // a row of zeros adds nothing
+#pragma unroll
+            for (int k = 0; k < KP; ++k) xr[k] = br[k] = gr[k] = dr[k] = dy[k] = raw_piece{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) st[j] = 0.0f;
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
             const Pc pc(k * G + lane, N);
@@ -223,8 +269,10 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
 #pragma unroll
     for (int k = 0; k < KP; ++k) xr[k] = br[k] = gr[k] = dr[k] = dy[k] = raw_piece{0, 0, 0, 0};
     fetch(row);
-    Params<W, V> par[KP == 1 ? 1 : KP];
-    if constexpr (KP == 1) par[0].load(p, Pc(lane, N).at, post);
+    Params<W, V> par[KP];
+    if constexpr (KP <= HOLD)
+#pragma unroll
+        for (int k = 0; k < KP; ++k) par[k].load(p, Pc(k * G + lane, N).at, POST);
     float sum[KP][5][V];
 #pragma unroll
     for (int k = 0; k < KP; ++k)
@@ -234,6 +282,9 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
             for (int i = 0; i < V; ++i) sum[k][j][i] = 0.0f;
     for (unsigned r0 = blockIdx.x * RPB; r0 < rows; r0 += step, row += step) {
         const bool now = at.ok, in = row < rows;
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+            if (KP <= HOLD && !POST) par[k].stay();
         const size_t dense = (size_t)row * N;
         const float mean = st[0], rstd = st[1], mean_o = st[2], rstd_o = st[3];
         // h: x, then r, then its norm; kh: the branch, then its norm; e: dr, then the gradient of r;
@@ -243,7 +294,7 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
             const Pc pc(k * G + lane, N);
-            if constexpr (KP > 1) par[k].load(p, pc.at, post);
+            if constexpr (KP > HOLD) par[k].load(p, pc.at, POST);
             unpack<T>(xr[k], h[k]);
             unpack<T>(br[k], kh[k]);
             unpack<T>(dr[k], e[k]);
@@ -255,13 +306,11 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
                 sg[k][i] = 1.0f;
                 qg[k][i] = 0.0f;
                 if (gated) sigmoids(z[i], sg[k][i], qg[k][i]);
-                if (post) kh[k][i] = (kh[k][i] - mean_o) * rstd_o;
-                const float f = post ? fmaf(kh[k][i], par[k].p[i], par[k].q[i]) : kh[k][i];
+                if (POST) kh[k][i] = (kh[k][i] - mean_o) * rstd_o;
+                const float f = POST ? fmaf(kh[k][i], par[k].p[i], par[k].q[i]) : kh[k][i];
                 h[k][i] = (fmaf(par[k].c[i] * sg[k][i], f, h[k][i]) - mean) * rstd;
-                if (now) {
-                    sum[k][0][i] = fmaf(g[k][i], h[k][i], sum[k][0][i]);
-                    sum[k][1][i] += g[k][i];
-                }
+                sum[k][0][i] = fmaf(g[k][i], h[k][i], sum[k][0][i]);
+                sum[k][1][i] += g[k][i];
                 g[k][i] *= par[k].w[i];
                 const float t = MODE == EXACT || counted(pc, i, N) ? g[k][i] : 0.0f;
                 s0 += t;
@@ -279,17 +328,16 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
             float dz[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                e[k][i] = now ? fmaf(rstd, g[k][i] - s0 - h[k][i] * s1, e[k][i]) : 0.0f;
-                const float f = post ? fmaf(kh[k][i], par[k].p[i], par[k].q[i]) : kh[k][i];
+                e[k][i] = fmaf(rstd, g[k][i] - s0 - h[k][i] * s1, e[k][i]);
+                const float f = POST ? fmaf(kh[k][i], par[k].p[i], par[k].q[i]) : kh[k][i];
                 const float es = e[k][i] * sg[k][i], d = es * par[k].c[i];
                 dz[i] = now ? d * f * qg[k][i] : 0.0f;
-                if (now) sum[k][2][i] = fmaf(es, f, sum[k][2][i]);
+                sum[k][2][i] = fmaf(es, f, sum[k][2][i]);
+                e[k][i] = now ? e[k][i] : 0.0f;      // weights that are not finite stay out of padding
                 g[k][i] = d;
-                if (post) {
-                    if (now) {
-                        sum[k][3][i] = fmaf(d, kh[k][i], sum[k][3][i]);
-                        sum[k][4][i] += d;
-                    }
+                if constexpr (POST) {
+                    sum[k][3][i] = fmaf(d, kh[k][i], sum[k][3][i]);
+                    sum[k][4][i] += d;
                     g[k][i] = d * par[k].p[i];
                     const float t = MODE == EXACT || counted(pc, i, N) ? g[k][i] : 0.0f;
                     t0 += t;
@@ -301,7 +349,7 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
                 if (gated) store_piece<T>((T*)a.grad_gate + dense, pc, N, dz);
             }
         }
-        if (post) {
+        if constexpr (POST) {
             row_sums<G>(t0, t1, red, slot);
             t0 *= cinv;
             t1 *= inv;
@@ -309,9 +357,11 @@ __global__ __launch_bounds__(NT) void k_residual_norm_grad(const ResArgs a, floa
         if (!in) continue;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            if (post)
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[k][i] = now ? rstd_o * (g[k][i] - t0 - kh[k][i] * t1) : 0.0f;
+            for (int i = 0; i < V; ++i) {
+                if (POST) g[k][i] = rstd_o * (g[k][i] - t0 - kh[k][i] * t1);
+                g[k][i] = now ? g[k][i] : 0.0f;
+            }
             store_piece<T>((T*)a.grad_branch + dense, Pc(k * G + lane, N), N, g[k]);
         }
     }
@@ -384,13 +434,19 @@ RowShape row_shape(int N, int V) {
 }
 constexpr int row_threads(int G) { return G > 64 ? G : 256; }
 
-// Workgroups of NT threads for the rows: at most as many as make `waves` wavefronts a SIMD.
-int row_wgs(long rows, int G, int waves) {
+// Workgroups of NT threads for the rows: at most as many as make `per_simd` wavefronts a SIMD.
+int row_wgs(long rows, int G, int per_simd) {
     const int NT = row_threads(G);
-    const long need = (rows + NT / G - 1) / (NT / G), most = 1024l * waves / (NT / 64);
+    const long need = (rows + NT / G - 1) / (NT / G), most = 1024l * per_simd / (NT / 64);
     return (int)(need < most ? need : most);
 }
-constexpr int WAVES = 8, GRAD_WAVES = 4;
+// As many wavefronts a SIMD as the kernels' registers leave room for: more workgroups than run at once make a
+// second, short round, and in the gradient more partial rows (25,600 ragged rows of 1,024 bfloat16, everything
+// there: 105 us and 19 for the partials' sum at 4, 97 and 8 at 2; 400,000 of 512 without a norm of the
+// branch: 705 and 9 at 4, 645 and 6 at 3).
+template <class T>
+constexpr int waves(bool norm_branch) { return sizeof(T) == 4 ? (norm_branch ? 6 : 8) : norm_branch ? 4 : 5; }
+constexpr int GRAD_WAVES = 2, GRAD_WAVES_PLAIN = 3;
 
 template <int V, class F>
 hipError_t with_row_shape(int N, F&& f) {
@@ -417,9 +473,13 @@ template <class T, class W>
 hipError_t run_residual(const ResArgs& a, hipStream_t stream) {
     return with_row_shape<16 / (int)sizeof(T)>(a.p.N, [&](auto g, auto kp, auto mode) {
         constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = row_threads(G);
-        const int nwg = row_wgs((long)a.p.B * a.p.T, G, WAVES);
-        hipLaunchKernelGGL((k_residual_norm<T, W, G, KP, NT, decltype(mode)::value>), dim3(nwg), dim3(NT), 0, stream,
-                           a);
+        const int nwg = row_wgs((long)a.p.B * a.p.T, G, waves<T>(a.p.norm_branch));
+        if (a.p.norm_branch)
+            hipLaunchKernelGGL((k_residual_norm<T, W, G, KP, NT, decltype(mode)::value, true>), dim3(nwg), dim3(NT), 0,
+                               stream, a);
+        else
+            hipLaunchKernelGGL((k_residual_norm<T, W, G, KP, NT, decltype(mode)::value, false>), dim3(nwg), dim3(NT), 0,
+                               stream, a);
         return hipGetLastError();
     });
 }
@@ -428,9 +488,13 @@ template <class T, class W>
 hipError_t run_residual_grad(const ResArgs& a, float* part, hipStream_t stream) {
     return with_row_shape<16 / (int)sizeof(T)>(a.p.N, [&](auto g, auto kp, auto mode) {
         constexpr int G = decltype(g)::value, KP = decltype(kp)::value, NT = row_threads(G);
-        const int nwg = row_wgs((long)a.p.B * a.p.T, G, GRAD_WAVES);
-        hipLaunchKernelGGL((k_residual_norm_grad<T, W, G, KP, NT, decltype(mode)::value>), dim3(nwg), dim3(NT), 0,
-                           stream, a, part);
+        const int nwg = row_wgs((long)a.p.B * a.p.T, G, a.p.norm_branch ? GRAD_WAVES : GRAD_WAVES_PLAIN);
+        if (a.p.norm_branch)
+            hipLaunchKernelGGL((k_residual_norm_grad<T, W, G, KP, NT, decltype(mode)::value, true>), dim3(nwg), dim3(NT),
+                               0, stream, a, part);
+        else
+            hipLaunchKernelGGL((k_residual_norm_grad<T, W, G, KP, NT, decltype(mode)::value, false>), dim3(nwg),
+                               dim3(NT), 0, stream, a, part);
         if (a.grad_params)
             hipLaunchKernelGGL((k_residual_partials<W>), dim3((5 * a.p.N + 15) / 16), dim3(256), 0, stream, part, nwg,
                                a.p.N, (W*)a.grad_params);
@@ -447,7 +511,7 @@ hipError_t launch_residual_norm(const ResArgs& a, hipStream_t stream) {
 
 size_t residual_norm_grad_bytes(int B, int T, int N, int dtype) {
     const RowShape s = row_shape(N, dtype == SEMICRF_F32 ? 4 : 8);
-    return (size_t)row_wgs((long)B * T, s.G, GRAD_WAVES) * 5 * N * sizeof(float);
+    return (size_t)row_wgs((long)B * T, s.G, GRAD_WAVES_PLAIN) * 5 * N * sizeof(float);
 }
 
 hipError_t launch_residual_norm_grad(const ResArgs& a, void* ws, hipStream_t stream) {
