@@ -30,6 +30,13 @@ __all__ = ["gated_recurrence", "gated_recurrence_grad", "gated_recurrence_step",
 
 def _view(name, x, like, dev):
     """Refuses what is not a tensor like another with a dense last axis; its strides but the last."""
+    try:
+        if x.dtype is like.dtype and x.shape == like.shape and x.get_device() == dev:
+            s = x.stride()
+            if s[-1] == 1 or x.shape[-1] == 1:
+                return _native.Strides2(s[0], s[1] if len(s) == 3 else 0)
+    except AttributeError:
+        pass
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if x.get_device() != dev:
@@ -38,10 +45,7 @@ def _view(name, x, like, dev):
         raise TypeError(f"{name} must be {like.dtype}, got {x.dtype}")
     if x.shape != like.shape:
         raise ValueError(f"{name} must be {list(like.shape)}, got {list(x.shape)}")
-    s = x.stride()
-    if s[-1] != 1 and x.shape[-1] != 1:
-        raise ValueError(f"the last axis of {name} must be dense")
-    return _native.Strides2(s[0], s[1] if len(s) == 3 else 0)
+    raise ValueError(f"the last axis of {name} must be dense")
 
 
 # ---------------------------------------------------------------- gated recurrence
@@ -53,14 +57,14 @@ def _recurrence(x, decay_gate, input_gate, log_decay, lengths, state, pool, dims
     if x.dim() != dims:
         raise ValueError(f"x must be {'[B, T, N]' if dims == 3 else '[B, N]'}, got {list(x.shape)}")
     B, N = x.shape[0], x.shape[-1]
-    strides = [_view(n, t, x, dev) for n, t in (("x", x), ("decay_gate", decay_gate),
-                                                ("input_gate", input_gate))]
+    sx, sr, si = (_view("x", x, x, dev), _view("decay_gate", decay_gate, x, dev),
+                  _view("input_gate", input_gate, x, dev))
     _need("log_decay", log_decay, torch.float32, (N,), dev)
     _lengths(lengths, B, dev)
     if state is not None:
         _need("state", state, torch.float32, (B if pool is None else pool, N), dev)
     return dev, _native.Recurrence(
-        x.data_ptr(), decay_gate.data_ptr(), input_gate.data_ptr(), *strides, _ptr(lengths),
+        x.data_ptr(), decay_gate.data_ptr(), input_gate.data_ptr(), sx, sr, si, _ptr(lengths),
         log_decay.data_ptr(), _ptr(state), _TYPES[x.dtype], B, x.shape[1] if dims == 3 else 1, N)
 
 
@@ -190,17 +194,17 @@ def _residual(x, branch, weight, bias, gate, scale, norm_branch, branch_weight, 
     B, T, N = x.shape
     sb = _view("branch", branch, x, dev)
     sg = _native.Strides2(0, 0) if gate is None else _view("gate", gate, x, dev)
-    wtype = x.dtype
-    params = {"scale": scale, "weight": weight, "bias": bias, "branch_weight": branch_weight,
-              "branch_bias": branch_bias}
-    first = next((p for p in params.values() if p is not None), None)
-    if first is not None:
-        wtype = first.dtype
-        if wtype is not x.dtype and wtype is not torch.float32:
-            raise TypeError(f"weights must be {x.dtype} or float32, got {wtype}")
-    for name, p in params.items():
-        if p is not None:
-            _need(name, p, wtype, (N,), dev)
+    wtype, size = None, (N,)
+    for name, p in (("scale", scale), ("weight", weight), ("bias", bias),
+                    ("branch_weight", branch_weight), ("branch_bias", branch_bias)):
+        if p is None:
+            continue
+        if wtype is None:
+            wtype = getattr(p, "dtype", None)
+            if wtype is not x.dtype and wtype is not torch.float32:
+                raise TypeError(f"weights must be {x.dtype} or float32, got {wtype}")
+        _need(name, p, wtype, size, dev)
+    wtype = wtype or x.dtype
     _lengths(lengths, B, dev)
     return dev, _native.Residual(
         x.data_ptr(), branch.data_ptr(), _ptr(gate), sb, sg, _ptr(scale), _ptr(weight), _ptr(bias),
@@ -271,7 +275,7 @@ def _residual_grad(dev, a, wtype, grad_r, grad_y, x, gate, stats, want_params, w
         out["grad_gate"] = gg
     if want_params:
         names = ("weight", "bias", "scale") + (("branch_weight", "branch_bias") if a.norm_branch else ())
-        out.update({"grad_" + k: params[i] for i, k in enumerate(names)})
+        out.update(("grad_" + k, p) for k, p in zip(names, params.unbind(0)))
     return out
 
 
@@ -298,7 +302,6 @@ class _ResidualNorm(torch.autograd.Function):
             return (None,) * 13
 
         def grads():
-            # bias only says here that the weights' type may be its own
             dev, a, wtype = _residual(x, branch, weight, bias, gate, scale, ctx.norm_branch,
                                       branch_weight, branch_bias, ctx.center, 0.0, lengths)
             d = _residual_grad(dev, a, wtype, None if g_r is None else g_r.contiguous(),
