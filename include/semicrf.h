@@ -387,12 +387,14 @@ int semicrf_decay_attention_step(const semicrf_attention* attention, const int32
 
 /* ------------------------------------------------------------------ blocks and pretraining
  * What an encoder block needs beside attention, and what it is trained on before there are
- * segments.  Conventions as for the encoder operators. */
+ * segments.  Conventions as for the encoder operators.  A workspace serves one call at a time: calls,
+ * and replays of captured calls, that may overlap need one each. */
 
 /* Gated linear recurrence, a decay of its own for each position and channel:
  *   s_t = log_decay[n] sig(r_t),  a_t = exp(s_t),  h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sig(i_t) x_t,
  * sig(z) = 1 / (1 + exp(-z)), r the decay gate and i the input gate before their sigmoid, h_0 = `state`
- * or 0.  log_decay [N] is meant to be finite and <= 0: above 0, 1 - a^2 is negative and outputs are NaN. */
+ * or 0.  log_decay [N] is meant to be finite and <= 0: above 0, 1 - a^2 is negative and outputs are NaN.
+ * A value that is not finite spoils its channel from its position on, and no other. */
 typedef struct semicrf_recurrence {
     const void* x;               /* [B, T, N], as decay_gate and input_gate */
     const void* decay_gate;
@@ -404,7 +406,7 @@ typedef struct semicrf_recurrence {
     const float* log_decay;      /* [N] */
     const float* state;          /* [B, N] before the first position, or NULL for 0 */
     int dtype;                   /* of x, the gates and the outputs shaped like them */
-    int B, T, N;                 /* B < 2^16, N <= 2^20 */
+    int B, T, N;                 /* B < 2^16, N <= 2^20, B * (N / 64, rounded up) < 2^22 */
 } semicrf_recurrence;
 
 /* Whole sequences.  out [B, T, N] dense, 0 at padding; state_out [B, N] float32 after position
@@ -484,7 +486,8 @@ int semicrf_residual_norm_grad(const semicrf_residual* residual, const float* st
  * (target_bits 32 or 64), loss [B, T] float32.  A negative target marks a position with nothing to
  * predict: its x is not read and its loss is 0.  A target of V or more gives NaN and the status bit.
  * lse [B, T] float32, or NULL: the log sum, for the gradient (0 where there is nothing to predict).
- * The scores are formed in pieces and never kept.  B * T and V up to 2^22, N <= 32768.  Workspace:
+ * The scores are formed in pieces and never kept; the gradient holds up to 2 GB of what it makes of
+ * them in its workspace.  B * T and V up to 2^22, N <= 32768, (B * T + V) * N below 2^36.  Workspace:
  * semicrf_token_nll_bytes(..., 0), 256-byte aligned. */
 size_t semicrf_token_nll_bytes(int dtype, int B, int T, int V, int N, int grad);
 int semicrf_token_nll(const void* x, const void* table, int dtype, const void* targets,

@@ -149,11 +149,13 @@ __device__ __forceinline__ unsigned long long peek(const unsigned long long* p) 
 }
 
 // The next n <= U words of each lane, once all of them are there.  The wait ends: what is waited for
-// is held by a workgroup that waits for earlier tiles only.
+// is held by a workgroup that waits for earlier tiles only.  Should another call write to the same
+// workspace meanwhile, it ends all the same, after a second or so, and the outputs are NaN.
+constexpr int PATIENCE = 1 << 20;
 template <int U>
 __device__ __forceinline__ void await(const unsigned long long* p, size_t stride, int n,
                                       unsigned long long (&v)[U]) {
-    for (;;) {
+    for (int i = 0; i < PATIENCE; ++i) {
         bool missing = false;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -163,6 +165,9 @@ __device__ __forceinline__ void await(const unsigned long long* p, size_t stride
         if (!__any(missing)) return;
         __builtin_amdgcn_s_sleep(1);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (v[u] == EMPTY) v[u] = pack(Map{__builtin_nanf(""), __builtin_nanf("")});
 }
 
 // What a workgroup shares while it joins its spans and finds the state it starts from
@@ -176,8 +181,8 @@ struct Shared {
 };
 
 // The state before each span of tile k of chain `seq`, into sh.start: `order` is the wavefront's place in
-// part, `first` the state before tile 0 at a channel.  A lane takes whole channels here.  Call after a
-// barrier that follows the writes of part.
+// part, `first` the state before tile 0 at a channel.  A lane takes whole channels here.  Waits for all
+// wavefronts' writes of part.
 template <int CW, int W, class F>
 __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, long seq, int k, bool last, int order,
                                             F&& first) {
@@ -185,14 +190,17 @@ __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, 
     const int lane = threadIdx.x & 63;
     const int g = k / GROUP, j = k - g * GROUP;
     float h[PER];
+    // The first state is read before the barrier, and so before anything is published: the chain's last
+    // wavefront may overwrite it after that.
 #pragma unroll
-    for (int i = 0; i < PER; ++i) h[i] = g == 0 && lane + i * 64 < CW ? first(lane + i * 64) : 0.0f;
+    for (int i = 0; i < PER; ++i) {
+        h[i] = g == 0 && lane + i * 64 < CW ? first(lane + i * 64) : 0.0f;
+        asm volatile("" : "+v"(h[i]));
+    }
+    __syncthreads();
     if (W > 1 && ch.tickets) {                         // one span: one tile
         unsigned long long* words = ch.words + (size_t)seq * ch.tiles * CW;
         unsigned long long* states = ch.states + (size_t)seq * ch.groups * CW;
-        // the first state is read before anything is published: the last tile may overwrite it after that
-#pragma unroll
-        for (int i = 0; i < PER; ++i) asm volatile("" : "+v"(h[i]));
         Map own[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -366,7 +374,6 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 4) void k_recurrence(const Rec
             join_rows<false>(Map{expm1_neg(sum[c]), H[c]}, before[c], all);
             if (q == 0) sh.part[wave][l * CH + c] = all;
         }
-        __syncthreads();
         find_starts(ch, sh, seq, k, k == o.last, wave, [&](int c) {
             const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
             return p.state ? p.state[(size_t)o.b * p.N + at] : 0.0f;
@@ -520,7 +527,6 @@ __global__ __launch_bounds__(64 * W, 2) void k_recurrence_grad(const RecArgs a, 
             join_rows<true>(Map{M[c], F[c]}, before[c], all);
             if (q == 0) sh.part[W - 1 - wave][l * CH + c] = all;
         }
-        __syncthreads();
         find_starts(ch, sh, seq, k, k == o.last, W - 1 - wave, [&](int c) {
             const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
             return a.grad_state_out ? a.grad_state_out[(size_t)o.b * p.N + at] : 0.0f;

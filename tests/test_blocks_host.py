@@ -67,6 +67,11 @@ def test_recurrence_refusals(native):
         assert fwd(recurrence(native, **kw)) == bwd(recurrence(native, **kw)) == want, kw
         if not any(k in kw for k in ("x", "decay_gate", "input_gate", "log_decay")):
             assert size(recurrence(native, **kw), 0) == size(recurrence(native, **kw), 1) == 0
+    for kw in ({"B": 65535, "N": 64 * 65}, {"x_stride": native.Strides2(0, 1 << 25)},
+               {"input_stride": native.Strides2(0, -1)}):
+        assert fwd(recurrence(native, **kw)) == bwd(recurrence(native, **kw)) == UNSUPPORTED, kw
+        assert size(recurrence(native, **kw), 0) == 0
+    assert size(recurrence(native, T=1, x_stride=native.Strides2(0, 1 << 40)), 0) > 0
     a = recurrence(native)
     assert fwd(a, out=N0) == fwd(N0) == bwd(N0) == INVALID
     assert fwd(a, ws=N0) == fwd(a, n=need - 1) == fwd(a, ws=ctypes.c_void_p(0x1008)) == WORKSPACE
@@ -125,7 +130,8 @@ def test_token_nll_refusals(native):
     assert 0 < need < grad
     assert size(1, 2, 3000, 50, 16, 1) > grad and size(0, 2, 3, 50, 16, 0) > 0
     for bad in ((2, 2, 3, 50, 16), (1, 0, 3, 50, 16), (1, 2, 3, 0, 16), (1, 2, 3, 50, 0), (1, 2, 3, 50, 32769),
-                (1, 2, 3, (1 << 22) + 1, 16), (1, 1 << 11, (1 << 11) + 1, 50, 16)):
+                (1, 2, 3, (1 << 22) + 1, 16), (1, 1 << 11, (1 << 11) + 1, 50, 16),
+                (1, 1 << 11, 1 << 11, 1 << 22, 8192)):
         assert size(*bad, 0) == size(*bad, 1) == 0, bad
 
     def fwd(x=P, w=P, dtype=1, t=P, bits=32, B=2, T=3, V=50, N=16, scale=1.0, ws=P, n=need, loss=P):

@@ -199,6 +199,48 @@ def test_recurrence_carries_on(crf):  # noqa: F811
     near(second, h[:, 333:], eh[:, 333:], "f32", "second")
 
 
+@pytest.mark.parametrize("T", [1, 16, 17, 100, 128, 129, 900, 3000])
+def test_recurrence_state_in_place(crf, T):  # noqa: F811
+    """The final state may be written over the initial one, whatever the number of tiles."""
+    import torch
+    from semi_markov_crf_amd import _native, blocks
+    torch.manual_seed(T)
+    B, N = 3, 200
+    x, r, i = (torch.randn(B, T, N, device="cuda") for _ in range(3))
+    ld, state = dev(decays(N, "weak")), torch.randn(B, N, device="cuda")
+    want, end = crf.gated_recurrence(x, r, i, ld, state=state, want_state=True)
+    dev_index, a = blocks._recurrence(x, r, i, ld, None, state, None, 3)
+    n = _native.load().semicrf_gated_recurrence_bytes(a, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(x)
+    rc = _native.call(dev_index, "semicrf_gated_recurrence", a, torch.cuda.current_stream().cuda_stream, ws.data_ptr(),
+                      n, out.data_ptr(), state.data_ptr(), None, None)
+    torch.cuda.synchronize()
+    assert rc == 0 and torch.equal(out, want) and torch.equal(state, end)
+
+
+def test_recurrence_broadcast_inputs(crf):  # noqa: F811
+    """Gates that are one row for all positions or one sequence for all: views with strides of 0, whose
+    gradients autograd adds up."""
+    import torch
+    torch.manual_seed(2)
+    B, T, N = 3, 150, 36
+    x = torch.randn(B, T, N, device="cuda", requires_grad=True)
+    r = torch.randn(1, 1, N, device="cuda", requires_grad=True)
+    i = torch.randn(1, T, N, device="cuda", requires_grad=True)
+    ld, g = dev(decays(N, "spread")), torch.randn(B, T, N, device="cuda")
+    views = [x, r.expand(B, T, N), i.expand(B, T, N)]
+    h = crf.gated_recurrence(*views, ld)
+    full = [v.detach().contiguous().requires_grad_() for v in views]
+    want = crf.gated_recurrence(*full, ld)
+    assert torch.equal(h, want)
+    d, e = torch.autograd.grad(h, [x, r, i], g), torch.autograd.grad(want, full, g)
+    assert torch.equal(d[0], e[0])
+    # sums of 450 and 3 rows by torch, in an order of its own
+    assert torch.allclose(d[1], e[1].sum((0, 1), keepdim=True), atol=1e-4)
+    assert torch.allclose(d[2], e[2].sum(0, keepdim=True), atol=1e-5)
+
+
 STEP = [(1, 1, 1, "f32"), (1, 3, 1024, "bf16"), (7, 9, 39, "f32"), (64, 64, 130, "bf16"), (300, 301, 257, "f32")]
 
 
@@ -258,6 +300,8 @@ RESIDUAL = [  # B, T, N, typ, wtyp, lengths, gate, scale, norm_branch, center
     (2, 9, 2048, "bf16", "f32", "ragged", True, True, True, True),
     (1, 5, 4100, "bf16", "bf16", "full", True, True, True, True),
     (1, 6, 8192, "f32", "f32", "full", True, True, True, True),
+    (1, 3, 16384, "bf16", "f32", "full", True, True, True, True),
+    (1, 3, 16381, "f32", "f32", "full", False, True, True, False),
     (700, 3, 20, "bf16", "bf16", "ragged", True, True, True, True),       # more rows than one pass takes
     (1, 5000, 72, "f32", "f32", "full", True, False, True, False),
 ]
@@ -685,6 +729,8 @@ def test_refusals(crf):  # noqa: F811
         crf.residual_norm(x, x, eps=-1.0)
     with pytest.raises(crf.SemiCRFError):
         crf.token_nll(x, x[0], t, scale=float("inf"))
+    far = torch.zeros(2, device="cuda").as_strided((1, 1, 2), (2, 2, 1)).as_strided((1, 2, 1), (1, 1, 1))
+    assert crf.gated_recurrence(far, far, far, ld[:1].contiguous()).shape == (1, 2, 1)
     wide = torch.zeros(1, 1, 16385, device="cuda")
     with pytest.raises(crf.SemiCRFError):
         crf.residual_norm(wide, wide)
