@@ -20,22 +20,29 @@ namespace {
 constexpr int SPAN = SEMICRF_RECURRENCE_SPAN;
 
 // expm1 for s <= 0, and exp(s).  Below -1/4 the difference costs at most two bits; above, five terms
-// of the series leave s^6 / 5040 < 2^-24.  WEAK: s is above -1/4.
+// of the series leave s^6 / 5040 < 2^-24.  WEAK: s is known to be -1/4 or more.
+template <bool WEAK = false>
 __device__ __forceinline__ float expm1_neg(float s, float& e) {
     float p = fmaf(s, 1.0f / 720.0f, 1.0f / 120.0f);
     p = fmaf(s, p, 1.0f / 24.0f);
     p = fmaf(s, p, 1.0f / 6.0f);
     p = fmaf(s, p, 0.5f);
     p = fmaf(s * s, p, s);
-    e = fast_exp2(s * LOG2EF);
-    return s > -0.25f ? p : e - 1.0f;
+    e = WEAK ? 1.0f + p : fast_exp2(s * LOG2EF);
+    return WEAK || s > -0.25f ? p : e - 1.0f;
 }
+template <bool WEAK = false>
 __device__ __forceinline__ float expm1_neg(float s) {
     float e;
-    return expm1_neg(s, e);
+    return expm1_neg<WEAK>(s, e);
 }
 
 __device__ __forceinline__ float root(float x) { return __builtin_amdgcn_sqrtf(x); }
+
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
 
 template <class T>
 __device__ __forceinline__ const T* row(const void* p, const int64_t (&stride)[2], int b, int t) {
@@ -43,36 +50,56 @@ __device__ __forceinline__ const T* row(const void* p, const int64_t (&stride)[2
 }
 
 // ------------------------------------------------------------------ elements of a lane
-// A wavefront takes a span of 16 positions of 16 CH channels: lane 16 q + l holds CH neighbouring
-// channels at positions 4 q .. 4 q + 3.  Where N is no multiple of CH the last lanes start early, at
+// A wavefront takes a span of 16 positions of 32 CH channels: lane 32 q + l holds CH neighbouring
+// channels at positions 8 q .. 8 q + 7.  Where N is no multiple of CH the last lanes start early, at
 // N - CH, and compute channels that a neighbour has too.
-constexpr int POS = 4, LANES = 16;
+constexpr int POS = 8, LANES = 32;
 
+// As loaded, two bfloat16 to a register
 template <class T, int CH>
 struct Raw {
-    T v[CH];
+    unsigned w[(CH * sizeof(T) + 3) / 4];
+    __device__ __forceinline__ float operator[](int c) const {
+        if (sizeof(T) == 4) return __uint_as_float(w[c]);
+        return __uint_as_float(c % 2 ? w[c / 2] & 0xffff0000u : w[c / 2] << 16);
+    }
+    __device__ __forceinline__ void fill(unsigned bits) {
+#pragma unroll
+        for (unsigned& v : w) v = bits;
+    }
 };
 template <class T, int CH>
 __device__ __forceinline__ Raw<T, CH> load(const T* base, unsigned at) {
-    Raw<T, CH> r;
-    __builtin_memcpy(&r, (const char*)base + at * (unsigned)sizeof(T), sizeof(r));
+    Raw<T, CH> r{};
+    __builtin_memcpy(r.w, (const char*)base + at * (unsigned)sizeof(T), CH * sizeof(T));
     return r;
+}
+// True where no channel of the wavefront decays by more than 1/4 a position
+template <int CH>
+__device__ __forceinline__ bool all_weak(const Raw<float, CH>& lam) {
+    bool strong = false;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) strong |= lam[c] < -0.25f;
+    return !__any(strong);
 }
 // Positions past the length: a gate that is closed for good keeps the state, whatever else is there
 template <class T, int CH>
-__device__ __forceinline__ void close(Raw<T, CH> (&r)[POS], int first, int count) {
+__device__ __forceinline__ void close(Raw<T, CH> (&x)[POS], Raw<T, CH> (&r)[POS], Raw<T, CH> (&g)[POS], int first,
+                                      int count) {
 #pragma unroll
     for (int i = 0; i < POS; ++i)
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-            if (first + i >= count) r[i].v[c] = (T)-__builtin_inff();
+        if (first + i >= count) {
+            r[i].fill(sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u);      // -infinity
+            x[i].fill(0);
+            g[i].fill(0);
+        }
 }
 template <class T, int CH>
 __device__ __forceinline__ void store(T* base, unsigned at, const float (&x)[CH]) {
-    Raw<T, CH> r;
+    T r[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) r.v[c] = (T)x[c];
-    __builtin_memcpy((char*)base + at * (unsigned)sizeof(T), &r, sizeof(r));
+    for (int c = 0; c < CH; ++c) r[c] = (T)x[c];
+    __builtin_memcpy((char*)base + at * (unsigned)sizeof(T), r, sizeof(r));
 }
 
 // ------------------------------------------------------------------ joins
@@ -86,36 +113,25 @@ __device__ __forceinline__ Map then(Map a, Map b) {          // a first
 }
 __device__ __forceinline__ float apply(Map a, float h) { return h + fmaf(a.M, h, a.H); }
 
-// Of the four rows of 16 lanes: each pair's even one (or odd one), the lower half's value (or the upper)
-template <int ODD>
-__device__ __forceinline__ float of_pair(float v) {
-    const int i = __builtin_bit_cast(int, v);
-    return __builtin_bit_cast(float, (int)__builtin_amdgcn_permlane16_swap(i, i, false, false)[ODD]);
-}
+// The lower half's value, or the upper's
 template <int UPPER>
 __device__ __forceinline__ float of_half(float v) {
     const int i = __builtin_bit_cast(int, v);
     return __builtin_bit_cast(float, (int)__builtin_amdgcn_permlane32_swap(i, i, false, false)[UPPER]);
 }
 
-// Maps of the four rows, in order of position (REVERSED: from the last): what comes before the lane's
-// row, and all four.
+// Maps of the two halves, in order of position (REVERSED: from the last): what comes before the lane's
+// half, and both.
 template <bool REVERSED>
-__device__ __forceinline__ void join_rows(Map own, Map& before, Map& all) {
-    constexpr int FIRST = REVERSED ? 1 : 0;
-    const int q = (threadIdx.x & 63) / LANES;
-    const bool second = (q & 1) != FIRST, later = (q >> 1) != FIRST;
-    const Map first{of_pair<FIRST>(own.M), of_pair<FIRST>(own.H)};
-    const Map pair = then(first, Map{of_pair<!FIRST>(own.M), of_pair<!FIRST>(own.H)});
-    const Map half{of_half<FIRST>(pair.M), of_half<FIRST>(pair.H)};
-    all = then(half, Map{of_half<!FIRST>(pair.M), of_half<!FIRST>(pair.H)});
-    const Map m{second ? first.M : 0.0f, second ? first.H : 0.0f};
-    const Map n = then(half, m);
-    before = Map{later ? n.M : m.M, later ? n.H : m.H};
+__device__ __forceinline__ void join_halves(Map own, Map& before, Map& all) {
+    const bool later = ((threadIdx.x & 63) / LANES) != REVERSED;
+    const Map first{of_half<REVERSED>(own.M), of_half<REVERSED>(own.H)};
+    all = then(first, Map{of_half<!REVERSED>(own.M), of_half<!REVERSED>(own.H)});
+    before = Map{later ? first.M : 0.0f, later ? first.H : 0.0f};
 }
 
 // ------------------------------------------------------------------ tiles in order
-// A tile is W spans, a span a wavefront; a chain is the tiles of 16 CH channels of a sequence.  Every tile
+// A tile is W spans, a span a wavefront; a chain is the tiles of 32 CH channels of a sequence.  Every tile
 // finds its map by itself and then needs the state it starts from.  A workgroup serves one chain and takes
 // its tiles in order by a ticket, so that whoever waits waits for tiles that are at work already or done.
 // (One ticket for all chains costs 24 ns a tile, on one after another: more than the tile's bytes.)
@@ -155,6 +171,7 @@ constexpr int PATIENCE = 1 << 20;
 template <int U>
 __device__ __forceinline__ void await(const unsigned long long* p, size_t stride, int n,
                                       unsigned long long (&v)[U]) {
+#pragma unroll 1
     for (int i = 0; i < PATIENCE; ++i) {
         bool missing = false;
 #pragma unroll
@@ -187,7 +204,8 @@ template <int CW, int W, class F>
 __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, long seq, int k, bool last, int order,
                                             F&& first) {
     constexpr int U = (GROUP + W - 1) / W, PER = (CW + 63) / 64;
-    const int lane = threadIdx.x & 63;
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));                      // addresses are made anew
     const int g = k / GROUP, j = k - g * GROUP;
     float h[PER];
     // The first state is read before the barrier, and so before anything is published: the chain's last
@@ -265,144 +283,149 @@ __global__ __launch_bounds__(256) void k_recurrence_clear(unsigned long long* p,
     for (size_t i = at; i < m; i += step) tickets[i] = 0;
 }
 
-// The workgroup's tiles, one after another.  The next ticket is drawn while a tile is worked on.
-// work(chain, tile, pass) calls pass() before its last barrier.
-template <class F>
-__device__ __forceinline__ void each_tile(const Chain& ch, unsigned& slot, F&& work) {
-    const unsigned seq = blockIdx.x % ch.chains;
-    unsigned* ticket = ch.tickets + (size_t)seq * TICKET;
-    int k = 0;
-    if (ch.tickets) {
-        if (threadIdx.x == 0) slot = atomicAdd(ticket, 1u);
-        __syncthreads();
-        k = __builtin_amdgcn_readfirstlane((int)slot);
-    }
-    while (k < ch.tiles) {
-        unsigned next = ch.tiles;
-        if (ch.tickets && threadIdx.x == 0) next = atomicAdd(ticket, 1u);
-        work(seq, k, [&] {
-            if (threadIdx.x == 0) slot = next;
-        });
-        k = __builtin_amdgcn_readfirstlane((int)slot);
-    }
-}
-
-// Where a tile lies
+// The chain that a workgroup serves: sequence b, channels from column col on
 struct Place {
-    int b, col, L, last, t0, count;
+    unsigned seq;
+    int b, col, L, last;
 };
-template <int W, bool REVERSED>
-__device__ __forceinline__ Place place(const semicrf_recurrence& p, const Chain& ch, unsigned seq, int k, int wave,
-                                       int32_t* status) {
+template <int W>
+__device__ __forceinline__ Place place(const semicrf_recurrence& p, const Chain& ch, int32_t* status) {
     Place o;
-    o.b = (int)(seq / ch.cols);
-    o.col = (int)(seq - o.b * ch.cols);
+    o.seq = blockIdx.x % ch.chains;
+    o.b = (int)(o.seq / ch.cols);
+    o.col = (int)(o.seq - o.b * ch.cols);
     o.L = __builtin_amdgcn_readfirstlane(seq_length(p.lengths, o.b, p.T, status));
     o.last = o.L > 0 ? (o.L - 1) / (W * SPAN) : 0;
-    const int tile = REVERSED && k <= o.last ? o.last - k : k;     // tiles of padding come last
-    o.t0 = (tile * W + wave) * SPAN;
-    o.count = max(0, min(SPAN, o.L - o.t0));
     return o;
+}
+
+// The workgroup's first tile; the next ones' tickets are drawn while a tile is worked on
+__device__ __forceinline__ unsigned draw(const Chain& ch, unsigned seq, unsigned none) {
+    return ch.tickets && threadIdx.x == 0 ? atomicAdd(ch.tickets + (size_t)seq * TICKET, 1u) : none;
+}
+__device__ __forceinline__ int first_tile(const Chain& ch, unsigned seq, unsigned& slot) {
+    if (!ch.tickets) return 0;
+    const unsigned k = draw(ch, seq, 0);
+    if (threadIdx.x == 0) slot = k;
+    __syncthreads();
+    const int got = __builtin_amdgcn_readfirstlane((int)slot);
+    __syncthreads();
+    return got;
 }
 
 // Forward.  Reads x and the gates once: the positions' m and b u stay in registers while the state before
 // them is found.
+//
+// Bound by the vector ALU: an element is about 35 instructions of a cycle a lane row and five of four
+// (two sigmoids and the root), which is 300 us for 4 x 100,000 x 512, as long as its 1.7 GB take.  That
+// shape takes 470 us in bfloat16 (3.6 TB/s), 1 x 250,001 x 256 in float32 257 (4.0 TB/s).
+//   Two rows of 32 lanes with two channels each, not four of 16 with four: half the maps to make and
+// one join in place of two.  Where no decay of the wavefront's channels is strong the exponential of
+// expm1_neg is not taken: both together 525 -> 497 us.  Three workgroups a compute unit (80 registers):
+// 497 -> 470.  Loading the next tile while the state is found needs 128 registers and gained nothing
+// (537), nor did tiles of 12 or 16 wavefronts (467 and 502; 32 x 800 x 1,024: 57 and 69 in place of 55).
 template <class T, int CH, int W>
-__global__ __launch_bounds__(64 * W, W == 1 ? 2 : 4) void k_recurrence(const RecArgs a, const Chain ch) {
+__global__ __launch_bounds__(64 * W, W == 1 ? 2 : 6) void k_recurrence(const RecArgs a, const Chain ch) {
     constexpr int CW = CH * LANES;
     __shared__ Shared<CW, W> sh;
     const semicrf_recurrence& p = a.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int q = lane / LANES, l = lane % LANES;
+    int q = lane / LANES;
+    const int l = lane % LANES;
     const int spans = (p.T + SPAN - 1) / SPAN;
-    each_tile(ch, sh.slot, [&](unsigned seq, int k, auto pass) __attribute__((always_inline)) {
-        const Place o = place<W, false>(p, ch, seq, k, wave, a.status);
-        const unsigned n = min((o.col * LANES + l) * CH, p.N - CH);
-        const bool mine = (o.col * LANES + l) * CH < p.N;
-        T* out = (T*)a.out + ((size_t)o.b * p.T + o.t0) * p.N;
-        if (k > o.last) {                             // all padding
-            const float zero[CH] = {};
-            if (mine)
-                for (int i = q; i < SPAN && o.t0 + i < p.T; i += 4) store<T, CH>(out, i * p.N + n, zero);
-            __syncthreads();                            // all have read the ticket
-            pass();
-            __syncthreads();
-            return;
-        }
-        float m[POS][CH], bu[POS][CH], sum[CH], H[CH];
-        if (o.count > 0) {
-            Raw<T, CH> x[POS], r[POS], g[POS];
-            const T* px = row<T>(p.x, p.x_stride, o.b, o.t0);
-            const T* pr = row<T>(p.decay_gate, p.decay_stride, o.b, o.t0);
-            const T* pg = row<T>(p.input_gate, p.input_stride, o.b, o.t0);
+    const Place o = place<W>(p, ch, a.status);
+    unsigned n = min((o.col * LANES + l) * CH, p.N - CH);
+    const bool mine = (o.col * LANES + l) * CH < p.N;
+    const Raw<float, CH> lam = load<float, CH>(p.log_decay, n);
+    Raw<T, CH> x[POS], r[POS], g[POS];
+    auto fetch = [&](int tile) __attribute__((always_inline)) {      // rows past the length: the last one again
+        const int end = max(o.L, 1) - 1, t0 = min((tile * W + wave) * SPAN, end);
+        const T* px = row<T>(p.x, p.x_stride, o.b, t0);
+        const T* pr = row<T>(p.decay_gate, p.decay_stride, o.b, t0);
+        const T* pg = row<T>(p.input_gate, p.input_stride, o.b, t0);
 #pragma unroll
-            for (int i = 0; i < POS; ++i) {
-                const unsigned at = min(q * POS + i, o.count - 1);
-                x[i] = load<T, CH>(px, at * (unsigned)p.x_stride[1] + n);
-                r[i] = load<T, CH>(pr, at * (unsigned)p.decay_stride[1] + n);
-                g[i] = load<T, CH>(pg, at * (unsigned)p.input_stride[1] + n);
+        for (int i = 0; i < POS; ++i) {
+            const unsigned at = min(q * POS + i, end - t0);
+            x[i] = load<T, CH>(px, at * (unsigned)p.x_stride[1] + n);
+            r[i] = load<T, CH>(pr, at * (unsigned)p.decay_stride[1] + n);
+            g[i] = load<T, CH>(pg, at * (unsigned)p.input_stride[1] + n);
+        }
+    };
+    auto tiles = [&](auto w) __attribute__((always_inline)) {
+        int k = first_tile(ch, o.seq, sh.slot);
+        while (k < ch.tiles) {
+            asm volatile("" : "+v"(n), "+v"(q));        // addresses are made anew: no registers to spare for them
+            const unsigned ticket = draw(ch, o.seq, ch.tiles);
+            const int t0 = (k * W + wave) * SPAN, count = max(0, min(SPAN, o.L - t0));
+            T* out = (T*)a.out + ((size_t)o.b * p.T + t0) * p.N;
+            if (k > o.last) {                           // all padding
+                const float zero[CH] = {};
+                if (mine)
+                    for (int i = q; i < SPAN && t0 + i < p.T; i += 2) store<T, CH>(out, i * p.N + n, zero);
+                __syncthreads();                        // all have read the ticket
+                if (threadIdx.x == 0) sh.slot = ticket;
+                __syncthreads();
+                k = __builtin_amdgcn_readfirstlane((int)sh.slot);
+                continue;
             }
-            const Raw<float, CH> lam = load<float, CH>(p.log_decay, n);
+            fetch(k);
+            __builtin_amdgcn_sched_barrier(0);          // the loads first, then a few elements at a time
+            float m[POS][CH], bu[POS][CH], sum[CH], H[CH];
 #pragma unroll
             for (int c = 0; c < CH; ++c) sum[c] = H[c] = 0.0f;
-            __builtin_amdgcn_sched_barrier(0);          // the loads first, then a few elements at a time
-            if (o.count < SPAN) close(r, q * POS, o.count);
+            if (count < SPAN) close(x, r, g, q * POS, count);
 #pragma unroll
             for (int i = 0; i < POS; ++i) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const float s = lam.v[c] * sigmoid((float)r[i].v[c]);
-                    m[i][c] = expm1_neg(s);
-                    bu[i][c] = root(-m[i][c] * (m[i][c] + 2.0f)) * (sigmoid((float)g[i].v[c]) * (float)x[i].v[c]);
+                    const float s = lam[c] * sigmoid(r[i][c]);
+                    m[i][c] = expm1_neg<w.value>(s);
+                    bu[i][c] = root(-m[i][c] * (m[i][c] + 2.0f)) * (sigmoid(g[i][c]) * x[i][c]);
                     sum[c] += s;
                     H[c] += fmaf(m[i][c], H[c], bu[i][c]);
-                    if (c % 2) __builtin_amdgcn_sched_barrier(0);
                 }
+                __builtin_amdgcn_sched_barrier(0);      // a few elements at a time
             }
-        } else {
+            Map before[CH];
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                sum[c] = H[c] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < POS; ++i) m[i][c] = bu[i][c] = 0.0f;
+                Map all;
+                join_halves<false>(Map{expm1_neg(sum[c]), H[c]}, before[c], all);
+                if (q == 0) sh.part[wave][l * CH + c] = all;
             }
-        }
-        Map before[CH];
+            find_starts(ch, sh, o.seq, k, k == o.last, wave, [&](int c) __attribute__((always_inline)) {
+                const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
+                return p.state ? p.state[(size_t)o.b * p.N + at] : 0.0f;
+            });
+            if (mine) {
+                float h[CH];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            Map all;
-            join_rows<false>(Map{expm1_neg(sum[c]), H[c]}, before[c], all);
-            if (q == 0) sh.part[wave][l * CH + c] = all;
-        }
-        find_starts(ch, sh, seq, k, k == o.last, wave, [&](int c) {
-            const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
-            return p.state ? p.state[(size_t)o.b * p.N + at] : 0.0f;
-        });
-        if (mine) {
-            float h[CH];
+                for (int c = 0; c < CH; ++c) h[c] = sh.start[wave][l * CH + c];
+                if (a.starts && count > 0 && q == 0)
+                    store<float, CH>(a.starts + ((size_t)o.b * spans + t0 / SPAN) * p.N, n, h);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) h[c] = sh.start[wave][l * CH + c];
-            if (a.starts && o.count > 0 && q == 0)
-                store<float, CH>(a.starts + ((size_t)o.b * spans + o.t0 / SPAN) * p.N, n, h);
+                for (int c = 0; c < CH; ++c) h[c] = apply(before[c], h[c]);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) h[c] = apply(before[c], h[c]);
+                for (int i = 0; i < POS; ++i) {
+                    float y[CH];
+                    const int at = q * POS + i;
 #pragma unroll
-            for (int i = 0; i < POS; ++i) {
-                float y[CH];
-                const int at = q * POS + i;
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    h[c] += fmaf(m[i][c], h[c], bu[i][c]);
-                    y[c] = at < o.count ? h[c] : 0.0f;
+                    for (int c = 0; c < CH; ++c) {
+                        h[c] += fmaf(m[i][c], h[c], bu[i][c]);
+                        y[c] = at < count ? h[c] : 0.0f;
+                    }
+                    if (t0 + at < p.T) store<T, CH>(out, at * p.N + n, y);
                 }
-                if (o.t0 + at < p.T) store<T, CH>(out, at * p.N + n, y);
+                if (a.state_out && k == o.last && wave == W - 1 && q == 1)
+                    store<float, CH>(a.state_out + (size_t)o.b * p.N, n, h);
             }
-            if (a.state_out && k == o.last && wave == W - 1 && q == 3)
-                store<float, CH>(a.state_out + (size_t)o.b * p.N, n, h);
+            if (threadIdx.x == 0) sh.slot = ticket;
+            __syncthreads();                            // before the next tile's part
+            k = __builtin_amdgcn_readfirstlane((int)sh.slot);
         }
-        pass();
-        __syncthreads();                                // before the next tile's part
-    });
+    };
+    if (all_weak<CH>(lam)) tiles(Flag<true>{});
+    else tiles(Flag<false>{});
 }
 
 // Backward, from the last tile to the first.  What later positions pass on to earlier ones, f_t = a_t (g_t +
@@ -411,63 +434,79 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 4) void k_recurrence(const Rec
 //   dx = e kx,  di = e ki,  dr = e kr,  dlog_decay += e kl
 // kx = b sig(i), ki = kx x (1 - sig i), kl = a (h' - a u / b) sig(r), kr = kl log_decay (1 - sig r); h' runs
 // forward from the span's stored start.  dpart [tile x sequence][N]: the tile's share of dlog_decay.
+//
+// Five factors an element stay in registers (168), so that inputs are read and exponentials taken once.
+// Bound by the vector ALU at three wavefronts on a SIMD: about 80 instructions an element, of them six of
+// four cycles.  One workgroup of 12 wavefronts a compute unit: 4 x 100,000 x 512 in bfloat16 840 us (3.5
+// TB/s), against 890 with 8 and 1,110 with two workgroups of 6.
 template <class T, int CH, int W>
-__global__ __launch_bounds__(64 * W, 2) void k_recurrence_grad(const RecArgs a, const Chain ch, float* dpart) {
+__global__ __launch_bounds__(64 * W, W == 1 ? 2 : 3) void k_recurrence_grad(const RecArgs a, const Chain ch,
+                                                                                  float* dpart) {
     constexpr int CW = CH * LANES;
     __shared__ Shared<CW, W> sh;
     __shared__ float dl[W][CW];
     const semicrf_recurrence& p = a.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int q = lane / LANES, l = lane % LANES;
+    int q = lane / LANES;
+    const int l = lane % LANES;
     const int spans = (p.T + SPAN - 1) / SPAN;
-    each_tile(ch, sh.slot, [&](unsigned seq, int k, auto pass) __attribute__((always_inline)) {
-        const Place o = place<W, true>(p, ch, seq, k, wave, a.status);
-        const unsigned n = min((o.col * LANES + l) * CH, p.N - CH);
-        const bool mine = (o.col * LANES + l) * CH < p.N;
-        const size_t at0 = ((size_t)o.b * p.T + o.t0) * p.N;
-        T *gx = (T*)a.grad_x + at0, *gr = (T*)a.grad_decay + at0, *gi = (T*)a.grad_input + at0;
-        float* dout = dpart + ((size_t)(o.t0 / (W * SPAN)) * p.B + o.b) * p.N;
-        if (k > o.last) {
-            const float zero[CH] = {};
-            if (mine) {
-                for (int i = q; i < SPAN && o.t0 + i < p.T; i += 4) {
-                    store<T, CH>(gx, i * p.N + n, zero);
-                    store<T, CH>(gr, i * p.N + n, zero);
-                    store<T, CH>(gi, i * p.N + n, zero);
-                }
-                if (wave == 0 && q == 0) store<float, CH>(dout, n, zero);
-            }
-            __syncthreads();                            // all have read the ticket
-            pass();
-            __syncthreads();
-            return;
-        }
-        float m[POS][CH], kx[POS][CH], ki[POS][CH], kr[POS][CH], kl[POS][CH], M[CH], F[CH];
-        Raw<T, CH> d[POS];
-        if (o.count > 0) {
-            Raw<T, CH> x[POS], r[POS], g[POS];
-            const T* px = row<T>(p.x, p.x_stride, o.b, o.t0);
-            const T* pr = row<T>(p.decay_gate, p.decay_stride, o.b, o.t0);
-            const T* pg = row<T>(p.input_gate, p.input_stride, o.b, o.t0);
-            const T* po = (const T*)a.grad_out + at0;
+    const Place o = place<W>(p, ch, a.status);
+    unsigned n = min((o.col * LANES + l) * CH, p.N - CH);
+    const bool mine = (o.col * LANES + l) * CH < p.N;
+    const Raw<float, CH> lam = load<float, CH>(p.log_decay, n);
+    Raw<T, CH> x[POS], r[POS], g[POS], d[POS];
+    Raw<float, CH> first;
+    auto fetch = [&](int tile) __attribute__((always_inline)) {      // rows past the length: the last one again
+        const int end = max(o.L, 1) - 1, t0 = min((tile * W + wave) * SPAN, end);
+        const T* px = row<T>(p.x, p.x_stride, o.b, t0);
+        const T* pr = row<T>(p.decay_gate, p.decay_stride, o.b, t0);
+        const T* pg = row<T>(p.input_gate, p.input_stride, o.b, t0);
+        const T* po = (const T*)a.grad_out + ((size_t)o.b * p.T + t0) * p.N;
 #pragma unroll
-            for (int i = 0; i < POS; ++i) {
-                const unsigned at = min(q * POS + i, o.count - 1);
-                x[i] = load<T, CH>(px, at * (unsigned)p.x_stride[1] + n);
-                r[i] = load<T, CH>(pr, at * (unsigned)p.decay_stride[1] + n);
-                g[i] = load<T, CH>(pg, at * (unsigned)p.input_stride[1] + n);
-                d[i] = load<T, CH>(po, at * (unsigned)p.N + n);
+        for (int i = 0; i < POS; ++i) {
+            const unsigned at = min(q * POS + i, end - t0);
+            x[i] = load<T, CH>(px, at * (unsigned)p.x_stride[1] + n);
+            r[i] = load<T, CH>(pr, at * (unsigned)p.decay_stride[1] + n);
+            g[i] = load<T, CH>(pg, at * (unsigned)p.input_stride[1] + n);
+            d[i] = load<T, CH>(po, at * (unsigned)p.N + n);
+        }
+        first = load<float, CH>(a.starts_in + ((size_t)o.b * spans + t0 / SPAN) * p.N, n);
+    };
+    auto tiles = [&](auto w) __attribute__((always_inline)) {
+        int k = first_tile(ch, o.seq, sh.slot);
+        while (k < ch.tiles) {
+            asm volatile("" : "+v"(n), "+v"(q));        // addresses are made anew: no registers to spare for them
+            const unsigned ticket = draw(ch, o.seq, ch.tiles);
+            const int tile = k <= o.last ? o.last - k : k;  // tiles of padding come last
+            const int t0 = (tile * W + wave) * SPAN, count = max(0, min(SPAN, o.L - t0));
+            const size_t at0 = ((size_t)o.b * p.T + t0) * p.N;
+            T *gx = (T*)a.grad_x + at0, *gr = (T*)a.grad_decay + at0, *gi = (T*)a.grad_input + at0;
+            float* dout = dpart + ((size_t)tile * p.B + o.b) * p.N;
+            if (k > o.last) {
+                const float zero[CH] = {};
+                if (mine) {
+                    for (int i = q; i < SPAN && t0 + i < p.T; i += 2) {
+                        store<T, CH>(gx, i * p.N + n, zero);
+                        store<T, CH>(gr, i * p.N + n, zero);
+                        store<T, CH>(gi, i * p.N + n, zero);
+                    }
+                    if (wave == 0 && q == 0) store<float, CH>(dout, n, zero);
+                }
+                __syncthreads();                        // all have read the ticket
+                if (threadIdx.x == 0) sh.slot = ticket;
+                __syncthreads();
+                k = __builtin_amdgcn_readfirstlane((int)sh.slot);
+                continue;
             }
-            const Raw<float, CH> lam = load<float, CH>(p.log_decay, n);
-            const Raw<float, CH> first = load<float, CH>(a.starts_in + ((size_t)o.b * spans + o.t0 / SPAN) * p.N, n);
+            fetch(tile);
             __builtin_amdgcn_sched_barrier(0);
-            if (o.count < SPAN) {
-                close(r, q * POS, o.count);
+            float m[POS][CH], kx[POS][CH], ki[POS][CH], kr[POS][CH], kl[POS][CH], M[CH], F[CH];
+            if (count < SPAN) {
+                close(x, r, g, q * POS, count);
 #pragma unroll
                 for (int i = 0; i < POS; ++i)
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        if (q * POS + i >= o.count) d[i].v[c] = (T)0.0f;
+                    if (q * POS + i >= count) d[i].fill(0);
+                if (count == 0) first = Raw<float, CH>{};   // a span without a stored start
             }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -475,12 +514,12 @@ __global__ __launch_bounds__(64 * W, 2) void k_recurrence_grad(const RecArgs a, 
 #pragma unroll
                 for (int i = 0; i < POS; ++i) {
                     float si, qi;
-                    sigmoids((float)r[i].v[c], sr[i], qr[i]);
-                    sigmoids((float)g[i].v[c], si, qi);
-                    const float s = lam.v[c] * sr[i], mm = m[i][c] = expm1_neg(s, av[i]);
+                    sigmoids(r[i][c], sr[i], qr[i]);
+                    sigmoids(g[i][c], si, qi);
+                    const float s = lam[c] * sr[i], mm = m[i][c] = expm1_neg<w.value>(s, av[i]);
                     const float bb = -mm * (mm + 2.0f), bv = root(bb);
                     const float ib = bb > 0x1p-123f ? __builtin_amdgcn_rsqf(bb) : 0.0f;
-                    const float xv = (float)x[i].v[c], u = si * xv;
+                    const float xv = x[i][c], u = si * xv;
                     bu[i] = bv * u;
                     sum += s;
                     H += fmaf(m[i][c], H, bu[i]);
@@ -490,18 +529,18 @@ __global__ __launch_bounds__(64 * W, 2) void k_recurrence_grad(const RecArgs a, 
                 }
                 M[c] = expm1_neg(sum);
                 Map before, all;
-                join_rows<false>(Map{M[c], H}, before, all);
-                float h = apply(before, first.v[c]);
+                join_halves<false>(Map{M[c], H}, before, all);
+                float h = apply(before, first[c]);
 #pragma unroll
                 for (int i = 0; i < POS; ++i) {
                     kl[i][c] = av[i] * (h - aub[i]) * sr[i];
-                    kr[i][c] = kl[i][c] * lam.v[c] * qr[i];
+                    kr[i][c] = kl[i][c] * lam[c] * qr[i];
                     h += fmaf(m[i][c], h, bu[i]);
                 }
                 float f = 0.0f;
 #pragma unroll
                 for (int i = POS - 1; i >= 0; --i) {
-                    const float e = f + (float)d[i].v[c];
+                    const float e = f + d[i][c];
                     f = fmaf(m[i][c], e, e);
                     // held until f is known: not moved to where they are used, with what they are made of
                     asm volatile("" : "+v"(m[i][c]), "+v"(kx[i][c]), "+v"(ki[i][c]), "+v"(kl[i][c]), "+v"(kr[i][c]));
@@ -509,72 +548,64 @@ __global__ __launch_bounds__(64 * W, 2) void k_recurrence_grad(const RecArgs a, 
                 F[c] = f;
                 __builtin_amdgcn_sched_barrier(0);
             }
-        } else {
+            Map before[CH];
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                M[c] = F[c] = 0.0f;
+                Map all;
+                join_halves<true>(Map{M[c], F[c]}, before[c], all);
+                if (q == 0) sh.part[W - 1 - wave][l * CH + c] = all;
+            }
+            find_starts(ch, sh, o.seq, k, k == o.last, W - 1 - wave, [&](int c) __attribute__((always_inline)) {
+                const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
+                return a.grad_state_out ? a.grad_state_out[(size_t)o.b * p.N + at] : 0.0f;
+            });
+            float f[CH], dlam[CH];
 #pragma unroll
-                for (int i = 0; i < POS; ++i) {
-                    m[i][c] = kx[i][c] = ki[i][c] = kr[i][c] = kl[i][c] = 0.0f;
-                    d[i].v[c] = (T)0.0f;
+            for (int c = 0; c < CH; ++c) {
+                f[c] = apply(before[c], sh.start[W - 1 - wave][l * CH + c]);
+                dlam[c] = 0.0f;
+            }
+#pragma unroll
+            for (int i = POS - 1; i >= 0; --i) {
+                float dx[CH], dr[CH], di[CH];
+                const int at = q * POS + i;
+                const bool in = at < count;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const float e = f[c] + d[i][c];
+                    dx[c] = in ? e * kx[i][c] : 0.0f;
+                    di[c] = in ? e * ki[i][c] : 0.0f;
+                    dr[c] = in ? e * kr[i][c] : 0.0f;
+                    dlam[c] += in ? e * kl[i][c] : 0.0f;
+                    f[c] = fmaf(m[i][c], e, e);
+                }
+                if (mine && t0 + at < p.T) {
+                    store<T, CH>(gx, at * p.N + n, dx);
+                    store<T, CH>(gr, at * p.N + n, dr);
+                    store<T, CH>(gi, at * p.N + n, di);
                 }
             }
-        }
-        Map before[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            Map all;
-            join_rows<true>(Map{M[c], F[c]}, before[c], all);
-            if (q == 0) sh.part[W - 1 - wave][l * CH + c] = all;
-        }
-        find_starts(ch, sh, seq, k, k == o.last, W - 1 - wave, [&](int c) {
-            const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
-            return a.grad_state_out ? a.grad_state_out[(size_t)o.b * p.N + at] : 0.0f;
-        });
-        float f[CH], dlam[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            f[c] = apply(before[c], sh.start[W - 1 - wave][l * CH + c]);
-            dlam[c] = 0.0f;
-        }
-#pragma unroll
-        for (int i = POS - 1; i >= 0; --i) {
-            float dx[CH], dr[CH], di[CH];
-            const int at = q * POS + i;
-            const bool in = at < o.count;
+            if (mine && a.grad_state && k == o.last && wave == 0 && q == 0)
+                store<float, CH>(a.grad_state + (size_t)o.b * p.N, n, f);
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const float e = f[c] + (float)d[i].v[c];
-                dx[c] = in ? e * kx[i][c] : 0.0f;
-                di[c] = in ? e * ki[i][c] : 0.0f;
-                dr[c] = in ? e * kr[i][c] : 0.0f;
-                dlam[c] += in ? e * kl[i][c] : 0.0f;
-                f[c] = fmaf(m[i][c], e, e);
+                dlam[c] = of_half<0>(dlam[c]) + of_half<1>(dlam[c]);
+                if (q == 0) dl[wave][l * CH + c] = dlam[c];
             }
-            if (mine && o.t0 + at < p.T) {
-                store<T, CH>(gx, at * p.N + n, dx);
-                store<T, CH>(gr, at * p.N + n, dr);
-                store<T, CH>(gi, at * p.N + n, di);
+            if (threadIdx.x == 0) sh.slot = ticket;
+            __syncthreads();
+            if (wave == 0 && q == 0 && mine) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int w = 1; w < W; ++w) dlam[c] += dl[w][l * CH + c];
+                store<float, CH>(dout, n, dlam);
             }
+            k = __builtin_amdgcn_readfirstlane((int)sh.slot);
         }
-        if (mine && a.grad_state && k == o.last && wave == 0 && q == 0)
-            store<float, CH>(a.grad_state + (size_t)o.b * p.N, n, f);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            dlam[c] = of_pair<0>(dlam[c]) + of_pair<1>(dlam[c]);
-            dlam[c] = of_half<0>(dlam[c]) + of_half<1>(dlam[c]);
-            if (q == 0) dl[wave][l * CH + c] = dlam[c];
-        }
-        pass();
-        __syncthreads();
-        if (wave == 0 && q == 0 && mine) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int w = 1; w < W; ++w) dlam[c] += dl[w][l * CH + c];
-            store<float, CH>(dout, n, dlam);
-        }
-    });
+    };
+    if (all_weak<CH>(lam)) tiles(Flag<true>{});
+    else tiles(Flag<false>{});
 }
 
 // grid (ceil(N / 16)), block 1024: 16 columns, 64 groups of partial rows, joined in order
@@ -624,7 +655,7 @@ __global__ __launch_bounds__(256) void k_recurrence_step(const semicrf_recurrenc
 }
 
 // ------------------------------------------------------------------ host
-constexpr int WIDE = 8, WIDE_GRAD = 8;       // wavefronts a workgroup
+constexpr int WIDE = 8, WIDE_GRAD = 12;      // wavefronts a workgroup: measured at the kernels
 constexpr int SERVE = 2048;                  // workgroups of a launch
 
 // How a call is laid out: channels a lane, wavefronts a workgroup, and the workspace
@@ -638,7 +669,7 @@ struct Plan {
 
 Plan make_plan(const semicrf_recurrence& p, bool grad) {
     Plan q{};
-    q.CH = p.N < 4 ? 1 : 4;
+    q.CH = p.N < 2 ? 1 : 2;
     q.W = p.T <= SPAN ? 1 : grad ? WIDE_GRAD : WIDE;
     Chain& c = q.chain;
     c.tiles = (p.T + q.W * SPAN - 1) / (q.W * SPAN);
@@ -691,11 +722,15 @@ size_t gated_recurrence_bytes(const semicrf_recurrence& p, bool grad) {
 hipError_t launch_gated_recurrence(const RecArgs& a, void* ws, hipStream_t stream) {
     Plan q = make_plan(a.p, false);
     prepare(q, ws, stream);
-#define RUN(T, CH)                                                                                                       if (q.W == 1)                                                                                                            hipLaunchKernelGGL((k_recurrence<T, CH, 1>), dim3(q.grid), dim3(64), 0, stream, a, q.chain);                     else                                                                                                                     hipLaunchKernelGGL((k_recurrence<T, CH, WIDE>), dim3(q.grid), dim3(64 * WIDE), 0, stream, a, q.chain);
+#define RUN(T, CH)                                                                                             \
+    if (q.W == 1)                                                                                              \
+        hipLaunchKernelGGL((k_recurrence<T, CH, 1>), dim3(q.grid), dim3(64), 0, stream, a, q.chain);           \
+    else                                                                                                       \
+        hipLaunchKernelGGL((k_recurrence<T, CH, WIDE>), dim3(q.grid), dim3(64 * WIDE), 0, stream, a, q.chain);
     if (a.p.dtype == SEMICRF_F32) {
-        if (q.CH == 4) { RUN(float, 4) } else { RUN(float, 1) }
+        if (q.CH == 2) { RUN(float, 2) } else { RUN(float, 1) }
     } else {
-        if (q.CH == 4) { RUN(bf16, 4) } else { RUN(bf16, 1) }
+        if (q.CH == 2) { RUN(bf16, 2) } else { RUN(bf16, 1) }
     }
 #undef RUN
     return hipGetLastError();
@@ -705,11 +740,16 @@ hipError_t launch_gated_recurrence_grad(const RecArgs& a, void* ws, hipStream_t 
     Plan q = make_plan(a.p, true);
     prepare(q, ws, stream);
     float* part = (float*)((char*)ws + q.part);
-#define RUN(T, CH)                                                                                                       if (q.W == 1)                                                                                                            hipLaunchKernelGGL((k_recurrence_grad<T, CH, 1>), dim3(q.grid), dim3(64), 0, stream, a, q.chain, part);          else                                                                                                                     hipLaunchKernelGGL((k_recurrence_grad<T, CH, WIDE_GRAD>), dim3(q.grid), dim3(64 * WIDE_GRAD), 0, stream, a, q.chain,                              part);
+#define RUN(T, CH)                                                                                             \
+    if (q.W == 1)                                                                                              \
+        hipLaunchKernelGGL((k_recurrence_grad<T, CH, 1>), dim3(q.grid), dim3(64), 0, stream, a, q.chain, part); \
+    else                                                                                                       \
+        hipLaunchKernelGGL((k_recurrence_grad<T, CH, WIDE_GRAD>), dim3(q.grid), dim3(64 * WIDE_GRAD), 0, stream, a, \
+                           q.chain, part);
     if (a.p.dtype == SEMICRF_F32) {
-        if (q.CH == 4) { RUN(float, 4) } else { RUN(float, 1) }
+        if (q.CH == 2) { RUN(float, 2) } else { RUN(float, 1) }
     } else {
-        if (q.CH == 4) { RUN(bf16, 4) } else { RUN(bf16, 1) }
+        if (q.CH == 2) { RUN(bf16, 2) } else { RUN(bf16, 1) }
     }
 #undef RUN
     if (a.grad_log_decay)
