@@ -85,8 +85,9 @@ int check_nll_shape(int dtype, int B, int T, int V, int N) {
     const int rc = check_rows(B, T, N);
     if (rc) return rc;
     if ((long)B * T > NLL_MAX_ROWS || V > NLL_MAX_ROWS || N > NLL_MAX_N) return SEMICRF_ERR_UNSUPPORTED;
-    // x and the table are laid out by blocks of 64 x 64 in one launch, of less than 2^32 threads
-    return (((long)B * T + V) / 64 + 16) * ((N + 63) / 64) < (1l << 24) ? SEMICRF_OK : SEMICRF_ERR_UNSUPPORTED;
+    // x and the table are laid out by blocks of 64 x 64 in one launch, of less than 2^32 threads; pieces of the
+    // vocabulary, rounded up, add less than 2^16 words
+    return (((long)B * T + V) / 64 + 1040) * ((N + 63) / 64) < (1l << 24) ? SEMICRF_OK : SEMICRF_ERR_UNSUPPORTED;
 }
 
 int check_nll(const void* x, const void* table, const void* targets, int target_bits, int dtype, int B,
