@@ -20,6 +20,11 @@
 // products in fp16, scaled by powers of two to the top of its range: W and x lose nothing within 2^29
 // of their largest value, and p has 11 bits down to 2^-29, so that the gradients' own rounding is
 // what is seen (p in bfloat16 would add an error as large as that).  In float32 everything is float32.
+//
+// Bound by the matrix cores.  16,000 rows of 1,024 over 50,001 words in bfloat16, 1.64 * 10^12 operations a
+// product (a large product of the library reaches 1,230 TFLOP/s): scores 1,416 us (1,160 TFLOP/s), p 1,603
+// (1,020: it stores 1.6 GB), dx 1,309 (1,250), dW 1,344 (1,220); all else of a loss and its gradient 140.  The
+// gradient forms the scores a second time: the forward pass would have to keep 1.6 GB for it.
 #include "common.h"
 #include "encoder.h"
 
@@ -343,6 +348,8 @@ __global__ __launch_bounds__(LIST_THREADS) void k_nll_list(const NllArgs a, Cont
 
 __host__ __device__ __forceinline__ int tiles(int rows, int tile) { return (rows + tile - 1) / tile; }
 
+constexpr int MAX_WGS = 512, MAX_THREADS = 1024;
+
 // The largest finite magnitude of n elements, by blocks `first` .. of the grid's `blocks`
 template <class T>
 __device__ __forceinline__ unsigned largest(const T* src, long n, int block, int blocks) {
@@ -352,8 +359,8 @@ __device__ __forceinline__ unsigned largest(const T* src, long n, int block, int
         const unsigned bits = __float_as_uint(x) & 0x7fffffffu;
         if (bits < 0x7f800000u) most = max(most, bits);
     };
-    const long step = (long)blocks * 256 * V;
-    long i = ((long)block * 256 + threadIdx.x) * V;
+    const long step = (long)blocks * MAX_THREADS * V;
+    long i = ((long)block * MAX_THREADS + threadIdx.x) * V;
     for (; i + V <= n; i += step) {
         const raw_piece r = *(const loose_piece*)(src + i);
         float x[V];
@@ -365,16 +372,16 @@ __device__ __forceinline__ unsigned largest(const T* src, long n, int block, int
     return most;
 }
 
-// max_x over the listed rows, max_w over the table: a quarter of the workgroups for x
+// max_x over the listed rows, by the first x_wgs workgroups, and max_w over the table
 template <class T>
-__global__ __launch_bounds__(256) void k_nll_max(const NllArgs a, Control* ctl, const int* row) {
-    const int quarter = gridDim.x / 4, lane = threadIdx.x & 63;
-    const bool of_x = (int)blockIdx.x < quarter;
+__global__ __launch_bounds__(MAX_THREADS) void k_nll_max(const NllArgs a, Control* ctl, const int* row, int x_wgs) {
+    const int lane = threadIdx.x & 63, rows = ctl->rows;
+    const bool of_x = (int)blockIdx.x < x_wgs;
     unsigned most = 0;
     if (of_x) {
         // a wavefront a row
         constexpr int V = 16 / sizeof(T);
-        for (int r = blockIdx.x * 4 + (threadIdx.x >> 6); r < ctl->rows; r += quarter * 4) {
+        for (int r = blockIdx.x * (MAX_THREADS / 64) + (threadIdx.x >> 6); r < rows; r += x_wgs * (MAX_THREADS / 64)) {
             const T* from = (const T*)a.x + (size_t)row[r] * a.N;
             for (int c = lane * V; c < a.N; c += 64 * V) {
                 if (c + V <= a.N) {
@@ -395,15 +402,15 @@ __global__ __launch_bounds__(256) void k_nll_max(const NllArgs a, Control* ctl, 
             }
         }
     } else {
-        most = largest((const T*)a.table, (long)a.V * a.N, blockIdx.x - quarter, gridDim.x - quarter);
+        most = largest((const T*)a.table, (long)a.V * a.N, blockIdx.x - x_wgs, gridDim.x - x_wgs);
     }
     // one atomic a workgroup at most: on one address they take some 20 ns each, one after another
-    __shared__ unsigned s[4];
+    __shared__ unsigned s[MAX_THREADS / 64];
     for (int off = 32; off >= 1; off >>= 1) most = max(most, (unsigned)__shfl_xor((int)most, off, 64));
     if (lane == 0) s[threadIdx.x >> 6] = most;
     __syncthreads();
     if (threadIdx.x == 0) {
-        most = max(max(s[0], s[1]), max(s[2], s[3]));
+        for (int i = 1; i < MAX_THREADS / 64; ++i) most = max(most, s[i]);
         unsigned* to = of_x ? &ctl->max_x : &ctl->max_w;
         if (most > __hip_atomic_load(to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(to, most);
     }
@@ -419,6 +426,8 @@ __device__ __forceinline__ float held_scale(unsigned bits) {
 // p's scale: |p| <= 1
 template <class H>
 constexpr float P_SCALE = sizeof(H) == 4 ? 1.0f : 32768.0f;
+template <class H>
+constexpr float P_EXPONENT = sizeof(H) == 4 ? 0.0f : 15.0f;
 // What the rows' gradients are divided by where x carries them into dW: the largest one
 __device__ __forceinline__ float grad_unit(unsigned bits) { return fmaxf(__uint_as_float(bits), 0x1p-120f); }
 
@@ -534,6 +543,7 @@ template <class T, class Tl>
 __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Control* ctl, const int* target,
                                                        float2* part, float* at_target) {
     __shared__ __align__(16) char lds[2 * Tl::STAGE];
+    __shared__ int words[2][Tl::BB];         // targets of a tile's rows, by turns
     const int rows = __builtin_amdgcn_readfirstlane(ctl->rows);
     const int mt = tiles(rows, Tl::BB), vt = tiles(p.V, Tl::BA), S = vocab_split(mt, vt, gridDim.x);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wa = wave / Tl::WB, wb = wave % Tl::WB;
@@ -548,8 +558,13 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Con
         point(item, item % S * vt / S);
         t.fetch(0, lds);
     }
-    for (; item < mt * S; item += gridDim.x) {
+    for (int turn = 0; item < mt * S; item += gridDim.x, turn ^= 1) {
         const int m0 = item / S * Tl::BB, v1 = (item % S + 1) * vt / S;
+        // seen by all after the first step of a product; the turn before may still be read
+        if ((int)threadIdx.x < Tl::BB) {
+            const int m = m0 + threadIdx.x;
+            words[turn][threadIdx.x] = m < rows ? target[m] : -1;
+        }
         float top[Tl::MB], sum[Tl::MB];
 #pragma unroll
         for (int j = 0; j < Tl::MB; ++j) {
@@ -580,7 +595,7 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Con
                     most = fmaxf(most, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
                 }
                 const int m = m0 + col + j * 16;
-                const int hit = (m < rows ? target[m] : -1) - first;      // the target is one of the lane's words
+                const int hit = words[turn][col + j * 16] - first;        // the target is one of the lane's words
                 if (hit >= 0 && hit < Tl::MA * 16 && hit % 16 < 4) {
 #pragma unroll
                     for (int i = 0; i < Tl::MA; ++i)
@@ -654,6 +669,21 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_p(const Scores s, const Control*
         t.fetch(0, lds);
     }
     for (; tile < mt * vt; tile += gridDim.x) {
+        int mi, v;
+        in_groups(tile, mt, vt, mi, v);
+        // read and waited for here, where the product's first step waits as well: after the product they would
+        // wait for what it has fetched ahead
+        float log_sum[Tl::MB];
+        int word[Tl::MB];
+#pragma unroll
+        for (int j = 0; j < Tl::MB; ++j) {
+            const int m = mi * Tl::BB + wb * (Tl::BB / Tl::WB) + j * 16 + (lane & 15);
+            // a row past the last has an infinite log sum: its p is 0
+            log_sum[j] = m < rows ? lse[m] : __builtin_inff();
+            word[j] = m < rows ? target[m] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < Tl::MB; ++j) asm volatile("" : "+v"(log_sum[j]), "+v"(word[j]));
         t.product(0, s.nk, lds, [&](int& k) {
             const int after = tile + gridDim.x;
             if (after >= mt * vt) return false;
@@ -661,29 +691,58 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_p(const Scores s, const Control*
             k = 0;
             return true;
         });
-        int mi, v;
-        in_groups(tile, mt, vt, mi, v);
         const int first = v * Tl::BA + wa * (Tl::BA / Tl::WA) + lane / 16 * 4;
         const bool whole = v0 + (v + 1) * Tl::BA <= s.V;
 #pragma unroll
         for (int j = 0; j < Tl::MB; ++j) {
             const int m = mi * Tl::BB + wb * (Tl::BB / Tl::WB) + j * 16 + (lane & 15);
-            const bool in_rows = m < rows;
-            // a row past the last has an infinite log sum: its p is 0
-            const float l = in_rows ? lse[m] : __builtin_inff();
-            const int hit = (in_rows ? target[m] - v0 : -1) - first;
-#pragma unroll
-            for (int i = 0; i < Tl::MA; ++i) {
-                H out[4];
+            const float l = log_sum[j] - P_EXPONENT<H>;       // p's scale goes into the exponent
+            const int hit = word[j] - v0 - first;             // a row past the last: negative
+            auto words = [&](int i, auto seen, H (&out)[4]) __attribute__((always_inline)) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float q = fast_exp2(fmaf(t.acc[i][j][k], s.scale, -l));
-                    if (hit == i * 16 + k) q -= 1.0f;
+                    if (decltype(seen)::value && hit == i * 16 + k) q -= P_SCALE<H>;
                     if (!whole && v0 + first + i * 16 + k >= s.V) q = 0.0f;
-                    out[k] = (H)(q * P_SCALE<H>);
+                    out[k] = (H)q;
                 }
-                __builtin_memcpy(p + (size_t)m * ldp + first + i * 16, out, sizeof(out));
-            }
+            };
+            auto tiles = [&](auto seen) __attribute__((always_inline)) {
+                if constexpr (sizeof(H) == 2) {
+                    // Two tiles at a time, so that a lane has 16 bytes of its row and four lanes 64: lane 16 g + r
+                    // gives up words 4 g .. 4 g + 3 of either tile for words 8 g .. 8 g + 7 of both.  (8 bytes a lane
+                    // and 32 a row: 1,790 us in place of 1,630 for 16,000 rows over 50,001 words.)
+                    H* to = p + (size_t)m * ldp + first - lane / 16 * 4 + lane / 16 * 8;
+#pragma unroll
+                    for (int i = 0; i < Tl::MA; i += 2) {
+                        H one[4], two[4];
+                        words(i, seen, one);
+                        words(i + 1, seen, two);
+                        unsigned x[2], y[2];
+                        __builtin_memcpy(x, one, 8);
+                        __builtin_memcpy(y, two, 8);
+                        raw_piece v;
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) {
+                            const auto half = __builtin_amdgcn_permlane32_swap(x[d], y[d], false, false);
+                            const auto row = __builtin_amdgcn_permlane16_swap(half[0], half[1], false, false);
+                            v[d] = row[0];
+                            v[2 + d] = row[1];
+                        }
+                        *(raw_piece*)(to + i * 16) = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < Tl::MA; ++i) {
+                        H out[4];
+                        words(i, seen, out);
+                        __builtin_memcpy(p + (size_t)m * ldp + first + i * 16, out, sizeof(out));
+                    }
+                }
+            };
+            // few tiles hold the target of a row: the others compare nothing
+            if (__any(hit >= 0 && hit < Tl::MA * 16)) tiles(std::true_type());
+            else tiles(std::false_type());
         }
     }
 }
@@ -961,8 +1020,14 @@ Scores gather(const NllArgs& a, const Plan& p, const Listed& list, Layout& l, vo
         hipLaunchKernelGGL(k_nll_count, dim3(blocks), dim3(LIST_THREADS), 0, stream, a, ctl, counts);
     hipLaunchKernelGGL(k_nll_list<GRAD>, dim3(blocks), dim3(LIST_THREADS), 0, stream, a, ctl,
                        blocks > 1 ? counts : nullptr, list);
-    if (GRAD && sizeof(H) == 2)
-        hipLaunchKernelGGL(k_nll_max<T>, dim3(2048), dim3(256), 0, stream, a, ctl, list.row);
+    if (GRAD && sizeof(H) == 2) {
+        // shared out by rows, a quarter at least to either: a row of x waits for its place in the list
+        // (15,000 of 100,000 rows of 512, 4,096 words: 19 us, 26 where x always has a quarter; and 11 with 512
+        // workgroups of 1,024 threads in place of 2,048 of 256, by fewer atomics)
+        const long share = MAX_WGS * p.rows / (p.rows + a.V);
+        hipLaunchKernelGGL(k_nll_max<T>, dim3(MAX_WGS), dim3(MAX_THREADS), 0, stream, a, ctl, list.row,
+                           (int)(share < MAX_WGS / 4 ? MAX_WGS / 4 : share > MAX_WGS * 3 / 4 ? MAX_WGS * 3 / 4 : share));
+    }
     l.x = in<T>(ws, p.x);
     l.w = p.copy_w ? in<T>(ws, p.w) : (void*)a.table;
     l.ld = (int)p.ld;
