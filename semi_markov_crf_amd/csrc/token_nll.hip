@@ -38,7 +38,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 using f16 = _Float16;
 
-constexpr float LOG2EF = 1.44269504088896f, LN2F = 0.69314718055994531f;
+// log2 e and ln 2 with what their floats leave over: a log sum of 10 loses 2^-21 to one of them
+constexpr float LOG2EF = 1.44269504088896f, LOG2E_REST = (float)(1.4426950408889634074 - (double)LOG2EF);
+constexpr float LN2F = 0.69314718055994531f, LN2_REST = (float)(0.69314718055994530942 - (double)LN2F);
 constexpr int ROW_TILE = 256;        // rows of x are padded to it
 constexpr int STEP = 128;            // bytes of a row a step of a product takes
 
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(LIST_THREADS) void k_nll_count(const NllArgs a, Con
 struct Listed {
     int* row;                // place among all rows
     int* target;
-    float *lse, *grad;       // gradients only; lse in log2 units
+    float *lse, *grad;       // gradients only
 };
 
 // counts NULL: one workgroup, which also clears the control block
@@ -324,7 +326,7 @@ __global__ __launch_bounds__(LIST_THREADS) void k_nll_list(const NllArgs a, Cont
         list.target[at] = target[i];
         if (GRAD) {
             const float g = a.grad_loss[row];
-            list.lse[at] = a.lse_in[row] * LOG2EF;
+            list.lse[at] = a.lse_in[row];
             list.grad[at] = g;
             const unsigned bits = __float_as_uint(g) & 0x7fffffffu;
             if (bits < 0x7f800000u) most = max(most, bits);
@@ -534,7 +536,7 @@ struct Scores {
     const char *w, *x;
     unsigned ld;             // bytes
     int V, nk;
-    float scale;             // to log2 units
+    float scale, rest;       // to log2 units, and what the float leaves over (of use in float32 only)
 };
 
 // part[(item, wavefront row)][BB] = (maximum, sum) of the scores of a share of the vocabulary, item =
@@ -587,7 +589,11 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Con
 #pragma unroll
                 for (int i = 0; i < Tl::MA; ++i) {
                     f32x4& z = t.acc[i][j];
-                    z *= p.scale;
+                    if constexpr (sizeof(T) == 4)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) z[k] = fmaf(z[k], p.scale, z[k] * p.rest);
+                    else
+                        z *= p.scale;
                     if (!whole)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -644,7 +650,7 @@ __global__ __launch_bounds__(256) void k_nll_loss(const Control* ctl, const int*
     for (int i = 0; i < S * WA; ++i) sum += p[(size_t)i * BB].y * fast_exp2(p[(size_t)i * BB].x - ref);
     const float l = fast_log2(sum);
     loss[row[m]] = (l + (ref - at_target[m])) * LN2F;
-    if (lse) lse[row[m]] = (l + ref) * LN2F;
+    if (lse) lse[row[m]] = fmaf(ref, LN2F, fmaf(ref, LN2_REST, l * LN2F));
 }
 
 // ------------------------------------------------------------------ gradients
@@ -696,12 +702,18 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_p(const Scores s, const Control*
 #pragma unroll
         for (int j = 0; j < Tl::MB; ++j) {
             const int m = mi * Tl::BB + wb * (Tl::BB / Tl::WB) + j * 16 + (lane & 15);
-            const float l = log_sum[j] - P_EXPONENT<H>;       // p's scale goes into the exponent
+            float l = log_sum[j] * LOG2EF, rest = 0.0f;
+            if (sizeof(H) == 4 && fabsf(l) < 1e30f)
+                rest = fmaf(log_sum[j], LOG2EF, -l) + log_sum[j] * LOG2E_REST;
+            l -= P_EXPONENT<H>;                                // p's scale goes into the exponent
             const int hit = word[j] - v0 - first;             // a row past the last: negative
             auto words = [&](int i, auto seen, H (&out)[4]) __attribute__((always_inline)) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float q = fast_exp2(fmaf(t.acc[i][j][k], s.scale, -l));
+                    const float z = t.acc[i][j][k];
+                    float q = fmaf(z, s.scale, -l);
+                    if (sizeof(H) == 4) q += fmaf(z, s.rest, -rest);
+                    q = fast_exp2(q);
                     if (decltype(seen)::value && hit == i * 16 + k) q -= P_SCALE<H>;
                     if (!whole && v0 + first + i * 16 + k >= s.V) q = 0.0f;
                     out[k] = (H)q;
@@ -1044,7 +1056,9 @@ Scores gather(const NllArgs& a, const Plan& p, const Listed& list, Layout& l, vo
     s.ld = (unsigned)(p.ld * sizeof(T));
     s.V = a.V;
     s.nk = p.nk;
-    s.scale = a.scale * LOG2EF;
+    const double log2_scale = (double)a.scale * 1.4426950408889634074;
+    s.scale = (float)log2_scale;
+    s.rest = (float)(log2_scale - s.scale);
     return s;
 }
 
