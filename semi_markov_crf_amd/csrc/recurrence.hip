@@ -28,8 +28,10 @@ __device__ __forceinline__ float expm1_neg(float s, float& e) {
     p = fmaf(s, p, 1.0f / 6.0f);
     p = fmaf(s, p, 0.5f);
     p = fmaf(s * s, p, s);
-    e = WEAK ? 1.0f + p : fast_exp2(s * LOG2EF);
-    return WEAK || s > -0.25f ? p : e - 1.0f;
+    const float full = WEAK ? 0.0f : fast_exp2(s * LOG2EF);
+    const bool weak = WEAK || s >= -0.25f;
+    e = weak ? 1.0f + p : full;
+    return weak ? p : full - 1.0f;
 }
 template <bool WEAK = false>
 __device__ __forceinline__ float expm1_neg(float s) {
@@ -52,7 +54,8 @@ __device__ __forceinline__ const T* row(const void* p, const int64_t (&stride)[2
 // ------------------------------------------------------------------ elements of a lane
 // A wavefront takes a span of 16 positions of 32 CH channels: lane 32 q + l holds CH neighbouring
 // channels at positions 8 q .. 8 q + 7.  Where N is no multiple of CH the last lanes start early, at
-// N - CH, and compute channels that a neighbour has too.
+// N - CH, and compute channels that a neighbour has too (of the same wavefront: a width that leaves one
+// channel to the last takes CH = 1).
 constexpr int POS = 8, LANES = 32;
 
 // As loaded, two bfloat16 to a register
@@ -669,7 +672,9 @@ struct Plan {
 
 Plan make_plan(const semicrf_recurrence& p, bool grad) {
     Plan q{};
-    q.CH = p.N < 2 ? 1 : 2;
+    // One channel left over would be computed beside a neighbour that another workgroup has as well, whose final
+    // state may be there already, over the initial one
+    q.CH = p.N % (2 * LANES) == 1 ? 1 : 2;
     q.W = p.T <= SPAN ? 1 : grad ? WIDE_GRAD : WIDE;
     Chain& c = q.chain;
     c.tiles = (p.T + q.W * SPAN - 1) / (q.W * SPAN);

@@ -199,13 +199,14 @@ def test_recurrence_carries_on(crf):  # noqa: F811
     near(second, h[:, 333:], eh[:, 333:], "f32", "second")
 
 
+@pytest.mark.parametrize("N", [1, 65, 200, 257])
 @pytest.mark.parametrize("T", [1, 16, 17, 100, 128, 129, 900, 3000])
-def test_recurrence_state_in_place(crf, T):  # noqa: F811
+def test_recurrence_state_in_place(crf, T, N):  # noqa: F811
     """The final state may be written over the initial one, whatever the number of tiles."""
     import torch
     from semi_markov_crf_amd import _native, blocks
     torch.manual_seed(T)
-    B, N = 3, 200
+    B = 700 if T < 20 else 3
     x, r, i = (torch.randn(B, T, N, device="cuda") for _ in range(3))
     ld, state = dev(decays(N, "weak")), torch.randn(B, N, device="cuda")
     want, end = crf.gated_recurrence(x, r, i, ld, state=state, want_state=True)
