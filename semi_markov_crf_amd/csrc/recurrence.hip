@@ -141,13 +141,14 @@ __device__ __forceinline__ void join_halves(Map own, Map& before, Map& all) {
 // Tile k publishes its map, and the last of each GROUP tiles the state it ends with; tile k reads the
 // state of the group before and the maps since, and joins them in order: the same additions on every
 // call.  A publication is one 8-byte store, with a pattern that no map has as "not there yet".
+// Where there are chains enough a workgroup of the backward pass has its chain to itself and publishes nothing.
 constexpr int GROUP = 16;
 constexpr unsigned long long EMPTY = ~0ull;
 
 struct Chain {
     unsigned long long* words;   // [sequence x columns][tiles][channels of a tile]: maps
     unsigned long long* states;  // [sequence x columns][groups][channels of a tile]: (0, state)
-    unsigned* tickets;           // [sequence x columns][TICKET], or NULL where a chain is one tile
+    unsigned* tickets;           // [sequence x columns][TICKET], or NULL where a workgroup has the whole chain
     int tiles, groups, cols;
     unsigned chains;
 };
@@ -195,15 +196,15 @@ template <int CW, int W>
 struct Shared {
     Map part[W][CW];             // maps of the spans, in the order in which the state goes through them
     Map look[W][CW];             // maps of a wavefront's share of the tiles since the last group
-    float base[CW];              // the state at the end of the last group
+    float base[2][CW];           // the state at the end of the last group, or of the last tile, by turns
     float start[W][CW];          // the state each span starts from
     unsigned slot;
 };
 
 // The state before each span of tile k of chain `seq`, into sh.start: `order` is the wavefront's place in
 // part, `first` the state before tile 0 at a channel.  A lane takes whole channels here.  Waits for all
-// wavefronts' writes of part.
-template <int CW, int W, class F>
+// wavefronts' writes of part.  CARRY: the workgroup may have the chain to itself.
+template <bool CARRY, int CW, int W, class F>
 __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, long seq, int k, bool last, int order,
                                             F&& first) {
     constexpr int U = (GROUP + W - 1) / W, PER = (CW + 63) / 64;
@@ -215,11 +216,11 @@ __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, 
     // wavefront may overwrite it after that.
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        h[i] = g == 0 && lane + i * 64 < CW ? first(lane + i * 64) : 0.0f;
+        h[i] = (!CARRY || ch.tickets ? g == 0 : k == 0) && lane + i * 64 < CW ? first(lane + i * 64) : 0.0f;
         asm volatile("" : "+v"(h[i]));
     }
     __syncthreads();
-    if (W > 1 && ch.tickets) {                         // one span: one tile
+    if (W > 1 && ch.tickets) {
         unsigned long long* words = ch.words + (size_t)seq * ch.tiles * CW;
         unsigned long long* states = ch.states + (size_t)seq * ch.groups * CW;
         Map own[PER];
@@ -249,7 +250,7 @@ __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, 
             if (order == W - 1 && g > 0) {
                 unsigned long long s[1];
                 await(states + (size_t)(g - 1) * CW + c, 0, 1, s);
-                sh.base[c] = unpack_map(s[0]).H;
+                sh.base[0][c] = unpack_map(s[0]).H;
             }
         }
         __syncthreads();
@@ -257,7 +258,7 @@ __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, 
         for (int i = 0; i < PER; ++i) {
             const int c = lane + i * 64;
             if (CW % 64 && c >= CW) continue;
-            if (g > 0) h[i] = sh.base[c];
+            if (g > 0) h[i] = sh.base[0][c];
 #pragma unroll
             for (int w = 0; w < W; ++w) h[i] = apply(sh.look[w][c], h[i]);
             if (order == 0 && !last && j == GROUP - 1)
@@ -268,10 +269,12 @@ __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, 
     for (int i = 0; i < PER; ++i) {
         const int c = lane + i * 64;
         if (CW % 64 && c >= CW) continue;
+        if (CARRY && W > 1 && !ch.tickets && k > 0) h[i] = sh.base[k & 1][c];
 #pragma unroll
         for (int w = 0; w < W - 1; ++w)
             if (w < order) h[i] = apply(sh.part[w][c], h[i]);
         sh.start[order][c] = h[i];
+        if (CARRY && W > 1 && !ch.tickets && order == W - 1) sh.base[(k + 1) & 1][c] = apply(sh.part[W - 1][c], h[i]);
     }
     // read by the same wavefront only
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -358,7 +361,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 6) void k_recurrence(const Rec
         int k = first_tile(ch, o.seq, sh.slot);
         while (k < ch.tiles) {
             asm volatile("" : "+v"(n), "+v"(q));        // addresses are made anew: no registers to spare for them
-            const unsigned ticket = draw(ch, o.seq, ch.tiles);
+            const unsigned ticket = draw(ch, o.seq, k + 1);
             const int t0 = (k * W + wave) * SPAN, count = max(0, min(SPAN, o.L - t0));
             T* out = (T*)a.out + ((size_t)o.b * p.T + t0) * p.N;
             if (k > o.last) {                           // all padding
@@ -396,7 +399,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 6) void k_recurrence(const Rec
                 join_halves<false>(Map{expm1_neg(sum[c]), H[c]}, before[c], all);
                 if (q == 0) sh.part[wave][l * CH + c] = all;
             }
-            find_starts(ch, sh, o.seq, k, k == o.last, wave, [&](int c) __attribute__((always_inline)) {
+            find_starts<false>(ch, sh, o.seq, k, k == o.last, wave, [&](int c) __attribute__((always_inline)) {
                 const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
                 return p.state ? p.state[(size_t)o.b * p.N + at] : 0.0f;
             });
@@ -479,7 +482,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 3) void k_recurrence_grad(cons
         int k = first_tile(ch, o.seq, sh.slot);
         while (k < ch.tiles) {
             asm volatile("" : "+v"(n), "+v"(q));        // addresses are made anew: no registers to spare for them
-            const unsigned ticket = draw(ch, o.seq, ch.tiles);
+            const unsigned ticket = draw(ch, o.seq, k + 1);
             const int tile = k <= o.last ? o.last - k : k;  // tiles of padding come last
             const int t0 = (tile * W + wave) * SPAN, count = max(0, min(SPAN, o.L - t0));
             const size_t at0 = ((size_t)o.b * p.T + t0) * p.N;
@@ -558,7 +561,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 3) void k_recurrence_grad(cons
                 join_halves<true>(Map{M[c], F[c]}, before[c], all);
                 if (q == 0) sh.part[W - 1 - wave][l * CH + c] = all;
             }
-            find_starts(ch, sh, o.seq, k, k == o.last, W - 1 - wave, [&](int c) __attribute__((always_inline)) {
+            find_starts<true>(ch, sh, o.seq, k, k == o.last, W - 1 - wave, [&](int c) __attribute__((always_inline)) {
                 const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
                 return a.grad_state_out ? a.grad_state_out[(size_t)o.b * p.N + at] : 0.0f;
             });
@@ -661,12 +664,21 @@ __global__ __launch_bounds__(256) void k_recurrence_step(const semicrf_recurrenc
 constexpr int WIDE = 8, WIDE_GRAD = 12;      // wavefronts a workgroup: measured at the kernels
 constexpr int SERVE = 2048;                  // workgroups of a launch
 
+// Backward, whether each chain is one workgroup's, which carries what it passes on along and waits for no one:
+// where there are chains for all compute units, and their last round leaves few of them idle.  In bfloat16 16 x
+// 5,000 x 1,024 (256 chains) 297 us against 350 and 5 to clear what tiles wait for, 32 x 800 114 against 132
+// and 5.  Forward, with three workgroups a compute unit to wait on one another, it is 112 against 118 and 5 at
+// 64 x 800, but 202 against 172 at 16 x 5,000 and 56 against 50 and 5 at 32 x 800 ragged: not taken there.
+bool alone(long chains, bool grad) {
+    return grad && chains >= 256 && ((chains + 255) / 256 * 256 - chains) * 10 <= chains;
+}
+
 // How a call is laid out: channels a lane, wavefronts a workgroup, and the workspace
 struct Plan {
     int CH, W;
     Chain chain;
     int grid;
-    bool fits;
+    bool fits, shared;           // whether workgroups share a chain
     size_t words, states, ticket, part, total;
 };
 
@@ -685,7 +697,8 @@ Plan make_plan(const semicrf_recurrence& p, bool grad) {
     c.chains = (unsigned)seqs;
     // enough workgroups on a chain that all of them together fill the GPU a few times over (chains of
     // short sequences end early)
-    long serve = (SERVE + seqs - 1) / seqs;
+    const bool single = alone(seqs, grad);
+    long serve = single ? 1 : (SERVE + seqs - 1) / seqs;
     serve = serve < c.tiles ? serve : c.tiles;
     q.grid = (int)(seqs * serve);
     size_t at = 0;
@@ -694,8 +707,9 @@ Plan make_plan(const semicrf_recurrence& p, bool grad) {
         at += (bytes + 255) / 256 * 256;
         return r;
     };
-    q.ticket = region(c.tiles > 1 ? seqs * TICKET * sizeof(unsigned) : 1);
-    if (c.tiles > 1) {
+    q.shared = c.tiles > 1 && !single;
+    q.ticket = region(q.shared ? seqs * TICKET * sizeof(unsigned) : 1);
+    if (q.shared) {
         q.words = region(seqs * c.tiles * q.CH * LANES * 8);
         q.states = region(seqs * c.groups * q.CH * LANES * 8);
     }
@@ -706,7 +720,7 @@ Plan make_plan(const semicrf_recurrence& p, bool grad) {
 
 // Binds the plan to its workspace and clears what tiles wait for
 void prepare(Plan& q, void* ws, hipStream_t stream) {
-    if (q.chain.tiles == 1) return;
+    if (!q.shared) return;
     char* w = (char*)ws;
     q.chain.tickets = (unsigned*)(w + q.ticket);
     q.chain.words = (unsigned long long*)(w + q.words);

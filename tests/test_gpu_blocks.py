@@ -206,7 +206,7 @@ def test_recurrence_state_in_place(crf, T, N):  # noqa: F811
     import torch
     from semi_markov_crf_amd import _native, blocks
     torch.manual_seed(T)
-    B = 700 if T < 20 else 3
+    B = 700 if T < 20 or T == 900 else 3
     x, r, i = (torch.randn(B, T, N, device="cuda") for _ in range(3))
     ld, state = dev(decays(N, "weak")), torch.randn(B, N, device="cuda")
     want, end = crf.gated_recurrence(x, r, i, ld, state=state, want_state=True)
@@ -218,6 +218,37 @@ def test_recurrence_state_in_place(crf, T, N):  # noqa: F811
                       n, out.data_ptr(), state.data_ptr(), None, None)
     torch.cuda.synchronize()
     assert rc == 0 and torch.equal(out, want) and torch.equal(state, end)
+
+
+@pytest.mark.parametrize("case", [(300, 200, 128, "bf16", "spread"), (256, 500, 33, "f32", "weak"),
+                                  (520, 300, 8, "f32", "spread"), (800, 150, 40, "bf16", "spread"),
+                                  (1030, 140, 2, "f32", "strong")], ids=lambda c: "-".join(map(str, c)))
+def test_recurrence_of_many_sequences(crf, case):  # noqa: F811
+    """Chains for every compute unit and more, in rounds that come out even or not.  All but a few
+    sequences get no gradient; those few are compared."""
+    import torch
+    B, T, N, typ, dk = case
+    rng = np.random.default_rng(B + T)
+    some = np.array([0, 1, B // 2, B - 2, B - 1])
+    lengths = rng.integers(0, T + 1, B).astype(np.int32)
+    lengths[some[:4]] = T, 0, T - 1, 129
+    x, r, i = (values(rng, (B, T, N), typ) for _ in range(3))
+    g = np.zeros((B, T, N), np.float32)
+    g[some] = values(rng, (5, T, N), typ)
+    lam, state, gs = decays(N, dk), rng.standard_normal((B, N)).astype(np.float32), np.zeros((B, N), np.float32)
+    gs[some] = rng.standard_normal((5, N))
+    args, ln = [put(v, typ, lengths) for v in (x, r, i)] + [dev(lam)], dev(lengths)
+    got, end, starts = crf.gated_recurrence(*args, lengths=ln, state=dev(state), want_state=True, want_starts=True)
+    h, last, eh, elast, _ = ref.recurrence(x[some], r[some], i[some], lam, lengths[some], state[some])
+    at = torch.tensor(some, device="cuda")
+    near(got[at], h, eh, typ, "h")
+    near(end[at], last, elast, "f32", "state")
+    d = crf.gated_recurrence_grad(put(g, typ), *args, starts, lengths=ln, state=dev(state), grad_state=dev(gs))
+    want, bound = ref.recurrence_grad(g[some], x[some], r[some], i[some], lam, lengths[some], state[some], gs[some])
+    for k, v in want.items():
+        near(d["grad_" + k] if k == "log_decay" else d["grad_" + k][at], v, bound[k],
+             "f32" if k in ("log_decay", "state") else typ, k)
+    assert not got[~(torch.arange(T, device="cuda")[None] < ln[:, None])].any()
 
 
 def test_recurrence_broadcast_inputs(crf):  # noqa: F811
