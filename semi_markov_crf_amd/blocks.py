@@ -78,7 +78,7 @@ def gated_recurrence(x, decay_gate, input_gate, log_decay, *, lengths=None, stat
     before every 16th position, which gated_recurrence_grad takes and which carry no gradient."""
     if _tracked(x, decay_gate, input_gate, log_decay, state):
         h, end, starts = _GatedRecurrence.apply(x, decay_gate, input_gate, log_decay, lengths, state,
-                                                want_state, check_status)
+                                                want_state, want_starts, check_status)
     else:
         h, end, starts = _run_recurrence(x, decay_gate, input_gate, log_decay, lengths, state,
                                          want_state, want_starts, workspace, check_status)
@@ -131,16 +131,24 @@ def gated_recurrence_grad(grad_out, x, decay_gate, input_gate, log_decay, starts
 
 class _GatedRecurrence(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, decay_gate, input_gate, log_decay, lengths, state, want_state, check_status):
+    def forward(ctx, x, decay_gate, input_gate, log_decay, lengths, state, want_state, want_starts,
+                check_status):
         h, end, starts = _run_recurrence(x, decay_gate, input_gate, log_decay, lengths, state,
                                          want_state, True, None, check_status)
         ctx.save_for_backward(x, decay_gate, input_gate, log_decay, lengths, state, starts)
+        ctx.set_materialize_grads(False)
+        if not want_starts:
+            return h, end, None
         ctx.mark_non_differentiable(starts)
         return h, end, starts
 
     @staticmethod
     def backward(ctx, g, g_state, _starts):
+        if g is None and g_state is None:
+            return (None,) * 9
         x, decay_gate, input_gate, log_decay, lengths, state, starts = ctx.saved_tensors
+        if g is None:
+            g = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
 
         def grads():
             d = gated_recurrence_grad(g.contiguous(), x, decay_gate, input_gate, log_decay, starts,
@@ -151,7 +159,7 @@ class _GatedRecurrence(torch.autograd.Function):
 
         gx, gr, gi, gl, gs = first_order("gated_recurrence", grads, g, g_state, x, decay_gate,
                                          input_gate, log_decay, state)
-        return gx, gr, gi, gl, None, gs, None, None
+        return gx, gr, gi, gl, None, gs, None, None, None
 
 
 def gated_recurrence_step(x, decay_gate, input_gate, log_decay, state, *, slots=None,
@@ -342,7 +350,7 @@ def token_nll(x, table, targets, *, scale=1.0, lengths=None, want_lse=False, wor
     more gives NaN.  The scores are formed in pieces and not kept.  With want_lse, (loss, lse
     [B, T] float32), which token_nll_grad takes; lse carries no gradient."""
     if _tracked(x, table):
-        loss, lse = _TokenNll.apply(x, table, targets, float(scale), lengths, check_status)
+        loss, lse = _TokenNll.apply(x, table, targets, float(scale), lengths, want_lse, check_status)
     else:
         loss, lse = _run_nll(x, table, targets, scale, lengths, want_lse, workspace, check_status)
     return (loss, lse) if want_lse else loss
@@ -386,15 +394,20 @@ def token_nll_grad(grad_loss, x, table, targets, lse, *, scale=1.0, lengths=None
 
 class _TokenNll(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, table, targets, scale, lengths, check_status):
+    def forward(ctx, x, table, targets, scale, lengths, want_lse, check_status):
         loss, lse = _run_nll(x, table, targets, scale, lengths, True, None, check_status)
         ctx.save_for_backward(x, table, targets, lengths, lse)
         ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        if not want_lse:
+            return loss, None
         ctx.mark_non_differentiable(lse)
         return loss, lse
 
     @staticmethod
     def backward(ctx, g, _lse):
+        if g is None:
+            return (None,) * 7
         x, table, targets, lengths, lse = ctx.saved_tensors
         need_x, need_table = ctx.needs_input_grad[:2]
 
@@ -403,4 +416,4 @@ class _TokenNll(torch.autograd.Function):
                                want_x=need_x, want_table=need_table)
             return d.get("grad_x"), d.get("grad_table")
 
-        return *first_order("token_nll", grads, g, x, table), None, None, None, None
+        return *first_order("token_nll", grads, g, x, table), None, None, None, None, None
