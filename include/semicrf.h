@@ -488,8 +488,7 @@ int semicrf_residual_norm_grad(const semicrf_residual* residual, const float* st
  * lse [B, T] float32, or NULL: the log sum, for the gradient (0 where there is nothing to predict).
  * The scores are formed in pieces and never kept; the gradient holds up to 2 GB of what it makes of
  * them in its workspace.  B * T and V up to 2^22, N <= 32768, (B * T + V + 2^17) * N below 2^36.
- * Workspace:
- * semicrf_token_nll_bytes(..., 0), 256-byte aligned. */
+ * Workspace: semicrf_token_nll_bytes(..., 0), 256-byte aligned. */
 size_t semicrf_token_nll_bytes(int dtype, int B, int T, int V, int N, int grad);
 int semicrf_token_nll(const void* x, const void* table, int dtype, const void* targets,
                       int target_bits, const int32_t* lengths, int B, int T, int V, int N,
