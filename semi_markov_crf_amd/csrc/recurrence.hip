@@ -7,8 +7,9 @@
 //
 // A decay next to 1 is kept as its distance from 1: m = a - 1 = expm1(s) has a relative rounding
 // error, where a = 1 + m would lose what is below 2^-24 and with it time constants of many
-// positions.  h_t = h_{t-1} + m h_{t-1} + b u, and 1 - a^2 = -m (m + 2).  The gradient's factor a, which
-// may be far below 1, is the exponential itself.
+// positions.  h_t = h_{t-1} + m h_{t-1} + b u, and 1 - a^2 = -m (m + 2).  A strong decay is kept as a itself,
+// h_t = a h_{t-1} + b u: by its distance from 1 the state before would leave an error of 2^-24 of its own
+// size, however little of it is left.
 #include "common.h"
 #include "encoder.h"
 #include "gates.h"
@@ -19,25 +20,27 @@ namespace {
 
 constexpr int SPAN = SEMICRF_RECURRENCE_SPAN;
 
-// expm1 for s <= 0, and exp(s).  Below -1/4 the difference costs at most two bits; above, five terms
-// of the series leave s^6 / 5040 < 2^-24.  WEAK: s is known to be -1/4 or more.
+// A decay factor exp(s), s <= 0, as c: a - 1 where the decay is weak (s >= -1/4), else a.  m = a - 1 and e = a in
+// any case.  Below -1/4 the difference costs at most two bits; above, five terms of the series leave
+// s^6 / 5040 < 2^-24.  WEAK: s is known to be -1/4 or more.
 template <bool WEAK = false>
-__device__ __forceinline__ float expm1_neg(float s, float& e) {
+__device__ __forceinline__ float decay(float s, bool& weak, float& m, float& e) {
     float p = fmaf(s, 1.0f / 720.0f, 1.0f / 120.0f);
     p = fmaf(s, p, 1.0f / 24.0f);
     p = fmaf(s, p, 1.0f / 6.0f);
     p = fmaf(s, p, 0.5f);
     p = fmaf(s * s, p, s);
     const float full = WEAK ? 0.0f : fast_exp2(s * LOG2EF);
-    const bool weak = WEAK || s >= -0.25f;
+    weak = WEAK || s >= -0.25f;
     e = weak ? 1.0f + p : full;
-    return weak ? p : full - 1.0f;
+    m = weak ? p : full - 1.0f;
+    return weak ? p : full;
 }
-template <bool WEAK = false>
-__device__ __forceinline__ float expm1_neg(float s) {
-    float e;
-    return expm1_neg<WEAK>(s, e);
+// a v + add, a v
+__device__ __forceinline__ float decayed(bool weak, float c, float v, float add) {
+    return (weak ? v : 0.0f) + fmaf(c, v, add);
 }
+__device__ __forceinline__ float decayed(bool weak, float c, float v) { return fmaf(c, v, weak ? v : 0.0f); }
 
 __device__ __forceinline__ float root(float x) { return __builtin_amdgcn_sqrtf(x); }
 
@@ -106,15 +109,28 @@ __device__ __forceinline__ void store(T* base, unsigned at, const float (&x)[CH]
 }
 
 // ------------------------------------------------------------------ joins
-// The state goes through a stretch of positions as h + (M h + H), M = (product of the a) - 1 and H what
-// the stretch makes of 0.
+// The state goes through a stretch of positions as A h + H, A the product of the a and H what the stretch
+// makes of 0.  M stands for A as c does for a; a weak one has its sign bit set, also where A = 1.
 struct Map {
     float M, H;
 };
-__device__ __forceinline__ Map then(Map a, Map b) {          // a first
-    return {a.M + fmaf(b.M, a.M, b.M), a.H + fmaf(b.M, a.H, b.H)};
+constexpr Map SAME{-0.0f, 0.0f};
+__device__ __forceinline__ bool is_weak(float c) { return (int)__float_as_uint(c) < 0; }
+__device__ __forceinline__ float mark(bool weak, float c) { return weak ? __builtin_copysignf(c, -1.0f) : c; }
+// The product of decays whose logarithms add up to s
+__device__ __forceinline__ float product_of(float s) {
+    bool weak;
+    float m, e;
+    const float c = decay(s, weak, m, e);
+    return mark(weak, c);
 }
-__device__ __forceinline__ float apply(Map a, float h) { return h + fmaf(a.M, h, a.H); }
+__device__ __forceinline__ float apply(Map a, float h) { return decayed(is_weak(a.M), a.M, h, a.H); }
+__device__ __forceinline__ Map then(Map a, Map b) {          // a first
+    const bool wa = is_weak(a.M), wb = is_weak(b.M);
+    const float p = decayed(wb, b.M, a.M, wa ? b.M : 0.0f);
+    // many weak ones make a strong one
+    return {wa && wb ? (p < -0.25f ? 1.0f + p : mark(true, p)) : p, apply(b, a.H)};
+}
 
 // The lower half's value, or the upper's
 template <int UPPER>
@@ -130,7 +146,7 @@ __device__ __forceinline__ void join_halves(Map own, Map& before, Map& all) {
     const bool later = ((threadIdx.x & 63) / LANES) != REVERSED;
     const Map first{of_half<REVERSED>(own.M), of_half<REVERSED>(own.H)};
     all = then(first, Map{of_half<!REVERSED>(own.M), of_half<!REVERSED>(own.H)});
-    before = Map{later ? first.M : 0.0f, later ? first.H : 0.0f};
+    before = Map{later ? first.M : SAME.M, later ? first.H : SAME.H};
 }
 
 // ------------------------------------------------------------------ tiles in order
@@ -195,6 +211,7 @@ __device__ __forceinline__ void await(const unsigned long long* p, size_t stride
 template <int CW, int W>
 struct Shared {
     Map part[W][CW];             // maps of the spans, in the order in which the state goes through them
+    float logs[W][CW];           // and the logarithms of their decays
     Map look[W][CW];             // maps of a wavefront's share of the tiles since the last group
     float base[2][CW];           // the state at the end of the last group, or of the last tile, by turns
     float start[W][CW];          // the state each span starts from
@@ -227,11 +244,16 @@ __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, 
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int c = lane + i * 64;
-            own[i] = Map{0.0f, 0.0f};
+            own[i] = SAME;
             if (CW % 64 && c >= CW) continue;
             if (order == 0 && !last) {
+                float log = 0.0f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) own[i] = then(own[i], sh.part[w][c]);
+                for (int w = 0; w < W; ++w) {
+                    log += sh.logs[w][c];
+                    own[i].H = apply(sh.part[w][c], own[i].H);
+                }
+                own[i].M = product_of(log);
                 if (j < GROUP - 1) publish(words + (size_t)k * CW + c, pack(own[i]));
             }
         }
@@ -241,7 +263,7 @@ __device__ __forceinline__ void find_starts(const Chain& ch, Shared<CW, W>& sh, 
             if (CW % 64 && c >= CW) continue;
             unsigned long long v[U];
             const int n = min(U, j - order * U);
-            Map m{0.0f, 0.0f};
+            Map m = SAME;
             if (n > 0) await(words + (size_t)(g * GROUP + order * U) * CW + c, CW, n, v);
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -319,7 +341,7 @@ __device__ __forceinline__ int first_tile(const Chain& ch, unsigned seq, unsigne
     return got;
 }
 
-// Forward.  Reads x and the gates once: the positions' m and b u stay in registers while the state before
+// Forward.  Reads x and the gates once: the positions' decays and b u stay in registers while the state before
 // them is found.
 //
 // Bound by the vector ALU: an element is about 35 instructions of a cycle a lane row and five of four
@@ -327,7 +349,7 @@ __device__ __forceinline__ int first_tile(const Chain& ch, unsigned seq, unsigne
 // shape takes 470 us in bfloat16 (3.6 TB/s), 1 x 250,001 x 256 in float32 257 (4.0 TB/s).
 //   Two rows of 32 lanes with two channels each, not four of 16 with four: half the maps to make and
 // one join in place of two.  Where no decay of the wavefront's channels is strong the exponential of
-// expm1_neg is not taken: both together 525 -> 497 us.  Three workgroups a compute unit (80 registers):
+// decay is not taken: both together 525 -> 497 us.  Three workgroups a compute unit (80 registers):
 // 497 -> 470.  Loading the next tile while the state is found needs 128 registers and gained nothing
 // (537), nor did tiles of 12 or 16 wavefronts (467 and 502; 32 x 800 x 1,024: 57 and 69 in place of 55).
 template <class T, int CH, int W>
@@ -376,7 +398,8 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 6) void k_recurrence(const Rec
             }
             fetch(k);
             __builtin_amdgcn_sched_barrier(0);          // the loads first, then a few elements at a time
-            float m[POS][CH], bu[POS][CH], sum[CH], H[CH];
+            float a1[POS][CH], bu[POS][CH], sum[CH], H[CH];
+            bool weak[POS][CH];
 #pragma unroll
             for (int c = 0; c < CH; ++c) sum[c] = H[c] = 0.0f;
             if (count < SPAN) close(x, r, g, q * POS, count);
@@ -385,10 +408,11 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 6) void k_recurrence(const Rec
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     const float s = lam[c] * sigmoid(r[i][c]);
-                    m[i][c] = expm1_neg<w.value>(s);
-                    bu[i][c] = root(-m[i][c] * (m[i][c] + 2.0f)) * (sigmoid(g[i][c]) * x[i][c]);
+                    float m, e;
+                    a1[i][c] = decay<w.value>(s, weak[i][c], m, e);
+                    bu[i][c] = root(-m * (m + 2.0f)) * (sigmoid(g[i][c]) * x[i][c]);
                     sum[c] += s;
-                    H[c] += fmaf(m[i][c], H[c], bu[i][c]);
+                    H[c] = decayed(weak[i][c], a1[i][c], H[c], bu[i][c]);
                 }
                 __builtin_amdgcn_sched_barrier(0);      // a few elements at a time
             }
@@ -396,8 +420,12 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 6) void k_recurrence(const Rec
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 Map all;
-                join_halves<false>(Map{expm1_neg(sum[c]), H[c]}, before[c], all);
-                if (q == 0) sh.part[wave][l * CH + c] = all;
+                join_halves<false>(Map{product_of(sum[c]), H[c]}, before[c], all);
+                sum[c] = of_half<0>(sum[c]) + of_half<1>(sum[c]);
+                if (q == 0) {
+                    sh.part[wave][l * CH + c] = all;
+                    sh.logs[wave][l * CH + c] = sum[c];
+                }
             }
             find_starts<false>(ch, sh, o.seq, k, k == o.last, wave, [&](int c) __attribute__((always_inline)) {
                 const int at = min((o.col * LANES + c / CH) * CH, p.N - CH) + c % CH;
@@ -417,7 +445,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 6) void k_recurrence(const Rec
                     const int at = q * POS + i;
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
-                        h[c] += fmaf(m[i][c], h[c], bu[i][c]);
+                        h[c] = decayed(weak[i][c], a1[i][c], h[c], bu[i][c]);
                         y[c] = at < count ? h[c] : 0.0f;
                     }
                     if (t0 + at < p.T) store<T, CH>(out, at * p.N + n, y);
@@ -506,7 +534,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 3) void k_recurrence_grad(cons
             }
             fetch(tile);
             __builtin_amdgcn_sched_barrier(0);
-            float m[POS][CH], kx[POS][CH], ki[POS][CH], kr[POS][CH], kl[POS][CH], M[CH], F[CH];
+            float a1[POS][CH], kx[POS][CH], ki[POS][CH], kr[POS][CH], kl[POS][CH], M[CH], F[CH];
             if (count < SPAN) {
                 close(x, r, g, q * POS, count);
 #pragma unroll
@@ -522,18 +550,24 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 3) void k_recurrence_grad(cons
                     float si, qi;
                     sigmoids(r[i][c], sr[i], qr[i]);
                     sigmoids(g[i][c], si, qi);
-                    const float s = lam[c] * sr[i], mm = m[i][c] = expm1_neg<w.value>(s, av[i]);
-                    const float bb = -mm * (mm + 2.0f), bv = root(bb);
+                    const float s = lam[c] * sr[i];
+                    float m;
+                    bool weak;
+                    a1[i][c] = decay<w.value>(s, weak, m, av[i]);
+                    if (!w.value) a1[i][c] = mark(weak, a1[i][c]);      // masks would take 32 scalar registers
+                    const float bb = -m * (m + 2.0f), bv = root(bb);
                     const float ib = bb > 0x1p-123f ? __builtin_amdgcn_rsqf(bb) : 0.0f;
                     const float xv = x[i][c], u = si * xv;
                     bu[i] = bv * u;
                     sum += s;
-                    H += fmaf(m[i][c], H, bu[i]);
+                    H = decayed(w.value || is_weak(a1[i][c]), a1[i][c], H, bu[i]);
                     aub[i] = av[i] * ib * u;
                     kx[i][c] = bv * si;
                     ki[i][c] = kx[i][c] * xv * qi;
                 }
-                M[c] = expm1_neg(sum);
+                M[c] = product_of(sum);
+                sum = of_half<0>(sum) + of_half<1>(sum);
+                if (q == 0) sh.logs[W - 1 - wave][l * CH + c] = sum;
                 Map before, all;
                 join_halves<false>(Map{M[c], H}, before, all);
                 float h = apply(before, first[c]);
@@ -541,15 +575,15 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 3) void k_recurrence_grad(cons
                 for (int i = 0; i < POS; ++i) {
                     kl[i][c] = av[i] * (h - aub[i]) * sr[i];
                     kr[i][c] = kl[i][c] * lam[c] * qr[i];
-                    h += fmaf(m[i][c], h, bu[i]);
+                    h = decayed(w.value || is_weak(a1[i][c]), a1[i][c], h, bu[i]);
                 }
                 float f = 0.0f;
 #pragma unroll
                 for (int i = POS - 1; i >= 0; --i) {
                     const float e = f + d[i][c];
-                    f = fmaf(m[i][c], e, e);
+                    f = decayed(w.value || is_weak(a1[i][c]), a1[i][c], e);
                     // held until f is known: not moved to where they are used, with what they are made of
-                    asm volatile("" : "+v"(m[i][c]), "+v"(kx[i][c]), "+v"(ki[i][c]), "+v"(kl[i][c]), "+v"(kr[i][c]));
+                    asm volatile("" : "+v"(a1[i][c]), "+v"(kx[i][c]), "+v"(ki[i][c]), "+v"(kl[i][c]), "+v"(kr[i][c]));
                 }
                 F[c] = f;
                 __builtin_amdgcn_sched_barrier(0);
@@ -583,7 +617,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 3) void k_recurrence_grad(cons
                     di[c] = in ? e * ki[i][c] : 0.0f;
                     dr[c] = in ? e * kr[i][c] : 0.0f;
                     dlam[c] += in ? e * kl[i][c] : 0.0f;
-                    f[c] = fmaf(m[i][c], e, e);
+                    f[c] = decayed(w.value || is_weak(a1[i][c]), a1[i][c], e);
                 }
                 if (mine && t0 + at < p.T) {
                     store<T, CH>(gx, at * p.N + n, dx);
@@ -654,8 +688,10 @@ __global__ __launch_bounds__(256) void k_recurrence_step(const semicrf_recurrenc
     const float x = (float)row<T>(p.x, p.x_stride, b, 0)[n];
     const float r = (float)row<T>(p.decay_gate, p.decay_stride, b, 0)[n];
     const float i = (float)row<T>(p.input_gate, p.input_stride, b, 0)[n];
-    const float m = expm1_neg(p.log_decay[n] * sigmoid(r)), h0 = p.state[at];
-    const float h = fmaf(m, h0, root(-m * (m + 2.0f)) * (sigmoid(i) * x)) + h0;
+    bool weak;
+    float m, e;
+    const float c = decay(p.log_decay[n] * sigmoid(r), weak, m, e);
+    const float h = decayed(weak, c, p.state[at], root(-m * (m + 2.0f)) * (sigmoid(i) * x));
     state_out[at] = h;
     out[o] = (T)h;
 }
