@@ -251,14 +251,15 @@ def _run_residual(x, branch, weight, bias, gate, scale, branch_weight, branch_bi
     return r, y, stats
 
 
-def residual_norm_grad(grad_r, grad_y, x, branch, weight, stats, *, gate=None, scale=None,
+def residual_norm_grad(grad_r, grad_y, x, branch, weight, stats, *, bias=None, gate=None, scale=None,
                        norm_branch=False, branch_weight=None, branch_bias=None, center=True,
                        lengths=None, want_params=True, workspace=None, check_status=False) -> dict:
     """Gradients of residual_norm from those of r and y [B, T, N] (None: 0) and the stats it left: a
     dict with grad_x, grad_branch, with a gate grad_gate and, unless want_params is False,
     grad_weight, grad_bias, grad_scale and, with norm_branch, grad_branch_weight and
-    grad_branch_bias [N] in the weights' type (x's where there are none)."""
-    dev, a, wtype = _residual(x, branch, weight, None, gate, scale, norm_branch, branch_weight,
+    grad_branch_bias [N] in the weights' type (x's where there are none).  bias counts for that type
+    only: no gradient depends on it."""
+    dev, a, wtype = _residual(x, branch, weight, bias, gate, scale, norm_branch, branch_weight,
                               branch_bias, center, 0.0, lengths)
     return _residual_grad(dev, a, wtype, grad_r, grad_y, x, gate, stats, want_params, workspace,
                           check_status)
