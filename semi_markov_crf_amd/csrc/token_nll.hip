@@ -610,12 +610,17 @@ __global__ __launch_bounds__(Tl::NT) void k_nll_scores(const Scores p, const Con
                             if (hit == i * 16 + k) at_target[m] = t.acc[i][j][k];
                 }
                 const float ref = most == -__builtin_inff() ? 0.0f : most;
-                float s = sum[j] * fast_exp2(top[j] - ref);
+                // The tile's words first: added to the running sum one by one, V / 8 roundings in a row, those
+                // below half a step of it would be lost however many they are.
+                float s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < Tl::MA; ++i)
+                for (int i = 0; i < Tl::MA; ++i) {
+                    float e[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) s += fast_exp2(t.acc[i][j][k] - ref);
-                sum[j] = s;
+                    for (int k = 0; k < 4; ++k) e[k] = fast_exp2(t.acc[i][j][k] - ref);
+                    s += (e[0] + e[1]) + (e[2] + e[3]);
+                }
+                sum[j] = fmaf(sum[j], fast_exp2(top[j] - ref), s);
                 top[j] = most;
             }
         }
