@@ -486,10 +486,13 @@ int semicrf_residual_norm_grad(const semicrf_residual* residual, const float* st
  * (target_bits 32 or 64), loss [B, T] float32.  A negative target marks a position with nothing to
  * predict: its x is not read and its loss is 0.  A target of V or more gives NaN and the status bit.
  * lse [B, T] float32, or NULL: the log sum, for the gradient (0 where there is nothing to predict).
- * The scores are formed in pieces and never kept; the gradient holds up to 2 GB of what it makes of
- * them in its workspace.  B * T and V up to 2^22, N <= 32768, (B * T + V + 2^17) * N below 2^36.
- * Workspace: semicrf_token_nll_bytes(..., 0), 256-byte aligned. */
+ * The scores are formed in pieces and never kept.  B * T and V up to 2^22, N <= 32768, (B * T + V + 2^17)
+ * * N below 2^36.  Workspace: semicrf_token_nll_bytes(..., 0), 256-byte aligned, is enough for any table;
+ * semicrf_token_nll_table_bytes is what a call with this table needs, which leaves out a copy of it where N
+ * is a multiple of 64 and the table 16-byte aligned (but in the float32 gradient).  Both are for B * T
+ * listed positions, whose number is known on the GPU only. */
 size_t semicrf_token_nll_bytes(int dtype, int B, int T, int V, int N, int grad);
+size_t semicrf_token_nll_table_bytes(int dtype, int B, int T, int V, int N, const void* table, int grad);
 int semicrf_token_nll(const void* x, const void* table, int dtype, const void* targets,
                       int target_bits, const int32_t* lengths, int B, int T, int V, int N,
                       float scale, hipStream_t stream, void* workspace, size_t workspace_bytes,
@@ -497,7 +500,10 @@ int semicrf_token_nll(const void* x, const void* table, int dtype, const void* t
 
 /* Its gradients from those of loss (grad_loss [B, T] float32) and the lse of the forward call:
  * grad_x [B, T, N] (0 where there is nothing to predict) and grad_table [V, N], both of type dtype; either
- * may be NULL.  A target of V or more counts for nothing.  Workspace: semicrf_token_nll_bytes(..., 1). */
+ * may be NULL.  A target of V or more counts for nothing.  Workspace: semicrf_token_nll_bytes(..., 1), or
+ * _table_bytes: two copies of x, one of the table, and softmaxes less targets for a piece of the vocabulary at a
+ * time, of up to 2 GB or, where that is more, 256 words (4 GB for 2^22 positions in float32); with several
+ * pieces also a float32 array shaped like x. */
 int semicrf_token_nll_grad(const float* grad_loss, const void* x, const void* table, int dtype,
                            const void* targets, int target_bits, const int32_t* lengths,
                            const float* lse, int B, int T, int V, int N, float scale,

@@ -110,6 +110,7 @@ SIGNATURES = {
     "semicrf_residual_norm_grad": (_c_int, [_res, _vp, _vp, _vp, _vp, _vp, _c_size, _vp, _vp, _vp,
                                             _vp, _vp]),
     "semicrf_token_nll_bytes": (_c_size, [_c_int] * 6),
+    "semicrf_token_nll_table_bytes": (_c_size, [_c_int] * 5 + [_vp, _c_int]),
     "semicrf_token_nll": (_c_int, [_vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
                                    _c_int, _c_float, _vp, _vp, _c_size, _vp, _vp, _vp]),
     "semicrf_token_nll_grad": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _c_int,

@@ -360,7 +360,7 @@ def token_nll(x, table, targets, *, scale=1.0, lengths=None, want_lse=False, wor
 def _run_nll(x, table, targets, scale, lengths, want_lse, workspace, check_status):
     dev, B, T, V, N, bits = _nll_args(x, table, targets, lengths)
     typ = _TYPES[x.dtype]
-    n = _native.load().semicrf_token_nll_bytes(typ, B, T, V, N, 0)
+    n = _native.load().semicrf_token_nll_table_bytes(typ, B, T, V, N, table.data_ptr(), 0)
     ws = _workspace("semicrf_token_nll", n, x.device, workspace)
     loss = x.new_empty((B, T), dtype=torch.float32)
     lse = torch.empty_like(loss) if want_lse else None
@@ -382,7 +382,7 @@ def token_nll_grad(grad_loss, x, table, targets, lse, *, scale=1.0, lengths=None
     _need("grad_loss", grad_loss, torch.float32, (B, T), dev)
     _need("lse", lse, torch.float32, (B, T), dev)
     typ = _TYPES[x.dtype]
-    n = _native.load().semicrf_token_nll_bytes(typ, B, T, V, N, 1)
+    n = _native.load().semicrf_token_nll_table_bytes(typ, B, T, V, N, table.data_ptr(), 1)
     ws = _workspace("semicrf_token_nll_grad", n, x.device, workspace)
     gx = torch.empty_like(x) if want_x else None
     gt = torch.empty_like(table) if want_table else None

@@ -206,7 +206,8 @@ struct NllArgs {
 };
 constexpr long NLL_MAX_ROWS = 1l << 22;        // of x and of the table: 256 rows of a transposed copy span less than 2^32 bytes
 constexpr int NLL_MAX_N = 32768;
-size_t token_nll_bytes(int dtype, int B, int T, int V, int N, bool grad);
+// table: the array, or NULL for what is enough for any
+size_t token_nll_bytes(int dtype, int B, int T, int V, int N, const void* table, bool grad);
 hipError_t launch_token_nll(const NllArgs& a, void* ws, hipStream_t stream);
 hipError_t launch_token_nll_grad(const NllArgs& a, void* ws, hipStream_t stream);
 

@@ -288,7 +288,11 @@ int semicrf_residual_norm_grad(const semicrf_residual* residual, const float* st
 }
 
 size_t semicrf_token_nll_bytes(int dtype, int B, int T, int V, int N, int grad) {
-    return check_nll_shape(dtype, B, T, V, N) ? 0 : token_nll_bytes(dtype, B, T, V, N, grad != 0);
+    return semicrf_token_nll_table_bytes(dtype, B, T, V, N, nullptr, grad);
+}
+
+size_t semicrf_token_nll_table_bytes(int dtype, int B, int T, int V, int N, const void* table, int grad) {
+    return check_nll_shape(dtype, B, T, V, N) ? 0 : token_nll_bytes(dtype, B, T, V, N, table, grad != 0);
 }
 
 int semicrf_token_nll(const void* x, const void* table, int dtype, const void* targets,
@@ -298,7 +302,7 @@ int semicrf_token_nll(const void* x, const void* table, int dtype, const void* t
     int rc = check_nll(x, table, targets, target_bits, dtype, B, T, V, N, scale);
     if (rc) return rc;
     if (!loss) return SEMICRF_ERR_INVALID;
-    if ((rc = check_ws(workspace, workspace_bytes, token_nll_bytes(dtype, B, T, V, N, false)))) return rc;
+    if ((rc = check_ws(workspace, workspace_bytes, token_nll_bytes(dtype, B, T, V, N, table, false)))) return rc;
     NllArgs a{};
     a.x = x; a.table = table; a.targets = targets; a.target_bits = target_bits; a.lengths = lengths;
     a.dtype = dtype; a.B = B; a.T = T; a.V = V; a.N = N; a.scale = scale;
@@ -314,7 +318,7 @@ int semicrf_token_nll_grad(const float* grad_loss, const void* x, const void* ta
     int rc = check_nll(x, table, targets, target_bits, dtype, B, T, V, N, scale);
     if (rc) return rc;
     if (!grad_loss || !lse || (!grad_x && !grad_table)) return SEMICRF_ERR_INVALID;
-    if ((rc = check_ws(workspace, workspace_bytes, token_nll_bytes(dtype, B, T, V, N, true)))) return rc;
+    if ((rc = check_ws(workspace, workspace_bytes, token_nll_bytes(dtype, B, T, V, N, table, true)))) return rc;
     NllArgs a{};
     a.x = x; a.table = table; a.targets = targets; a.target_bits = target_bits; a.lengths = lengths;
     a.grad_loss = grad_loss; a.lse_in = lse;

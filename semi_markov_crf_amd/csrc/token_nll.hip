@@ -967,7 +967,7 @@ size_t region(size_t& at, size_t bytes) {
     return r;
 }
 
-// `table`: the array, or NULL where only the size is asked for (then it is taken as unaligned)
+// `table`: the array, or NULL where the size for any is asked for (then it is taken as unaligned)
 Plan make_plan(int dtype, int B, int T, int V, int N, bool grad, const void* table) {
     Plan p{};
     const long e = dtype == SEMICRF_F32 ? 4 : 2;
@@ -1156,8 +1156,8 @@ hipError_t run_nll_grad(const NllArgs& a, void* ws, hipStream_t stream) {
 
 }  // namespace
 
-size_t token_nll_bytes(int dtype, int B, int T, int V, int N, bool grad) {
-    return make_plan(dtype, B, T, V, N, grad, nullptr).total;
+size_t token_nll_bytes(int dtype, int B, int T, int V, int N, const void* table, bool grad) {
+    return make_plan(dtype, B, T, V, N, grad, table).total;
 }
 
 hipError_t launch_token_nll(const NllArgs& a, void* ws, hipStream_t stream) {
