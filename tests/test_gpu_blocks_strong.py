@@ -139,3 +139,28 @@ def test_a_reset_leaves_what_comes_after(crf):  # noqa: F811
         for h in (crf.gated_recurrence(x, big, big, ld, state=state)[0],
                   crf.gated_recurrence_step(x[0], big[0], big[0], ld, state)):
             assert np.all(np.abs(host(h) - want) <= (abs(lam) + 16) * U * want), lam
+
+
+@pytest.mark.parametrize("case", [(2, 16, 64, "f32"), (3, 333, 70, "f32"), (2, 900, 129, "bf16"), (1, 5000, 8, "f32")],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_weak_decays_that_add_up(crf, case):  # noqa: F811
+    """No decay is strong, but those of a few positions together are: a state of 1,000 fades to nothing beside inputs
+    that are kept out."""
+    B, T, N, typ = case
+    print(f"\n[recurrence, weak decays {case}]", flush=True)
+    rng = np.random.default_rng(T)
+    x, r, i, g, _, state, gs = draw(rng, B, T, N, typ)
+    i = host(dev(np.full(i.shape, -40.0, np.float32), typ))
+    g[:, : T - 1] *= 1e-12
+    g = host(dev(g.astype(np.float32), typ))
+    lam = np.resize(np.float32([-0.25, -0.2, -0.1, -0.05]), N)
+    L = np.full(B, T)
+    h, end, _, eh, eend, _ = recurrence(x, r, i, lam, L, state)
+    args = [dev(v.astype(np.float32), typ) for v in (x, r, i)] + [dev(lam)]
+    got, gend, starts = crf.gated_recurrence(*args, state=dev(state), want_state=True, want_starts=True)
+    near(got, h, U * eh, typ, "h")
+    near(gend, end, U * eend, "f32", "state")
+    d = crf.gated_recurrence_grad(dev(g.astype(np.float32), typ), *args, starts, state=dev(state), grad_state=dev(gs))
+    want, err = recurrence_grad(g, x, r, i, lam, L, state, gs)
+    for k, v in want.items():
+        near(d["grad_" + k], v, err[k], "f32" if k in ("log_decay", "state") else typ, k)
