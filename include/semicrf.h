@@ -500,7 +500,11 @@ int semicrf_token_nll(const void* x, const void* table, int dtype, const void* t
 
 /* Its gradients from those of loss (grad_loss [B, T] float32) and the lse of the forward call:
  * grad_x [B, T, N] (0 where there is nothing to predict) and grad_table [V, N], both of type dtype; either
- * may be NULL.  A target of V or more counts for nothing.  Workspace: semicrf_token_nll_bytes(..., 1), or
+ * may be NULL.  A target of V or more counts for nothing.  In bfloat16 the numbers that are multiplied are held
+ * in fp16, scaled to the top of its range, and summed in float32: softmax less target (11 bits down to 2^-29, 0
+ * below 2^-40, so that a word that is nowhere likelier has no gradient), the table (as it is down to 2^-28 of its
+ * largest value) and x times the row's grad_loss (11 bits down to 2^-28 of the largest |x| times the largest
+ * |grad_loss|, 0 from 2^-39 on; for grad_table only).  Workspace: semicrf_token_nll_bytes(..., 1), or
  * _table_bytes: two copies of x, one of the table, and softmaxes less targets for a piece of the vocabulary at a
  * time, of up to 2 GB or, where that is more, 256 words (4 GB for 2^22 positions in float32); with several
  * pieces also a float32 array shaped like x. */

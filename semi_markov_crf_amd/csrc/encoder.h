@@ -1,5 +1,6 @@
 // Shared by the encoder operators (embedding, layer norm, decayed linear attention, gated
-// recurrence, residual norm, token loss): element types, 16-byte pieces of rows, and the interfaces between encoder_api.cpp and the kernels.
+// recurrence, residual norm, token loss): element types, 16-byte pieces of rows, and the
+// interfaces between encoder_api.cpp and the kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -204,7 +205,7 @@ struct NllArgs {
     void *grad_x, *grad_table;
     int32_t* status;
 };
-constexpr long NLL_MAX_ROWS = 1l << 22;        // of x and of the table: 256 rows of a transposed copy span less than 2^32 bytes
+constexpr long NLL_MAX_ROWS = 1l << 22;        // of x and of the table: 256 rows of p span at most 2^32 bytes
 constexpr int NLL_MAX_N = 32768;
 // table: the array, or NULL for what is enough for any
 size_t token_nll_bytes(int dtype, int B, int T, int V, int N, const void* table, bool grad);

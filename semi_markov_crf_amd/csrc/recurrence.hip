@@ -344,9 +344,12 @@ __device__ __forceinline__ int first_tile(const Chain& ch, unsigned seq, unsigne
 // Forward.  Reads x and the gates once: the positions' decays and b u stay in registers while the state before
 // them is found.
 //
-// Bound by the vector ALU: an element is about 35 instructions of a cycle a lane row and five of four
-// (two sigmoids and the root), which is 300 us for 4 x 100,000 x 512, as long as its 1.7 GB take.  That
-// shape takes 470 us in bfloat16 (3.6 TB/s), 1 x 250,001 x 256 in float32 257 (4.0 TB/s).
+// Bound by neither alone: an element is about 35 instructions of a cycle a lane row and five of four (two
+// sigmoids and the root), which is 300 us for 4 x 100,000 x 512 in bfloat16, and its 1.7 GB are 327 us; it takes
+// 475 (3.6 TB/s).  A workgroup's loads wait for its arithmetic and the other way round, and three on a compute
+// unit make up for a part of it only.  1 x 250,001 x 256 in float32 takes 245 to 300 on different cards (4.2 to
+// 3.4 TB/s).  Strong decays in all channels cost 5 % on long sequences, 503 us for the first (32 x 800 x 1,024: 65
+// against 59).
 //   Two rows of 32 lanes with two channels each, not four of 16 with four: half the maps to make and
 // one join in place of two.  Where no decay of the wavefront's channels is strong the exponential of
 // decay is not taken: both together 525 -> 497 us.  Three workgroups a compute unit (80 registers):
@@ -470,9 +473,10 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 6) void k_recurrence(const Rec
 // forward from the span's stored start.  dpart [tile x sequence][N]: the tile's share of dlog_decay.
 //
 // Five factors an element stay in registers (168), so that inputs are read and exponentials taken once.
-// Bound by the vector ALU at three wavefronts on a SIMD: about 80 instructions an element, of them six of
-// four cycles.  One workgroup of 12 wavefronts a compute unit: 4 x 100,000 x 512 in bfloat16 840 us (3.5
-// TB/s), against 890 with 8 and 1,110 with two workgroups of 6.
+// About 80 instructions an element, of them six of four cycles: 510 us for 4 x 100,000 x 512 in bfloat16, where
+// the bytes take 565; with one workgroup of 12 wavefronts a compute unit, whose loads and arithmetic take turns,
+// 858 (3.4 TB/s), and 925 with strong decays in all channels.  (Before those were held as factors 840, against 890
+// with 8 wavefronts and 1,110 with two workgroups of 6.)
 template <class T, int CH, int W>
 __global__ __launch_bounds__(64 * W, W == 1 ? 2 : 3) void k_recurrence_grad(const RecArgs a, const Chain ch,
                                                                                   float* dpart) {
@@ -698,13 +702,18 @@ __global__ __launch_bounds__(256) void k_recurrence_step(const semicrf_recurrenc
 
 // ------------------------------------------------------------------ host
 constexpr int WIDE = 8, WIDE_GRAD = 12;      // wavefronts a workgroup: measured at the kernels
-constexpr int SERVE = 2048;                  // workgroups of a launch
+// Workgroups of a launch: 32 x 800 x 1,024 forward 56 us with 1,024 to 4,096, 63 with 512; longer sequences
+// within 3 % of one another, but 1 x 250,001 x 256 in float32 forward (260 with 512, 292 to 297 with more).
+constexpr int SERVE = 2048;
 
 // Backward, whether each chain is one workgroup's, which carries what it passes on along and waits for no one:
 // where there are chains for all compute units, and their last round leaves few of them idle.  In bfloat16 16 x
 // 5,000 x 1,024 (256 chains) 297 us against 350 and 5 to clear what tiles wait for, 32 x 800 114 against 132
-// and 5.  Forward, with three workgroups a compute unit to wait on one another, it is 112 against 118 and 5 at
-// 64 x 800, but 202 against 172 at 16 x 5,000 and 56 against 50 and 5 at 32 x 800 ragged: not taken there.
+// and 5.  Chains of 800 and of 3,000 positions: 240 (all at once, 6 % idle) 61 against 72 and 181 against 211; 480
+// (6 % of the last round idle) 117 against 137 and 343 against 397; 384 (25 %) 110 against 112, but 334 against
+// 322; 272 (47 %) 98 against 100, but 318 against 293.  Forward, with three workgroups a compute unit to wait on
+// one another, it is 112 against 118 and 5 at 64 x 800, but 202 against 172 at 16 x 5,000 and 56 against 50 and 5
+// at 32 x 800 ragged: not taken there.
 bool alone(long chains, bool grad) {
     return grad && chains >= 256 && ((chains + 255) / 256 * 256 - chains) * 10 <= chains;
 }

@@ -16,15 +16,20 @@
 // Scores are summed and exponentiated in registers; a lane holds scores of the same rows of x for all
 // tiles of the vocabulary it sees, so that maximum and sum run along without an exchange.
 //
-// Rounding (bfloat16): scores are exact products summed in fp32.  p, W and x enter the second
-// products in fp16, scaled by powers of two to the top of its range: W and x lose nothing within 2^29
-// of their largest value, and p has 11 bits down to 2^-29, so that the gradients' own rounding is
-// what is seen (p in bfloat16 would add an error as large as that).  In float32 everything is float32.
+// Rounding (bfloat16): scores are exact products summed in fp32.  The second products' operands are in
+// fp16, each scaled by a power of two to the top of its range: 11 bits down to 2^-28 of the largest, fewer
+// below, 0 from 2^-39 on.  W has 8 bits of its own and loses nothing down to 2^-28 of its largest value.  p
+// (at most 1) has 11 bits down to 2^-29, and is 0 below 2^-40: a word that is nowhere more likely, nor a target,
+// has no gradient.  x enters dW times its row's gradient, rounded to 11 bits; the largest |x| times the
+// largest |gradient| is the top.  So the gradients' own rounding is what is seen (p in bfloat16 would add an
+// error as large as that): off by 0.00167 in the 2-norm, as with everything in fp32.  In float32 everything is
+// float32.
 //
 // Bound by the matrix cores.  16,000 rows of 1,024 over 50,001 words in bfloat16, 1.64 * 10^12 operations a
-// product (a large product of the library reaches 1,230 TFLOP/s): scores 1,416 us (1,160 TFLOP/s), p 1,603
-// (1,020: it stores 1.6 GB), dx 1,309 (1,250), dW 1,344 (1,220); all else of a loss and its gradient 140.  The
-// gradient forms the scores a second time: the forward pass would have to keep 1.6 GB for it.
+// product (a large product of the library reaches 1,230 TFLOP/s): scores 1,400 us (1,170 TFLOP/s), p 1,560 to
+// 1,600 (1,040: it stores 1.6 GB), dx 1,290 (1,270), dW 1,360 (1,200); all else of a loss and its gradient 140.  The
+// gradient forms the scores a second time: the forward pass would have to keep 1.6 GB for it.  In float32 (a large
+// product: 153 TFLOP/s) 16,000 rows of 1,024 over 8,192 words take 1,958 us (137 TFLOP/s), their gradient 5,834 (138).
 #include "common.h"
 #include "encoder.h"
 
@@ -519,7 +524,8 @@ __device__ __forceinline__ void in_groups(int tile, int rows, int cols, int& r, 
 }
 
 // How many workgroups share the vocabulary of a tile of rows: the number that leaves the least for the
-// busiest one.  All lanes get the same.
+// busiest one, of up to four rounds of items.  All lanes get the same.  25,600 rows of 1,024 over 50,001 words:
+// one round at most 2,566 us, 2, 4 or 8 2,204 to 2,213; 100 to 16,000 rows within 2 % whichever.
 __device__ __forceinline__ int vocab_split(int mt, int vt, int wgs) {
     const int s = (threadIdx.x & 63) + 1;
     unsigned cost = 0xffffffffu;
@@ -783,7 +789,10 @@ struct Product {
 };
 
 // Tiles are taken whole, a round of all workgroups after the other; those of the last round, if they are
-// few, are shared out along the contracted axis, in shares of at least eight steps.
+// few, are shared out along the contracted axis, in at most 16 shares of at least eight steps.  The gradient of
+// 15,000 rows of 512 over 4,096 words in bfloat16: 284 us, 436 without shares; of 6,000 of 768 over 1,000 125 and
+// 163, 126 with at most 8 shares, 124 with 32.  Shares of 4 or 16 steps: 121 and 112 there, but 2,000 of 512 over
+// 3,000 words 85 with either in place of 81, 500 of 256 over 2,000 in float32 85 and 120 in place of 94.
 struct Rounds {
     int whole, rest, shares, total;      // whole tiles, tiles shared out, shares of each, items
 };
@@ -933,7 +942,10 @@ template <class T, Form FA, Form FB> using Small = Tile<T, FA, FB, 64, 64, 2, 2>
 long up(long n, long m) { return (n + m - 1) / m * m; }
 
 // The size whose busiest workgroup is done first: steps of the tiles and shares it takes, times what a step
-// takes with the CU's workgroups at work (a large tile's as unit).
+// takes with the CU's workgroups at work (a large tile's as unit).  Scores of 16,384 rows of 1,024 over 16,384 words
+// in bfloat16, whole rounds at every size, take 498, 665 and 849 us: 1, 0.67 and 0.43 a step.  What is picked is the
+// fastest or within 2 % of it: 4,096 x 1,024 x 4,096 60 us (71 and 81 with the others), gradient of x at 1,024 x
+// 512 x 2,048 49 (58, 78), in float32 85 (138, 239); but scores of 300 x 256 x 1,000 27 where medium takes 25.
 Size pick(long a, long b, long nk, bool split) {
     constexpr double step[3] = {1.0, 0.6, 0.4};
     Size best = LARGE;

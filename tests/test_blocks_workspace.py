@@ -33,7 +33,8 @@ def test_an_aligned_table_is_not_copied(lib, dtype, e, shape):
         # a call takes what its own table needs, and no less
         for at, need in ((0x1010, this), (0x1002, any_table)):
             if grad:
-                rc = lib.semicrf_token_nll_grad(P, P, at, dtype, P, 32, None, P, *shape, 1.0, None, P, need - 1, P, P, None)
+                rc = lib.semicrf_token_nll_grad(P, P, at, dtype, P, 32, None, P, *shape, 1.0, None, P, need - 1, P, P,
+                                                None)
             else:
                 rc = lib.semicrf_token_nll(P, at, dtype, P, 32, None, *shape, 1.0, None, P, need - 1, P, None, None)
             assert rc == WORKSPACE
@@ -41,7 +42,8 @@ def test_an_aligned_table_is_not_copied(lib, dtype, e, shape):
 
 def test_a_width_of_no_whole_steps_is_copied(lib):
     for N in (63, 65, 100):
-        assert lib.semicrf_token_nll_table_bytes(1, 2, 3, 50, N, 0x1000, 0) == lib.semicrf_token_nll_bytes(1, 2, 3, 50, N, 0)
+        size = lib.semicrf_token_nll_bytes(1, 2, 3, 50, N, 0)
+        assert lib.semicrf_token_nll_table_bytes(1, 2, 3, 50, N, 0x1000, 0) == size
     assert lib.semicrf_token_nll_table_bytes(1, 2, 3, 50, 0, 0x1000, 0) == 0
 
 

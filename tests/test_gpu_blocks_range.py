@@ -31,8 +31,8 @@ def held(v, top):
 def test_gradients_keep_their_range(crf, case):  # noqa: F811
     """Columns of x and of the table down to 2^-27 of the largest, row gradients over 2^20, words whose probability
     falls to 2^-60: gradients to within the rounding of what enters the products, element by element.  p, at most 1
-    and brought to 2^15, is held from 2^-40 on, in 11 bits from 2^-29 on; the table exactly to 2^-28 of its largest value; x times the row's
-    gradient as fp16 below the largest |x| times the largest gradient."""
+    and brought to 2^15, is held from 2^-40 on, in 11 bits from 2^-29 on; the table exactly to 2^-28 of its largest
+    value; x times the row's gradient as fp16 below the largest |x| times the largest gradient."""
     M, N, V = case
     rng = np.random.default_rng(M)
 
